@@ -45,6 +45,36 @@ class LayerDesc(ctypes.Structure):
     ]
 
 
+class Int4Desc(ctypes.Structure):
+    """Mirror of `oscar_int4_desc`."""
+    _fields_ = [
+        ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+        ("max_pages_per_seq", c_int32), ("max_len", c_int32), ("n_pages", c_int64),
+        ("tau_k", c_float), ("tau_v", c_float), ("pages", c_void_p), ("page_table", c_void_p),
+        ("seq_len", c_void_p), ("dev_status", c_void_p), ("quant_group_k", c_int32), ("quant_group_v", c_int32),
+    ]
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of `oscar_rope_desc`."""
+    _fields_ = [("cos_sin", c_void_p), ("n_positions", c_int64), ("rot_dim", c_int32), ("interleaved", c_int32)]
+
+
+class ScoreDesc(ctypes.Structure):
+    """Mirror of `oscar_score_desc`."""
+    _fields_ = [("scale", c_float), ("softcap", c_float), ("window", c_int32), ("reserved", c_int32),
+                ("slopes", c_void_p)]
+
+
+class PromptDesc(ctypes.Structure):
+    """Mirror of `oscar_prompt_desc`."""
+    _fields_ = [
+        ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+        ("max_q", c_int32), ("max_k", c_int32), ("causal", c_int32), ("reserved", c_int32),
+        ("total_q", c_int64), ("total_k", c_int64), ("dev_status", c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise RuntimeError("liboscar.so is not built (%s); run bit_rotated_kv_split_gb300.build" % LIB_PATH)
@@ -76,6 +106,11 @@ def _load():
         "oscar_decode_attention_static": (c_int32, [ctypes.POINTER(LayerDesc), P, P, P]),
         "oscar_decode_step": (c_int32, [ctypes.POINTER(LayerDesc), P, P, c_size_t, P, P, c_int64, c_int64, P, P,
                                         P, c_int32, P, P, P, P, P, c_size_t, P, ctypes.c_uint32, P]),
+        "oscar_int4_block_bytes": (c_int64, [c_int32, c_int32, c_int32]),
+        "oscar_rope_append_int4": (c_int32, [P, P, P, c_int64, P, c_int64, P, c_int64, P, P, P, c_int32, P, P, P]),
+        "oscar_gather_int4": (c_int32, [P, P, P, c_int32, P, c_int64, P, c_int64, P]),
+        "oscar_decode_attention_int4": (c_int32, [P, P, P, c_int64, P, P, P, P]),
+        "oscar_prompt_attention": (c_int32, [P, P, P, c_int64, P, c_int64, P, c_int64, P, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -289,3 +324,172 @@ def oscar_decode_attention_static(desc: LayerDesc, q, out, stream=None) -> None:
     """Decode attention with the library's fixed workspace (no allocation by anyone)."""
     _check("oscar_decode_attention_static", lib.oscar_decode_attention_static(
         ctypes.byref(desc), _ptr(q), _ptr(out), _stream(stream)))
+
+
+# ---------------------------------------------------------------- 4-bit layers
+
+def oscar_int4_block_bytes(head_dim: int, quant_group_k: int = 0, quant_group_v: int = 0) -> int:
+    """Bytes of one (page, KV head) block of a 4-bit layer; 0 for an invalid head size or group."""
+    return lib.oscar_int4_block_bytes(int(head_dim), int(quant_group_k), int(quant_group_v))
+
+
+def rope_desc(cos_sin, rot_dim: int, interleaved: bool = False) -> RopeDesc:
+    """Position rotation by cos_sin [n_positions][rot_dim] fp32 (device): rot_dim / 2 cosines, then the sines.
+
+    The descriptor keeps the tensor alive.
+    """
+    d = RopeDesc()
+    if rot_dim:
+        if cos_sin.dim() != 2 or cos_sin.shape[1] != rot_dim or str(cos_sin.dtype) != "torch.float32" \
+                or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be contiguous float32 [n_positions][rot_dim]")
+        d.cos_sin, d.n_positions = cos_sin.data_ptr(), cos_sin.shape[0]
+        d.keep = cos_sin
+    d.rot_dim, d.interleaved = int(rot_dim), int(bool(interleaved))
+    return d
+
+
+def score_desc(scale: float = 0.0, softcap: float = 0.0, window: int = 0, slopes=None) -> ScoreDesc:
+    """Form of the scores: scale (0 = 1 / sqrt(head_dim)), tanh cap, window, slopes [H_q] fp32 (device).
+
+    The descriptor keeps the slopes alive.
+    """
+    d = ScoreDesc()
+    d.scale, d.softcap, d.window = float(scale), float(softcap), int(window)
+    if slopes is not None:
+        if str(slopes.dtype) != "torch.float32" or slopes.dim() != 1 or not slopes.is_contiguous():
+            raise ValueError("slopes must be contiguous float32 [n_q_heads]")
+        d.slopes = slopes.data_ptr()
+        d.n_slopes, d.keep = slopes.shape[0], slopes
+    return d
+
+
+def prompt_desc(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_q: int, max_k: int, total_q: int,
+                total_k: int, causal: bool = True, dev_status=None) -> PromptDesc:
+    """A batch of packed prompts: bounds on one request's queries and keys, rows in all."""
+    d = PromptDesc()
+    d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim = int(batch), int(n_q_heads), int(n_kv_heads), int(head_dim)
+    d.max_q, d.max_k, d.total_q, d.total_k = int(max_q), int(max_k), int(total_q), int(total_k)
+    d.causal = int(bool(causal))
+    if dev_status is not None:
+        d.dev_status = dev_status.data_ptr()
+        d.keep = dev_status
+    return d
+
+
+def _heads(name, t, heads, d):
+    """Row stride of bf16 rows t [n][heads][d] (bfloat16, or its bits as uint16) whose heads lie side by side."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.element_size() != 2:
+        raise ValueError("%s must be bfloat16 [n][%d][%d]" % (name, heads, d))
+    st = t.stride()
+    if t.shape[0] == 0:
+        return heads * d
+    if st[2] != 1 or (heads > 1 and st[1] != d):
+        raise ValueError("%s: the heads of a row must lie side by side" % name)
+    return heads * d if t.shape[0] == 1 else st[0]
+
+
+def _index(name, t, n):
+    if t is not None and (t.dim() != 1 or t.shape[0] < n or t.stride(0) != 1 or str(t.dtype) != "torch.int32"):
+        raise ValueError("%s must be contiguous int32 with at least %d entries" % (name, n))
+
+
+def _contiguous(name, t, shape, itemsize):
+    if t is not None and (tuple(t.shape) != shape or t.element_size() != itemsize or not t.is_contiguous()):
+        raise ValueError("%s must be contiguous %s" % (name, list(shape)))
+
+
+def _on_device(name, t, stream, *args):
+    """Calls the library with t's device current and, without a stream, on that device's current stream."""
+    import torch
+    fn = getattr(lib, name)
+    index = t.device.index
+    if index is None or index == torch.cuda.current_device():
+        _check(name, fn(*args, _stream(stream)))
+        return
+    with torch.cuda.device(index):
+        _check(name, fn(*args, _stream(stream)))
+
+
+def _ref(d):
+    return None if d is None else ctypes.byref(d)
+
+
+def _slopes_ok(score, heads):
+    if score is not None and score.slopes and getattr(score, "n_slopes", heads) != heads:
+        raise ValueError("score: %d slopes for %d query heads" % (score.n_slopes, heads))
+
+
+def oscar_rope_append_int4(desc: Int4Desc, rope, q, k, v, dst_req, dst_pos, q_out, k_out=None, rope_pos=None,
+                           stream=None) -> None:
+    """Rotates q [n][H_q][d] and k [n][H_kv][d] (bf16) by position into q_out, k_out and appends k, v to the pages.
+
+    q and q_out may both be None; k_out may be None.  Rows may be strided (slices of one projection's output).
+    """
+    hq, hk, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, int(k.shape[0])
+    qs = _heads("q", q, hq, d) if q is not None else 0
+    ks, vs = _heads("k", k, hk, d), _heads("v", v, hk, d)
+    if v.shape[0] != n or (q is not None and q.shape[0] != n):
+        raise ValueError("q, k and v must have one row count")
+    _index("dst_req", dst_req, n), _index("dst_pos", dst_pos, n), _index("rope_pos", rope_pos, n)
+    _contiguous("q_out", q_out, (n, hq, d), 2)
+    _contiguous("k_out", k_out, (n, hk, d), 2)
+    _on_device("oscar_rope_append_int4", k, stream, ctypes.byref(desc), _ref(rope), _ptr(q), qs, _ptr(k), ks,
+               _ptr(v), vs, _ptr(dst_req), _ptr(dst_pos), _ptr(rope_pos), n, _ptr(q_out), _ptr(k_out))
+
+
+def oscar_gather_int4(desc: Int4Desc, src_req, src_pos, k_out, v_out, stream=None) -> None:
+    """Cached rows (src_req[i], src_pos[i]) as bf16 into k_out, v_out [n][H_kv][d] (rows may be strided)."""
+    hk, d, n = desc.n_kv_heads, desc.head_dim, int(k_out.shape[0])
+    ks, vs = _heads("k_out", k_out, hk, d), _heads("v_out", v_out, hk, d)
+    if v_out.shape[0] != n:
+        raise ValueError("k_out and v_out must have one row count")
+    _index("src_req", src_req, n), _index("src_pos", src_pos, n)
+    _on_device("oscar_gather_int4", k_out, stream, ctypes.byref(desc), _ptr(src_req), _ptr(src_pos), n,
+               _ptr(k_out), ks, _ptr(v_out), vs)
+
+
+def oscar_decode_int4_workspace_bytes(desc: Int4Desc) -> int:
+    size = c_size_t(0)
+    _check("oscar_decode_attention_int4", lib.oscar_decode_attention_int4(
+        ctypes.byref(desc), None, None, 0, None, None, ctypes.byref(size), None))
+    return size.value
+
+
+def oscar_decode_attention_int4(desc: Int4Desc, q, out, workspace, score=None, stream=None) -> None:
+    """out [B][H_q][d] bf16 = attention of one query per request q [B][H_q][d] over the 4-bit cache."""
+    hq, d, b = desc.n_q_heads, desc.head_dim, desc.batch
+    qs = _heads("q", q, hq, d)
+    if q.shape[0] != b:
+        raise ValueError("q must have one row per request")
+    _contiguous("out", out, (b, hq, d), 2)
+    _slopes_ok(score, hq)
+    size = c_size_t(workspace.numel() * workspace.element_size())
+    _on_device("oscar_decode_attention_int4", q, stream, ctypes.byref(desc), _ref(score), _ptr(q), qs, _ptr(out),
+               _ptr(workspace), ctypes.byref(size))
+
+
+def oscar_prompt_workspace_bytes(desc: PromptDesc) -> int:
+    size = c_size_t(0)
+    _check("oscar_prompt_attention", lib.oscar_prompt_attention(
+        ctypes.byref(desc), None, None, 0, None, 0, None, 0, None, None, None, None, None, None,
+        ctypes.byref(size), None))
+    return size.value
+
+
+def oscar_prompt_attention(desc: PromptDesc, q, k, v, cu_q, cu_k, out, workspace, score=None, prefix_len=None,
+                           lse=None, stream=None) -> None:
+    """out [total_q][H_q][d] bf16 (and lse [total_q][H_q] fp32) of packed prompts; rows cu_q / cu_k [B + 1] int32."""
+    hq, hk, d = desc.n_q_heads, desc.n_kv_heads, desc.head_dim
+    qs, ks, vs = _heads("q", q, hq, d), _heads("k", k, hk, d), _heads("v", v, hk, d)
+    if q.shape[0] != desc.total_q or k.shape[0] != desc.total_k or v.shape[0] != desc.total_k:
+        raise ValueError("q must have total_q rows, k and v total_k")
+    _index("cu_q", cu_q, desc.batch + 1), _index("cu_k", cu_k, desc.batch + 1)
+    _index("prefix_len", prefix_len, desc.batch)
+    _contiguous("out", out, (desc.total_q, hq, d), 2)
+    _contiguous("lse", lse, (desc.total_q, hq), 4)
+    _slopes_ok(score, hq)
+    size = c_size_t(workspace.numel() * workspace.element_size())
+    _on_device("oscar_prompt_attention", q, stream, ctypes.byref(desc), _ref(score), _ptr(q), qs, _ptr(k), ks,
+               _ptr(v), vs, _ptr(cu_q), _ptr(cu_k), _ptr(prefix_len), _ptr(out), _ptr(lse), _ptr(workspace),
+               ctypes.byref(size))

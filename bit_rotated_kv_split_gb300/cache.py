@@ -1,15 +1,16 @@
-"""Device storage of one attention layer's three-segment token pool.
+"""Device storage of one attention layer: the three-segment token pool of a
+two-bit layer (LayerCache) or the pages of a 4-bit layer (Int4Cache).
 
-Host-side plumbing only: it allocates the tensors that `oscar_layer_desc`
-points at (page pool, page table, lengths, BF16 sink and recent ring,
-rotations, device status word) and fills the descriptor.  All computation on
-them happens in liboscar.so.
+Host-side plumbing only: it allocates the tensors that `oscar_layer_desc` or
+`oscar_int4_desc` points at (page pool, page table, lengths, BF16 sink and
+recent ring, rotations, device status word) and fills the descriptor.  All
+computation on them happens in liboscar.so.
 """
 from __future__ import annotations
 
 import torch
 
-from .binding import LayerDesc, oscar_block_bytes
+from .binding import Int4Desc, LayerDesc, oscar_block_bytes, oscar_int4_block_bytes
 
 HEAD_DIM = 128
 PAGE_TOKENS = 16
@@ -69,5 +70,37 @@ class LayerCache:
                 d.levels_k[i], d.levels_v[i] = self.levels_k[i], self.levels_v[i]
         for name in ("pages", "page_table", "hist_len", "sink_k", "sink_v", "sink_len", "recent_k",
                      "recent_v", "recent_len", "recent_start", "r_k", "r_v", "dev_status"):
+            setattr(d, name, getattr(self, name).data_ptr())
+        return d
+
+
+class Int4Cache:
+    """Pages, page table and lengths of one 4-bit layer for `batch` requests."""
+
+    def __init__(self, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_pages_per_seq: int,
+                 n_pages: int, tau_k: float = 65504.0, tau_v: float = 65504.0, device="cuda",
+                 quant_group_k: int = 0, quant_group_v: int = 0):
+        self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim = batch, n_q_heads, n_kv_heads, head_dim
+        self.quant_group_k, self.quant_group_v = int(quant_group_k), int(quant_group_v)
+        self.block_bytes = oscar_int4_block_bytes(head_dim, self.quant_group_k, self.quant_group_v)
+        if self.block_bytes <= 0:
+            raise ValueError("head_dim must be 64 or 128, quantisation groups 32, 64 or 128 and at most head_dim")
+        self.max_pages_per_seq, self.n_pages = max_pages_per_seq, n_pages
+        self.tau_k, self.tau_v = float(tau_k), float(tau_v)
+        dev = torch.device(device)
+        self.pages = torch.zeros(n_pages * n_kv_heads * self.block_bytes, dtype=torch.uint8, device=dev)
+        self.page_table = torch.full((batch, max_pages_per_seq), -1, dtype=torch.int32, device=dev)
+        self.seq_len = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def desc(self, max_len: int = None) -> Int4Desc:
+        """The descriptor; max_len bounds every seq_len of the decodes it is used for (default: the page table's)."""
+        d = Int4Desc()
+        d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim = self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim
+        d.max_pages_per_seq, d.n_pages = self.max_pages_per_seq, self.n_pages
+        d.max_len = self.max_pages_per_seq * PAGE_TOKENS if max_len is None else int(max_len)
+        d.tau_k, d.tau_v = self.tau_k, self.tau_v
+        d.quant_group_k, d.quant_group_v = self.quant_group_k, self.quant_group_v
+        for name in ("pages", "page_table", "seq_len", "dev_status"):
             setattr(d, name, getattr(self, name).data_ptr())
         return d

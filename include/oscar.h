@@ -507,6 +507,207 @@ oscar_status oscar_decode_step(const oscar_layer_desc* desc, const void* host_in
 oscar_status oscar_decode_attention_static(const oscar_layer_desc* desc, const uint16_t* q,
                                            float* out, void* stream);
 
+/*
+ * ---------------------------------------------------------------- 4-bit layers
+ *
+ * A layer that two bits do not carry (the first and last layers of a model,
+ * a model without calibration data) keeps its whole KV cache at 4 bits: no
+ * rotation, no BF16 segments; every token goes to its page when it is
+ * appended, position-rotated on the way.  Layers of both kinds may share a
+ * model: every call takes one layer.
+ *
+ * Page pool layout of a 4-bit layer: head_dim d is 64 or 128, W = d / 32,
+ * 16 tokens per page, quantisation groups of g channels with G_K = d / g_K
+ * and G_V = d / g_V groups per vector.  A block of one (page p, KV head h)
+ * has 16 d + 64 (G_K + G_V) bytes (oscar_int4_block_bytes) and sits at byte
+ * (p * n_kv_heads + h) * block:
+ *   [0, 8 d)      K codes: token slot t has d / 2 bytes at t d / 2, 32-bit
+ *                 words; channel 32 w + 8 u + n (u < 4, n < 8) is nibble n
+ *                 (0 = lowest 4 bits) of word W u + w;
+ *   [8 d, 16 d)   V codes, two token slots to a word: channel 32 w + 4 u + n
+ *                 (u < 8, n < 4) of slot t is nibble 4 (t % 2) + n of word
+ *                 (8 (t / 2) + u) W + w;
+ *   [16 d, ...)   slot t: its G_K K (scale, zero) fp16 pairs, then its G_V V
+ *                 pairs, at 16 d + 4 (G_K + G_V) t.
+ * A value is zero + scale * code, code 0 .. 15.  (So that 4 bytes of K are 8
+ * adjacent channels of one token and 2 bytes of V 4 adjacent channels of
+ * one token, and one 16-byte load (d = 128) of a warp's lane holds a
+ * tensor-core operand's codes.)
+ * Logical position x of request b lives in page page_table[b][x / 16], slot
+ * x % 16.
+ */
+typedef struct oscar_int4_desc {
+  int32_t batch;              /* B >= 1                                         */
+  int32_t n_q_heads;          /* H_q, a multiple of n_kv_heads                  */
+  int32_t n_kv_heads;         /* H_kv >= 1                                      */
+  int32_t head_dim;           /* 64 or 128                                      */
+  int32_t max_pages_per_seq;  /* row length of page_table                       */
+  int32_t max_len;            /* host upper bound on every seq_len[b] (decode)  */
+  int64_t n_pages;            /* physical pages in the pool                     */
+  float tau_k;                /* keys are clamped to [-tau_k, tau_k]; 0 < tau <= 65504 */
+  float tau_v;                /* the same for values                            */
+  uint8_t* pages;             /* pool, 128-byte aligned (layout above)          */
+  const int32_t* page_table;  /* [B][max_pages_per_seq] physical page ids       */
+  const int32_t* seq_len;     /* [B] cached tokens of each request (decode)     */
+  int32_t* dev_status;        /* optional device word for OSCAR_DEV_* bits      */
+  int32_t quant_group_k;      /* g_K: 32, 64 or 128, at most d; 0 = d           */
+  int32_t quant_group_v;      /* g_V                                            */
+} oscar_int4_desc;
+
+/* Position rotation: pairs of channels of the first rot_dim channels of a
+ * head turn by the angle of the token's position. */
+typedef struct oscar_rope_desc {
+  const float* cos_sin;       /* device [n_positions][rot_dim] fp32, 16-byte aligned: */
+                              /* rot_dim / 2 cosines, then rot_dim / 2 sines    */
+  int64_t n_positions;        /* rows of cos_sin                                */
+  int32_t rot_dim;            /* a multiple of 16, 0 <= rot_dim <= head_dim;    */
+                              /* 0: no rotation (cos_sin may be NULL)           */
+  int32_t interleaved;        /* 0: pair i is channels (i, i + rot_dim / 2);    */
+                              /* 1: pair i is channels (2 i, 2 i + 1)           */
+} oscar_rope_desc;
+
+/* What becomes of a score before the softmax.  For query position i and key
+ * position j: t = scale (q . k); softcap > 0: t = softcap tanh(t / softcap);
+ * slopes: t -= slopes[h] |i - j|; window > 0: keys with i - j >= window are
+ * masked. */
+typedef struct oscar_score_desc {
+  float scale;                /* > 0 and finite; 0 = 1 / sqrt(head_dim)         */
+  float softcap;              /* > 0 and finite; 0 = none                       */
+  int32_t window;             /* >= 1; 0 = none                                 */
+  int32_t reserved;           /* 0                                              */
+  const float* slopes;        /* device [n_q_heads] fp32 or NULL                */
+} oscar_score_desc;
+
+/* Bytes of one (page, KV head) block of a 4-bit layer; 0 for an invalid head
+ * size or group.  Host-only. */
+int64_t oscar_int4_block_bytes(int32_t head_dim, int32_t quant_group_k, int32_t quant_group_v);
+
+/*
+ * oscar_rope_append_int4 - rotates the queries and keys of n tokens by their
+ * positions and appends their keys and values to a 4-bit layer's pages.  The
+ * sources quantise at two bits only; the codec is theirs (scale / zero per
+ * group) with sixteen codes.
+ *
+ *   For item i < n: q row i (q + i * q_stride, H_q heads of d bf16), k row i
+ *   and v row i (H_kv heads each).  q' and k' are q and k rotated by row
+ *   rope_pos[i] of rope->cos_sin (rope_pos NULL: dst_pos[i]), rounded once to
+ *   bf16: (a, b) -> (a cos - b sin, a sin + b cos).  q' goes to q_out and k'
+ *   to k_out ([n][heads][d], contiguous; each may be NULL, or q / k itself
+ *   where that is contiguous).  k' and v, clamped to [-tau, tau], are
+ *   quantised per group: scale = fp16((max - min) / 15), zero = fp16(min),
+ *   code = clamp(rint((x - zero) / scale), 0, 15) (0 if scale is 0), and
+ *   stored at position dst_pos[i] of request dst_req[i].
+ *
+ *   k' is rounded from its exact value (codes do not depend on how the
+ *   rotation is computed); q' is within one rounding of fp32 sums.  A NaN
+ *   is quantised as -tau; other rows are not affected.
+ *   dst_req[i] = -1 marks a padding row: nothing of it is read or written.
+ *   Any other request outside the batch, a position beyond the page table
+ *   or a rotation row outside cos_sin skips the item and sets
+ *   OSCAR_DEV_LENGTH; a page id outside the pool skips it and sets
+ *   OSCAR_DEV_PAGE_BOUNDS.  A skipped item writes nothing.
+ *
+ *   rope may be NULL (no rotation).  q and q_out may be NULL together.
+ *   dst_req, dst_pos, rope_pos: device int32 [n].  Rows 16-byte aligned,
+ *   strides multiples of 8 elements and at least one row.  seq_len is not
+ *   read: the caller advances it.  Items must name distinct (request,
+ *   position) pairs.  n = 0 is a no-op.  Async.
+ */
+oscar_status oscar_rope_append_int4(const oscar_int4_desc* desc, const oscar_rope_desc* rope,
+                                    const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                    const uint16_t* v, int64_t v_stride, const int32_t* dst_req,
+                                    const int32_t* dst_pos, const int32_t* rope_pos, int32_t n,
+                                    uint16_t* q_out, uint16_t* k_out, void* stream);
+
+/*
+ * oscar_gather_int4 - reads cached rows of a 4-bit layer back as bf16, for
+ * instance to go on with a prompt behind a cached prefix.
+ *
+ *   For item i < n: zero + scale * code, rounded to bf16, of position
+ *   src_pos[i] of request src_req[i], to row i of k_out and v_out
+ *   (k_out + i * k_stride, H_kv heads of d).  src_req[i] = -1 and the skips
+ *   are those of oscar_rope_append_int4: a skipped row is left as it was.
+ *   src_req, src_pos: device int32 [n].  Rows 16-byte aligned, strides
+ *   multiples of 8.  seq_len is not read.  n = 0 is a no-op.  Async.
+ */
+oscar_status oscar_gather_int4(const oscar_int4_desc* desc, const int32_t* src_req, const int32_t* src_pos,
+                               int32_t n, uint16_t* k_out, int64_t k_stride, uint16_t* v_out, int64_t v_stride,
+                               void* stream);
+
+/*
+ * oscar_decode_attention_int4 - one decode step of attention for every
+ * request of the batch over a 4-bit layer.
+ *
+ *   q: row b at q + b * q_stride, H_q heads of d bf16 (16-byte aligned, stride
+ *   a multiple of 8); out: [B][H_q][d] bf16 (16-byte aligned).  Request b's
+ *   query sits at position seq_len[b] - 1 (its token has been appended) and
+ *   attends positions 0 .. seq_len[b] - 1; query head j reads KV head
+ *   j / (H_q / H_kv), a group of 1 .. 16.  score may be NULL (all defaults).
+ *   Sums, softmax statistics and the output are fp32 until the one rounding
+ *   of out.  A request with no token gets zeros.  Codes, scales and zeros of
+ *   slots past seq_len may hold anything.  A length above max_len is
+ *   clamped and sets OSCAR_DEV_LENGTH, a negative one counts as 0 and sets
+ *   it; a page outside the pool is skipped and sets OSCAR_DEV_PAGE_BOUNDS.
+ *
+ *   Workspace as for oscar_decode_attention: NULL asks for the size; 256-byte
+ *   aligned, zero-filled before its first use; each call leaves it ready for
+ *   the next; calls that may overlap (other streams, two graphs replayed at
+ *   once) need workspaces of their own.  Async.
+ */
+oscar_status oscar_decode_attention_int4(const oscar_int4_desc* desc, const oscar_score_desc* score,
+                                         const uint16_t* q, int64_t q_stride, uint16_t* out, void* workspace,
+                                         size_t* workspace_bytes, void* stream);
+
+/* A batch of packed prompts (or documents of one packed sequence). */
+typedef struct oscar_prompt_desc {
+  int32_t batch;              /* B >= 1 requests                                */
+  int32_t n_q_heads;          /* H_q, a multiple of n_kv_heads                  */
+  int32_t n_kv_heads;         /* H_kv >= 1                                      */
+  int32_t head_dim;           /* 64 or 128                                      */
+  int32_t max_q;              /* host upper bound on a request's queries        */
+  int32_t max_k;              /* host upper bound on a request's keys           */
+  int32_t causal;             /* 1: keys after the query are masked; 0: not     */
+  int32_t reserved;           /* 0                                              */
+  int64_t total_q;            /* rows of q, out and lse                         */
+  int64_t total_k;            /* rows of k and v                                */
+  int32_t* dev_status;        /* optional device word for OSCAR_DEV_* bits      */
+} oscar_prompt_desc;
+
+/*
+ * oscar_prompt_attention - attention of prompt tokens over bf16 rows: the
+ * prefill that comes before a cache is decoded from.
+ *
+ *   Request b has the queries cu_q[b] .. cu_q[b+1] - 1 and the keys cu_k[b] ..
+ *   cu_k[b+1] - 1 (device int32 [B + 1], non-decreasing from >= 0): packed
+ *   documents do not see one another.  With n_q queries and n_k keys, query
+ *   r of the request sits at position i = n_k - n_q + r (the keys' last
+ *   n_q positions) and key c at position c.  causal: keys with j > i are
+ *   masked; window: keys with i - j >= window; of both, keys j <
+ *   prefix_len[b] are excepted (prefix_len NULL: none).  out row =
+ *   softmax(t) v over the keys left, t as in oscar_score_desc; a row with no
+ *   key left gets zeros and lse -inf.
+ *
+ *   q, k, v: bf16 rows of H_q / H_kv heads of d, q_stride / k_stride /
+ *   v_stride elements apart (multiples of 8), 16-byte aligned; out:
+ *   [total_q][H_q][d] bf16 (16-byte aligned); lse: optional [total_q][H_q]
+ *   fp32, the natural logarithm of the sum of exp(t).  Scores, statistics and
+ *   output sums are fp32; exp(t - max) is rounded to bf16 for its product
+ *   with v.  Rows of out and lse outside every request are left as they
+ *   were; rows of k and v outside a request never reach it, whatever they
+ *   hold.  A request's own rows must be finite.  Lengths above max_q / max_k
+ *   or rows outside total_q / total_k are clamped and set OSCAR_DEV_LENGTH.
+ *
+ *   Workspace: NULL asks for the size (which depends on desc and the current
+ *   device); otherwise 256-byte aligned, zero-filled before its first use;
+ *   each call leaves it ready for the next; calls that may overlap need
+ *   workspaces of their own.  Async.
+ */
+oscar_status oscar_prompt_attention(const oscar_prompt_desc* desc, const oscar_score_desc* score,
+                                    const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                                    const uint16_t* v, int64_t v_stride, const int32_t* cu_q, const int32_t* cu_k,
+                                    const int32_t* prefix_len, uint16_t* out, float* lse, void* workspace,
+                                    size_t* workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,167 @@
+"""Prompt attention on the GPU against the float64 oracle.
+
+Tolerance: one bf16 rounding of the result (2^-8 of it), one of each weight
+(2^-8 of sum p |v|), and fp32 scores (2^-14 covers |t| up to some hundreds).
+"""
+import numpy as np
+import pytest
+
+import oracle as O
+
+pytestmark = pytest.mark.gpu
+HALF_BF16 = 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda(built_lib):
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def dev_bf16(x):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).cuda().to(torch.bfloat16)
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def i32(x):
+    import torch
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def run(case_seed, nq, nk, hq, hk, d, causal=True, prefix=None, gap=0, lead=0, packed=False, check=True, **mods):
+    """One call over requests of nq[i] queries and nk[i] keys; `gap` rows of NaN keys and values (and untouched query
+    rows) before the first and after the last request.  Returns (out, lse, status) after checking them."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g = np.random.default_rng(case_seed)
+    tq, tk = sum(nq) + 2 * gap, sum(nk) + 2 * gap
+    q, k, v = O.bf16(g.standard_normal((tq, hq, d))), O.bf16(g.standard_normal((tk, hk, d))), O.bf16(g.standard_normal((tk, hk, d)) + 0.2)
+    cu_q, cu_k = gap + np.r_[0, np.cumsum(nq)], gap + np.r_[0, np.cumsum(nk)]
+    dq, dk, dv = dev_bf16(q), dev_bf16(k), dev_bf16(v)
+    if gap:
+        for t in (dk, dv):
+            t[:gap], t[tk - gap:] = float("nan"), float("inf")
+    if packed:
+        both = torch.cat([dq, dk, dv], 1)
+        dq, dk, dv = both.split([hq, hk, hk], 1)
+    out = torch.full((tq, hq, d), -3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((tq, hq), -3.0, dtype=torch.float32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    desc = B.prompt_desc(len(nq), hq, hk, d, max(nq), max(nk), tq, tk, causal, st)
+    sl = None
+    slopes = np.zeros(hq, np.float32)
+    if mods.pop("slopes", False):
+        slopes = np.exp2(-8.0 * np.arange(1, hq + 1) / hq).astype(np.float32)
+        sl = torch.from_numpy(slopes).cuda()
+    score = B.score_desc(mods.get("scale", 0.0), mods.get("softcap", 0.0), mods.get("window", 0), sl)
+    ws = torch.zeros(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    args = (desc, dq, dk, dv, i32(cu_q), i32(cu_k), out, ws)
+    kw = dict(score=score, prefix_len=None if prefix is None else i32(prefix), lse=lse)
+    B.oscar_prompt_attention(*args, **kw)
+    torch.cuda.synchronize()
+    first = out.clone()
+    B.oscar_prompt_attention(*args, **kw)           # the workspace serves again
+    torch.cuda.synchronize()
+    assert bool((first.view(torch.int16) == out.view(torch.int16)).all())
+    got, got_l = host(out), lse.cpu().numpy().astype(np.float64)
+    if gap:
+        for t in (got, got_l):
+            assert (t[:gap] == -3.0).all() and (t[tq - gap:] == -3.0).all()
+    assert int(st.item()) == 0
+    for b in range(len(nq)):
+        for h in range(hq):
+            kb, vb = k[cu_k[b]:cu_k[b + 1], h // (hq // hk)], v[cu_k[b]:cu_k[b + 1], h // (hq // hk)]
+            t = O.modified_scores(q[cu_q[b]:cu_q[b + 1], h], kb, nk[b] - nq[b], slope=float(slopes[h]), causal=causal,
+                                  prefix=0 if prefix is None else prefix[b], **mods)
+            r, r_abs, l = O.masked_attention(t, vb)
+            o = got[cu_q[b]:cu_q[b + 1], h]
+            err = np.abs(o - r)
+            bound = HALF_BF16 * (np.abs(r) + r_abs) + 2.0 ** -14
+            assert (err <= bound).all(), "request %d head %d: worst %.3g of its bound" % (b, h, np.nanmax(err / bound))
+            gl = got_l[cu_q[b]:cu_q[b + 1], h]
+            empty = np.isneginf(l)
+            assert np.isneginf(gl[empty]).all() and (o[empty] == 0).all()
+            assert np.abs(gl[~empty] - l[~empty]).max(initial=0.0) <= 2.0 ** -14
+    return out, lse
+
+
+CASES = [
+    # nq, nk, hq, hk, d, kwargs
+    ([1], [1], 1, 1, 128, {}),
+    ([300], [300], 4, 1, 128, {}),
+    ([129, 5, 128], [129, 5, 128], 8, 2, 64, dict(packed=True)),
+    ([64, 0, 33], [64, 17, 33], 6, 2, 128, dict(gap=40)),
+    ([7, 20], [700, 20], 8, 1, 128, dict(gap=3)),
+    ([50], [20], 4, 4, 64, {}),                                  # the first 30 queries see nothing
+    ([50, 9], [0, 0], 4, 2, 128, {}),                            # no key at all
+    ([200, 31], [200, 300], 5, 1, 64, dict(window=50, gap=9)),
+    ([150], [400], 16, 1, 128, dict(softcap=10.0, window=130)),
+    ([260, 100], [260, 100], 3, 3, 128, dict(prefix=[70, 200])),
+    ([260], [500], 4, 2, 64, dict(prefix=[130], window=20, softcap=3.0)),
+    ([130, 60], [130, 200], 12, 4, 128, dict(causal=False)),
+    ([130], [280], 8, 2, 128, dict(causal=False, window=64, slopes=True)),
+    ([333], [333], 10, 2, 64, dict(slopes=True)),
+    ([96], [1100], 16, 2, 64, dict(slopes=True, softcap=20.0, scale=0.3, prefix=[10], gap=17)),
+    ([1], [4000], 32, 8, 128, {}),
+    ([24, 2], [3100, 2000], 8, 2, 128, dict(window=1500)),
+    ([1000], [1000], 2, 1, 128, {}),
+    ([3] * 30, [3] * 30, 4, 1, 64, {}),
+    ([257], [257], 7, 1, 128, dict(packed=True)),
+]
+
+
+@pytest.mark.parametrize("nq,nk,hq,hk,d,kw", CASES)
+def test_prompt_matches_oracle(nq, nk, hq, hk, d, kw):
+    run(sum(nq) + sum(nk) + hq + d, nq, nk, hq, hk, d, **kw)
+
+
+def test_prompt_clamps_and_reports_bad_rows():
+    """Lengths above the bounds and rows outside the tensors are clamped and reported; other requests are not affected."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g = np.random.default_rng(4)
+    q, k, v = (dev_bf16(g.standard_normal((60, h, 64))) for h in (4, 2, 2))
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+
+    def call(cu_q, cu_k, max_q, max_k):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        desc = B.prompt_desc(2, 4, 2, 64, max_q, max_k, 60, 60, True, st)
+        w = torch.zeros(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+        out = torch.full_like(q, 9.0)
+        B.oscar_prompt_attention(desc, q, k, v, i32(cu_q), i32(cu_k), out, w)
+        torch.cuda.synchronize()
+        return out, int(st.item())
+    good, status = call([0, 20, 50], [0, 20, 50], 30, 30)
+    assert status == 0 and bool((good[50:] == 9.0).all())
+    for cu_q, cu_k, mq, mk in (([0, 20, 70], [0, 20, 60], 60, 60), ([0, 20, 10], [0, 20, 50], 30, 30), ([0, 20, 50], [0, 20, 50], 20, 30),
+                               ([0, 20, 50], [0, 20, 90], 30, 60), ([0, 20, 30], [0, 20, -5], 30, 30)):
+        out, status = call(cu_q, cu_k, mq, mk)
+        assert status == 2
+        assert bool((out[:20] == good[:20]).all())
+    del ws
+
+
+def test_prompt_on_another_stream_and_in_a_graph():
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g = np.random.default_rng(6)
+    q, k, v = (dev_bf16(g.standard_normal((200, h, 128))) for h in (8, 2, 2))
+    desc = B.prompt_desc(1, 8, 2, 128, 200, 200, 200, 200)
+    cu = i32([0, 200])
+    ws = [torch.zeros(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out = [torch.zeros_like(q) for _ in range(2)]
+    B.oscar_prompt_attention(desc, q, k, v, cu, cu, out[0], ws[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        B.oscar_prompt_attention(desc, q, k, v, cu, cu, out[1], ws[1])
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert bool((out[0] == out[1]).all())
