@@ -1,6 +1,29 @@
-// Decode attention over a 4-bit layer: one query token per request.
+// Decode attention over a 4-bit layer: one query token per request, split over
+// the pages of its context and joined by the last CTA of each (request, KV
+// head) to finish.
+//
+// A CTA of 8 warps takes one split of one (request, KV head, up to 8 query
+// heads); a warp takes every 8th page of the split with an online softmax of
+// its own, so nothing in the scan waits for another warp.  The pages' blocks
+// come by bulk copies into a ring of the warp's own.
+//
+// Per page, on the tensor cores with 16 tokens or 16 channels as the rows and
+// 8 query heads as the columns:
+//   S = K q:   A = the K codes as they are: a code c in the low bits of an fp16
+//              is c 2^-24 exactly (and c 2^-20 one nibble higher), so one mask
+//              turns a word into two operands.  q is scaled by a power of two
+//              per head to just below fp16's end, which is exact for bf16.
+//              x = sum over groups of s (sum c q) + z (sum q).
+//   O += P V:  A = the V codes the same way, B = p s_V in fp16; the zeros are
+//              summed apart as p z_V in fp32.  The 11 bits of p s_V are the one
+//              rounding below fp32 (bf16 output has 8).
+// The weights' reference is raised only when a score exceeds it by 2^8, and
+// the values' scales are taken relative to a power of two above them, raised
+// when a larger one comes: both by one vote per page.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "kernels.h"
 #include "oscar.h"
@@ -10,88 +33,411 @@
 namespace oscar {
 namespace {
 
-constexpr int kDecodeWarps = 8;
+constexpr int kWarps = 8;
+constexpr int kStages = 4;
+constexpr int kHeads = 8;             // query heads per CTA (MMA columns)
+constexpr int kSlots = 152 * 2;       // CTAs the GPU holds at a time
+constexpr int kRounds = 24;           // rounds of them that a grid is split into, at most
+// Merge tickets sit at the same place of the workspace whatever the call's
+// sizes, so that calls of different batches share one: no call writes partial
+// states where another keeps tickets.  A grid is split (2 splits or more) only
+// below this many (request, head set) pairs.
+constexpr int kTickets = 4096;
+static_assert(kSlots * kRounds / 2 <= kTickets, "every split pair has a ticket");
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
-// One CTA per (query head, request); a warp takes every kDecodeWarps-th
-// token with an online softmax of its own, and the warps are joined in
-// shared memory.  A lane holds D / 32 adjacent channels.
-template <int D>
-__global__ void __launch_bounds__(32 * kDecodeWarps) decode_int4_kernel(const Int4DecodeParams p) {
+struct SplitPlan {
+  int splits;          // per (request, head set), at most
+  int halves;          // head sets per KV head
+  size_t off_ml, off_o, bytes;
+};
+
+// Pages of a request are split so that the grid is a whole number of rounds
+// of the CTAs that the GPU holds, each of at least 16 pages a warp where the
+// context has them, and at least 4.
+SplitPlan plan_splits(const Int4Cache& c, const ScoreParams& s) {
+  SplitPlan r{};
+  const int group = c.n_q / c.n_kv;
+  r.halves = (group + kHeads - 1) / kHeads;
+  int64_t tokens = c.max_len;
+  if (s.window) tokens = std::min<int64_t>(tokens, int64_t(s.window) + kInt4Page);
+  const int64_t pages = std::max<int64_t>(1, (tokens + kInt4Page - 1) / kInt4Page);
+  const int64_t pairs = int64_t(c.batch) * c.n_kv * r.halves;
+  const int64_t round = int64_t(kSlots) * kWarps * 16;
+  const int64_t rounds = std::min<int64_t>(kRounds, std::max<int64_t>(1, (pairs * pages + round / 2) / round));
+  const int64_t most = std::max<int64_t>(1, pages / (kWarps * 4));
+  r.splits = int(std::min<int64_t>(most, std::max<int64_t>(1, kSlots * rounds / pairs)));
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  r.off_ml = up(size_t(kTickets) * 4);
+  r.off_o = r.off_ml + up(size_t(pairs) * r.splits * kHeads * 8);
+  r.bytes = r.off_o + up(size_t(pairs) * r.splits * kHeads * c.d * 4);
+  if (r.splits == 1) r.bytes = 256;   // nothing is kept there
+  return r;
+}
+
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t (&w)[W], const uint8_t* p) {
+  if constexpr (W == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+
+// The groups of one token's K or V as (scale, zero) floats.
+template <int N>
+__device__ __forceinline__ void lds_pairs(float2 (&sz)[N], const uint8_t* p) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) sz[i] = half2_to_float2(*reinterpret_cast<const uint32_t*>(p + 4 * i));
+}
+
+__device__ __forceinline__ float max_over_rows(float v) {   // over the 8 lanes of a column pair
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float sum_over_rows(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+template <int D, int NGK, int NGV>
+__global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4DecodeParams p, const SplitPlan plan) {
+  constexpr int W = D / 32, kBlock = int4_block_bytes(D, NGK, NGV), kPairs = 16 * D;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
+  __shared__ int sm_last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+  if (lane < kStages) mbar_init(&bars[warp][lane], 1);
+  fence_mbar_init();
+  __syncwarp();
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kC = D / 32;
-  __shared__ float sm_m[kDecodeWarps], sm_l[kDecodeWarps], sm_o[kDecodeWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int hq = blockIdx.x, b = blockIdx.y;
   const Int4Cache& c = p.c;
-  const int hk = hq / (c.n_q / c.n_kv);
+  const int b = blockIdx.z, hk = blockIdx.y / plan.halves, set = blockIdx.y % plan.halves;
+  const int group = c.n_q / c.n_kv, heads = min(kHeads, group - set * kHeads);
+  const int hq0 = hk * group + set * kHeads;
   int len = c.seq_len[b];
   if (len < 0 || len > c.max_len) {
     if (threadIdx.x == 0 && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_LENGTH);
     len = min(max(len, 0), c.max_len);
   }
   const int first = p.s.window ? max(0, len - p.s.window) : 0;
-  const float slope = p.s.slopes ? p.s.slopes[hq] * kLog2e : 0.f;
-  float q[kC], o[kC];
-  for (int e = 0; e < kC; ++e) {
-    q[e] = __uint_as_float(uint32_t(p.q[b * p.q_stride + hq * D + kC * lane + e]) << 16);
-    o[e] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const int64_t block_bytes = int4_block_bytes(D, c.ng_k, c.ng_v);
-  for (int j = first + warp; j < len; j += kDecodeWarps) {
-    const int page = c.page_table[int64_t(b) * c.max_pages + j / kInt4Page], t = j % kInt4Page;
-    if (page < 0 || page >= c.n_pages) {
-      if (lane == 0 && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
-      continue;
+  const int page0 = first / kInt4Page, page1 = (len + kInt4Page - 1) / kInt4Page;
+  // this request's own split: as many as its pages need of the grid's
+  const int pages = page1 - page0, most = max(1, pages / (kWarps * 4));
+  const int splits = min(plan.splits, most), split = blockIdx.x;
+  if (split >= splits) return;
+  const int begin = page0 + int(int64_t(pages) * split / splits), end = page0 + int(int64_t(pages) * (split + 1) / splits);
+  const int n_it = max(0, (end - begin - warp + kWarps - 1) / kWarps);
+
+  const int32_t* table = c.page_table + int64_t(b) * c.max_pages + begin + warp;
+  uint8_t* ring = smem + warp * (kStages * kBlock);
+  int ids = lane < n_it ? table[kWarps * lane] : 0, ids_next = 0;
+  uint32_t live = 0;                      // stage i holds a page of the pool
+  auto issue = [&](int it) {
+    if ((it & 31) == 0) {
+      if (it) ids = ids_next;
+      ids_next = it + 32 + lane < n_it ? table[kWarps * (it + 32 + lane)] : 0;
     }
-    const uint8_t* block = c.pages + (int64_t(page) * c.n_kv + hk) * block_bytes;
-    float x = 0.f, v[kC];
-    for (int e = 0; e < kC; ++e) {
-      const int ch = kC * lane + e;
-      const uint32_t kw = *reinterpret_cast<const uint32_t*>(block + int4_k_word(D, t, ch >> 3));
-      const uint32_t vh = *reinterpret_cast<const uint16_t*>(block + int4_v_half(D, t, ch >> 2));
-      const float2 sk = half2_to_float2(
-          *reinterpret_cast<const uint32_t*>(block + int4_pair(D, c.ng_k, c.ng_v, t, ch * c.ng_k / D)));
-      const float2 sv = half2_to_float2(
-          *reinterpret_cast<const uint32_t*>(block + int4_pair(D, c.ng_k, c.ng_v, t, c.ng_k + ch * c.ng_v / D)));
-      x = fmaf(q[e], fmaf(float((kw >> (4 * (ch & 7))) & 15u), sk.x, sk.y), x);
-      v[e] = fmaf(float((vh >> (4 * (ch & 3))) & 15u), sv.x, sv.y);
+    const int id = __shfl_sync(0xffffffffu, ids, it & 31), st = it % kStages;
+    const bool ok = id >= 0 && id < c.n_pages;
+    live = ok ? live | (1u << st) : live & ~(1u << st);
+    if (lane == 0) {
+      if (ok) {
+        mbar_arrive_expect_tx(&bars[warp][st], kBlock);
+        bulk_copy_g2s(ring + st * kBlock, c.pages + (int64_t(id) * c.n_kv + hk) * kBlock, kBlock, &bars[warp][st]);
+      } else {
+        mbar_arrive(&bars[warp][st]);
+        if (c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+      }
     }
-    for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    const float y = (p.s.cap_log2 != 0.f ? capped(x, p.s) : x * p.s.scale_log2) - slope * float(len - 1 - j);
-    const float mn = fmaxf(m, y), f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(y - mn);
-    m = mn;
-    l = l * f + w;
-    for (int e = 0; e < kC; ++e) o[e] = fmaf(w, v[e], o[e] * f);
+  };
+  int issued = min(n_it, kStages);
+  for (int i = 0; i < issued; ++i) issue(i);
+
+  // Query operands of column gid: head hq0 + gid, scaled by 2^(141 - ex) so
+  // that its largest channel is in [2^14, 2^15).
+  uint32_t qb[2 * W][2];
+  float qs[NGK][2], unscale[2], slope[2];
+  {
+    float q[W][8], top = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (gid < heads)
+        u = *reinterpret_cast<const uint4*>(p.q + b * p.q_stride + int64_t(hq0 + gid) * D + 32 * w + 8 * tig);
+      q[w][0] = bf16_lo(u.x), q[w][1] = bf16_hi(u.x), q[w][2] = bf16_lo(u.y), q[w][3] = bf16_hi(u.y);
+      q[w][4] = bf16_lo(u.z), q[w][5] = bf16_hi(u.z), q[w][6] = bf16_lo(u.w), q[w][7] = bf16_hi(u.w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(q[w][i]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int ex = min(max((__float_as_int(top) >> 23) & 255, 14), 243);
+    const float up = pow2i(141 - ex);
+    float sum[NGK];
+#pragma unroll
+    for (int g = 0; g < NGK; ++g) sum[g] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        q[w][i] *= up;
+        sum[w * NGK / W] += q[w][i];
+      }
+      // k-step 2 w: nibbles (0, 4) and (1, 5); 2 w + 1: (2, 6) and (3, 7);
+      // the odd ones are masked in place and stand for 16 c
+      qb[2 * w][0] = pack_half2(q[w][0], q[w][4]);
+      qb[2 * w][1] = pack_half2(q[w][1] * 0.0625f, q[w][5] * 0.0625f);
+      qb[2 * w + 1][0] = pack_half2(q[w][2], q[w][6]);
+      qb[2 * w + 1][1] = pack_half2(q[w][3] * 0.0625f, q[w][7] * 0.0625f);
+    }
+    const float un = pow2i(ex - 117);     // 2^24 / up
+#pragma unroll
+    for (int g = 0; g < NGK; ++g) {
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+      sum[g] *= 5.9604644775390625e-8f;   // 2^-24, as the codes carry
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {         // to the lanes of columns 2 tig, 2 tig + 1
+      const int from = 4 * (2 * tig + e);
+#pragma unroll
+      for (int g = 0; g < NGK; ++g) qs[g][e] = __shfl_sync(0xffffffffu, sum[g], from);
+      unscale[e] = __shfl_sync(0xffffffffu, un, from);
+      if (p.s.cap_log2 == 0.f) unscale[e] *= p.s.scale_log2;
+      slope[e] = p.s.slopes && 2 * tig + e < heads ? p.s.slopes[hq0 + 2 * tig + e] * kLog2e : 0.f;
+    }
   }
-  if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
-  for (int e = 0; e < kC; ++e) sm_o[warp][kC * lane + e] = o[e];
+  const bool cap = p.s.cap_log2 != 0.f;
+
+  float o[2 * W][4], zs[NGV][2], m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
+  int ve = -24;                           // the V scales seen are at most 2^ve
+  float vs_top = pow2i(-24), vs_mul = pow2i(31);   // 2^(7 - ve): p s_V 2^(7 - ve) <= 2^15
+#pragma unroll
+  for (int t = 0; t < 2 * W; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+#pragma unroll
+  for (int g = 0; g < NGV; ++g) zs[g][0] = zs[g][1] = 0.f;
+
+  bool dead = false;
+  for (int it = 0; it < issued; ++it) {
+    const int st = it % kStages;
+    const bool landed = mbar_wait_bounded(&bars[warp][st], (it / kStages) & 1, kDefaultWaitNs);
+    if (!__all_sync(0xffffffffu, landed)) {
+      if (lane == 0 && !dead && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_TIMEOUT);
+      dead = true;                        // nothing more is issued; what is in flight is still waited for
+    }
+    if (!dead && ((live >> st) & 1)) {
+      const uint8_t* blk = ring + st * kBlock;
+      const int tok = (begin + warp + kWarps * it) * kInt4Page;
+      // S: rows gid and gid + 8 are tokens, columns 2 tig and 2 tig + 1 heads
+      float acc[NGK][4];
+#pragma unroll
+      for (int g = 0; g < NGK; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+      uint32_t k0[W], k1[W];
+      lds_words(k0, blk + gid * (D / 2) + tig * (4 * W));
+      lds_words(k1, blk + (gid + 8) * (D / 2) + tig * (4 * W));
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        mma_f16(acc[w * NGK / W], k0[w] & kLow, k1[w] & kLow, k0[w] & kHigh, k1[w] & kHigh, qb[2 * w][0], qb[2 * w][1]);
+        const uint32_t a = k0[w] >> 8, d = k1[w] >> 8;
+        mma_f16(acc[w * NGK / W], a & kLow, d & kLow, a & kHigh, d & kHigh, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+      }
+      float y[2][2];
+      float2 vp[2][NGV];
+      const bool edge = tok < first || tok + kInt4Page > len;
+      bool grow = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int t = gid + 8 * r, j = tok + t;
+        const uint8_t* pr = blk + kPairs + 4 * (NGK + NGV) * t;
+        float2 kp[NGK];
+        lds_pairs(kp, pr);
+        lds_pairs(vp[r], pr + 4 * NGK);
+        const float away = float(j - (len - 1));
+        const bool seen = !edge || (j >= first && j < len);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = 0.f;
+#pragma unroll
+          for (int g = 0; g < NGK; ++g) x = fmaf(kp[g].x, acc[g][2 * r + e], fmaf(kp[g].y, qs[g][e], x));
+          x *= unscale[e];
+          if (cap) x = capped(x, p.s);
+          y[r][e] = seen ? fmaf(slope[e], away, x) : -INFINITY;
+          grow |= y[r][e] > m[e] + 8.f;
+        }
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) {
+          if (!seen) vp[r][g] = make_float2(0.f, 0.f);   // a stale slot may hold anything
+          grow |= vp[r][g].x > vs_top;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        float top = 0.f;
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) top = fmaxf(top, fmaxf(vp[0][g].x, vp[1][g].x));
+        top = max_over_rows(top);
+        // 2^e >= top for the exponent e of top plus one
+        const int ne = max(ve, ((__float_as_int(top) >> 23) & 255) - 126);
+        const float fv = ne - ve < 126 ? pow2i(ve - ne) : 0.f;
+        ve = ne;
+        vs_top = pow2i(ve);
+        vs_mul = pow2i(7 - ve);
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mn = fmaxf(m[e], max_over_rows(fmaxf(y[0][e], y[1][e])));
+          f[e] = exp2_fast(m[e] - mn);
+          m[e] = mn;
+          l[e] *= f[e];
+#pragma unroll
+          for (int g = 0; g < NGV; ++g) zs[g][e] *= f[e];
+          f[e] *= fv;
+        }
+#pragma unroll
+        for (int t = 0; t < 2 * W; ++t) o[t][0] *= f[0], o[t][1] *= f[1], o[t][2] *= f[0], o[t][3] *= f[1];
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[r][e] = exp2_fast(y[r][e] - m[e]);
+          l[e] += y[r][e];
+#pragma unroll
+          for (int g = 0; g < NGV; ++g) zs[g][e] = fmaf(y[r][e], vp[r][g].y, zs[g][e]);
+        }
+      // O: rows are channels; k = tokens 2 tig, 2 tig + 1 (and + 8)
+      uint32_t v0[W], v1[W];
+      lds_words(v0, blk + 8 * D + (8 * tig + gid) * (4 * W));
+      lds_words(v1, blk + 8 * D + (8 * (tig + 4) + gid) * (4 * W));
+#pragma unroll
+      for (int g = 0; g < NGV; ++g) {
+        const float s0 = vp[0][g].x * vs_mul, s1 = vp[1][g].x * vs_mul;
+        const uint32_t b0 = movmatrix_trans(pack_half2(y[0][0] * s0, y[0][1] * s0));
+        const uint32_t b1 = movmatrix_trans(pack_half2(y[1][0] * s1, y[1][1] * s1));
+#pragma unroll
+        for (int w = g * W / NGV; w < (g + 1) * W / NGV; ++w) {
+          mma_f16(o[2 * w], v0[w] & kLow, v0[w] & kHigh, v1[w] & kLow, v1[w] & kHigh, b0, b1);
+          const uint32_t a = v0[w] >> 8, d = v1[w] >> 8;
+          mma_f16(o[2 * w + 1], a & kLow, a & kHigh, d & kLow, d & kHigh, b0, b1);
+        }
+      }
+    }
+    __syncwarp();                         // the stage has been read
+    if (!dead && issued < n_it) issue(issued++);
+  }
+
+  // the warps' states in shared memory, over the rings
   __syncthreads();
-  if (threadIdx.x < D) {
-    float mx = -INFINITY, sum = 0.f, acc = 0.f;
-    for (int w = 0; w < kDecodeWarps; ++w) mx = fmaxf(mx, sm_m[w]);
-    for (int w = 0; w < kDecodeWarps; ++w) {
-      const float f = sm_m[w] == -INFINITY ? 0.f : exp2f(sm_m[w] - mx);
-      sum += f * sm_l[w];
-      acc += f * sm_o[w][threadIdx.x];
+  float* buf = reinterpret_cast<float*>(smem);
+  const float un = pow2i(17 + ve);        // 2^24 of the codes, 2^(ve - 7) of the scales
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int h = 2 * tig + e;
+    const float lt = sum_over_rows(l[e]);
+    float z[NGV];
+#pragma unroll
+    for (int g = 0; g < NGV; ++g) z[g] = sum_over_rows(zs[g][e]);
+    if (gid == 0) sm_m[warp][h] = m[e], sm_l[warp][h] = lt;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float zg = z[w * NGV / W];
+      float4 v = make_float4(fmaf(o[2 * w][e], un, zg), fmaf(o[2 * w][2 + e], un * 0.0625f, zg),
+                             fmaf(o[2 * w + 1][e], un, zg), fmaf(o[2 * w + 1][2 + e], un * 0.0625f, zg));
+      *reinterpret_cast<float4*>(buf + (warp * kHeads + h) * D + 32 * w + 4 * gid) = v;
     }
-    p.out[(int64_t(b) * c.n_q + hq) * D + threadIdx.x] =
-        __bfloat16_as_ushort(__float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f));
   }
+  __syncthreads();
+  // (the request, head set) pair's partial states
+  const int64_t pair = (int64_t(b) * c.n_kv + hk) * plan.halves + set;
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  float2* ml = reinterpret_cast<float2*>(ws + plan.off_ml) + pair * plan.splits * kHeads;
+  float* po = reinterpret_cast<float*>(ws + plan.off_o) + pair * plan.splits * kHeads * D;
+  uint16_t* out = p.out + (int64_t(b) * c.n_q + hq0) * D;
+  for (int i = threadIdx.x; i < heads * D; i += 32 * kWarps) {
+    const int h = i / D, ch = i % D;
+    float mx = sm_m[0][h], sum = 0.f, v = 0.f;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][h]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2_fast(sm_m[w][h] - mx);
+      sum = fmaf(f, sm_l[w][h], sum);
+      v = fmaf(f, buf[(w * kHeads + h) * D + ch], v);
+    }
+    if (splits == 1) {
+      out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(sum > 0.f ? v / sum : 0.f));
+    } else {
+      po[(split * kHeads + h) * D + ch] = v;
+      if (ch == 0) ml[split * kHeads + h] = make_float2(mx, sum);
+    }
+  }
+  if (splits == 1) return;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t* ticket = reinterpret_cast<uint32_t*>(ws) + pair;
+    sm_last = atom_add_acq_rel_gpu(ticket, 1) == uint32_t(splits - 1);
+    if (sm_last) *ticket = 0;             // ready for the next call
+  }
+  __syncthreads();
+  if (!sm_last) return;
+  for (int i = threadIdx.x; i < heads * D; i += 32 * kWarps) {
+    const int h = i / D, ch = i % D;
+    float mx = -FLT_MAX, sum = 0.f, v = 0.f;
+    for (int s = 0; s < splits; ++s) mx = fmaxf(mx, __ldcg(&ml[s * kHeads + h]).x);
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {
+      const float2 x = __ldcg(&ml[s * kHeads + h]);
+      const float f = exp2_fast(x.x - mx);
+      sum = fmaf(f, x.y, sum);
+      v = fmaf(f, __ldcg(&po[(s * kHeads + h) * D + ch]), v);
+    }
+    out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(sum > 0.f ? v / sum : 0.f));
+  }
+}
+
+template <int D, int NGK, int NGV>
+cudaError_t launch(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
+  constexpr int ring = kWarps * kStages * int4_block_bytes(D, NGK, NGV), join = kWarps * kHeads * D * 4;
+  constexpr int bytes = ring > join ? ring : join;
+  const cudaError_t e = set_smem_limit<decode_int4_kernel<D, NGK, NGV>>(bytes);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(unsigned(plan.splits), unsigned(p.c.n_kv * plan.halves), unsigned(p.c.batch));
+  return launch_pdl(decode_int4_kernel<D, NGK, NGV>, grid, dim3(32 * kWarps), bytes, stream, p, plan);
+}
+
+template <int D, int NGK>
+cudaError_t launch_v(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
+  if (p.c.ng_v == 1) return launch<D, NGK, 1>(p, plan, stream);
+  if (p.c.ng_v == 2) return launch<D, NGK, 2>(p, plan, stream);
+  if constexpr (D == 128) return launch<D, NGK, 4>(p, plan, stream);
+  return cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch_k(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
+  if (p.c.ng_k == 1) return launch_v<D, 1>(p, plan, stream);
+  if (p.c.ng_k == 2) return launch_v<D, 2>(p, plan, stream);
+  if constexpr (D == 128) return launch_v<D, 4>(p, plan, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t int4_decode_workspace_bytes(const Int4Cache&, const ScoreParams&, cudaError_t* err) {
+size_t int4_decode_workspace_bytes(const Int4Cache& c, const ScoreParams&, cudaError_t* err) {
   *err = cudaSuccess;
-  return 256;
+  return plan_splits(c, ScoreParams{}).bytes;
 }
 
 cudaError_t launch_decode_int4(const Int4DecodeParams& p, cudaStream_t stream) {
-  const dim3 grid(unsigned(p.c.n_q), unsigned(p.c.batch));
-  return p.c.d == 128 ? launch_pdl(decode_int4_kernel<128>, grid, dim3(32 * kDecodeWarps), 0, stream, p)
-                      : launch_pdl(decode_int4_kernel<64>, grid, dim3(32 * kDecodeWarps), 0, stream, p);
+  const SplitPlan plan = plan_splits(p.c, p.s);
+  return p.c.d == 128 ? launch_k<128>(p, plan, stream) : launch_k<64>(p, plan, stream);
 }
 
 }  // namespace oscar
