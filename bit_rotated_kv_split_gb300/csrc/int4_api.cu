@@ -66,7 +66,7 @@ oscar_status check_score(const oscar_score_desc* d, int32_t head_dim, oscar::Sco
   s->scale_log2 = float(scale * log2e);
   s->cap_in = d->softcap > 0.f ? float(2.0 * scale / double(d->softcap) * log2e) : 0.f;
   s->cap_log2 = float(double(d->softcap) * log2e);
-  if (!std::isfinite(s->scale_log2) || !std::isfinite(s->cap_in) || !std::isfinite(2.f * s->cap_log2))
+  if (!std::isnormal(s->scale_log2) || !std::isfinite(s->cap_in) || !std::isfinite(2.f * s->cap_log2))
     return OSCAR_ERR_INVALID_ARG;
   s->window = d->window;
   s->slopes = d->slopes;

@@ -1,5 +1,26 @@
-// Attention of packed prompts over bf16 rows.
+// Attention of packed prompts over bf16 rows, on the tensor cores (tcgen05).
+//
+// A CTA takes 2 x 128 query rows of one KV head: rows are (token, head) pairs
+// of a power-of-two share of the query heads that read it, so that short
+// prompts fill the tiles and K and V are read once for those heads.  Keys come
+// in tiles of 128.  Ten warps: one brings Q, K and V by TMA, one issues the
+// MMAs, and four for each of the two row tiles do the softmax, one thread a
+// row.  Per key tile and row tile:
+//   S = Q K^T   A and B in shared memory, the 128 x 128 result in TMEM;
+//   P = 2^(S - m) in the thread's registers, written over S in TMEM as bf16 (the
+//               one rounding below fp32: the tensor cores take 16-bit operands);
+//   O += P V    A = P in TMEM, B = V as it lies in memory (MN-major), O in TMEM.
+// While one row tile's softmax runs, the tensor cores work for the other.  The
+// reference m of a row is raised only when a score exceeds it by 2^8: then its
+// thread rescales O in TMEM after the last product is done (rare after the
+// first tiles).  Tiles of keys that the mask rules out for all rows are not
+// visited.  A few rows over many keys are split over the keys; the parts'
+// unnormalised sums go to the workspace and a second kernel joins them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "kernels.h"
 #include "oscar.h"
@@ -9,7 +30,42 @@
 namespace oscar {
 namespace {
 
-constexpr int kPromptWarps = 4;
+constexpr int kTile = 128;            // rows of a tile, of queries and of keys
+constexpr int kPanel = kTile * 128;   // bytes of 128 rows of 64 channels
+constexpr int kThreads = 384;         // three warpgroups: two of softmax, one of which two warps work
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kSms = 152;
+template <int D>
+constexpr int kStages = D == 128 ? 2 : 4;
+
+struct PromptPlan {
+  int pack;        // query heads in a tile's rows
+  int sets;        // head sets
+  int blocks;      // row blocks of the longest request
+  int splits;      // parts of the keys
+  size_t off_ml, off_o, bytes;
+};
+
+PromptPlan plan_prompt(const PromptParams& p) {
+  PromptPlan r{};
+  const int group = p.n_q / p.n_kv;
+  r.pack = 1;
+  while (r.pack < 16 && group % (2 * r.pack) == 0) r.pack *= 2;
+  r.sets = p.n_q / r.pack;
+  r.blocks = int((int64_t(p.max_q) * r.pack + 2 * kTile - 1) / (2 * kTile));
+  const int64_t ctas = int64_t(r.blocks) * r.sets * p.batch;
+  const int64_t tiles = (int64_t(p.max_k) + kTile - 1) / kTile;
+  r.splits = int(std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(1, ctas), tiles / 4)));
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  if (r.splits > 1) {
+    const size_t rows = size_t(ctas) * r.splits * 2 * kTile;
+    r.off_o = up(rows * 8);
+    r.bytes = r.off_o + rows * p.d * 4;
+  } else {
+    r.bytes = 256;
+  }
+  return r;
+}
 
 // The rows of request b: first query and key row, clamped counts.
 struct PromptSpan {
@@ -30,57 +86,445 @@ __device__ __forceinline__ PromptSpan prompt_span(const PromptParams& p, int b, 
   return r;
 }
 
-// One warp per (query row, head), keys one after the other.
+struct Barriers {
+  uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_done[2], fin;
+  uint32_t tmem;
+  int dead;
+};
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
 template <int D>
-__global__ void __launch_bounds__(32 * kPromptWarps) prompt_kernel(const PromptParams p) {
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ PromptParams p, const PromptPlan plan, const __grid_constant__ CUtensorMap tq,
+                  const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  constexpr int kPanels = D / 64, kTileBytes = kPanels * kPanel, kSt = kStages<D>;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile), kIdescO = idesc_bf16_f32_bmn(kTile, D);
+  constexpr uint32_t kColO = 2 * kTile;          // TMEM columns: S0, S1, O0, O1
+  extern __shared__ uint8_t raw[];
+  __shared__ Barriers bar;
+  uint8_t* sq = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
+  uint8_t* sk = sq + 2 * kTileBytes;
+  uint8_t* sv = sk + kSt * kTileBytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.fin, 1);
+    for (int i = 0; i < kSt; ++i) {
+      mbar_init(&bar.k_full[i], 1);
+      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], 1);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&bar.s_full[w], 1);
+      mbar_init(&bar.p_full[w], kTile);
+      mbar_init(&bar.o_done[w], 1);
+    }
+    bar.dead = 0;
+    fence_mbar_init();
+  }
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kC = D / 32;
-  const int lane = threadIdx.x & 31, hq = blockIdx.y, b = blockIdx.z;
-  const int r = blockIdx.x * kPromptWarps + (threadIdx.x >> 5);
-  const PromptSpan sp = prompt_span(p, b, threadIdx.x == 0 && blockIdx.x == 0 && hq == 0);
-  if (r >= sp.n_q) return;
-  const int hk = hq / (p.n_q / p.n_kv), i = sp.n_k - sp.n_q + r;
-  const float slope = p.s.slopes ? p.s.slopes[hq] * kLog2e : 0.f;
-  float q[kC], o[kC];
-  for (int e = 0; e < kC; ++e) {
-    q[e] = __uint_as_float(uint32_t(p.q[(sp.q0 + r) * p.q_stride + hq * D + kC * lane + e]) << 16);
-    o[e] = 0.f;
+
+  const int set = blockIdx.x % plan.sets, blk = plan.blocks - 1 - int(blockIdx.x / plan.sets);
+  const int b = blockIdx.y, split = blockIdx.z;
+  const PromptSpan sp = prompt_span(p, b, tid == 0 && blockIdx.x == 0 && split == 0);
+  const int pack = plan.pack, per_tile = kTile / pack;   // tokens of a tile
+  const int tok0 = blk * 2 * per_tile;
+  if (tok0 >= sp.n_q) return;
+  const int hq0 = set * pack, hk = hq0 / (p.n_q / p.n_kv), shift = sp.n_k - sp.n_q;   // position = shift + token
+
+  // key tiles that some row sees: the prefix's, then those from the window's
+  // first to the last row's last; n[w]: as far as row tile w goes
+  int n_pre = 0, from = 0, n[2];
+  const int tiles = (sp.n_k + kTile - 1) / kTile;
+  if (p.s.window) from = min(max(0, shift + tok0 - p.s.window + 1) / kTile, tiles);
+  n_pre = min((sp.prefix + kTile - 1) / kTile, from);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int last = min(tok0 + (w + 1) * per_tile, sp.n_q) - 1;     // last token of the tile
+    int to = tiles;
+    if (p.causal) to = max((sp.prefix + kTile - 1) / kTile, (max(0, min(shift + last + 1, sp.n_k)) + kTile - 1) / kTile);
+    n[w] = tok0 + w * per_tile < sp.n_q ? n_pre + max(0, to - from) : 0;
   }
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < sp.n_k; ++j) {
-    const bool seen = j < sp.prefix || ((!p.causal || j <= i) && (!p.s.window || i - j < p.s.window));
-    if (!seen) continue;
-    float x = 0.f, v[kC];
-    for (int e = 0; e < kC; ++e) {
-      const int ch = hk * D + kC * lane + e;
-      x = fmaf(q[e], __uint_as_float(uint32_t(p.k[(sp.k0 + j) * p.k_stride + ch]) << 16), x);
-      v[e] = __uint_as_float(uint32_t(p.v[(sp.k0 + j) * p.v_stride + ch]) << 16);
+  // this part of them
+  const int all = max(n[0], n[1]);
+  const int lo = int(int64_t(all) * split / plan.splits), hi = int(int64_t(all) * (split + 1) / plan.splits);
+  n[0] = max(0, min(n[0], hi) - lo);
+  n[1] = max(0, min(n[1], hi) - lo);
+  const int n_all = hi - lo;
+  auto tile_of = [&](int j) { return j + lo < n_pre ? j + lo : j + lo - n_pre + from; };
+
+  if (n_all > 0) {
+    if (warp == kMmaWarp) tmem_alloc(&bar.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  const uint32_t tmem = bar.tmem;
+  volatile int* dead = &bar.dead;
+  // a wait that ran out: reported once, and every later wait of the CTA is passed over
+  auto wait = [&](uint64_t* at, uint32_t parity) {
+    if (*dead) return false;
+    if (mbar_wait_bounded(at, parity, kDefaultWaitNs)) return true;
+    *dead = 1;
+    if (p.dev_status) atomicOr(p.dev_status, OSCAR_DEV_TIMEOUT);
+    return false;
+  };
+
+  // Registers: the launch's 168 a thread, 504 over the three warpgroups; a
+  // softmax thread holds a row's 128 scores.
+  if (warp < kMmaWarp)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == kLoadWarp) {
+    if (lane == 0 && n_all > 0) {
+      const int tiles_q = n[1] > 0 || tok0 + per_tile < sp.n_q ? 2 : 1;
+      mbar_arrive_expect_tx(&bar.q_full, uint32_t(tiles_q * kTileBytes));
+      for (int w = 0; w < tiles_q; ++w)
+        for (int c = 0; c < kPanels; ++c)
+          tma_load_3d(sq + w * kTileBytes + c * kPanel, &tq, 64 * c, hq0, int(sp.q0) + tok0 + w * per_tile, &bar.q_full);
+      int j = 0;
+      for (; j < n_all; ++j) {
+        const int st = j % kSt, row = int(sp.k0) + tile_of(j) * kTile;
+        if (j >= kSt && !wait(&bar.k_empty[st], (j / kSt - 1) & 1)) break;
+        mbar_arrive_expect_tx(&bar.k_full[st], kTileBytes);
+        for (int c = 0; c < kPanels; ++c)
+          tma_load_3d(sk + st * kTileBytes + c * kPanel, &tk, 64 * c, hk, row, &bar.k_full[st]);
+        if (j >= kSt && !wait(&bar.v_empty[st], (j / kSt - 1) & 1)) {
+          ++j;
+          break;
+        }
+        mbar_arrive_expect_tx(&bar.v_full[st], kTileBytes);
+        for (int c = 0; c < kPanels; ++c)
+          tma_load_3d(sv + st * kTileBytes + c * kPanel, &tv, 64 * c, hk, row, &bar.v_full[st]);
+      }
+      // what was issued has landed before the CTA's shared memory goes
+      mbar_wait_bounded(&bar.q_full, 0, kDrainWaitNs);
+      for (int i = max(0, j - kSt); i < j; ++i) {
+        mbar_wait_bounded(&bar.k_full[i % kSt], (i / kSt) & 1, kDrainWaitNs);
+        mbar_wait_bounded(&bar.v_full[i % kSt], (i / kSt) & 1, kDrainWaitNs);
+      }
     }
-    for (int s = 16; s; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    const float y = (p.s.cap_log2 != 0.f ? capped(x, p.s) : x * p.s.scale_log2) - slope * fabsf(float(i - j));
-    const float mn = fmaxf(m, y), f = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(y - mn);
-    m = mn;
-    l = l * f + w;
-    for (int e = 0; e < kC; ++e) o[e] = fmaf(w, v[e], o[e] * f);
+  } else if (warp == kMmaWarp) {
+    auto issue_s = [&](int w, int j) {
+      if (lane == 0) {
+        const uint32_t a = smem_addr(sq + w * kTileBytes), bb = smem_addr(sk + (j % kSt) * kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * kPanel + (kk % 4) * 32;
+          umma_f16_ss(tmem + w * kTile, smem_desc_kmajor_sw128(a + off), smem_desc_kmajor_sw128(bb + off), kIdescS, kk > 0);
+        }
+        umma_commit(&bar.s_full[w]);
+      }
+    };
+    bool ok = n_all > 0 && wait(&bar.q_full, 0) && wait(&bar.k_full[0], 0);
+    if (ok) {
+      for (int w = 0; w < 2; ++w)
+        if (n[w] > 0) issue_s(w, 0);
+      if (lane == 0) umma_commit(&bar.k_empty[0]);
+    }
+    for (int j = 0; j < n_all && ok; ++j) {
+      const int st = j % kSt;
+      if (j + 1 < n_all) ok = wait(&bar.k_full[(j + 1) % kSt], ((j + 1) / kSt) & 1);
+      ok = ok && wait(&bar.v_full[st], (j / kSt) & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      uint8_t* v = sv + st * kTileBytes;
+      // rows behind the request's last key may hold anything: 0 times that is not 0
+      const int valid = sp.n_k - tile_of(j) * kTile;
+      if (valid < kTile) {
+        for (int i = valid * 8 + lane; i < kTile * 8; i += 32)
+#pragma unroll
+          for (int c = 0; c < kPanels; ++c) *reinterpret_cast<uint4*>(v + c * kPanel + 16 * i) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (j < n[w]) {
+          ok = wait(&bar.p_full[w], j & 1);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t bb = smem_addr(v);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              umma_f16_ts(tmem + kColO + w * D, tmem + w * kTile + 8 * kk, smem_desc_mnmajor_sw128(bb + 2048 * kk, kPanel),
+                          kIdescO, j > 0 || kk > 0);
+            umma_commit(&bar.o_done[w]);
+          }
+        }
+        if (j + 1 < n[w]) issue_s(w, j + 1);
+      }
+      if (!ok) break;
+      if (lane == 0) {
+        umma_commit(&bar.v_empty[st]);
+        if (j + 1 < n_all) umma_commit(&bar.k_empty[(j + 1) % kSt]);
+      }
+    }
+    if (lane == 0 && n_all > 0) {   // every MMA issued is done before TMEM is given back
+      umma_commit(&bar.fin);
+      mbar_wait_bounded(&bar.fin, 0, kDrainWaitNs);
+    }
+  } else if (warp < kMmaWarp) {
+    const int w = warp >> 2, row = tid & (kTile - 1);
+    const int tok = tok0 + w * per_tile + row / pack, head = hq0 + row % pack;
+    const bool mine = tok < sp.n_q;
+    const int pos = shift + tok;
+    const int row_lo = p.s.window ? max(0, pos - p.s.window + 1) : 0;
+    const int row_hi = p.causal ? min(pos + 1, sp.n_k) : sp.n_k;
+    const float slope = p.s.slopes ? p.s.slopes[head] * kLog2e : 0.f;
+    const bool cap = p.s.cap_log2 != 0.f, formed = cap || p.s.slopes;
+    const float sc = formed ? 1.f : p.s.scale_log2;
+    const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
+    const uint32_t t_s = tmem + lanes + w * kTile, t_o = tmem + lanes + kColO + w * D;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n[w]; ++j) {
+      ok = wait(&bar.s_full[w], j & 1);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float s[kTile];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
+      tc_wait_ld();
+      const int k0 = tile_of(j) * kTile;
+      if (formed) {
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) {
+          const float t = cap ? capped(s[i], p.s) : s[i] * p.s.scale_log2;
+          s[i] = fmaf(-slope, fabsf(float(pos - k0 - i)), t);
+        }
+      }
+      const bool full = (k0 >= row_lo && k0 + kTile <= row_hi) || k0 + kTile <= sp.prefix;
+      if (!__all_sync(0xffffffffu, full)) {
+        // k0 + i in [row_lo, row_hi) or below the prefix
+        const uint32_t width = uint32_t(max(0, row_hi - row_lo));
+        const int a = k0 - row_lo, pre = sp.prefix - k0;
+#pragma unroll
+        for (int i = 0; i < kTile; ++i)
+          if (uint32_t(a + i) >= width && i >= pre) s[i] = -INFINITY;
+      }
+      float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int i = 4; i < kTile; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
+      const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      // (nothing seen yet, nothing here: -inf - -inf is no growth)
+      if (__any_sync(0xffffffffu, (mt - m) * sc > 8.f)) {
+        const float mn = fmaxf(m, mt);
+        const float f = m == -INFINITY ? 0.f : exp2_fast((m - mn) * sc);
+        m = mn;
+        l *= f;
+        if (j > 0) {
+          ok = wait(&bar.o_done[w], (j - 1) & 1);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            asm volatile(
+                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+                  "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+                : "r"(t_o + 16 * c)
+                : "memory");
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(t_o + 16 * c, o);
+          }
+        }
+      }
+      const float off = m == -INFINITY ? 0.f : -m * sc;
+      float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float2 e = fma2(make_float2(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]), make_float2(sc, sc), make_float2(off, off));
+          e.x = exp2_fast(e.x);
+          e.y = exp2_fast(e.y);
+          sum[i & 1] = add2(sum[i & 1], e);
+          pk[i] = pack_bf162(e.x, e.y);
+        }
+        tmem_st16(t_s + 16 * c, pk);
+      }
+      const float2 both = add2(sum[0], sum[1]);
+      l = both.x + both.y;
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bar.p_full[w]);
+    }
+    if (ok && n[w] > 0) {
+      ok = wait(&bar.o_done[w], (n[w] - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    const int64_t cta = (int64_t(b) * plan.blocks + blk) * plan.sets + set;
+    if (plan.splits > 1) {
+      uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+      const int64_t at = (cta * plan.splits + split) * 2 * kTile + w * kTile + row;
+      // (a part without keys, or a row without visible ones: l = 0, its sums are not read)
+      if (mine) reinterpret_cast<float2*>(ws + plan.off_ml)[at] = make_float2(m == -INFINITY ? 0.f : m * sc, ok ? l : 0.f);
+      if (ok && n[w] > 0) {
+        float* po = reinterpret_cast<float*>(ws + plan.off_o) + at * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(t_o + 32 * c, o);
+          tc_wait_ld();
+          if (mine)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4*>(po + 32 * c)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+    } else {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      uint16_t* out = p.out + ((sp.q0 + tok) * p.n_q + head) * D;
+      if (mine && p.lse) p.lse[(sp.q0 + tok) * p.n_q + head] = l > 0.f ? (m * sc + log2f(l)) * kLn2 : -INFINITY;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (ok && n[w] > 0) {
+          tmem_ld32(t_o + 32 * c, o);
+          tc_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t q[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              q[e] = pack_bf162(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+            reinterpret_cast<uint4*>(out + 32 * c)[i] = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+        }
+      }
+    }
+    if (n_all > 0) tc_fence_before();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int e = 0; e < kC; ++e)
-    p.out[((sp.q0 + r) * p.n_q + hq) * D + kC * lane + e] = __bfloat16_as_ushort(__float2bfloat16_rn(o[e] * inv));
-  if (p.lse && lane == 0) p.lse[(sp.q0 + r) * p.n_q + hq] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (n_all > 0) {
+    __syncthreads();
+    if (warp == kMmaWarp) {
+      tc_fence_after();
+      tmem_dealloc(tmem, 512);
+    }
+  }
+}
+
+// Joins the parts of each row: one warp a row.
+template <int D>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, const PromptPlan plan) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, row = (blockIdx.x % 32) * 8 + (threadIdx.x >> 5);
+  const int64_t cta = blockIdx.x / 32;
+  const int set = int(cta % plan.sets), blk = int(cta / plan.sets % plan.blocks), b = int(cta / plan.sets / plan.blocks);
+  const PromptSpan sp = prompt_span(p, b, false);
+  const int tok = blk * 2 * (kTile / plan.pack) + row / plan.pack, head = set * plan.pack + row % plan.pack;
+  if (tok >= sp.n_q) return;
+  const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
+  const float2* ml = reinterpret_cast<const float2*>(ws + plan.off_ml) + cta * plan.splits * 2 * kTile + row;
+  const float* po = reinterpret_cast<const float*>(ws + plan.off_o) + (cta * plan.splits * 2 * kTile + row) * D;
+  constexpr int kC = D / 32;
+  float mx = -INFINITY, sum = 0.f, o[kC] = {};
+  for (int s = 0; s < plan.splits; ++s) {
+    const float2 x = __ldcg(&ml[int64_t(s) * 2 * kTile]);
+    if (x.y > 0.f) mx = fmaxf(mx, x.x);
+  }
+  for (int s = 0; s < plan.splits; ++s) {
+    const float2 x = __ldcg(&ml[int64_t(s) * 2 * kTile]);
+    if (!(x.y > 0.f)) continue;
+    const float f = exp2_fast(x.x - mx);
+    sum = fmaf(f, x.y, sum);
+#pragma unroll
+    for (int e = 0; e < kC; ++e) o[e] = fmaf(f, __ldcg(&po[int64_t(s) * 2 * kTile * D + kC * lane + e]), o[e]);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((sp.q0 + tok) * p.n_q + head) * D + kC * lane);
+#pragma unroll
+  for (int e = 0; e < kC / 2; ++e) out[e] = pack_bf162(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (p.lse && lane == 0) p.lse[(sp.q0 + tok) * p.n_q + head] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+// rows [total][heads][d] bf16, `stride` elements apart, in boxes of 64 channels
+bool encode_rows(CUtensorMap* map, const uint16_t* x, int d, int heads, int64_t total, int64_t stride, int box_heads,
+                 int box_rows) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn)
+      return false;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(std::max<int64_t>(1, total))};
+  const cuuint64_t strides[2] = {cuuint64_t(d) * 2, cuuint64_t(stride) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(x), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t stream) {
+  CUtensorMap tq, tk, tv;
+  const uint16_t* k = p.total_k ? p.k : p.q;   // no key, no load: the maps only have to be well-formed
+  const uint16_t* v = p.total_k ? p.v : p.q;
+  if (!encode_rows(&tq, p.q, D, p.n_q, p.total_q, p.q_stride, plan.pack, kTile / plan.pack) ||
+      !encode_rows(&tk, k, D, p.n_kv, p.total_k, p.k_stride, 1, kTile) ||
+      !encode_rows(&tv, v, D, p.n_kv, p.total_k, p.v_stride, 1, kTile))
+    return cudaErrorInvalidValue;
+  constexpr int bytes = 1024 + (2 + 2 * kStages<D>) * (D / 64) * kPanel;
+  cudaError_t e = set_smem_limit<prompt_kernel<D>>(bytes);
+  if (e != cudaSuccess) return e;
+  const int64_t x = int64_t(plan.blocks) * plan.sets;
+  if (x > 0x7fffffff || x * p.batch > 0x7fffffff / 32) return cudaErrorInvalidValue;
+  const dim3 grid(unsigned(x), unsigned(p.batch), unsigned(plan.splits));
+  e = launch_pdl(prompt_kernel<D>, grid, dim3(kThreads), bytes, stream, p, plan, tq, tk, tv);
+  if (e != cudaSuccess || plan.splits == 1) return e;
+  return launch_pdl(prompt_join_kernel<D>, dim3(unsigned(x * p.batch * 32)), dim3(256), 0, stream, p, plan);
 }
 
 }  // namespace
 
-size_t prompt_workspace_bytes(const PromptParams&, cudaError_t* err) {
+size_t prompt_workspace_bytes(const PromptParams& p, cudaError_t* err) {
   *err = cudaSuccess;
-  return 256;
+  return plan_prompt(p).bytes;
 }
 
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
-  const dim3 grid(unsigned((p.max_q + kPromptWarps - 1) / kPromptWarps), unsigned(p.n_q), unsigned(p.batch));
-  return p.d == 128 ? launch_pdl(prompt_kernel<128>, grid, dim3(32 * kPromptWarps), 0, stream, p)
-                    : launch_pdl(prompt_kernel<64>, grid, dim3(32 * kPromptWarps), 0, stream, p);
+  const PromptPlan plan = plan_prompt(p);
+  return p.d == 128 ? launch<128>(p, plan, stream) : launch<64>(p, plan, stream);
 }
 
 }  // namespace oscar
