@@ -188,9 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Registers: the launch's 168 a thread, 504 over the three warpgroups; a
   // softmax thread holds a row's 128 scores.
-  if (warp < kMmaWarp)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-  else
+  if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kLoadWarp) {
     if (lane == 0 && n_all > 0) {
@@ -281,7 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(&bar.fin);
       mbar_wait_bounded(&bar.fin, 0, kDrainWaitNs);
     }
-  } else if (warp < kMmaWarp) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int w = warp >> 2, row = tid & (kTile - 1);
     const int tok = tok0 + w * per_tile + row / pack, head = hq0 + row % pack;
     const bool mine = tok < sp.n_q;
