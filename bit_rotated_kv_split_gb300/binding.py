@@ -379,36 +379,49 @@ def prompt_desc(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_
 
 def _heads(name, t, heads, d):
     """Row stride of bf16 rows t [n][heads][d] (bfloat16, or its bits as uint16) whose heads lie side by side."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.element_size() != 2:
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.element_size() != 2:
         raise ValueError("%s must be bfloat16 [n][%d][%d]" % (name, heads, d))
-    st = t.stride()
-    if t.shape[0] == 0:
+    if shape[0] == 0:
         return heads * d
-    if st[2] != 1 or (heads > 1 and st[1] != d):
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != d):
         raise ValueError("%s: the heads of a row must lie side by side" % name)
-    return heads * d if t.shape[0] == 1 else st[0]
+    return heads * d if shape[0] == 1 else row
 
 
 def _index(name, t, n):
-    if t is not None and (t.dim() != 1 or t.shape[0] < n or t.stride(0) != 1 or str(t.dtype) != "torch.int32"):
+    if t is not None and (t.dim() != 1 or t.numel() < n or t.element_size() != 4 or t.is_floating_point()
+                          or not t.is_contiguous()):
         raise ValueError("%s must be contiguous int32 with at least %d entries" % (name, n))
 
 
 def _contiguous(name, t, shape, itemsize):
-    if t is not None and (tuple(t.shape) != shape or t.element_size() != itemsize or not t.is_contiguous()):
+    if t is not None and (t.shape != shape or t.element_size() != itemsize or not t.is_contiguous()):
         raise ValueError("%s must be contiguous %s" % (name, list(shape)))
 
 
-def _on_device(name, t, stream, *args):
-    """Calls the library with t's device current and, without a stream, on that device's current stream."""
-    import torch
-    fn = getattr(lib, name)
-    index = t.device.index
-    if index is None or index == torch.cuda.current_device():
-        _check(name, fn(*args, _stream(stream)))
-        return
-    with torch.cuda.device(index):
-        _check(name, fn(*args, _stream(stream)))
+_torch = None
+
+
+def _on_device(name, stream, tensors, fn, args):
+    """Calls the library with the tensors' device current and, without a stream, on that device's current stream."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    cuda = _torch.cuda
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != index or index < 0):
+            raise ValueError("%s: every tensor must be on one CUDA device" % name)
+    if index != cuda.current_device():
+        with cuda.device(index):
+            status = fn(*args, _stream(stream))
+    else:
+        status = fn(*args, cuda.current_stream().cuda_stream if stream is None else _stream(stream))
+    if status != OSCAR_OK:
+        raise OscarError(name, status)
 
 
 def _ref(d):
@@ -434,8 +447,10 @@ def oscar_rope_append_int4(desc: Int4Desc, rope, q, k, v, dst_req, dst_pos, q_ou
     _index("dst_req", dst_req, n), _index("dst_pos", dst_pos, n), _index("rope_pos", rope_pos, n)
     _contiguous("q_out", q_out, (n, hq, d), 2)
     _contiguous("k_out", k_out, (n, hk, d), 2)
-    _on_device("oscar_rope_append_int4", k, stream, ctypes.byref(desc), _ref(rope), _ptr(q), qs, _ptr(k), ks,
-               _ptr(v), vs, _ptr(dst_req), _ptr(dst_pos), _ptr(rope_pos), n, _ptr(q_out), _ptr(k_out))
+    _on_device("oscar_rope_append_int4", stream, (k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos),
+               lib.oscar_rope_append_int4, (
+                   ctypes.byref(desc), _ref(rope), _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, dst_req.data_ptr(),
+                   dst_pos.data_ptr(), _ptr(rope_pos), n, _ptr(q_out), _ptr(k_out)))
 
 
 def oscar_gather_int4(desc: Int4Desc, src_req, src_pos, k_out, v_out, stream=None) -> None:
@@ -445,8 +460,8 @@ def oscar_gather_int4(desc: Int4Desc, src_req, src_pos, k_out, v_out, stream=Non
     if v_out.shape[0] != n:
         raise ValueError("k_out and v_out must have one row count")
     _index("src_req", src_req, n), _index("src_pos", src_pos, n)
-    _on_device("oscar_gather_int4", k_out, stream, ctypes.byref(desc), _ptr(src_req), _ptr(src_pos), n,
-               _ptr(k_out), ks, _ptr(v_out), vs)
+    _on_device("oscar_gather_int4", stream, (k_out, v_out, src_req, src_pos), lib.oscar_gather_int4, (
+        ctypes.byref(desc), src_req.data_ptr(), src_pos.data_ptr(), n, k_out.data_ptr(), ks, v_out.data_ptr(), vs))
 
 
 def oscar_decode_int4_workspace_bytes(desc: Int4Desc) -> int:
@@ -465,8 +480,8 @@ def oscar_decode_attention_int4(desc: Int4Desc, q, out, workspace, score=None, s
     _contiguous("out", out, (b, hq, d), 2)
     _slopes_ok(score, hq)
     size = c_size_t(workspace.numel() * workspace.element_size())
-    _on_device("oscar_decode_attention_int4", q, stream, ctypes.byref(desc), _ref(score), _ptr(q), qs, _ptr(out),
-               _ptr(workspace), ctypes.byref(size))
+    _on_device("oscar_decode_attention_int4", stream, (q, out, workspace), lib.oscar_decode_attention_int4, (
+        ctypes.byref(desc), _ref(score), q.data_ptr(), qs, out.data_ptr(), workspace.data_ptr(), ctypes.byref(size)))
 
 
 def oscar_prompt_workspace_bytes(desc: PromptDesc) -> int:
@@ -490,6 +505,8 @@ def oscar_prompt_attention(desc: PromptDesc, q, k, v, cu_q, cu_k, out, workspace
     _contiguous("lse", lse, (desc.total_q, hq), 4)
     _slopes_ok(score, hq)
     size = c_size_t(workspace.numel() * workspace.element_size())
-    _on_device("oscar_prompt_attention", q, stream, ctypes.byref(desc), _ref(score), _ptr(q), qs, _ptr(k), ks,
-               _ptr(v), vs, _ptr(cu_q), _ptr(cu_k), _ptr(prefix_len), _ptr(out), _ptr(lse), _ptr(workspace),
-               ctypes.byref(size))
+    _on_device("oscar_prompt_attention", stream, (q, k, v, cu_q, cu_k, out, workspace, prefix_len, lse),
+               lib.oscar_prompt_attention, (
+                   ctypes.byref(desc), _ref(score), q.data_ptr(), qs, _ptr(k), ks, _ptr(v), vs, cu_q.data_ptr(),
+                   cu_k.data_ptr(), _ptr(prefix_len), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                   ctypes.byref(size)))

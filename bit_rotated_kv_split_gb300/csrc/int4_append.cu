@@ -11,6 +11,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "int4.h"
 #include "kernels.h"
 #include "oscar.h"
@@ -29,41 +31,68 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
   return make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]), pack_bf162(x[4], x[5]), pack_bf162(x[6], x[7]));
 }
 
-// x c + y s, so that its rounding to bf16 is that of the exact value.  The
-// fp32 result is within e of it; where e spans a rounding border of bf16
-// (about one value in 2^12) the sum is formed in 64 bits, whose products are
-// exact and whose sum is rounded at 2^-53.
-__device__ __forceinline__ float rotate_exact(float x, float c, float y, float s) {
-  const float t = y * s;
-  const float r = fmaf(x, c, t);
-  const float e = (fabsf(t) + fabsf(r)) * 1.1920929e-7f;
-  const uint32_t both = pack_bf162(r - e, r + e);
-  if ((both & 0xFFFFu) != (both >> 16)) return float(fma(double(x), double(c), double(y) * double(s)));
-  return r;
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {   // a NaN wins
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
-// Codes of the 8 values of this lane (x - zero over scale, to nearest even,
-// 0 .. 15) in a group of `lanes` lanes; *pair = (scale, zero) as fp16 bits.
-__device__ __forceinline__ uint32_t quantise8(float (&x)[8], float tau, int lanes, uint32_t* pair) {
-  float lo = tau, hi = -tau;
+// Codes of the 8 bf16 values u of this lane (x - zero over scale, to nearest
+// even, 0 .. 15) in a group of `lanes` lanes; *pair = (scale, zero), fp16 bits.
+//
+// The group's extremes are taken on packed bf16 (max x, max -x).  rint(t / s)
+// is taken as rint(t / s by an approximate reciprocal) and checked: where the
+// remainder t - k s (one fma) comes within 2^-19 of half a step, the quotients
+// are divided out.  (With a division for every value the kernel had a third
+// more instructions.)
+__device__ __forceinline__ uint32_t quantise8(const uint4& u, float tau, int lanes, uint32_t* pair) {
+  uint32_t hi2 = max_bf16x2(max_bf16x2(u.x, u.y), max_bf16x2(u.z, u.w));
+  uint32_t lo2 = max_bf16x2(max_bf16x2(u.x ^ 0x80008000u, u.y ^ 0x80008000u),
+                            max_bf16x2(u.z ^ 0x80008000u, u.w ^ 0x80008000u));
+  uint32_t ends = max_bf16x2(prmt(hi2, lo2, 0x5410), prmt(hi2, lo2, 0x7632));   // (max x, max -x)
+  for (int m = 1; m < lanes; m <<= 1) ends = max_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
+  float hi = bf16_lo(ends), lo = -bf16_hi(ends);
+  float x[8];
+  unpack_bf16x8(u, x);
+  if (!(hi <= tau && lo >= -tau)) {       // clamped values, or a NaN, which becomes -tau
+    hi = -tau, lo = tau;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[i] = fminf(fmaxf(x[i], -tau), tau);   // (a NaN becomes -tau)
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
-  for (int m = 1; m < lanes; m <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+    for (int i = 0; i < 8; ++i) {
+      x[i] = fminf(fmaxf(x[i], -tau), tau);
+      hi = fmaxf(hi, x[i]);
+      lo = fminf(lo, x[i]);
+    }
+    // (the whole group is here: the test is the group's)
+    const uint32_t group = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1) << (threadIdx.x & 31 & ~(lanes - 1));
+    for (int m = 1; m < lanes; m <<= 1) {
+      hi = fmaxf(hi, __shfl_xor_sync(group, hi, m));
+      lo = fminf(lo, __shfl_xor_sync(group, lo, m));
+    }
   }
   const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f)), zh = __float2half_rn(lo);
   const float s = __half2float(sh), z = __half2float(zh);
   *pair = uint32_t(__half_as_ushort(sh)) | (uint32_t(__half_as_ushort(zh)) << 16);
+  const float inv = rcp_fast(s), top = 15.f * s, half = s * 0.499999f;
+  constexpr float kRound = 12582912.f;   // 1.5 2^23: the sum's low bits are the rounded integer
   uint32_t word = 0;
+  bool near = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float u = s > 0.f ? rintf(__fdiv_rn(x[i] - z, s)) : 0.f;
-    word |= uint32_t(fminf(fmaxf(u, 0.f), 15.f)) << (4 * i);
+    x[i] = fminf(fmaxf(x[i] - z, 0.f), top);
+    const float k = fmaf(x[i], inv, kRound);
+    near = near | (fabsf(fmaf(kRound - k, s, x[i])) >= half);
+    word += (__float_as_uint(k) - 0x4B400000u) << (4 * i);
+  }
+  if (!(s > 0.f)) return 0;
+  if (near) {
+    word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) word |= uint32_t(rintf(__fdiv_rn(x[i], s))) << (4 * i);
   }
   return word;
 }
@@ -88,30 +117,118 @@ __device__ __forceinline__ uint8_t* token_block(const Int4Cache& c, int req, int
   return c.pages + int64_t(page) * c.n_kv * int4_block_bytes(c.d, c.ng_k, c.ng_v);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const AppendParams p, int slots_per_warp) {
+// What a lane needs to turn an octet: octet o of a half-split head turns with
+// o mod h, h = rot / 16, and takes its partner's channels from `partner`; an
+// interleaved octet has the 4 angles 4 o ..
+struct Turn {
+  float c[8], s[8];   // s carries the sign of this half
+  int partner;
+  bool on;
+};
+
+// Value i of the turned octet: a c + b s.
+__device__ __forceinline__ void operands(const Turn& t, bool interleaved, const float (&x)[8], const float (&y)[8],
+                                         int i, float* a, float* c, float* b, float* s) {
+  if (!interleaved) {
+    *a = x[i], *c = t.c[i], *b = y[i], *s = t.s[i];
+  } else {
+    *a = x[i & ~1], *b = x[i | 1];
+    *c = (i & 1) ? t.s[i >> 1] : t.c[i >> 1];
+    *s = (i & 1) ? t.c[i >> 1] : -t.s[i >> 1];
+  }
+}
+
+// Rotates the octet held in `raw`; whole warps call it.  Exact: the rounding to
+// bf16 is that of the exact value.  The fp32 result r is within e of it; where
+// r - e and r + e round apart (about one value in 2^13) the octet is formed in
+// 64 bits, whose products are exact and whose sums are rounded at 2^-53.
+template <bool Exact, bool Interleaved>
+__device__ __forceinline__ void rotate8(uint4& raw, const Turn& t) {
+  uint4 other = make_uint4(0, 0, 0, 0);
+  if (!Interleaved) {
+    other.x = __shfl_sync(0xffffffffu, raw.x, t.partner);
+    other.y = __shfl_sync(0xffffffffu, raw.y, t.partner);
+    other.z = __shfl_sync(0xffffffffu, raw.z, t.partner);
+    other.w = __shfl_sync(0xffffffffu, raw.w, t.partner);
+  }
+  if (!t.on) return;
+  float x[8], y[8];
+  unpack_bf16x8(raw, x);
+  unpack_bf16x8(other, y);
+  uint32_t out[4], apart = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float r[2], e[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float a, c, b, s;
+      operands(t, Interleaved, x, y, 2 * i + u, &a, &c, &b, &s);
+      const float bs = b * s;
+      r[u] = fmaf(a, c, bs);
+      if (Exact) e[u] = (fabsf(bs) + fabsf(r[u])) * 1.1920929e-7f;
+    }
+    if (Exact) {
+      out[i] = pack_bf162(r[0] - e[0], r[1] - e[1]);
+      apart |= out[i] ^ pack_bf162(r[0] + e[0], r[1] + e[1]);
+    } else {
+      out[i] = pack_bf162(r[0], r[1]);
+    }
+  }
+  if (Exact && apart) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      float r[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float a = 0.f, c = 0.f, b = 0.f, s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (w == i) operands(t, Interleaved, x, y, 2 * w + u, &a, &c, &b, &s);
+        r[u] = float(fma(double(a), double(c), double(b) * double(s)));
+      }
+      const uint32_t v = pack_bf162(r[0], r[1]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (w == i) out[w] = v;
+    }
+  }
+  raw = make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+__device__ __forceinline__ void load8(float (&x)[8], const float* p, int n) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (4 * i < n) {
+      const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
+      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+    }
+}
+
+// One warp takes `slots_per_warp` slots of one token: its q heads four slots at
+// a time, whose loads are in flight together, then k and v heads with the next
+// slot's load ahead of the present one's work.
+template <int D, bool Interleaved>
+__global__ void __launch_bounds__(kAppendThreads, 6)
+    rope_append_kernel(const __grid_constant__ AppendParams p, int slots_per_warp) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
   const int lane = threadIdx.x & 31, o = lane % kLanes, sub = lane / kLanes;
-  const int sq = (p.c.n_q + kRows - 1) / kRows, sk = (p.c.n_kv + kRows - 1) / kRows;
-  const int first_q = p.q ? 0 : sq, slots = sq + 2 * sk - first_q;
-  const int warps_per_token = (slots + slots_per_warp - 1) / slots_per_warp;
+  const int sq = p.q ? (p.c.n_q + kRows - 1) / kRows : 0, sk = (p.c.n_kv + kRows - 1) / kRows;
+  const int slots = sq + 2 * sk, warps_per_token = (slots + slots_per_warp - 1) / slots_per_warp;
   const int64_t w = (int64_t(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
   const int64_t i = w / warps_per_token;
   if (i >= p.n) return;
-  const int part = int(w % warps_per_token);
+  const int part = int(w - i * warps_per_token);
   const int pos = p.dst_pos[i];
   const bool report = part == 0 && lane == 0;
   uint8_t* base = token_block(p.c, p.dst_req[i], pos, report);
   if (!base) return;
   const int slot = pos % kInt4Page;
-  // this lane's angles: octet o of a half-split head turns with o mod h, h =
-  // rot / 16; an interleaved octet has the 4 angles 4 o ..
+  Turn turn;
   const int h = p.rot / 16;
-  const bool turns = o < 2 * h;
-  float cs[8], sn[8];
-  int partner = lane;
+  turn.on = o < 2 * h;
+  turn.partner = lane;
   if (p.rot) {
     const int64_t at = p.rope_pos ? p.rope_pos[i] : pos;
     if (at < 0 || at >= p.n_positions) {
@@ -119,72 +236,74 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const Appen
       return;
     }
     const float* row = p.cos_sin + at * p.rot;
-    if (turns && !p.interleaved) {
+    if (turn.on && !Interleaved) {
       const int j = o < h ? o : o - h;
-      partner = o < h ? lane + h : lane - h;
+      turn.partner = o < h ? lane + h : lane - h;
+      load8(turn.c, row + 8 * j, 8);
+      load8(turn.s, row + 8 * (h + j), 8);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) cs[e] = row[8 * j + e], sn[e] = row[8 * (h + j) + e];
-    } else if (turns) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) cs[e] = row[4 * o + e], sn[e] = row[8 * h + 4 * o + e];
+      for (int e = 0; e < 8; ++e) turn.s[e] = o < h ? -turn.s[e] : turn.s[e];
+    } else if (turn.on) {
+      load8(turn.c, row + 4 * o, 4);
+      load8(turn.s, row + 8 * h + 4 * o, 4);
     }
   }
-  const int end = min(slots, (part + 1) * slots_per_warp);
-  for (int t = part * slots_per_warp; t < end; ++t) {
-    const int s = t + first_q;
-    const int kind = s < sq ? 0 : s < sq + sk ? 1 : 2;   // q, k, v
-    const int head = (s - (kind == 0 ? 0 : kind == 1 ? sq : sq + sk)) * kRows + sub;
-    const bool valid = head < (kind == 0 ? p.c.n_q : p.c.n_kv);
-    const uint16_t* src = kind == 0 ? p.q + i * p.q_stride : kind == 1 ? p.k + i * p.k_stride : p.v + i * p.v_stride;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (valid) raw = *reinterpret_cast<const uint4*>(src + int64_t(head) * D + 8 * o);
-    float x[8];
-    unpack_bf16x8(raw, x);
-    if (kind < 2 && p.rot) {
-      if (!p.interleaved) {
-        uint4 other;
-        other.x = __shfl_sync(0xffffffffu, raw.x, partner);
-        other.y = __shfl_sync(0xffffffffu, raw.y, partner);
-        other.z = __shfl_sync(0xffffffffu, raw.z, partner);
-        other.w = __shfl_sync(0xffffffffu, raw.w, partner);
-        float y[8];
-        unpack_bf16x8(other, y);
-        if (turns) {
-          const float sign = o < h ? -1.f : 1.f;
+  const int begin = part * slots_per_warp, end = min(slots, begin + slots_per_warp);
+  // q
+  const int end_q = min(end, sq);
+  const uint16_t* src = p.q + i * p.q_stride + sub * D + 8 * o;
+  uint16_t* dst = p.q_out + (i * p.c.n_q + sub) * D + 8 * o;
+  for (int s0 = begin; s0 < end_q; s0 += kBatch) {
+    uint4 raw[kBatch];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            x[e] = kind == 0 ? fmaf(x[e], cs[e], y[e] * (sign * sn[e])) : rotate_exact(x[e], cs[e], y[e], sign * sn[e]);
-        }
-      } else if (turns) {
+    for (int u = 0; u < kBatch; ++u) {
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (s0 + u < end_q && (s0 + u) * kRows + sub < p.c.n_q)
+        raw[u] = *reinterpret_cast<const uint4*>(src + (s0 + u) * (kRows * D));
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = x[2 * e], b = x[2 * e + 1];
-          x[2 * e] = kind == 0 ? fmaf(a, cs[e], b * -sn[e]) : rotate_exact(a, cs[e], b, -sn[e]);
-          x[2 * e + 1] = kind == 0 ? fmaf(a, sn[e], b * cs[e]) : rotate_exact(a, sn[e], b, cs[e]);
-        }
-      }
-      raw = pack_bf16x8(x);
-      if (kind == 1) unpack_bf16x8(raw, x);   // the codes are those of the rounded row
+    for (int u = 0; u < kBatch; ++u) {
+      if (s0 + u >= end_q) break;
+      if (p.rot) rotate8<false, Interleaved>(raw[u], turn);
+      if ((s0 + u) * kRows + sub < p.c.n_q) *reinterpret_cast<uint4*>(dst + (s0 + u) * (kRows * D)) = raw[u];
     }
-    if (kind < 2) {
-      uint16_t* out = kind == 0 ? p.q_out : p.k_out;
-      if (out && valid) *reinterpret_cast<uint4*>(out + (i * (kind == 0 ? p.c.n_q : p.c.n_kv) + head) * D + 8 * o) = raw;
+  }
+  // k, then v
+  const int ng_k = p.c.ng_k, ng_v = p.c.ng_v, block_bytes = int4_block_bytes(D, ng_k, ng_v);
+  auto load = [&](int s) {
+    uint4 r = make_uint4(0, 0, 0, 0);
+    const bool is_v = s >= sk;
+    const int head = (is_v ? s - sk : s) * kRows + sub;
+    const uint16_t* x = is_v ? p.v + i * p.v_stride : p.k + i * p.k_stride;
+    if (s < end - sq && head < p.c.n_kv) r = *reinterpret_cast<const uint4*>(x + head * D + 8 * o);
+    return r;
+  };
+  int s = max(0, begin - sq);
+  uint4 next = load(s);
+#pragma unroll 1
+  for (; s < end - sq; ++s) {
+    uint4 raw = next;
+    next = load(s + 1);
+    const bool is_v = s >= sk;
+    const int head = (is_v ? s - sk : s) * kRows + sub;
+    const bool valid = head < p.c.n_kv;
+    if (!is_v) {
+      if (p.rot) rotate8<true, Interleaved>(raw, turn);
+      if (p.k_out && valid) *reinterpret_cast<uint4*>(p.k_out + (i * p.c.n_kv + head) * D + 8 * o) = raw;
     }
-    if (kind == 0) continue;
-    const int ng_k = p.c.ng_k, ng_v = p.c.ng_v;
-    const int lanes = kLanes / (kind == 1 ? ng_k : ng_v);
+    const int lanes = kLanes / (is_v ? ng_v : ng_k);
     uint32_t pair;
-    const uint32_t word = quantise8(x, kind == 1 ? p.tau_k : p.tau_v, lanes, &pair);
+    const uint32_t word = quantise8(raw, is_v ? p.tau_v : p.tau_k, lanes, &pair);   // of the rounded row
     if (!valid) continue;
-    uint8_t* block = base + int64_t(head) * int4_block_bytes(D, ng_k, ng_v);
-    if (kind == 1) {
+    uint8_t* block = base + int64_t(head) * block_bytes;
+    if (!is_v) {
       *reinterpret_cast<uint32_t*>(block + int4_k_word(D, slot, o)) = word;
     } else {
       *reinterpret_cast<uint16_t*>(block + int4_v_half(D, slot, 2 * o)) = uint16_t(word);
       *reinterpret_cast<uint16_t*>(block + int4_v_half(D, slot, 2 * o + 1)) = uint16_t(word >> 16);
     }
     if (o % lanes == 0)
-      *reinterpret_cast<uint32_t*>(block + int4_pair(D, ng_k, ng_v, slot, (kind == 1 ? 0 : ng_k) + o / lanes)) = pair;
+      *reinterpret_cast<uint32_t*>(block + int4_pair(D, ng_k, ng_v, slot, (is_v ? ng_k : 0) + o / lanes)) = pair;
   }
 }
 
@@ -233,12 +352,15 @@ cudaError_t grid_of(int64_t warps, unsigned* blocks) {
 cudaError_t launch_rope_append_int4(const AppendParams& p, cudaStream_t stream) {
   const int rows = 32 / (p.c.d / 8);
   const int slots = (p.q ? (p.c.n_q + rows - 1) / rows : 0) + 2 * ((p.c.n_kv + rows - 1) / rows);
-  const int slots_per_warp = 1;
+  // a warp takes as much of a token as leaves the GPU 24 warps an SM: the
+  // angles and places of a token are then read once, not once a slot
+  const int slots_per_warp = int(std::min<int64_t>(slots, std::max<int64_t>(1, int64_t(p.n) * slots / (152 * 24))));
   unsigned blocks = 0;
   const cudaError_t e = grid_of(int64_t(p.n) * ((slots + slots_per_warp - 1) / slots_per_warp), &blocks);
   if (e != cudaSuccess) return e;
-  return p.c.d == 128 ? launch_pdl(rope_append_kernel<128>, dim3(blocks), dim3(kAppendThreads), 0, stream, p, slots_per_warp)
-                      : launch_pdl(rope_append_kernel<64>, dim3(blocks), dim3(kAppendThreads), 0, stream, p, slots_per_warp);
+  auto* kernel = p.c.d == 128 ? (p.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
+                              : (p.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
+  return launch_pdl(kernel, dim3(blocks), dim3(kAppendThreads), 0, stream, p, slots_per_warp);
 }
 
 cudaError_t launch_gather_int4(const GatherParams& p, cudaStream_t stream) {
