@@ -44,6 +44,7 @@ constexpr int kRounds = 24;           // rounds of them that a grid is split int
 // below this many (request, head set) pairs.
 constexpr int kTickets = 4096;
 static_assert(kSlots * kRounds / 2 <= kTickets, "every split pair has a ticket");
+constexpr int kMostSplits = 512;      // their weights fit the joining CTA's shared memory
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
 struct SplitPlan {
@@ -66,7 +67,7 @@ SplitPlan plan_splits(const Int4Cache& c, const ScoreParams& s) {
   const int64_t round = int64_t(kSlots) * kWarps * 16;
   const int64_t rounds = std::min<int64_t>(kRounds, std::max<int64_t>(1, (pairs * pages + round / 2) / round));
   const int64_t most = std::max<int64_t>(1, pages / (kWarps * 4));
-  r.splits = int(std::min<int64_t>(most, std::max<int64_t>(1, kSlots * rounds / pairs)));
+  r.splits = int(std::min<int64_t>(std::min<int64_t>(most, kMostSplits), std::max<int64_t>(1, kSlots * rounds / pairs)));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   r.off_ml = up(size_t(kTickets) * 4);
   r.off_o = r.off_ml + up(size_t(pairs) * r.splits * kHeads * 8);
@@ -91,6 +92,14 @@ template <int N>
 __device__ __forceinline__ void lds_pairs(float2 (&sz)[N], const uint8_t* p) {
 #pragma unroll
   for (int i = 0; i < N; ++i) sz[i] = half2_to_float2(*reinterpret_cast<const uint32_t*>(p + 4 * i));
+}
+
+// D += A (16x16 f16, row) * B (16x8 f16, col); free for the compiler to move.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float max_over_rows(float v) {   // over the 8 lanes of a column pair
@@ -136,25 +145,34 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
   const int begin = page0 + int(int64_t(pages) * split / splits), end = page0 + int(int64_t(pages) * (split + 1) / splits);
   const int n_it = max(0, (end - begin - warp + kWarps - 1) / kWarps);
 
+  // Lane i brings page 32 n + i of the warp's: its place in the pool is worked
+  // out once for 32 pages.
   const int32_t* table = c.page_table + int64_t(b) * c.max_pages + begin + warp;
   uint8_t* ring = smem + warp * (kStages * kBlock);
-  int ids = lane < n_it ? table[kWarps * lane] : 0, ids_next = 0;
-  uint32_t live = 0;                      // stage i holds a page of the pool
+  uint64_t* wbars = bars[warp];
+  auto page_of = [&](int i) {
+    const int id = i < n_it ? table[kWarps * i] : 0;
+    if (id >= 0 && id < c.n_pages) return c.pages + (int64_t(id) * c.n_kv + hk) * kBlock;
+    if (c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+    return static_cast<uint8_t*>(nullptr);
+  };
+  const uint8_t *src = page_of(lane), *src_next = nullptr;
+  uint32_t live = __ballot_sync(0xffffffffu, src != nullptr), live_next = 0;   // of the pages in src, src_next
+  uint32_t ring_live = 0;                 // bit i: stage i holds a page of the pool
   auto issue = [&](int it) {
-    if ((it & 31) == 0) {
-      if (it) ids = ids_next;
-      ids_next = it + 32 + lane < n_it ? table[kWarps * (it + 32 + lane)] : 0;
+    const int at = it & 31, st = it % kStages;
+    if (at == 0) {
+      if (it) src = src_next, live = live_next;
+      src_next = page_of(it + 32 + lane);
+      live_next = __ballot_sync(0xffffffffu, src_next != nullptr);
     }
-    const int id = __shfl_sync(0xffffffffu, ids, it & 31), st = it % kStages;
-    const bool ok = id >= 0 && id < c.n_pages;
-    live = ok ? live | (1u << st) : live & ~(1u << st);
-    if (lane == 0) {
-      if (ok) {
-        mbar_arrive_expect_tx(&bars[warp][st], kBlock);
-        bulk_copy_g2s(ring + st * kBlock, c.pages + (int64_t(id) * c.n_kv + hk) * kBlock, kBlock, &bars[warp][st]);
+    ring_live = (ring_live & ~(1u << st)) | (((live >> at) & 1u) << st);
+    if (lane == at) {
+      if (src) {
+        mbar_arrive_expect_tx(wbars + st, kBlock);
+        bulk_copy_g2s(ring + st * kBlock, src, kBlock, wbars + st);
       } else {
-        mbar_arrive(&bars[warp][st]);
-        if (c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+        mbar_arrive(wbars + st);
       }
     }
   };
@@ -211,13 +229,19 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
 #pragma unroll
       for (int g = 0; g < NGK; ++g) qs[g][e] = __shfl_sync(0xffffffffu, sum[g], from);
       unscale[e] = __shfl_sync(0xffffffffu, un, from);
-      if (p.s.cap_log2 == 0.f) unscale[e] *= p.s.scale_log2;
+      if (p.s.cap_log2 == 0.f) unscale[e] *= p.s.scale_log2;   // (with a cap, capped() takes the scale)
       slope[e] = p.s.slopes && 2 * tig + e < heads ? p.s.slopes[hq0 + 2 * tig + e] * kLog2e : 0.f;
     }
   }
   const bool cap = p.s.cap_log2 != 0.f;
 
-  float o[2 * W][4], zs[NGV][2], m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
+  // x is in the dot product's own scale, or in log2 units where the score has a
+  // form of its own; us takes it to log2 units, thr is m + 8 / us.
+  const bool formed = cap || p.s.slopes;
+  float us[2], thr[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) us[e] = formed ? 1.f : fmaxf(unscale[e], FLT_MIN), thr[e] = -FLT_MAX;
+  float o[2 * W][4], zs[NGV][2], m[2] = {-FLT_MAX, -FLT_MAX}, off[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
   int ve = -24;                           // the V scales seen are at most 2^ve
   float vs_top = pow2i(-24), vs_mul = pow2i(31);   // 2^(7 - ve): p s_V 2^(7 - ve) <= 2^15
 #pragma unroll
@@ -225,17 +249,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
 #pragma unroll
   for (int g = 0; g < NGV; ++g) zs[g][0] = zs[g][1] = 0.f;
 
-  bool dead = false;
-  for (int it = 0; it < issued; ++it) {
+  int it = 0;
+  for (; it < issued; ++it) {
     const int st = it % kStages;
-    const bool landed = mbar_wait_bounded(&bars[warp][st], (it / kStages) & 1, kDefaultWaitNs);
-    if (!__all_sync(0xffffffffu, landed)) {
-      if (lane == 0 && !dead && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_TIMEOUT);
-      dead = true;                        // nothing more is issued; what is in flight is still waited for
-    }
-    if (!dead && ((live >> st) & 1)) {
+    const uint32_t parity = (it / kStages) & 1;
+    if (!__all_sync(0xffffffffu, mbar_try_wait(wbars + st, parity)) &&
+        !__all_sync(0xffffffffu, mbar_wait_bounded(wbars + st, parity, kDefaultWaitNs)))
+      break;
+    if ((ring_live >> st) & 1) {
       const uint8_t* blk = ring + st * kBlock;
-      const int tok = (begin + warp + kWarps * it) * kInt4Page;
       // S: rows gid and gid + 8 are tokens, columns 2 tig and 2 tig + 1 heads
       float acc[NGK][4];
 #pragma unroll
@@ -243,40 +265,56 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
       uint32_t k0[W], k1[W];
       lds_words(k0, blk + gid * (D / 2) + tig * (4 * W));
       lds_words(k1, blk + (gid + 8) * (D / 2) + tig * (4 * W));
+      float2 kp[2][NGK], vp[2][NGV];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint8_t* pr = blk + kPairs + 4 * (NGK + NGV) * (gid + 8 * r);
+        lds_pairs(kp[r], pr);
+        lds_pairs(vp[r], pr + 4 * NGK);
+      }
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        mma_f16(acc[w * NGK / W], k0[w] & kLow, k1[w] & kLow, k0[w] & kHigh, k1[w] & kHigh, qb[2 * w][0], qb[2 * w][1]);
+        mma(acc[w * NGK / W], k0[w] & kLow, k1[w] & kLow, k0[w] & kHigh, k1[w] & kHigh, qb[2 * w][0], qb[2 * w][1]);
         const uint32_t a = k0[w] >> 8, d = k1[w] >> 8;
-        mma_f16(acc[w * NGK / W], a & kLow, d & kLow, a & kHigh, d & kHigh, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        mma(acc[w * NGK / W], a & kLow, d & kLow, a & kHigh, d & kHigh, qb[2 * w + 1][0], qb[2 * w + 1][1]);
       }
       float y[2][2];
-      float2 vp[2][NGV];
-      const bool edge = tok < first || tok + kInt4Page > len;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[r][e] = 0.f;
+#pragma unroll
+          for (int g = 0; g < NGK; ++g)
+            y[r][e] = fmaf(kp[r][g].x, acc[g][2 * r + e], fmaf(kp[r][g].y, qs[g][e], y[r][e]));
+        }
+      const int tok = (begin + warp + kWarps * it) * kInt4Page;
+      if (formed) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = y[r][e] * unscale[e];
+            y[r][e] = fmaf(slope[e], float(tok + gid + 8 * r - (len - 1)), cap ? capped(x, p.s) : x);
+          }
+      }
+      if (tok < first || tok + kInt4Page > len) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int j = tok + gid + 8 * r;
+          if (j < first || j >= len) {
+            y[r][0] = y[r][1] = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < NGV; ++g) vp[r][g] = make_float2(0.f, 0.f);   // a stale slot may hold anything
+          }
+        }
+      }
       bool grow = false;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int t = gid + 8 * r, j = tok + t;
-        const uint8_t* pr = blk + kPairs + 4 * (NGK + NGV) * t;
-        float2 kp[NGK];
-        lds_pairs(kp, pr);
-        lds_pairs(vp[r], pr + 4 * NGK);
-        const float away = float(j - (len - 1));
-        const bool seen = !edge || (j >= first && j < len);
+        grow = grow | (y[r][0] > thr[0]) | (y[r][1] > thr[1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = 0.f;
-#pragma unroll
-          for (int g = 0; g < NGK; ++g) x = fmaf(kp[g].x, acc[g][2 * r + e], fmaf(kp[g].y, qs[g][e], x));
-          x *= unscale[e];
-          if (cap) x = capped(x, p.s);
-          y[r][e] = seen ? fmaf(slope[e], away, x) : -INFINITY;
-          grow |= y[r][e] > m[e] + 8.f;
-        }
-#pragma unroll
-        for (int g = 0; g < NGV; ++g) {
-          if (!seen) vp[r][g] = make_float2(0.f, 0.f);   // a stale slot may hold anything
-          grow |= vp[r][g].x > vs_top;
-        }
+        for (int g = 0; g < NGV; ++g) grow = grow | (vp[r][g].x > vs_top);
       }
       if (__any_sync(0xffffffffu, grow)) {
         float top = 0.f;
@@ -293,8 +331,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float mn = fmaxf(m[e], max_over_rows(fmaxf(y[0][e], y[1][e])));
-          f[e] = exp2_fast(m[e] - mn);
+          f[e] = exp2_fast((m[e] - mn) * us[e]);
           m[e] = mn;
+          off[e] = -mn * us[e];
+          thr[e] = mn + 8.f / us[e];
           l[e] *= f[e];
 #pragma unroll
           for (int g = 0; g < NGV; ++g) zs[g][e] *= f[e];
@@ -303,19 +343,19 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
 #pragma unroll
         for (int t = 0; t < 2 * W; ++t) o[t][0] *= f[0], o[t][1] *= f[1], o[t][2] *= f[0], o[t][3] *= f[1];
       }
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          y[r][e] = exp2_fast(y[r][e] - m[e]);
-          l[e] += y[r][e];
-#pragma unroll
-          for (int g = 0; g < NGV; ++g) zs[g][e] = fmaf(y[r][e], vp[r][g].y, zs[g][e]);
-        }
       // O: rows are channels; k = tokens 2 tig, 2 tig + 1 (and + 8)
       uint32_t v0[W], v1[W];
       lds_words(v0, blk + 8 * D + (8 * tig + gid) * (4 * W));
       lds_words(v1, blk + 8 * D + (8 * (tig + 4) + gid) * (4 * W));
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[r][e] = exp2_fast(fmaf(y[r][e], us[e], off[e]));
+          l[e] += y[r][e];
+#pragma unroll
+          for (int g = 0; g < NGV; ++g) zs[g][e] = fmaf(y[r][e], vp[r][g].y, zs[g][e]);
+        }
 #pragma unroll
       for (int g = 0; g < NGV; ++g) {
         const float s0 = vp[0][g].x * vs_mul, s1 = vp[1][g].x * vs_mul;
@@ -323,14 +363,23 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
         const uint32_t b1 = movmatrix_trans(pack_half2(y[1][0] * s1, y[1][1] * s1));
 #pragma unroll
         for (int w = g * W / NGV; w < (g + 1) * W / NGV; ++w) {
-          mma_f16(o[2 * w], v0[w] & kLow, v0[w] & kHigh, v1[w] & kLow, v1[w] & kHigh, b0, b1);
+          mma(o[2 * w], v0[w] & kLow, v0[w] & kHigh, v1[w] & kLow, v1[w] & kHigh, b0, b1);
           const uint32_t a = v0[w] >> 8, d = v1[w] >> 8;
-          mma_f16(o[2 * w + 1], a & kLow, a & kHigh, d & kLow, d & kHigh, b0, b1);
+          mma(o[2 * w + 1], a & kLow, a & kHigh, d & kLow, d & kHigh, b0, b1);
         }
       }
     }
     __syncwarp();                         // the stage has been read
-    if (!dead && issued < n_it) issue(issued++);
+    if (issued < n_it) issue(issued++);
+  }
+  if (it < issued) {
+    // a copy did not land in time: nothing more is issued, and what is in
+    // flight is still waited for before its shared memory goes
+    if (lane == 0 && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_TIMEOUT);
+    for (int i = 0; i < kStages; ++i)
+      if (issued - 1 - i >= 0)
+        mbar_wait_bounded(wbars + (issued - 1 - i) % kStages, ((issued - 1 - i) / kStages) & 1, kDrainWaitNs);
+    __syncwarp();
   }
 
   // the warps' states in shared memory, over the rings
@@ -344,7 +393,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
     float z[NGV];
 #pragma unroll
     for (int g = 0; g < NGV; ++g) z[g] = sum_over_rows(zs[g][e]);
-    if (gid == 0) sm_m[warp][h] = m[e], sm_l[warp][h] = lt;
+    if (gid == 0) sm_m[warp][h] = lt > 0.f ? m[e] * us[e] : -FLT_MAX, sm_l[warp][h] = lt;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float zg = z[w * NGV / W];
@@ -387,25 +436,57 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
   }
   __syncthreads();
   if (!sm_last) return;
-  for (int i = threadIdx.x; i < heads * D; i += 32 * kWarps) {
-    const int h = i / D, ch = i % D;
-    float mx = -FLT_MAX, sum = 0.f, v = 0.f;
-    for (int s = 0; s < splits; ++s) mx = fmaxf(mx, __ldcg(&ml[s * kHeads + h]).x);
-#pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
-      const float2 x = __ldcg(&ml[s * kHeads + h]);
-      const float f = exp2_fast(x.x - mx);
-      sum = fmaf(f, x.y, sum);
-      v = fmaf(f, __ldcg(&po[(s * kHeads + h) * D + ch]), v);
+  // The last CTA: the parts' weights in shared memory, then 4 channels a
+  // thread; where the heads leave threads over, each takes every n-th part.
+  float* wt = reinterpret_cast<float*>(smem);           // [split][head]
+  for (int i = threadIdx.x; i < splits * kHeads; i += 32 * kWarps)
+    wt[i] = (i % kHeads) < heads ? __ldcg(&ml[i]).x : -FLT_MAX;
+  __syncthreads();
+  {                                                     // warp h: head h
+    float mx = -FLT_MAX, sum = 0.f;
+    for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, wt[s * kHeads + warp]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+    for (int s = lane; s < splits; s += 32) {
+      const float f = exp2_fast(wt[s * kHeads + warp] - mx);
+      wt[s * kHeads + warp] = f;
+      if (warp < heads) sum = fmaf(f, __ldcg(&ml[s * kHeads + warp]).y, sum);
     }
-    out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(sum > 0.f ? v / sum : 0.f));
+#pragma unroll
+    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    if (lane == 0) sm_l[0][warp] = sum;
+  }
+  __syncthreads();
+  const int units = heads * (D / 4), parts = 32 * kWarps / units, part = threadIdx.x / units, unit = threadIdx.x % units;
+  const int h = unit / (D / 4);
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (part < parts) {
+    const float4* from = reinterpret_cast<const float4*>(po) + unit;
+#pragma unroll 8
+    for (int s = part; s < splits; s += parts) {
+      const float f = wt[s * kHeads + h];
+      const float4 x = __ldcg(from + s * (kHeads * D / 4));
+      v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+    }
+  }
+  float4* sums = reinterpret_cast<float4*>(wt + splits * kHeads);
+  sums[threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.x < units) {
+    for (int i = 1; i < parts; ++i) {
+      const float4 x = sums[i * units + unit];
+      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+    }
+    const float inv = sm_l[0][h] > 0.f ? 1.f / sm_l[0][h] : 0.f;
+    reinterpret_cast<uint2*>(out)[unit] = make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
   }
 }
 
 template <int D, int NGK, int NGV>
 cudaError_t launch(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
   constexpr int ring = kWarps * kStages * int4_block_bytes(D, NGK, NGV), join = kWarps * kHeads * D * 4;
-  constexpr int bytes = ring > join ? ring : join;
+  constexpr int last = kMostSplits * kHeads * 4 + 32 * kWarps * 16;
+  constexpr int bytes = std::max(ring, std::max(join, last));
   const cudaError_t e = set_smem_limit<decode_int4_kernel<D, NGK, NGV>>(bytes);
   if (e != cudaSuccess) return e;
   const dim3 grid(unsigned(plan.splits), unsigned(p.c.n_kv * plan.halves), unsigned(p.c.batch));
