@@ -34,7 +34,6 @@ namespace oscar {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kStages = 4;
 constexpr int kHeads = 8;             // query heads per CTA (MMA columns)
 constexpr int kSlots = 152 * 2;       // CTAs the GPU holds at a time
 constexpr int kRounds = 24;           // rounds of them that a grid is split into, at most
@@ -76,22 +75,26 @@ SplitPlan plan_splits(const Int4Cache& c, const ScoreParams& s) {
   return r;
 }
 
-template <int W>
-__device__ __forceinline__ void lds_words(uint32_t (&w)[W], const uint8_t* p) {
-  if constexpr (W == 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x, w[1] = v.y;
-  }
-}
-
-// The groups of one token's K or V as (scale, zero) floats.
+// N consecutive 32-bit words, by the widest loads that the alignment of N
+// words times any index allows.
 template <int N>
-__device__ __forceinline__ void lds_pairs(float2 (&sz)[N], const uint8_t* p) {
+__device__ __forceinline__ void lds_n(uint32_t (&v)[N], const uint8_t* p) {
+  if constexpr (N % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) sz[i] = half2_to_float2(*reinterpret_cast<const uint32_t*>(p + 4 * i));
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+    }
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const uint2 x = reinterpret_cast<const uint2*>(p)[i];
+      v[2 * i] = x.x, v[2 * i + 1] = x.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
 }
 
 // D += A (16x16 f16, row) * B (16x8 f16, col); free for the compiler to move.
@@ -114,9 +117,14 @@ __device__ __forceinline__ float sum_over_rows(float v) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
-template <int D, int NGK, int NGV>
+// Ring stages of a warp, each two pages: three where two CTAs' rings fit an
+// SM's shared memory, else two.
+constexpr int stages_of(int block) { return 2 * kWarps * 2 * 3 * block <= 212 * 1024 ? 3 : 2; }
+
+// Formed: the scores have a cap or a distance bias.
+template <int D, int NGK, int NGV, bool Formed>
 __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4DecodeParams p, const SplitPlan plan) {
-  constexpr int W = D / 32, kBlock = int4_block_bytes(D, NGK, NGV), kPairs = 16 * D;
+  constexpr int W = D / 32, kBlock = int4_block_bytes(D, NGK, NGV), kPairs = 16 * D, kStages = stages_of(kBlock);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
@@ -143,38 +151,49 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
   const int splits = min(plan.splits, most), split = blockIdx.x;
   if (split >= splits) return;
   const int begin = page0 + int(int64_t(pages) * split / splits), end = page0 + int(int64_t(pages) * (split + 1) / splits);
-  const int n_it = max(0, (end - begin - warp + kWarps - 1) / kWarps);
+  // a warp takes every 8th pair of pages
+  const int n_it = max(0, ((end - begin + 1) / 2 - warp + kWarps - 1) / kWarps);
 
-  // Lane i brings page 32 n + i of the warp's: its place in the pool is worked
-  // out once for 32 pages.
-  const int32_t* table = c.page_table + int64_t(b) * c.max_pages + begin + warp;
-  uint8_t* ring = smem + warp * (kStages * kBlock);
+  // Lane i knows pairs 32 n + i of the warp's and brings them.
+  const int32_t* table = c.page_table + int64_t(b) * c.max_pages;
+  uint8_t* ring = smem + warp * (kStages * 2 * kBlock);
   uint64_t* wbars = bars[warp];
-  auto page_of = [&](int i) {
-    const int id = i < n_it ? table[kWarps * i] : 0;
-    if (id >= 0 && id < c.n_pages) return c.pages + (int64_t(id) * c.n_kv + hk) * kBlock;
-    if (c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
-    return static_cast<uint8_t*>(nullptr);
-  };
-  const uint8_t *src = page_of(lane), *src_next = nullptr;
-  uint32_t live = __ballot_sync(0xffffffffu, src != nullptr), live_next = 0;   // of the pages in src, src_next
-  uint32_t ring_live = 0;                 // bit i: stage i holds a page of the pool
-  auto issue = [&](int it) {
-    const int at = it & 31, st = it % kStages;
-    if (at == 0) {
-      if (it) src = src_next, live = live_next;
-      src_next = page_of(it + 32 + lane);
-      live_next = __ballot_sync(0xffffffffu, src_next != nullptr);
-    }
-    ring_live = (ring_live & ~(1u << st)) | (((live >> at) & 1u) << st);
-    if (lane == at) {
-      if (src) {
-        mbar_arrive_expect_tx(wbars + st, kBlock);
-        bulk_copy_g2s(ring + st * kBlock, src, kBlock, wbars + st);
-      } else {
-        mbar_arrive(wbars + st);
+  auto pages_of = [&](int i, int (&id)[2]) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int at = begin + 2 * (warp + kWarps * i) + g;
+      id[g] = i < n_it && at < end ? table[at] : -1;
+      if (id[g] < 0 || id[g] >= c.n_pages) {
+        if (i < n_it && at < end && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+        id[g] = -1;
       }
     }
+  };
+  int id[2], id_next[2] = {-1, -1};
+  pages_of(lane, id);
+  uint32_t ring_dead = 0;                 // bits 2 i, 2 i + 1: stage i's pages that are not there
+  int st_issue = 0;
+  auto issue = [&](int it) {
+    const int at = it & 31;
+    if (at == 0) {
+      if (it) id[0] = id_next[0], id[1] = id_next[1];
+      pages_of(it + 32 + lane, id_next);
+    }
+    const uint32_t none = __shfl_sync(0xffffffffu, (id[0] < 0 ? 1u : 0u) | (id[1] < 0 ? 2u : 0u), at);
+    ring_dead = (ring_dead & ~(3u << (2 * st_issue))) | (none << (2 * st_issue));
+    if (lane == at) {
+      uint8_t* to = ring + st_issue * 2 * kBlock;
+      uint64_t* bar = wbars + st_issue;
+      const int n = 2 - __popc(none);
+      if (n)
+        mbar_arrive_expect_tx(bar, n * kBlock);
+      else
+        mbar_arrive(bar);
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (id[g] >= 0) bulk_copy_g2s(to + g * kBlock, c.pages + (int64_t(id[g]) * c.n_kv + hk) * kBlock, kBlock, bar);
+    }
+    st_issue = st_issue + 1 == kStages ? 0 : st_issue + 1;
   };
   int issued = min(n_it, kStages);
   for (int i = 0; i < issued; ++i) issue(i);
@@ -237,10 +256,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
 
   // x is in the dot product's own scale, or in log2 units where the score has a
   // form of its own; us takes it to log2 units, thr is m + 8 / us.
-  const bool formed = cap || p.s.slopes;
   float us[2], thr[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) us[e] = formed ? 1.f : fmaxf(unscale[e], FLT_MIN), thr[e] = -FLT_MAX;
+  for (int e = 0; e < 2; ++e) us[e] = Formed ? 1.f : fmaxf(unscale[e], FLT_MIN), thr[e] = -FLT_MAX;
   float o[2 * W][4], zs[NGV][2], m[2] = {-FLT_MAX, -FLT_MAX}, off[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
   int ve = -24;                           // the V scales seen are at most 2^ve
   float vs_top = pow2i(-24), vs_mul = pow2i(31);   // 2^(7 - ve): p s_V 2^(7 - ve) <= 2^15
@@ -249,118 +267,129 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
 #pragma unroll
   for (int g = 0; g < NGV; ++g) zs[g][0] = zs[g][1] = 0.f;
 
-  int it = 0;
+  int it = 0, st = 0;
+  uint32_t parity = 0;
+  int tok = (begin + 2 * warp) * kInt4Page;
   for (; it < issued; ++it) {
-    const int st = it % kStages;
-    const uint32_t parity = (it / kStages) & 1;
     if (!__all_sync(0xffffffffu, mbar_try_wait(wbars + st, parity)) &&
         !__all_sync(0xffffffffu, mbar_wait_bounded(wbars + st, parity, kDefaultWaitNs)))
       break;
-    if ((ring_live >> st) & 1) {
-      const uint8_t* blk = ring + st * kBlock;
-      // S: rows gid and gid + 8 are tokens, columns 2 tig and 2 tig + 1 heads
+    const uint8_t* blk = ring + st * 2 * kBlock;
+    // S: rows gid and gid + 8 of each page are tokens, columns 2 tig and 2 tig + 1 heads
+    float y[4][2], vp[4][NGV][2];
+#pragma unroll
+    for (int g2 = 0; g2 < 2; ++g2) {
+      const uint8_t* page = blk + g2 * kBlock;
       float acc[NGK][4];
 #pragma unroll
       for (int g = 0; g < NGK; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
       uint32_t k0[W], k1[W];
-      lds_words(k0, blk + gid * (D / 2) + tig * (4 * W));
-      lds_words(k1, blk + (gid + 8) * (D / 2) + tig * (4 * W));
-      float2 kp[2][NGK], vp[2][NGV];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint8_t* pr = blk + kPairs + 4 * (NGK + NGV) * (gid + 8 * r);
-        lds_pairs(kp[r], pr);
-        lds_pairs(vp[r], pr + 4 * NGK);
-      }
+      lds_n(k0, page + gid * (D / 2) + tig * (4 * W));
+      lds_n(k1, page + (gid + 8) * (D / 2) + tig * (4 * W));
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         mma(acc[w * NGK / W], k0[w] & kLow, k1[w] & kLow, k0[w] & kHigh, k1[w] & kHigh, qb[2 * w][0], qb[2 * w][1]);
         const uint32_t a = k0[w] >> 8, d = k1[w] >> 8;
         mma(acc[w * NGK / W], a & kLow, d & kLow, a & kHigh, d & kHigh, qb[2 * w + 1][0], qb[2 * w + 1][1]);
       }
-      float y[2][2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          y[r][e] = 0.f;
-#pragma unroll
-          for (int g = 0; g < NGK; ++g)
-            y[r][e] = fmaf(kp[r][g].x, acc[g][2 * r + e], fmaf(kp[r][g].y, qs[g][e], y[r][e]));
-        }
-      const int tok = (begin + warp + kWarps * it) * kInt4Page;
-      if (formed) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = y[r][e] * unscale[e];
-            y[r][e] = fmaf(slope[e], float(tok + gid + 8 * r - (len - 1)), cap ? capped(x, p.s) : x);
-          }
-      }
-      if (tok < first || tok + kInt4Page > len) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int j = tok + gid + 8 * r;
-          if (j < first || j >= len) {
-            y[r][0] = y[r][1] = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < NGV; ++g) vp[r][g] = make_float2(0.f, 0.f);   // a stale slot may hold anything
-          }
-        }
-      }
-      bool grow = false;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        grow = grow | (y[r][0] > thr[0]) | (y[r][1] > thr[1]);
+        uint32_t pr[NGK + NGV];
+        lds_n(pr, page + kPairs + 4 * (NGK + NGV) * (gid + 8 * r));
 #pragma unroll
-        for (int g = 0; g < NGV; ++g) grow = grow | (vp[r][g].x > vs_top);
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-        float top = 0.f;
+        for (int g = 0; g < NGK; ++g) {
+          const float2 sz = half2_to_float2(pr[g]);
 #pragma unroll
-        for (int g = 0; g < NGV; ++g) top = fmaxf(top, fmaxf(vp[0][g].x, vp[1][g].x));
-        top = max_over_rows(top);
-        // 2^e >= top for the exponent e of top plus one
-        const int ne = max(ve, ((__float_as_int(top) >> 23) & 255) - 126);
-        const float fv = ne - ve < 126 ? pow2i(ve - ne) : 0.f;
-        ve = ne;
-        vs_top = pow2i(ve);
-        vs_mul = pow2i(7 - ve);
-        float f[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mn = fmaxf(m[e], max_over_rows(fmaxf(y[0][e], y[1][e])));
-          f[e] = exp2_fast((m[e] - mn) * us[e]);
-          m[e] = mn;
-          off[e] = -mn * us[e];
-          thr[e] = mn + 8.f / us[e];
-          l[e] *= f[e];
-#pragma unroll
-          for (int g = 0; g < NGV; ++g) zs[g][e] *= f[e];
-          f[e] *= fv;
+          for (int e = 0; e < 2; ++e) {
+            const float z = g ? fmaf(sz.y, qs[g][e], y[2 * g2 + r][e]) : sz.y * qs[g][e];
+            y[2 * g2 + r][e] = fmaf(sz.x, acc[g][2 * r + e], z);
+          }
         }
 #pragma unroll
-        for (int t = 0; t < 2 * W; ++t) o[t][0] *= f[0], o[t][1] *= f[1], o[t][2] *= f[0], o[t][3] *= f[1];
+        for (int g = 0; g < NGV; ++g) {
+          const float2 sz = half2_to_float2(pr[NGK + g]);
+          vp[2 * g2 + r][g][0] = sz.x, vp[2 * g2 + r][g][1] = sz.y;
+        }
       }
-      // O: rows are channels; k = tokens 2 tig, 2 tig + 1 (and + 8)
+    }
+    if (Formed) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = y[r][e] * unscale[e];
+          y[r][e] = fmaf(slope[e], float(tok + gid + 8 * r - (len - 1)), cap ? capped(x, p.s) : x);
+        }
+    }
+    const uint32_t gone = (ring_dead >> (2 * st)) & 3u;
+    if (gone || tok < first || tok + 2 * kInt4Page > len) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int j = tok + gid + 8 * r;
+        if (j < first || j >= len || ((gone >> (r >> 1)) & 1u)) {
+          y[r][0] = y[r][1] = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < NGV; ++g) vp[r][g][0] = vp[r][g][1] = 0.f;   // a stale slot may hold anything
+        }
+      }
+    }
+    bool grow = false;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      grow = grow | (y[r][0] > thr[0]) | (y[r][1] > thr[1]);
+#pragma unroll
+      for (int g = 0; g < NGV; ++g) grow = grow | (vp[r][g][0] > vs_top);
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+      float top = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) top = fmaxf(top, vp[r][g][0]);
+      top = max_over_rows(top);
+      // 2^e >= top for the exponent e of top plus one
+      const int ne = max(ve, ((__float_as_int(top) >> 23) & 255) - 126);
+      const float fv = ne - ve < 126 ? pow2i(ve - ne) : 0.f;
+      ve = ne;
+      vs_top = pow2i(ve);
+      vs_mul = pow2i(7 - ve);
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(m[e], max_over_rows(fmaxf(fmaxf(y[0][e], y[1][e]), fmaxf(y[2][e], y[3][e]))));
+        f[e] = exp2_fast((m[e] - mn) * us[e]);
+        m[e] = mn;
+        off[e] = -mn * us[e];
+        thr[e] = mn + 8.f / us[e];
+        l[e] *= f[e];
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) zs[g][e] *= f[e];
+        f[e] *= fv;
+      }
+#pragma unroll
+      for (int t = 0; t < 2 * W; ++t) o[t][0] *= f[0], o[t][1] *= f[1], o[t][2] *= f[0], o[t][3] *= f[1];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        y[r][e] = exp2_fast(fmaf(y[r][e], us[e], off[e]));
+        l[e] += y[r][e];
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) zs[g][e] = fmaf(y[r][e], vp[r][g][1], zs[g][e]);
+      }
+    // O: rows are channels; k = tokens 2 tig, 2 tig + 1 (and + 8)
+#pragma unroll
+    for (int g2 = 0; g2 < 2; ++g2) {
+      const uint8_t* page = blk + g2 * kBlock;
       uint32_t v0[W], v1[W];
-      lds_words(v0, blk + 8 * D + (8 * tig + gid) * (4 * W));
-      lds_words(v1, blk + 8 * D + (8 * (tig + 4) + gid) * (4 * W));
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          y[r][e] = exp2_fast(fmaf(y[r][e], us[e], off[e]));
-          l[e] += y[r][e];
-#pragma unroll
-          for (int g = 0; g < NGV; ++g) zs[g][e] = fmaf(y[r][e], vp[r][g].y, zs[g][e]);
-        }
+      lds_n(v0, page + 8 * D + (8 * tig + gid) * (4 * W));
+      lds_n(v1, page + 8 * D + (8 * (tig + 4) + gid) * (4 * W));
 #pragma unroll
       for (int g = 0; g < NGV; ++g) {
-        const float s0 = vp[0][g].x * vs_mul, s1 = vp[1][g].x * vs_mul;
-        const uint32_t b0 = movmatrix_trans(pack_half2(y[0][0] * s0, y[0][1] * s0));
-        const uint32_t b1 = movmatrix_trans(pack_half2(y[1][0] * s1, y[1][1] * s1));
+        const float s0 = vp[2 * g2][g][0] * vs_mul, s1 = vp[2 * g2 + 1][g][0] * vs_mul;
+        const uint32_t b0 = movmatrix_trans(pack_half2(y[2 * g2][0] * s0, y[2 * g2][1] * s0));
+        const uint32_t b1 = movmatrix_trans(pack_half2(y[2 * g2 + 1][0] * s1, y[2 * g2 + 1][1] * s1));
 #pragma unroll
         for (int w = g * W / NGV; w < (g + 1) * W / NGV; ++w) {
           mma(o[2 * w], v0[w] & kLow, v0[w] & kHigh, v1[w] & kLow, v1[w] & kHigh, b0, b1);
@@ -371,14 +400,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
     }
     __syncwarp();                         // the stage has been read
     if (issued < n_it) issue(issued++);
+    tok += 2 * kWarps * kInt4Page;
+    if (++st == kStages) st = 0, parity ^= 1;
   }
   if (it < issued) {
     // a copy did not land in time: nothing more is issued, and what is in
     // flight is still waited for before its shared memory goes
     if (lane == 0 && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_TIMEOUT);
-    for (int i = 0; i < kStages; ++i)
-      if (issued - 1 - i >= 0)
-        mbar_wait_bounded(wbars + (issued - 1 - i) % kStages, ((issued - 1 - i) / kStages) & 1, kDrainWaitNs);
+    for (int i = max(it, issued - kStages); i < issued; ++i)
+      mbar_wait_bounded(wbars + i % kStages, (i / kStages) & 1, kDrainWaitNs);
     __syncwarp();
   }
 
@@ -482,22 +512,28 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
   }
 }
 
-template <int D, int NGK, int NGV>
+template <int D, int NGK, int NGV, bool Formed>
 cudaError_t launch(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
-  constexpr int ring = kWarps * kStages * int4_block_bytes(D, NGK, NGV), join = kWarps * kHeads * D * 4;
-  constexpr int last = kMostSplits * kHeads * 4 + 32 * kWarps * 16;
+  constexpr int block = int4_block_bytes(D, NGK, NGV), ring = kWarps * stages_of(block) * 2 * block;
+  constexpr int join = kWarps * kHeads * D * 4, last = kMostSplits * kHeads * 4 + 32 * kWarps * 16;
   constexpr int bytes = std::max(ring, std::max(join, last));
-  const cudaError_t e = set_smem_limit<decode_int4_kernel<D, NGK, NGV>>(bytes);
+  const cudaError_t e = set_smem_limit<decode_int4_kernel<D, NGK, NGV, Formed>>(bytes);
   if (e != cudaSuccess) return e;
   const dim3 grid(unsigned(plan.splits), unsigned(p.c.n_kv * plan.halves), unsigned(p.c.batch));
-  return launch_pdl(decode_int4_kernel<D, NGK, NGV>, grid, dim3(32 * kWarps), bytes, stream, p, plan);
+  return launch_pdl(decode_int4_kernel<D, NGK, NGV, Formed>, grid, dim3(32 * kWarps), bytes, stream, p, plan);
+}
+
+template <int D, int NGK, int NGV>
+cudaError_t launch_f(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
+  return p.s.cap_log2 != 0.f || p.s.slopes ? launch<D, NGK, NGV, true>(p, plan, stream)
+                                           : launch<D, NGK, NGV, false>(p, plan, stream);
 }
 
 template <int D, int NGK>
 cudaError_t launch_v(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
-  if (p.c.ng_v == 1) return launch<D, NGK, 1>(p, plan, stream);
-  if (p.c.ng_v == 2) return launch<D, NGK, 2>(p, plan, stream);
-  if constexpr (D == 128) return launch<D, NGK, 4>(p, plan, stream);
+  if (p.c.ng_v == 1) return launch_f<D, NGK, 1>(p, plan, stream);
+  if (p.c.ng_v == 2) return launch_f<D, NGK, 2>(p, plan, stream);
+  if constexpr (D == 128) return launch_f<D, NGK, 4>(p, plan, stream);
   return cudaErrorInvalidValue;
 }
 
