@@ -33,10 +33,11 @@ namespace {
 constexpr int kTile = 128;            // rows of a tile, of queries and of keys
 constexpr int kPanel = kTile * 128;   // bytes of 128 rows of 64 channels
 constexpr int kThreads = 384;         // three warpgroups: two of softmax, one of which two warps work
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;
 constexpr int kSms = 152;
+// tiles of K and V in flight or in use: a ring in the order K0 V0 K1 V1 ..
 template <int D>
-constexpr int kStages = D == 128 ? 2 : 4;
+constexpr int kRing = D == 128 ? 5 : 10;
 
 struct PromptPlan {
   int pack;        // query heads in a tile's rows
@@ -87,7 +88,7 @@ __device__ __forceinline__ PromptSpan prompt_span(const PromptParams& p, int b, 
 }
 
 struct Barriers {
-  uint64_t q_full, k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_done[2], fin;
+  uint64_t q_full, full[10], empty[10], tail, s_full[2], p_full[2], o_done[2], fin;
   uint32_t tmem;
   int dead;
 };
@@ -107,27 +108,31 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const PromptPlan plan, const __grid_constant__ CUtensorMap tq,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
-  constexpr int kPanels = D / 64, kTileBytes = kPanels * kPanel, kSt = kStages<D>;
+  constexpr int kPanels = D / 64, kTileBytes = kPanels * kPanel, kR = kRing<D>;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile), kIdescO = idesc_bf16_f32_bmn(kTile, D);
   constexpr uint32_t kColO = 2 * kTile;          // TMEM columns: S0, S1, O0, O1
   extern __shared__ uint8_t raw[];
   __shared__ Barriers bar;
   uint8_t* sq = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
-  uint8_t* sk = sq + 2 * kTileBytes;
-  uint8_t* sv = sk + kSt * kTileBytes;
+  uint8_t* ring = sq + 2 * kTileBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     mbar_init(&bar.q_full, 1);
+    mbar_init(&bar.tail, 1);
     mbar_init(&bar.fin, 1);
-    for (int i = 0; i < kSt; ++i) {
-      mbar_init(&bar.k_full[i], 1);
-      mbar_init(&bar.k_empty[i], 1);
-      mbar_init(&bar.v_full[i], 1);
-      mbar_init(&bar.v_empty[i], 1);
+    for (int i = 0; i < kR; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bar.s_full[w], 1);
@@ -177,109 +182,133 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = bar.tmem;
   volatile int* dead = &bar.dead;
-  // a wait that ran out: reported once, and every later wait of the CTA is passed over
+  // False where a wait ran out: reported once, and every other wait of the CTA ends soon after.
   auto wait = [&](uint64_t* at, uint32_t parity) {
-    if (*dead) return false;
-    if (mbar_wait_bounded(at, parity, kDefaultWaitNs)) return true;
-    *dead = 1;
-    if (p.dev_status) atomicOr(p.dev_status, OSCAR_DEV_TIMEOUT);
-    return false;
+    if (mbar_try_wait(at, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_sleep(at, parity, 10000)) {
+      if (*dead) return false;
+      if (global_timer_ns() - t0 > kDefaultWaitNs) {
+        *dead = 1;
+        if (p.dev_status) atomicOr(p.dev_status, OSCAR_DEV_TIMEOUT);
+        return false;
+      }
+    }
+    return true;
   };
+  // The request's last key tile, where the keys end inside it, is the list's
+  // last.  Rows of V behind the last key may hold anything, and 0 times that is
+  // not 0: a warp of its own clears them between the load and the product.
+  const bool tail = n_all > 0 && tile_of(n_all - 1) == tiles - 1 && sp.n_k % kTile != 0;
 
   // Registers: the launch's 168 a thread, 504 over the three warpgroups; a
   // softmax thread holds a row's 128 scores.
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == kLoadWarp) {
-    if (lane == 0 && n_all > 0) {
-      const int tiles_q = n[1] > 0 || tok0 + per_tile < sp.n_q ? 2 : 1;
+    if (warp == kLoadWarp && lane == 0 && n_all > 0) {
+      const int tiles_q = tok0 + per_tile < sp.n_q ? 2 : 1;
       mbar_arrive_expect_tx(&bar.q_full, uint32_t(tiles_q * kTileBytes));
       for (int w = 0; w < tiles_q; ++w)
         for (int c = 0; c < kPanels; ++c)
           tma_load_3d(sq + w * kTileBytes + c * kPanel, &tq, 64 * c, hq0, int(sp.q0) + tok0 + w * per_tile, &bar.q_full);
-      int j = 0;
-      for (; j < n_all; ++j) {
-        const int st = j % kSt, row = int(sp.k0) + tile_of(j) * kTile;
-        if (j >= kSt && !wait(&bar.k_empty[st], (j / kSt - 1) & 1)) break;
-        mbar_arrive_expect_tx(&bar.k_full[st], kTileBytes);
+      int t = 0, st = 0, turn = 0;           // t = 2 j is K of step j, 2 j + 1 its V
+      for (; t < 2 * n_all; ++t) {
+        if (turn > 0 && !wait(&bar.empty[st], (turn - 1) & 1)) break;
+        const int row = int(sp.k0) + tile_of(t >> 1) * kTile;
+        uint64_t* at = tail && t == 2 * n_all - 1 ? &bar.tail : &bar.full[st];
+        mbar_arrive_expect_tx(at, kTileBytes);
         for (int c = 0; c < kPanels; ++c)
-          tma_load_3d(sk + st * kTileBytes + c * kPanel, &tk, 64 * c, hk, row, &bar.k_full[st]);
-        if (j >= kSt && !wait(&bar.v_empty[st], (j / kSt - 1) & 1)) {
-          ++j;
-          break;
-        }
-        mbar_arrive_expect_tx(&bar.v_full[st], kTileBytes);
-        for (int c = 0; c < kPanels; ++c)
-          tma_load_3d(sv + st * kTileBytes + c * kPanel, &tv, 64 * c, hk, row, &bar.v_full[st]);
+          tma_load_3d(ring + st * kTileBytes + c * kPanel, (t & 1) ? &tv : &tk, 64 * c, hk, row, at);
+        if (++st == kR) st = 0, ++turn;
       }
       // what was issued has landed before the CTA's shared memory goes
       mbar_wait_bounded(&bar.q_full, 0, kDrainWaitNs);
-      for (int i = max(0, j - kSt); i < j; ++i) {
-        mbar_wait_bounded(&bar.k_full[i % kSt], (i / kSt) & 1, kDrainWaitNs);
-        mbar_wait_bounded(&bar.v_full[i % kSt], (i / kSt) & 1, kDrainWaitNs);
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    auto issue_s = [&](int w, int j) {
-      if (lane == 0) {
-        const uint32_t a = smem_addr(sq + w * kTileBytes), bb = smem_addr(sk + (j % kSt) * kTileBytes);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * kPanel + (kk % 4) * 32;
-          umma_f16_ss(tmem + w * kTile, smem_desc_kmajor_sw128(a + off), smem_desc_kmajor_sw128(bb + off), kIdescS, kk > 0);
-        }
-        umma_commit(&bar.s_full[w]);
-      }
-    };
-    bool ok = n_all > 0 && wait(&bar.q_full, 0) && wait(&bar.k_full[0], 0);
-    if (ok) {
-      for (int w = 0; w < 2; ++w)
-        if (n[w] > 0) issue_s(w, 0);
-      if (lane == 0) umma_commit(&bar.k_empty[0]);
-    }
-    for (int j = 0; j < n_all && ok; ++j) {
-      const int st = j % kSt;
-      if (j + 1 < n_all) ok = wait(&bar.k_full[(j + 1) % kSt], ((j + 1) / kSt) & 1);
-      ok = ok && wait(&bar.v_full[st], (j / kSt) & 1);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      uint8_t* v = sv + st * kTileBytes;
-      // rows behind the request's last key may hold anything: 0 times that is not 0
-      const int valid = sp.n_k - tile_of(j) * kTile;
-      if (valid < kTile) {
+      for (int i = max(0, t - kR); i < t; ++i)
+        if (tail && i == 2 * n_all - 1)
+          mbar_wait_bounded(&bar.tail, 0, kDrainWaitNs);
+        else
+          mbar_wait_bounded(&bar.full[i % kR], (i / kR) & 1, kDrainWaitNs);
+    } else if (warp == kTailWarp && tail) {
+      const int t = 2 * n_all - 1, valid = sp.n_k % kTile;
+      if (__all_sync(0xffffffffu, wait(&bar.tail, 0))) {
+        uint8_t* v = ring + (t % kR) * kTileBytes;
         for (int i = valid * 8 + lane; i < kTile * 8; i += 32)
 #pragma unroll
           for (int c = 0; c < kPanels; ++c) *reinterpret_cast<uint4*>(v + c * kPanel + 16 * i) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.full[t % kR]);
       }
+    } else if (warp == kMmaWarp && n_all > 0) {
+      // Per step and row tile: O += P V of this step, then S of the next, so
+      // that the other row tile's softmax runs beside them.  The whole warp
+      // walks through the steps and one thread issues: the MMAs' operands stay
+      // in uniform registers (in a branch of one thread each MMA took three
+      // times as long to issue as to run).
+      const uint64_t dq = smem_desc_kmajor_sw128(smem_addr(sq)), dk = smem_desc_kmajor_sw128(smem_addr(ring));
+      const uint64_t dv = smem_desc_mnmajor_sw128(smem_addr(ring), kPanel);
+      auto arrived = [&](uint64_t* at, uint32_t parity) { return __all_sync(0xffffffffu, wait(at, parity)) != 0; };
+      auto issue_s = [&](int w, int st) {
+        const uint64_t a = dq + uint64_t(w * (kTileBytes >> 4)), bb = dk + uint64_t(st * (kTileBytes >> 4));
+        if (elect_one()) {
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (j < n[w]) {
-          ok = wait(&bar.p_full[w], j & 1);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t bb = smem_addr(v);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk / 4) * (kPanel >> 4) + (kk % 4) * 2;
+            umma_f16_ss(tmem + w * kTile, a + off, bb + off, kIdescS, kk > 0);
+          }
+          umma_commit(&bar.s_full[w]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* at) {
+        if (elect_one()) umma_commit(at);
+        __syncwarp();
+      };
+      bool ok = arrived(&bar.q_full, 0) && arrived(&bar.full[0], 0);
+      if (ok) {
+        for (int w = 0; w < 2; ++w)
+          if (n[w] > 0) issue_s(w, 0);
+        commit(&bar.empty[0]);
+      }
+      int sk = 0, sv = 1;                    // ring places of K and V of the step
+      uint32_t pk = 0, pv = 0;               // and the parities of their turns
+      for (int j = 0; j < n_all && ok; ++j) {
+        sk += 2;
+        if (sk >= kR) sk -= kR, pk ^= 1;     // K of step j + 1
+        ok = arrived(&bar.full[sv], pv);
+        bool next = false;
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_f16_ts(tmem + kColO + w * D, tmem + w * kTile + 8 * kk, smem_desc_mnmajor_sw128(bb + 2048 * kk, kPanel),
-                          kIdescO, j > 0 || kk > 0);
-            umma_commit(&bar.o_done[w]);
+        for (int w = 0; w < 2; ++w) {
+          if (ok && j < n[w]) {
+            const uint64_t bb = dv + uint64_t(sv * (kTileBytes >> 4));
+            const uint32_t a = tmem + w * kTile, d = tmem + kColO + w * D;
+            ok = arrived(&bar.p_full[w], j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk) umma_f16_ts(d, a + 8 * kk, bb + 128 * kk, kIdescO, j > 0 || kk > 0);
+              umma_commit(&bar.o_done[w]);
+            }
+            __syncwarp();
+          }
+          if (ok && j + 1 < n[w]) {
+            if (!next) ok = arrived(&bar.full[sk], pk);
+            next = true;
+            if (ok) issue_s(w, sk);
           }
         }
-        if (j + 1 < n[w]) issue_s(w, j + 1);
+        if (ok) {
+          commit(&bar.empty[sv]);
+          if (next) commit(&bar.empty[sk]);
+        }
+        sv += 2;
+        if (sv >= kR) sv -= kR, pv ^= 1;
       }
-      if (!ok) break;
-      if (lane == 0) {
-        umma_commit(&bar.v_empty[st]);
-        if (j + 1 < n_all) umma_commit(&bar.k_empty[(j + 1) % kSt]);
-      }
-    }
-    if (lane == 0 && n_all > 0) {   // every MMA issued is done before TMEM is given back
-      umma_commit(&bar.fin);
+      // every MMA issued is done before TMEM is given back
+      commit(&bar.fin);
       mbar_wait_bounded(&bar.fin, 0, kDrainWaitNs);
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int w = warp >> 2, row = tid & (kTile - 1);
@@ -325,7 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int i = 4; i < kTile; ++i) m4[i & 3] = fmaxf(m4[i & 3], s[i]);
+      for (int i = 4; i < kTile - 4; i += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[kTile - 4 + e]);
       const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       // (nothing seen yet, nothing here: -inf - -inf is no growth)
       if (__any_sync(0xffffffffu, (mt - m) * sc > 8.f)) {
@@ -504,7 +537,7 @@ cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t s
       !encode_rows(&tk, k, D, p.n_kv, p.total_k, p.k_stride, 1, kTile) ||
       !encode_rows(&tv, v, D, p.n_kv, p.total_k, p.v_stride, 1, kTile))
     return cudaErrorInvalidValue;
-  constexpr int bytes = 1024 + (2 + 2 * kStages<D>) * (D / 64) * kPanel;
+  constexpr int bytes = 1024 + (2 + kRing<D>) * (D / 64) * kPanel;
   cudaError_t e = set_smem_limit<prompt_kernel<D>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t x = int64_t(plan.blocks) * plan.sets;
