@@ -1,7 +1,7 @@
 // Attention of packed prompts over bf16 rows, on the tensor cores (tcgen05).
 //
 // A CTA takes 2 x 128 query rows of one KV head: rows are (token, head) pairs
-// of a power-of-two share of the query heads that read it, so that short
+// of the query heads that read it (up to 16), so that short
 // prompts fill the tiles and K and V are read once for those heads.  Keys come
 // in tiles of 128.  Ten warps: one brings Q, K and V by TMA, one issues the
 // MMAs, and four for each of the two row tiles do the softmax, one thread a
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kTile = 128;            // rows of a tile, of queries and of keys
 constexpr int kPanel = kTile * 128;   // bytes of 128 rows of 64 channels
-constexpr int kThreads = 384;         // three warpgroups: two of softmax, one of which two warps work
+constexpr int kThreads = 384;         // three warpgroups: two of softmax, one of single warps
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;
 constexpr int kSms = 152;
 // tiles of K and V in flight or in use: a ring in the order K0 V0 K1 V1 ..
@@ -40,24 +40,29 @@ template <int D>
 constexpr int kRing = D == 128 ? 5 : 10;
 
 struct PromptPlan {
-  int pack;        // query heads in a tile's rows
+  int pack;        // query heads in a tile's rows: row = token * pack + head, 128 / pack tokens
   int sets;        // head sets
   int blocks;      // row blocks of the longest request
   int splits;      // parts of the keys
+  int dual;        // 1: the rows fit one tile, and the row tiles take every other key tile of them
   size_t off_ml, off_o, bytes;
 };
 
 PromptPlan plan_prompt(const PromptParams& p) {
   PromptPlan r{};
   const int group = p.n_q / p.n_kv;
-  r.pack = 1;
-  while (r.pack < 16 && group % (2 * r.pack) == 0) r.pack *= 2;
+  // all the heads of a KV head where a tile holds them with few rows to spare,
+  // else their largest divisor that does
+  for (r.pack = std::min(group, 16); group % r.pack; --r.pack) {
+  }
   r.sets = p.n_q / r.pack;
-  r.blocks = int((int64_t(p.max_q) * r.pack + 2 * kTile - 1) / (2 * kTile));
+  const int per_tile = kTile / r.pack;
+  r.blocks = int((int64_t(p.max_q) + 2 * per_tile - 1) / (2 * per_tile));
   const int64_t ctas = int64_t(r.blocks) * r.sets * p.batch;
   const int64_t tiles = (int64_t(p.max_k) + kTile - 1) / kTile;
   r.splits = int(std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(1, ctas), tiles / 4)));
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  r.dual = r.splits > 1 && p.max_q <= per_tile;
   if (r.splits > 1) {
     const size_t rows = size_t(ctas) * r.splits * 2 * kTile;
     r.off_o = up(rows * 8);
@@ -108,13 +113,47 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// The capped score where |x| scale / cap <= 1: tanh(y) = y P(y^2), P of degree 7
+// interpolated at the Chebyshev points of [0, 1] (5e-8 of the value in fp32).
+// A tile of 128 x 128 scores takes a third of the time that it takes by powers
+// and reciprocals, which the special function unit bounds.
+__device__ __forceinline__ float2 capped_near(float2 x, float cap_in, float cap_log2) {
+  constexpr float kP[8] = {1.f,          -0.3333328068256378f,  0.13332191109657288f,   -0.053872738033533096f,
+                           0.02146998f, -0.007924946025013924f, 0.0022876455914229155f, -0.0003548834065441042f};
+  const float2 y = mul2(x, make_float2(cap_in, cap_in)), u = mul2(y, y);
+  float2 r = make_float2(kP[7], kP[7]);
+#pragma unroll
+  for (int k = 6; k >= 0; --k) r = fma2(r, u, make_float2(kP[k], kP[k]));
+  return mul2(mul2(y, make_float2(cap_log2, cap_log2)), r);
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
-template <int D>
+__device__ __forceinline__ float row_max(const float (&s)[kTile]) {
+  float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int i = 4; i < kTile - 4; i += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = max3(m[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], s[kTile - 4 + e]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Formed: the scores have a cap or a distance bias.
+template <int D, bool Formed>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const PromptPlan plan, const __grid_constant__ CUtensorMap tq,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
@@ -126,22 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sq = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   uint8_t* ring = sq + 2 * kTileBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    mbar_init(&bar.q_full, 1);
-    mbar_init(&bar.tail, 1);
-    mbar_init(&bar.fin, 1);
-    for (int i = 0; i < kR; ++i) {
-      mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 1);
-    }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&bar.s_full[w], 1);
-      mbar_init(&bar.p_full[w], kTile);
-      mbar_init(&bar.o_done[w], 1);
-    }
-    bar.dead = 0;
-    fence_mbar_init();
-  }
   pdl_wait();
   pdl_launch_dependents();
 
@@ -149,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b = blockIdx.y, split = blockIdx.z;
   const PromptSpan sp = prompt_span(p, b, tid == 0 && blockIdx.x == 0 && split == 0);
   const int pack = plan.pack, per_tile = kTile / pack;   // tokens of a tile
-  const int tok0 = blk * 2 * per_tile;
+  const int dual = plan.dual, tok0 = blk * 2 * per_tile;
   if (tok0 >= sp.n_q) return;
   const int hq0 = set * pack, hk = hq0 / (p.n_q / p.n_kv), shift = sp.n_k - sp.n_q;   // position = shift + token
 
@@ -169,12 +192,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   // this part of them
   const int all = max(n[0], n[1]);
   const int lo = int(int64_t(all) * split / plan.splits), hi = int(int64_t(all) * (split + 1) / plan.splits);
-  n[0] = max(0, min(n[0], hi) - lo);
-  n[1] = max(0, min(n[1], hi) - lo);
   const int n_all = hi - lo;
+  n[0] = dual ? (n_all + 1) / 2 : max(0, min(n[0], hi) - lo);
+  n[1] = dual ? n_all / 2 : max(0, min(n[1], hi) - lo);
   auto tile_of = [&](int j) { return j + lo < n_pre ? j + lo : j + lo - n_pre + from; };
 
   if (n_all > 0) {
+    if (tid == 0) {
+      mbar_init(&bar.q_full, 1);
+      mbar_init(&bar.tail, 1);
+      mbar_init(&bar.fin, 1);
+      for (int i = 0; i < kR; ++i) {
+        mbar_init(&bar.full[i], 1);
+        mbar_init(&bar.empty[i], 1);
+      }
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(&bar.s_full[w], 1);
+        mbar_init(&bar.p_full[w], kTile);
+        mbar_init(&bar.o_done[w], 1);
+      }
+      bar.dead = 0;
+      fence_mbar_init();
+    }
     if (warp == kMmaWarp) tmem_alloc(&bar.tmem, 512);
     tc_fence_before();
     __syncthreads();
@@ -201,13 +240,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // not 0: a warp of its own clears them between the load and the product.
   const bool tail = n_all > 0 && tile_of(n_all - 1) == tiles - 1 && sp.n_k % kTile != 0;
 
-  // Registers: the launch's 168 a thread, 504 over the three warpgroups; a
-  // softmax thread holds a row's 128 scores.
+  // Registers: the launch's 168 a thread, 504 over the three warpgroups.  A
+  // softmax thread holds a row's 128 scores; the issuing warp must not spill (at
+  // 56 registers it did, and an 8k prompt took 7 % longer).
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kLoadWarp && lane == 0 && n_all > 0) {
-      const int tiles_q = tok0 + per_tile < sp.n_q ? 2 : 1;
-      mbar_arrive_expect_tx(&bar.q_full, uint32_t(tiles_q * kTileBytes));
+      const int tiles_q = !dual && tok0 + per_tile < sp.n_q ? 2 : 1;
+      mbar_arrive_expect_tx(&bar.q_full, uint32_t(tiles_q * kPanels * pack * per_tile * 128));
       for (int w = 0; w < tiles_q; ++w)
         for (int c = 0; c < kPanels; ++c)
           tma_load_3d(sq + w * kTileBytes + c * kPanel, &tq, 64 * c, hq0, int(sp.q0) + tok0 + w * per_tile, &bar.q_full);
@@ -240,86 +280,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar.full[t % kR]);
       }
     } else if (warp == kMmaWarp && n_all > 0) {
+      // Step i of row tile w uses K and V of the list's entry i (dual: 2 i + w).
       // Per step and row tile: O += P V of this step, then S of the next, so
       // that the other row tile's softmax runs beside them.  The whole warp
       // walks through the steps and one thread issues: the MMAs' operands stay
       // in uniform registers (in a branch of one thread each MMA took three
-      // times as long to issue as to run).
+      // times as long to issue as to run).  One warp issues for both row tiles:
+      // two warps' MMAs interleaved took 8 % longer on an 8k prompt.
       const uint64_t dq = smem_desc_kmajor_sw128(smem_addr(sq)), dk = smem_desc_kmajor_sw128(smem_addr(ring));
       const uint64_t dv = smem_desc_mnmajor_sw128(smem_addr(ring), kPanel);
       auto arrived = [&](uint64_t* at, uint32_t parity) { return __all_sync(0xffffffffu, wait(at, parity)) != 0; };
-      auto issue_s = [&](int w, int st) {
-        const uint64_t a = dq + uint64_t(w * (kTileBytes >> 4)), bb = dk + uint64_t(st * (kTileBytes >> 4));
-        if (elect_one()) {
+      auto mma_s = [&](int w, int st) {
+        const uint64_t a = dq + uint64_t(dual ? 0 : w * (kTileBytes >> 4)), bb = dk + uint64_t(st * (kTileBytes >> 4));
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * (kPanel >> 4) + (kk % 4) * 2;
-            umma_f16_ss(tmem + w * kTile, a + off, bb + off, kIdescS, kk > 0);
-          }
-          umma_commit(&bar.s_full[w]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * (kPanel >> 4) + (kk % 4) * 2;
+          umma_f16_ss(tmem + w * kTile, a + off, bb + off, kIdescS, kk > 0);
         }
-        __syncwarp();
+        umma_commit(&bar.s_full[w]);
       };
-      auto commit = [&](uint64_t* at) {
-        if (elect_one()) umma_commit(at);
-        __syncwarp();
-      };
-      bool ok = arrived(&bar.q_full, 0) && arrived(&bar.full[0], 0);
-      if (ok) {
-        for (int w = 0; w < 2; ++w)
-          if (n[w] > 0) issue_s(w, 0);
-        commit(&bar.empty[0]);
+      // ring places of K (of the step to come) and V, and the parities of their turns
+      int ks[2], vs[2];
+      uint32_t kp[2] = {0, 0}, vp[2] = {0, 0};
+      bool ok = arrived(&bar.q_full, 0);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        ks[w] = dual ? 2 * w : 0;
+        vs[w] = ks[w] + 1;
+        if (ok && n[w] > 0) {
+          ok = arrived(&bar.full[ks[w]], 0);
+          if (ok && elect_one()) {
+            mma_s(w, ks[w]);
+            if (dual || w == 1 || n[1] == 0) umma_commit(&bar.empty[ks[w]]);
+          }
+          __syncwarp();
+        }
       }
-      int sk = 0, sv = 1;                    // ring places of K and V of the step
-      uint32_t pk = 0, pv = 0;               // and the parities of their turns
-      for (int j = 0; j < n_all && ok; ++j) {
-        sk += 2;
-        if (sk >= kR) sk -= kR, pk ^= 1;     // K of step j + 1
-        ok = arrived(&bar.full[sv], pv);
-        bool next = false;
+      const int stride = dual ? 4 : 2, rounds = max(n[0], n[1]);
+      for (int i = 0; i < rounds && ok; ++i) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if (ok && j < n[w]) {
-            const uint64_t bb = dv + uint64_t(sv * (kTileBytes >> 4));
-            const uint32_t a = tmem + w * kTile, d = tmem + kColO + w * D;
-            ok = arrived(&bar.p_full[w], j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
+          ks[w] += stride;
+          if (ks[w] >= kR) ks[w] -= kR, kp[w] ^= 1;
+          if (ok && i < n[w]) {
+            // K first, too: with P there the two products go out together.  (A
+            // dual part is bound by its loads, and does not wait for K here.)
+            const bool more = i + 1 < n[w];
+            if (w == 0 || dual || i >= n[0]) ok = arrived(&bar.full[vs[w]], vp[w]);
+            if (ok && more && !dual && (w == 0 || i + 1 >= n[0])) ok = arrived(&bar.full[ks[w]], kp[w]);
+            ok = ok && arrived(&bar.p_full[w], i & 1);
+            if (ok) {
+              tc_fence_after();
+              const uint64_t bb = dv + uint64_t(vs[w] * (kTileBytes >> 4));
+              if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk) umma_f16_ts(d, a + 8 * kk, bb + 128 * kk, kIdescO, j > 0 || kk > 0);
-              umma_commit(&bar.o_done[w]);
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  umma_f16_ts(tmem + kColO + w * D, tmem + w * kTile + 8 * kk, bb + 128 * kk, kIdescO, i > 0 || kk > 0);
+                umma_commit(&bar.o_done[w]);
+                // the last row tile to use a tile of keys lets it go
+                if (dual || w == 1 || i >= n[1]) umma_commit(&bar.empty[vs[w]]);
+                if (more && !dual) {
+                  mma_s(w, ks[w]);
+                  if (w == 1 || i + 1 >= n[1]) umma_commit(&bar.empty[ks[w]]);
+                }
+              }
+              __syncwarp();
+              if (more && dual) {
+                ok = arrived(&bar.full[ks[w]], kp[w]);
+                if (ok && elect_one()) {
+                  mma_s(w, ks[w]);
+                  umma_commit(&bar.empty[ks[w]]);
+                }
+                __syncwarp();
+              }
             }
-            __syncwarp();
           }
-          if (ok && j + 1 < n[w]) {
-            if (!next) ok = arrived(&bar.full[sk], pk);
-            next = true;
-            if (ok) issue_s(w, sk);
-          }
+          vs[w] += stride;
+          if (vs[w] >= kR) vs[w] -= kR, vp[w] ^= 1;
         }
-        if (ok) {
-          commit(&bar.empty[sv]);
-          if (next) commit(&bar.empty[sk]);
-        }
-        sv += 2;
-        if (sv >= kR) sv -= kR, pv ^= 1;
       }
       // every MMA issued is done before TMEM is given back
-      commit(&bar.fin);
+      if (elect_one()) umma_commit(&bar.fin);
+      __syncwarp();
       mbar_wait_bounded(&bar.fin, 0, kDrainWaitNs);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int w = warp >> 2, row = tid & (kTile - 1);
-    const int tok = tok0 + w * per_tile + row / pack, head = hq0 + row % pack;
-    const bool mine = tok < sp.n_q;
+    const int tok = tok0 + (dual ? 0 : w * per_tile) + row / pack, head = hq0 + row % pack;
+    const bool mine = row < pack * per_tile && tok < sp.n_q;   // (rows to spare hold anything)
     const int pos = shift + tok;
     const int row_lo = p.s.window ? max(0, pos - p.s.window + 1) : 0;
     const int row_hi = p.causal ? min(pos + 1, sp.n_k) : sp.n_k;
-    const float slope = p.s.slopes ? p.s.slopes[head] * kLog2e : 0.f;
-    const bool cap = p.s.cap_log2 != 0.f, formed = cap || p.s.slopes;
-    const float sc = formed ? 1.f : p.s.scale_log2;
+    const float slope = Formed && p.s.slopes ? p.s.slopes[head] * kLog2e : 0.f;
+    const bool cap = Formed && p.s.cap_log2 != 0.f;
+    const float sc = Formed ? 1.f : p.s.scale_log2;
+    const float cap_in = p.s.cap_in * (0.5f * kLn2);      // scale / cap
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t t_s = tmem + lanes + w * kTile, t_o = tmem + lanes + kColO + w * D;
     float m = -INFINITY, l = 0.f;
@@ -335,13 +391,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
       tc_wait_ld();
-      const int k0 = tile_of(j) * kTile;
-      if (formed) {
+      const int k0 = tile_of(dual ? 2 * j + w : j) * kTile;
+      if (cap) {
+        float far = 0.f;
 #pragma unroll
-        for (int i = 0; i < kTile; ++i) {
-          const float t = cap ? capped(s[i], p.s) : s[i] * p.s.scale_log2;
-          s[i] = fmaf(-slope, fabsf(float(pos - k0 - i)), t);
+        for (int i = 0; i < kTile; ++i) far = fmaxf(far, fabsf(s[i]));
+        // (a NaN is not above either: both ways keep it)
+        if (__any_sync(0xffffffffu, far * cap_in > 1.f)) {
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) s[i] = capped(s[i], p.s);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kTile / 2; ++i) {
+            const float2 t = capped_near(make_float2(s[2 * i], s[2 * i + 1]), cap_in, p.s.cap_log2);
+            s[2 * i] = t.x;
+            s[2 * i + 1] = t.y;
+          }
         }
+      }
+      if (Formed && p.s.slopes) {
+        const float away = float(pos - k0);
+#pragma unroll
+        for (int i = 0; i < kTile; ++i) s[i] = fmaf(-slope, fabsf(away - float(i)), cap ? s[i] : s[i] * p.s.scale_log2);
       }
       const bool full = (k0 >= row_lo && k0 + kTile <= row_hi) || k0 + kTile <= sp.prefix;
       if (!__all_sync(0xffffffffu, full)) {
@@ -352,14 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kTile; ++i)
           if (uint32_t(a + i) >= width && i >= pre) s[i] = -INFINITY;
       }
-      float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int i = 4; i < kTile - 4; i += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[i + e], s[i + 4 + e]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], s[kTile - 4 + e]);
-      const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      const float mt = row_max(s);
       // (nothing seen yet, nothing here: -inf - -inf is no growth)
       if (__any_sync(0xffffffffu, (mt - m) * sc > 8.f)) {
         const float mn = fmaxf(m, mt);
@@ -367,21 +431,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mn;
         l *= f;
         if (j > 0) {
-          ok = wait(&bar.o_done[w], (j - 1) & 1);
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, wait(&bar.o_done[w], (j - 1) & 1));
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
-            asm volatile(
-                "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                  "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                : "r"(t_o + 16 * c)
-                : "memory");
+            tmem_ld16(t_o + 16 * c, o);
             tc_wait_ld();
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
@@ -471,34 +527,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of each row: one warp a row.
+// Joins the parts of each row: one warp a row.  The parts' weights are worked
+// out by lane, so that the loads of the sums do not wait for one another.
 template <int D>
-__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, const PromptPlan plan) {
+__global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, const PromptPlan plan, int rows) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, row = (blockIdx.x % 32) * 8 + (threadIdx.x >> 5);
-  const int64_t cta = blockIdx.x / 32;
+  const int lane = threadIdx.x & 31, row = (blockIdx.x % (rows / 8)) * 8 + (threadIdx.x >> 5);
+  const int64_t cta = blockIdx.x / (rows / 8);
   const int set = int(cta % plan.sets), blk = int(cta / plan.sets % plan.blocks), b = int(cta / plan.sets / plan.blocks);
   const PromptSpan sp = prompt_span(p, b, false);
-  const int tok = blk * 2 * (kTile / plan.pack) + row / plan.pack, head = set * plan.pack + row % plan.pack;
-  if (tok >= sp.n_q) return;
+  const int per_tile = kTile / plan.pack, in_tile = row % kTile;
+  const int tok = (blk * 2 + row / kTile) * per_tile + in_tile / plan.pack, head = set * plan.pack + in_tile % plan.pack;
+  if (in_tile >= plan.pack * per_tile || tok >= sp.n_q) return;
   const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
-  const float2* ml = reinterpret_cast<const float2*>(ws + plan.off_ml) + cta * plan.splits * 2 * kTile + row;
-  const float* po = reinterpret_cast<const float*>(ws + plan.off_o) + (cta * plan.splits * 2 * kTile + row) * D;
+  const int parts = plan.splits * (1 + plan.dual);
+  const int64_t first = cta * plan.splits * 2 * kTile + row;    // parts are `rows` rows apart
+  const float2* ml = reinterpret_cast<const float2*>(ws + plan.off_ml) + first;
+  const float* po = reinterpret_cast<const float*>(ws + plan.off_o) + first * D + lane * (D / 32);
   constexpr int kC = D / 32;
-  float mx = -INFINITY, sum = 0.f, o[kC] = {};
-  for (int s = 0; s < plan.splits; ++s) {
-    const float2 x = __ldcg(&ml[int64_t(s) * 2 * kTile]);
+  float mx = -INFINITY;
+  for (int s = lane; s < parts; s += 32) {
+    const float2 x = __ldcg(&ml[int64_t(s) * rows]);
     if (x.y > 0.f) mx = fmaxf(mx, x.x);
   }
-  for (int s = 0; s < plan.splits; ++s) {
-    const float2 x = __ldcg(&ml[int64_t(s) * 2 * kTile]);
-    if (!(x.y > 0.f)) continue;
-    const float f = exp2_fast(x.x - mx);
-    sum = fmaf(f, x.y, sum);
 #pragma unroll
-    for (int e = 0; e < kC; ++e) o[e] = fmaf(f, __ldcg(&po[int64_t(s) * 2 * kTile * D + kC * lane + e]), o[e]);
+  for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+  float sum = 0.f, o[kC] = {};
+  for (int s0 = 0; s0 < parts; s0 += 32) {
+    float f = 0.f;
+    if (s0 + lane < parts) {
+      const float2 x = __ldcg(&ml[int64_t(s0 + lane) * rows]);
+      if (x.y > 0.f) {
+        f = exp2_fast(x.x - mx);
+        sum = fmaf(f, x.y, sum);
+      }
+    }
+    const int here = min(32, parts - s0);
+#pragma unroll 8
+    for (int s = 0; s < here; ++s) {
+      const float g = __shfl_sync(0xffffffffu, f, s);
+      float v[kC] = {};
+      if (g > 0.f) {                         // (a part without keys has written no sums)
+        const float* from = po + int64_t(s0 + s) * rows * D;
+        if constexpr (kC == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(from));
+          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(from));
+          v[0] = x.x, v[1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kC; ++e) o[e] = fmaf(g, v[e], o[e]);
+    }
   }
+#pragma unroll
+  for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((sp.q0 + tok) * p.n_q + head) * D + kC * lane);
 #pragma unroll
@@ -528,7 +613,7 @@ bool encode_rows(CUtensorMap* map, const uint16_t* x, int d, int heads, int64_t 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, bool Formed>
 cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t stream) {
   CUtensorMap tq, tk, tv;
   const uint16_t* k = p.total_k ? p.k : p.q;   // no key, no load: the maps only have to be well-formed
@@ -538,14 +623,15 @@ cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t s
       !encode_rows(&tv, v, D, p.n_kv, p.total_k, p.v_stride, 1, kTile))
     return cudaErrorInvalidValue;
   constexpr int bytes = 1024 + (2 + kRing<D>) * (D / 64) * kPanel;
-  cudaError_t e = set_smem_limit<prompt_kernel<D>>(bytes);
+  cudaError_t e = set_smem_limit<prompt_kernel<D, Formed>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t x = int64_t(plan.blocks) * plan.sets;
   if (x > 0x7fffffff || x * p.batch > 0x7fffffff / 32) return cudaErrorInvalidValue;
   const dim3 grid(unsigned(x), unsigned(p.batch), unsigned(plan.splits));
-  e = launch_pdl(prompt_kernel<D>, grid, dim3(kThreads), bytes, stream, p, plan, tq, tk, tv);
+  e = launch_pdl(prompt_kernel<D, Formed>, grid, dim3(kThreads), bytes, stream, p, plan, tq, tk, tv);
   if (e != cudaSuccess || plan.splits == 1) return e;
-  return launch_pdl(prompt_join_kernel<D>, dim3(unsigned(x * p.batch * 32)), dim3(256), 0, stream, p, plan);
+  const int rows = plan.dual ? kTile : 2 * kTile;
+  return launch_pdl(prompt_join_kernel<D>, dim3(unsigned(x * p.batch * (rows / 8))), dim3(256), 0, stream, p, plan, rows);
 }
 
 }  // namespace
@@ -557,7 +643,9 @@ size_t prompt_workspace_bytes(const PromptParams& p, cudaError_t* err) {
 
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   const PromptPlan plan = plan_prompt(p);
-  return p.d == 128 ? launch<128>(p, plan, stream) : launch<64>(p, plan, stream);
+  const bool formed = p.s.cap_log2 != 0.f || p.s.slopes;
+  if (p.d == 128) return formed ? launch<128, true>(p, plan, stream) : launch<128, false>(p, plan, stream);
+  return formed ? launch<64, true>(p, plan, stream) : launch<64, false>(p, plan, stream);
 }
 
 }  // namespace oscar
