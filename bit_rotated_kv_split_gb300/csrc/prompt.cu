@@ -121,18 +121,17 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
-// The capped score where |x| scale / cap <= 1: tanh(y) = y P(y^2), P of degree 7
-// interpolated at the Chebyshev points of [0, 1] (5e-8 of the value in fp32).
-// A tile of 128 x 128 scores takes a third of the time that it takes by powers
-// and reciprocals, which the special function unit bounds.
-__device__ __forceinline__ float2 capped_near(float2 x, float cap_in, float cap_log2) {
-  constexpr float kP[8] = {1.f,          -0.3333328068256378f,  0.13332191109657288f,   -0.053872738033533096f,
-                           0.02146998f, -0.007924946025013924f, 0.0022876455914229155f, -0.0003548834065441042f};
+// The capped score where |x| scale / cap <= 1 / 2: tanh(y) = y P(y^2), P of degree 4
+// fitted at the Chebyshev points of [0, 1 / 4] (6e-8 of the value in fp32); c
+// holds P's coefficients times cap.  By powers and reciprocals (two of the special
+// function unit's instructions a score, besides the softmax's one) a tile of 128
+// x 128 scores took twice as long.
+__device__ __forceinline__ float2 capped_near(float2 x, float cap_in, const float (&c)[5]) {
   const float2 y = mul2(x, make_float2(cap_in, cap_in)), u = mul2(y, y);
-  float2 r = make_float2(kP[7], kP[7]);
+  float2 r = make_float2(c[4], c[4]);
 #pragma unroll
-  for (int k = 6; k >= 0; --k) r = fma2(r, u, make_float2(kP[k], kP[k]));
-  return mul2(mul2(y, make_float2(cap_log2, cap_log2)), r);
+  for (int k = 3; k >= 0; --k) r = fma2(r, u, make_float2(c[k], c[k]));
+  return mul2(y, r);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -376,6 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool cap = Formed && p.s.cap_log2 != 0.f;
     const float sc = Formed ? 1.f : p.s.scale_log2;
     const float cap_in = p.s.cap_in * (0.5f * kLn2);      // scale / cap
+    constexpr float kP[5] = {1.f, -0.3333307206630707f, 0.13324828445911407f, -0.05298924073576927f, 0.017141319811344147f};
+    float near[5];   // P of capped_near
+#pragma unroll
+    for (int k = 0; k < 5; ++k) near[k] = kP[k] * p.s.cap_log2;
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t t_s = tmem + lanes + w * kTile, t_o = tmem + lanes + kColO + w * D;
     float m = -INFINITY, l = 0.f;
@@ -397,13 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kTile; ++i) far = fmaxf(far, fabsf(s[i]));
         // (a NaN is not above either: both ways keep it)
-        if (__any_sync(0xffffffffu, far * cap_in > 1.f)) {
+        if (__any_sync(0xffffffffu, far * cap_in > 0.5f)) {
 #pragma unroll
           for (int i = 0; i < kTile; ++i) s[i] = capped(s[i], p.s);
         } else {
 #pragma unroll
           for (int i = 0; i < kTile / 2; ++i) {
-            const float2 t = capped_near(make_float2(s[2 * i], s[2 * i + 1]), cap_in, p.s.cap_log2);
+            const float2 t = capped_near(make_float2(s[2 * i], s[2 * i + 1]), cap_in, near);
             s[2 * i] = t.x;
             s[2 * i + 1] = t.y;
           }
@@ -527,12 +530,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of each row: one warp a row.  The parts' weights are worked
-// out by lane, so that the loads of the sums do not wait for one another.
+// Joins the parts of each row: one warp a row, 16 parts at a time, whose sums
+// are asked for together with their maxima (a part that saw no key has written
+// no sums: what is read there is not used).
 template <int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, const PromptPlan plan, int rows) {
   pdl_wait();
   pdl_launch_dependents();
+  constexpr int kC = D / 32, kBatch = 16;
   const int lane = threadIdx.x & 31, row = (blockIdx.x % (rows / 8)) * 8 + (threadIdx.x >> 5);
   const int64_t cta = blockIdx.x / (rows / 8);
   const int set = int(cta % plan.sets), blk = int(cta / plan.sets % plan.blocks), b = int(cta / plan.sets / plan.blocks);
@@ -544,42 +549,39 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, 
   const int parts = plan.splits * (1 + plan.dual);
   const int64_t first = cta * plan.splits * 2 * kTile + row;    // parts are `rows` rows apart
   const float2* ml = reinterpret_cast<const float2*>(ws + plan.off_ml) + first;
-  const float* po = reinterpret_cast<const float*>(ws + plan.off_o) + first * D + lane * (D / 32);
-  constexpr int kC = D / 32;
-  float mx = -INFINITY;
-  for (int s = lane; s < parts; s += 32) {
-    const float2 x = __ldcg(&ml[int64_t(s) * rows]);
-    if (x.y > 0.f) mx = fmaxf(mx, x.x);
-  }
+  const float* po = reinterpret_cast<const float*>(ws + plan.off_o) + first * D + lane * kC;
+  float mx = -INFINITY, sum = 0.f, o[kC] = {};
+  for (int s0 = 0; s0 < parts; s0 += kBatch) {
+    float v[kBatch][kC];
+    float2 x = make_float2(0.f, 0.f);
+    if (lane < kBatch && s0 + lane < parts) x = __ldcg(&ml[int64_t(s0 + lane) * rows]);
 #pragma unroll
-  for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-  float sum = 0.f, o[kC] = {};
-  for (int s0 = 0; s0 < parts; s0 += 32) {
-    float f = 0.f;
-    if (s0 + lane < parts) {
-      const float2 x = __ldcg(&ml[int64_t(s0 + lane) * rows]);
-      if (x.y > 0.f) {
-        f = exp2_fast(x.x - mx);
-        sum = fmaf(f, x.y, sum);
+    for (int s = 0; s < kBatch; ++s) {
+      const float* from = po + int64_t(min(s0 + s, parts - 1)) * rows * D;
+      if constexpr (kC == 4) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(from));
+        v[s][0] = u.x, v[s][1] = u.y, v[s][2] = u.z, v[s][3] = u.w;
+      } else {
+        const float2 u = __ldcg(reinterpret_cast<const float2*>(from));
+        v[s][0] = u.x, v[s][1] = u.y;
       }
     }
-    const int here = min(32, parts - s0);
-#pragma unroll 8
-    for (int s = 0; s < here; ++s) {
-      const float g = __shfl_sync(0xffffffffu, f, s);
-      float v[kC] = {};
-      if (g > 0.f) {                         // (a part without keys has written no sums)
-        const float* from = po + int64_t(s0 + s) * rows * D;
-        if constexpr (kC == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(from));
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(from));
-          v[0] = x.x, v[1] = x.y;
-        }
-      }
+    float top = x.y > 0.f ? x.x : -INFINITY;
 #pragma unroll
-      for (int e = 0; e < kC; ++e) o[e] = fmaf(g, v[e], o[e]);
+    for (int i = 8; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    top = __shfl_sync(0xffffffffu, top, 0);
+    if (top == -INFINITY) continue;          // the same in all lanes
+    const float mn = fmaxf(mx, top), f = mx == -INFINITY ? 0.f : exp2_fast(mx - mn);
+    mx = mn;
+    const float g = x.y > 0.f ? exp2_fast(x.x - mn) : 0.f;
+    sum = fmaf(g, x.y, sum * f);             // of this lane's parts
+#pragma unroll
+    for (int e = 0; e < kC; ++e) o[e] *= f;
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) {
+      const float gs = __shfl_sync(0xffffffffu, g, s);
+#pragma unroll
+      for (int e = 0; e < kC; ++e) o[e] = gs > 0.f ? fmaf(gs, v[s][e], o[e]) : o[e];
     }
   }
 #pragma unroll
