@@ -80,7 +80,7 @@ struct Int4DecodeParams {
   uint16_t* out;
   void* workspace;
 };
-size_t int4_decode_workspace_bytes(const Int4Cache& c, const ScoreParams& s, cudaError_t* err);
+size_t int4_decode_workspace_bytes(const Int4Cache& c);
 cudaError_t launch_decode_int4(const Int4DecodeParams& p, cudaStream_t stream);
 
 struct PromptParams {
@@ -95,7 +95,7 @@ struct PromptParams {
   int32_t batch, n_q, n_kv, d, max_q, max_k, causal;
   int64_t total_q, total_k;
 };
-size_t prompt_workspace_bytes(const PromptParams& p, cudaError_t* err);
+size_t prompt_workspace_bytes(const PromptParams& p);
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream);
 
 }  // namespace oscar

@@ -76,7 +76,9 @@ oscar_status check_score(const oscar_score_desc* d, int32_t head_dim, oscar::Sco
 // rows of `heads` heads of d bf16, `stride` elements apart
 bool row_stride_ok(int64_t stride, int64_t heads, int32_t d) { return stride >= heads * d && stride % 8 == 0; }
 
-oscar_status done(cudaError_t e) { return e == cudaSuccess ? OSCAR_OK : OSCAR_ERR_CUDA; }
+oscar_status done(cudaError_t e) {
+  return e == cudaSuccess ? OSCAR_OK : e == cudaErrorNotSupported ? OSCAR_ERR_UNSUPPORTED : OSCAR_ERR_CUDA;
+}
 
 }  // namespace
 
@@ -175,9 +177,7 @@ extern "C" oscar_status oscar_decode_attention_int4(const oscar_int4_desc* desc,
   if (desc->n_q_heads / desc->n_kv_heads > 16) return OSCAR_ERR_UNSUPPORTED;
   st = check_score(score, desc->head_dim, &p.s);
   if (st != OSCAR_OK) return st;
-  cudaError_t err = cudaSuccess;
-  const size_t need = oscar::int4_decode_workspace_bytes(p.c, p.s, &err);
-  if (err != cudaSuccess) return OSCAR_ERR_CUDA;
+  const size_t need = oscar::int4_decode_workspace_bytes(p.c);
   if (!workspace) {
     *workspace_bytes = need;
     return OSCAR_OK;
@@ -218,9 +218,7 @@ extern "C" oscar_status oscar_prompt_attention(const oscar_prompt_desc* desc, co
   p.total_q = desc->total_q;
   p.total_k = desc->total_k;
   p.dev_status = desc->dev_status;
-  cudaError_t err = cudaSuccess;
-  const size_t need = oscar::prompt_workspace_bytes(p, &err);
-  if (err != cudaSuccess) return OSCAR_ERR_CUDA;
+  const size_t need = oscar::prompt_workspace_bytes(p);
   if (!workspace) {
     *workspace_bytes = need;
     return OSCAR_OK;

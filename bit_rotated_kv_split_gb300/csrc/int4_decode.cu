@@ -1,25 +1,33 @@
-// Decode attention over a 4-bit layer: one query token per request, split over
-// the pages of its context and joined by the last CTA of each (request, KV
-// head) to finish.
+// Decode attention over a 4-bit layer: one query token per request.
 //
-// A CTA of 8 warps takes one split of one (request, KV head, up to 8 query
-// heads); a warp takes every 8th page of the split with an online softmax of
-// its own, so nothing in the scan waits for another warp.  The pages' blocks
-// come by bulk copies into a ring of the warp's own.
+// The pages of all (request, KV head, up to 8 query heads) runs stand in one row,
+// and each of 304 lasting CTAs (two per SM) takes an equal share of it: a ragged
+// batch is as even as a uniform one, and only the first and the last run of a
+// share can be incomplete.  Those leave their unnormalised sums in the workspace,
+// and the last CTA of a run to finish joins its parts.  (A grid of one CTA for
+// every 16 pages a warp spent a third of its time in the CTAs' first loads and
+// last sums.)
+//
+// A warp takes every 8th pair of a run's pages with an online softmax of its own,
+// so nothing in the scan waits for another warp.  The pages' blocks come by bulk
+// copies into a ring of the warp's own, the next run's ahead of the present one's
+// end.
 //
 // Per page, on the tensor cores with 16 tokens or 16 channels as the rows and
 // 8 query heads as the columns:
-//   S = K q:   A = the K codes as they are: a code c in the low bits of an fp16
-//              is c 2^-24 exactly (and c 2^-20 one nibble higher), so one mask
-//              turns a word into two operands.  q is scaled by a power of two
-//              per head to just below fp16's end, which is exact for bf16.
-//              x = sum over groups of s (sum c q) + z (sum q).
-//   O += P V:  A = the V codes the same way, B = p s_V in fp16; the zeros are
-//              summed apart as p z_V in fp32.  The 11 bits of p s_V are the one
-//              rounding below fp32 (bf16 output has 8).
+//   S = K q:     A = the K codes as they are: a code c in the low bits of an fp16
+//                is c 2^-24 exactly (and c 2^-20 one nibble higher), so one mask
+//                turns a word into two operands.  q is scaled by a power of two per
+//                head to just below fp16's end, which is exact for bf16.
+//                x = sum over groups of s (sum c q) + z (sum q).
+//   O += V^T P:  A = the V codes the same way, B = P s_V.
+//   Z += (z_V; 1) P:  the zeros' share of O and the softmax's sum.
+// P and P s_V are rounded to fp16 (2^-11 each; the bf16 output has 2^-8); all sums
+// are fp32.  (e4m3 operands would need fewer masks, but their mma.sync is not
+// native here: 38 us against 32 for 100k tokens.)
 // The weights' reference is raised only when a score exceeds it by 2^8, and
 // the values' scales are taken relative to a power of two above them, raised
-// when a larger one comes: both by one vote per page.
+// when a larger one comes: both by one vote for two pages.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,50 +41,32 @@
 namespace oscar {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kHeads = 8;             // query heads per CTA (MMA columns)
-constexpr int kSlots = 152 * 2;       // CTAs the GPU holds at a time
-constexpr int kRounds = 24;           // rounds of them that a grid is split into, at most
-// Merge tickets sit at the same place of the workspace whatever the call's
-// sizes, so that calls of different batches share one: no call writes partial
-// states where another keeps tickets.  A grid is split (2 splits or more) only
-// below this many (request, head set) pairs.
-constexpr int kTickets = 4096;
-static_assert(kSlots * kRounds / 2 <= kTickets, "every split pair has a ticket");
-constexpr int kMostSplits = 512;      // their weights fit the joining CTA's shared memory
+constexpr int kStages = 2;            // ring stages of a warp, each two pages
+constexpr int kCtas = 152 * 2;        // CTAs the GPU holds at a time
+constexpr int kMinShare = 4 * kWarps; // pages
+// A run costs its CTA about as much as this many pages besides its own (the
+// query, the warps' join): a run takes up so many more places in the row.
+#ifndef KRUN
+#define KRUN 64
+#endif
+constexpr int kRunCost = KRUN;
+constexpr int kJoinHeads = 4;         // heads whose states are joined at a time
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
-struct SplitPlan {
-  int splits;          // per (request, head set), at most
-  int halves;          // head sets per KV head
-  size_t off_ml, off_o, bytes;
-};
+// Workspace: a ticket for each CTA (of the run that goes on behind its share),
+// then two partial states for each, of a run that began before its share and of one
+// that begins in it: (m, l) and the sums.
+constexpr size_t kOffMl = 4096, kOffO = kOffMl + size_t(kCtas) * 2 * kHeads * 8;
 
-// Pages of a request are split so that the grid is a whole number of rounds
-// of the CTAs that the GPU holds, each of at least 16 pages a warp where the
-// context has them, and at least 4.
-SplitPlan plan_splits(const Int4Cache& c, const ScoreParams& s) {
-  SplitPlan r{};
-  const int group = c.n_q / c.n_kv;
-  r.halves = (group + kHeads - 1) / kHeads;
-  int64_t tokens = c.max_len;
-  if (s.window) tokens = std::min<int64_t>(tokens, int64_t(s.window) + kInt4Page);
-  const int64_t pages = std::max<int64_t>(1, (tokens + kInt4Page - 1) / kInt4Page);
-  const int64_t pairs = int64_t(c.batch) * c.n_kv * r.halves;
-  const int64_t round = int64_t(kSlots) * kWarps * 16;
-  const int64_t rounds = std::min<int64_t>(kRounds, std::max<int64_t>(1, (pairs * pages + round / 2) / round));
-  const int64_t most = std::max<int64_t>(1, pages / (kWarps * 4));
-  r.splits = int(std::min<int64_t>(std::min<int64_t>(most, kMostSplits), std::max<int64_t>(1, kSlots * rounds / pairs)));
-  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-  r.off_ml = up(size_t(kTickets) * 4);
-  r.off_o = r.off_ml + up(size_t(pairs) * r.splits * kHeads * 8);
-  r.bytes = r.off_o + up(size_t(pairs) * r.splits * kHeads * c.d * 4);
-  if (r.splits == 1) r.bytes = 256;   // nothing is kept there
-  return r;
+template <int D>
+constexpr int join_bytes() {
+  // the warps' states of kJoinHeads heads; or the parts' weights and 256 partial sums
+  return std::max(kWarps * kJoinHeads * D * 4, (kCtas + 1) * kHeads * 4 + kThreads * 16);
 }
 
-// N consecutive 32-bit words, by the widest loads that the alignment of N
-// words times any index allows.
+// N consecutive 32-bit words at a multiple of N words.
 template <int N>
 __device__ __forceinline__ void lds_n(uint32_t (&v)[N], const uint8_t* p) {
   if constexpr (N % 4 == 0) {
@@ -104,31 +94,150 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 __device__ __forceinline__ float max_over_rows(float v) {   // over the 8 lanes of a column pair
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
 }
-__device__ __forceinline__ float sum_over_rows(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 4);
-  v += __shfl_xor_sync(0xffffffffu, v, 8);
-  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+__device__ __forceinline__ float max_over_quad(float v) {   // over the 4 lanes of a row
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
-// Ring stages of a warp, each two pages: three where two CTAs' rings fit an
-// SM's shared memory, else two.
-constexpr int stages_of(int block) { return 2 * kWarps * 2 * 3 * block <= 212 * 1024 ? 3 : 2; }
+// The tokens of a request that its query sees, and their pages.
+struct Span {
+  int len, first;
+  __device__ __forceinline__ int page0() const { return first / kInt4Page; }
+  __device__ __forceinline__ int pages() const { return (len + kInt4Page - 1) / kInt4Page - page0(); }
+};
+__device__ __forceinline__ Span span_of(const Int4DecodeParams& p, int b, bool report) {
+  int len = p.c.seq_len[b];
+  if (len < 0 || len > p.c.max_len) {
+    if (report && p.c.dev_status) atomicOr(p.c.dev_status, OSCAR_DEV_LENGTH);
+    len = min(max(len, 0), p.c.max_len);
+  }
+  return {len, p.s.window ? max(0, len - p.s.window) : 0};
+}
+
+// A run's pages, or the part of them in this CTA's share: pages lo .. hi - 1 of
+// request b, head set h; `off` pages of the run lie before it, `pages` in all; it
+// begins at place `at` of the row.
+struct Segment {
+  int b, h, lo, hi, off, pages, len, first, at;
+};
+
+// Walks through a share, run by run.
+struct Walk {
+  int b, h, off;        // where the next segment begins: `off` pages into the run
+  int at, end;          // its place, and the share's end
+  Span span;            // of request b
+  __device__ __forceinline__ bool next(const Int4DecodeParams& p, int sets, Segment* s) {
+    int pages = span.pages();
+    if (off >= pages && at < end) step(p, sets), pages = span.pages();   // (the share begins behind a run's pages)
+    if (at >= end) return false;
+    const int n = min(pages - off, end - at), lo = span.page0() + off;
+    *s = {b, h, lo, lo + n, off, pages, span.len, span.first, at};
+    off += n;
+    at += n;
+    if (off == pages) step(p, sets);
+    return true;
+  }
+  __device__ __forceinline__ void step(const Int4DecodeParams& p, int sets) {   // to the next run's first page
+    at += span.pages() + kRunCost - off;
+    off = 0;
+    if (++h < sets) return;
+    h = 0;
+    while (at < end && ++b < p.c.batch) {
+      span = span_of(p, b, false);
+      if (span.pages() > 0) return;
+    }
+    at = end;
+  }
+};
+
+// A run in more than one share: its place in the row, pages, request, first
+// query head and their number.
+struct Part {
+  int run, pages, b, hq0, heads;
+};
+
+// Joins the parts of a run; the whole CTA, 4 channels a thread.  Where the heads
+// leave threads over, each takes every n-th part.  (Small code: it runs once a
+// CTA, when its instructions have to come from far.)
+template <int D>
+__device__ __noinline__ void join_parts(const Int4DecodeParams& p, const Part& r, int share, float* wt, float* sum_of) {
+  const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = r.heads;
+  const int f = r.run / share, n = (r.run + r.pages - 1) / share - f + 1;
+  auto slot_of = [&](int i) { return 2 * (f + i) + (i == 0); };
+  const float2* ml = reinterpret_cast<const float2*>(ws + kOffMl) + warp;
+  if (warp < heads) {                     // warp h: head h
+    float mx = -FLT_MAX, sum = 0.f;
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      const float2 s = __ldcg(&ml[slot_of(i) * kHeads]);
+      const float m = s.y > 0.f ? s.x : -FLT_MAX, mn = fmaxf(mx, m);
+      sum = fmaf(exp2_fast(m - mn), s.y, sum * exp2_fast(mx - mn));
+      mx = mn;
+      wt[i * kHeads + warp] = m;
+    }
+    float all = mx;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, i));
+    sum *= exp2_fast(mx - all);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) wt[i * kHeads + warp] = exp2_fast(wt[i * kHeads + warp] - all);
+    if (lane == 0) sum_of[warp] = sum;
+  }
+  __syncthreads();
+  const int units = heads * (D / 4), ways = kThreads / units, way = threadIdx.x / units, unit = threadIdx.x % units;
+  const int h = unit / (D / 4);
+  const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (way < ways)
+#pragma unroll 8
+    for (int i = way; i < n; i += ways) {
+      const float g = wt[i * kHeads + h];
+      const float4 x = __ldcg(from + slot_of(i) * (kHeads * D / 4));
+      v.x = fmaf(g, x.x, v.x), v.y = fmaf(g, x.y, v.y), v.z = fmaf(g, x.z, v.z), v.w = fmaf(g, x.w, v.w);
+    }
+  float4* sums = reinterpret_cast<float4*>(wt + n * kHeads);
+  sums[threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.x < units) {
+#pragma unroll 1
+    for (int i = 1; i < ways; ++i) {
+      const float4 y = sums[i * units + unit];
+      v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+    }
+    const float inv = sum_of[h] > 0.f ? 1.f / sum_of[h] : 0.f;
+    reinterpret_cast<uint2*>(p.out + (int64_t(r.b) * p.c.n_q + r.hq0) * D)[unit] =
+        make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
+  }
+}
 
 // Formed: the scores have a cap or a distance bias.
 template <int D, int NGK, int NGV, bool Formed>
-__global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4DecodeParams p, const SplitPlan plan) {
-  constexpr int W = D / 32, kBlock = int4_block_bytes(D, NGK, NGV), kPairs = 16 * D, kStages = stages_of(kBlock);
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_int4_kernel(const __grid_constant__ Int4DecodeParams p, int halves) {
+  constexpr int W = D / 32, kBlock = int4_block_bytes(D, NGK, NGV), kPairs = 16 * D, NG = NGK + NGV;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
-  __shared__ int sm_last;
+  __shared__ int sm_scan[kWarps];
+  __shared__ Walk sm_walk, sm_walks[kWarps];
+  __shared__ Segment sm_next[kWarps];
+  __shared__ Part sm_part[2];
+  __shared__ int sm_last[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
   if (lane < kStages) mbar_init(&bars[warp][lane], 1);
   fence_mbar_init();
@@ -136,54 +245,113 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
   pdl_wait();
   pdl_launch_dependents();
   const Int4Cache& c = p.c;
-  const int b = blockIdx.z, hk = blockIdx.y / plan.halves, set = blockIdx.y % plan.halves;
-  const int group = c.n_q / c.n_kv, heads = min(kHeads, group - set * kHeads);
-  const int hq0 = hk * group + set * kHeads;
-  int len = c.seq_len[b];
-  if (len < 0 || len > c.max_len) {
-    if (threadIdx.x == 0 && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_LENGTH);
-    len = min(max(len, 0), c.max_len);
-  }
-  const int first = p.s.window ? max(0, len - p.s.window) : 0;
-  const int page0 = first / kInt4Page, page1 = (len + kInt4Page - 1) / kInt4Page;
-  // this request's own split: as many as its pages need of the grid's
-  const int pages = page1 - page0, most = max(1, pages / (kWarps * 4));
-  const int splits = min(plan.splits, most), split = blockIdx.x;
-  if (split >= splits) return;
-  const int begin = page0 + int(int64_t(pages) * split / splits), end = page0 + int(int64_t(pages) * (split + 1) / splits);
-  // a warp takes every 8th pair of pages
-  const int n_it = max(0, ((end - begin + 1) / 2 - warp + kWarps - 1) / kWarps);
+  const int sets = c.n_kv * halves, group = c.n_q / c.n_kv;
 
-  // Lane i knows pairs 32 n + i of the warp's and brings them.
-  const int32_t* table = c.page_table + int64_t(b) * c.max_pages;
-  uint8_t* ring = smem + warp * (kStages * 2 * kBlock);
-  uint64_t* wbars = bars[warp];
-  auto pages_of = [&](int i, int (&id)[2]) {
+  // this CTA's share: a prefix sum over the places of the requests' runs, a
+  // thread taking batch / 256 of them
+  const int per = (c.batch + kThreads - 1) / kThreads, b0 = min(c.batch, int(threadIdx.x) * per), b1 = min(c.batch, b0 + per);
+  int mine = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int n = span_of(p, b, blockIdx.x == 0).pages();
+    mine += n ? (n + kRunCost) * sets : 0;
+  }
+  int before = mine;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int at = begin + 2 * (warp + kWarps * i) + g;
-      id[g] = i < n_it && at < end ? table[at] : -1;
-      if (id[g] < 0 || id[g] >= c.n_pages) {
-        if (i < n_it && at < end && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
-        id[g] = -1;
+  for (int x = 1; x < 32; x <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, x);
+    if (lane >= x) before += v;
+  }
+  if (lane == 31) sm_scan[warp] = before;
+  __syncthreads();
+  int total = 0;
+  before -= mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sm_scan[w];
+    total += sm_scan[w];
+  }
+  const int share = max(kMinShare + kRunCost, int((unsigned(total) + gridDim.x - 1) / gridDim.x));
+  const int64_t start = int64_t(share) * blockIdx.x;
+  const bool any = start < total;
+  if (any && start >= before && start - before < mine) {
+    int b = b0, at = int(start) - before;
+    Span s = span_of(p, b, false);
+#pragma unroll 1
+    while (s.pages() == 0 || at >= (s.pages() + kRunCost) * sets) {
+      at -= s.pages() ? (s.pages() + kRunCost) * sets : 0;
+      s = span_of(p, ++b, false);
+    }
+    const int run = s.pages() + kRunCost;
+    sm_walk = {b, at / run, at % run, int(start), int(min(int64_t(total), start + share)), s};
+  }
+  // requests without a token
+  for (int b = blockIdx.x; b < c.batch; b += gridDim.x)
+    if (c.seq_len[b] <= 0 || c.max_len == 0)
+      for (int i = threadIdx.x; i < c.n_q * D / 8; i += kThreads)
+        reinterpret_cast<uint4*>(p.out + int64_t(b) * c.n_q * D)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  if (!any) return;
+
+  // Each warp walks by itself; the next segment waits in shared memory.
+  auto advance = [&]() {
+    bool ok = false;
+    if (lane == 0) ok = sm_walks[warp].next(p, sets, &sm_next[warp]);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+  };
+  if (lane == 0) sm_walks[warp] = sm_walk;
+  if (!advance()) return;                 // (nothing but places of a run's cost; the same in all warps)
+  Segment cur = sm_next[warp];
+  __syncwarp();
+  bool more = advance();
+
+  // The ring.  A warp's pairs of a segment begin with another warp each time,
+  // so that short segments spread over the warps.  Lane i knows pairs 32 n + i
+  // of the segment that is being brought in.
+  uint8_t* ring = smem + warp * (kStages * 2 * kBlock);
+  float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * kBlock);
+  uint64_t* wbars = bars[warp];
+  auto place = [&](const Segment& s) { return (warp - (s.at >> 1)) & (kWarps - 1); };
+  // the segment being brought in: its pages from this warp's first, KV head, request, and pairs
+  int in_lo, in_hi, in_hk, in_b, in_it = 0, in_n;
+  auto turn_to = [&](const Segment& s) {
+    in_lo = s.lo + 2 * place(s);
+    in_hi = s.hi;
+    in_hk = s.h / halves;
+    in_b = s.b;
+    in_it = 0;
+    in_n = max(0, (in_hi - in_lo + 2 * kWarps - 1) / (2 * kWarps));
+  };
+  turn_to(cur);
+  bool in_next = false, dead = false;     // it is the next one, not cur
+  int id[2] = {-1, -1}, st_in = 0, flying = 0;
+  uint32_t ring_dead = 0;                 // bits 2 i, 2 i + 1: stage i's pages that are not there
+  auto bring = [&]() {                    // one more pair; false if there is none to bring yet
+    if (in_it == in_n) {
+      if (in_next || !more || dead) return false;
+      in_next = true;
+      turn_to(sm_next[warp]);
+      if (in_n == 0) return false;
+    }
+    if ((in_it & 31) == 0) {
+      const int32_t* table = c.page_table + int64_t(in_b) * c.max_pages;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int page = in_lo + 2 * kWarps * (in_it + lane) + g;
+        id[g] = page < in_hi ? table[page] : -1;
+        if (page < in_hi && (id[g] < 0 || id[g] >= c.n_pages)) {
+          if (c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+          id[g] = -1;
+        }
       }
     }
-  };
-  int id[2], id_next[2] = {-1, -1};
-  pages_of(lane, id);
-  uint32_t ring_dead = 0;                 // bits 2 i, 2 i + 1: stage i's pages that are not there
-  int st_issue = 0;
-  auto issue = [&](int it) {
-    const int at = it & 31;
-    if (at == 0) {
-      if (it) id[0] = id_next[0], id[1] = id_next[1];
-      pages_of(it + 32 + lane, id_next);
-    }
-    const uint32_t none = __shfl_sync(0xffffffffu, (id[0] < 0 ? 1u : 0u) | (id[1] < 0 ? 2u : 0u), at);
-    ring_dead = (ring_dead & ~(3u << (2 * st_issue))) | (none << (2 * st_issue));
-    if (lane == at) {
-      uint8_t* to = ring + st_issue * 2 * kBlock;
-      uint64_t* bar = wbars + st_issue;
+    const int owner = in_it & 31;
+    const uint32_t none = __shfl_sync(0xffffffffu, (id[0] < 0 ? 1u : 0u) | (id[1] < 0 ? 2u : 0u), owner);
+    ring_dead = (ring_dead & ~(3u << (2 * st_in))) | (none << (2 * st_in));
+    if (lane == owner) {
+      uint8_t* to = ring + st_in * 2 * kBlock;
+      uint64_t* bar = wbars + st_in;
       const int n = 2 - __popc(none);
       if (n)
         mbar_arrive_expect_tx(bar, n * kBlock);
@@ -191,370 +359,402 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_int4_kernel(const Int4D
         mbar_arrive(bar);
 #pragma unroll
       for (int g = 0; g < 2; ++g)
-        if (id[g] >= 0) bulk_copy_g2s(to + g * kBlock, c.pages + (int64_t(id[g]) * c.n_kv + hk) * kBlock, kBlock, bar);
+        if (id[g] >= 0) bulk_copy_g2s(to + g * kBlock, c.pages + (int64_t(id[g]) * c.n_kv + in_hk) * kBlock, kBlock, bar);
     }
-    st_issue = st_issue + 1 == kStages ? 0 : st_issue + 1;
+    st_in ^= 1;
+    ++in_it;
+    ++flying;
+    return true;
   };
-  int issued = min(n_it, kStages);
-  for (int i = 0; i < issued; ++i) issue(i);
-
-  // Query operands of column gid: head hq0 + gid, scaled by 2^(141 - ex) so
-  // that its largest channel is in [2^14, 2^15).
-  uint32_t qb[2 * W][2];
-  float qs[NGK][2], unscale[2], slope[2];
-  {
-    float q[W][8], top = 0.f;
+  static_assert(kStages == 2, "st_in and st toggle");
+  // column gid's query, asked for before the copies: behind them it came 4 us late
+  uint4 uq[W];
+  auto ask_q = [&](const Segment& s) {
+    const int set = s.h % halves, head = s.h / halves * group + set * kHeads + gid;
+    const uint16_t* row = p.q + s.b * p.q_stride + int64_t(head) * D + 8 * tig;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (gid < heads)
-        u = *reinterpret_cast<const uint4*>(p.q + b * p.q_stride + int64_t(hq0 + gid) * D + 32 * w + 8 * tig);
-      q[w][0] = bf16_lo(u.x), q[w][1] = bf16_hi(u.x), q[w][2] = bf16_lo(u.y), q[w][3] = bf16_hi(u.y);
-      q[w][4] = bf16_lo(u.z), q[w][5] = bf16_hi(u.z), q[w][6] = bf16_lo(u.w), q[w][7] = bf16_hi(u.w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(q[w][i]));
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const int ex = min(max((__float_as_int(top) >> 23) & 255, 14), 243);
-    const float up = pow2i(141 - ex);
-    float sum[NGK];
-#pragma unroll
-    for (int g = 0; g < NGK; ++g) sum[g] = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        q[w][i] *= up;
-        sum[w * NGK / W] += q[w][i];
-      }
-      // k-step 2 w: nibbles (0, 4) and (1, 5); 2 w + 1: (2, 6) and (3, 7);
-      // the odd ones are masked in place and stand for 16 c
-      qb[2 * w][0] = pack_half2(q[w][0], q[w][4]);
-      qb[2 * w][1] = pack_half2(q[w][1] * 0.0625f, q[w][5] * 0.0625f);
-      qb[2 * w + 1][0] = pack_half2(q[w][2], q[w][6]);
-      qb[2 * w + 1][1] = pack_half2(q[w][3] * 0.0625f, q[w][7] * 0.0625f);
-    }
-    const float un = pow2i(ex - 117);     // 2^24 / up
-#pragma unroll
-    for (int g = 0; g < NGK; ++g) {
-      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-      sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-      sum[g] *= 5.9604644775390625e-8f;   // 2^-24, as the codes carry
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {         // to the lanes of columns 2 tig, 2 tig + 1
-      const int from = 4 * (2 * tig + e);
-#pragma unroll
-      for (int g = 0; g < NGK; ++g) qs[g][e] = __shfl_sync(0xffffffffu, sum[g], from);
-      unscale[e] = __shfl_sync(0xffffffffu, un, from);
-      if (p.s.cap_log2 == 0.f) unscale[e] *= p.s.scale_log2;   // (with a cap, capped() takes the scale)
-      slope[e] = p.s.slopes && 2 * tig + e < heads ? p.s.slopes[hq0 + 2 * tig + e] * kLog2e : 0.f;
-    }
+    for (int w = 0; w < W; ++w)
+      uq[w] = gid < min(kHeads, group - set * kHeads) ? *reinterpret_cast<const uint4*>(row + 32 * w) : make_uint4(0, 0, 0, 0);
+  };
+  ask_q(cur);
+  while (flying < kStages && bring()) {
   }
-  const bool cap = p.s.cap_log2 != 0.f;
 
-  // x is in the dot product's own scale, or in log2 units where the score has a
-  // form of its own; us takes it to log2 units, thr is m + 8 / us.
-  float us[2], thr[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) us[e] = Formed ? 1.f : fmaxf(unscale[e], FLT_MIN), thr[e] = -FLT_MAX;
-  float o[2 * W][4], zs[NGV][2], m[2] = {-FLT_MAX, -FLT_MAX}, off[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};
-  int ve = -24;                           // the V scales seen are at most 2^ve
-  float vs_top = pow2i(-24), vs_mul = pow2i(31);   // 2^(7 - ve): p s_V 2^(7 - ve) <= 2^15
-#pragma unroll
-  for (int t = 0; t < 2 * W; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
-#pragma unroll
-  for (int g = 0; g < NGV; ++g) zs[g][0] = zs[g][1] = 0.f;
-
-  int it = 0, st = 0;
+  int st = 0;
   uint32_t parity = 0;
-  int tok = (begin + 2 * warp) * kInt4Page;
-  for (; it < issued; ++it) {
-    if (!__all_sync(0xffffffffu, mbar_try_wait(wbars + st, parity)) &&
-        !__all_sync(0xffffffffu, mbar_wait_bounded(wbars + st, parity, kDefaultWaitNs)))
-      break;
-    const uint8_t* blk = ring + st * 2 * kBlock;
-    // S: rows gid and gid + 8 of each page are tokens, columns 2 tig and 2 tig + 1 heads
-    float y[4][2], vp[4][NGV][2];
-#pragma unroll
-    for (int g2 = 0; g2 < 2; ++g2) {
-      const uint8_t* page = blk + g2 * kBlock;
-      float acc[NGK][4];
-#pragma unroll
-      for (int g = 0; g < NGK; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
-      uint32_t k0[W], k1[W];
-      lds_n(k0, page + gid * (D / 2) + tig * (4 * W));
-      lds_n(k1, page + (gid + 8) * (D / 2) + tig * (4 * W));
+  int has_part = 0;                       // bits: of a run that began before this share, of one that goes on behind it
+  while (true) {
+    const int hk = cur.h / halves, set = cur.h % halves, heads = min(kHeads, group - set * kHeads);
+    const int hq0 = hk * group + set * kHeads, lo = cur.lo + 2 * place(cur);
+    const int n_it = max(0, (cur.hi - lo + 2 * kWarps - 1) / (2 * kWarps));
+
+    // Query operands of column gid: head hq0 + gid, scaled by 2^(141 - ex) so
+    // that its largest channel is in [2^14, 2^15).
+    uint32_t qb[2 * W][2];
+    float qs[NGK][2], unscale[2], slope[2];
+    {
+      float q[W][8], top = 0.f;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        mma(acc[w * NGK / W], k0[w] & kLow, k1[w] & kLow, k0[w] & kHigh, k1[w] & kHigh, qb[2 * w][0], qb[2 * w][1]);
-        const uint32_t a = k0[w] >> 8, d = k1[w] >> 8;
-        mma(acc[w * NGK / W], a & kLow, d & kLow, a & kHigh, d & kHigh, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        q[w][0] = bf16_lo(uq[w].x), q[w][1] = bf16_hi(uq[w].x), q[w][2] = bf16_lo(uq[w].y), q[w][3] = bf16_hi(uq[w].y);
+        q[w][4] = bf16_lo(uq[w].z), q[w][5] = bf16_hi(uq[w].z), q[w][6] = bf16_lo(uq[w].w), q[w][7] = bf16_hi(uq[w].w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(q[w][i]));
+      }
+      top = max_over_quad(top);
+      const int ex = min(max((__float_as_int(top) >> 23) & 255, 14), 243);
+      const float up = pow2i(141 - ex);
+      float sum[NGK];
+#pragma unroll
+      for (int g = 0; g < NGK; ++g) sum[g] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          q[w][i] *= up;
+          sum[w * NGK / W] += q[w][i];
+        }
+        // k-step 2 w: nibbles (0, 4) and (1, 5); 2 w + 1: (2, 6) and (3, 7);
+        // the odd ones are masked in place and stand for 16 c
+        qb[2 * w][0] = pack_half2(q[w][0], q[w][4]);
+        qb[2 * w][1] = pack_half2(q[w][1] * 0.0625f, q[w][5] * 0.0625f);
+        qb[2 * w + 1][0] = pack_half2(q[w][2], q[w][6]);
+        qb[2 * w + 1][1] = pack_half2(q[w][3] * 0.0625f, q[w][7] * 0.0625f);
+      }
+      const float un = pow2i(ex - 117);     // 2^24 / up
+#pragma unroll
+      for (int g = 0; g < NGK; ++g) {
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+        sum[g] *= 5.9604644775390625e-8f;   // 2^-24, as the codes carry
       }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t pr[NGK + NGV];
-        lds_n(pr, page + kPairs + 4 * (NGK + NGV) * (gid + 8 * r));
+      for (int e = 0; e < 2; ++e) {         // to the lanes of columns 2 tig, 2 tig + 1
+        const int from_lane = 4 * (2 * tig + e);
 #pragma unroll
-        for (int g = 0; g < NGK; ++g) {
-          const float2 sz = half2_to_float2(pr[g]);
+        for (int g = 0; g < NGK; ++g) qs[g][e] = __shfl_sync(0xffffffffu, sum[g], from_lane);
+        unscale[e] = __shfl_sync(0xffffffffu, un, from_lane);
+        if (p.s.cap_log2 == 0.f) unscale[e] *= p.s.scale_log2;   // (with a cap, capped() takes the scale)
+        slope[e] = Formed && p.s.slopes && 2 * tig + e < heads ? p.s.slopes[hq0 + 2 * tig + e] * kLog2e : 0.f;
+      }
+    }
+
+    // x is in the dot product's own scale, or in log2 units where the score has a
+    // form of its own; us takes it to log2 units, thr is m + 8 / us, off 7 - m us:
+    // the weights are 2^(7 + t - m) <= 2^15.
+    float us[2], thr[2], m[2] = {-FLT_MAX, -FLT_MAX}, off[2] = {0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float z = g ? fmaf(sz.y, qs[g][e], y[2 * g2 + r][e]) : sz.y * qs[g][e];
-            y[2 * g2 + r][e] = fmaf(sz.x, acc[g][2 * r + e], z);
+    for (int e = 0; e < 2; ++e) us[e] = Formed ? 1.f : fmaxf(unscale[e], FLT_MIN), thr[e] = -FLT_MAX;
+    // rows: channels 32 w + 4 gid + (0, 1 | 2, 3); of zl: g < NGV the zeros' sums
+    // of group g, NGV the weights' sum.  Columns: heads 2 tig, 2 tig + 1.
+    float o[2 * W][4], zl[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 2 * W; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    int ve = -14;                           // the V scales seen are at most 2^ve
+    uint32_t vs_top = 0x0400u, vs_mul = 0x74007400u;   // 2^ve, and 2^-ve twice, in fp16
+    const uint32_t z_keep = gid < NGV ? 0xffffffffu : 0u, z_one = gid == NGV ? 0x3C003C00u : 0u;
+
+    int tok = lo * kInt4Page;
+    for (int it = 0; it < n_it && !dead; ++it) {
+      if (!__all_sync(0xffffffffu, mbar_try_wait(wbars + st, parity)) &&
+          !__all_sync(0xffffffffu, mbar_wait_bounded(wbars + st, parity, kDefaultWaitNs))) {
+        // a copy did not land in time: nothing more is brought in, and what is in
+        // flight is still waited for before its shared memory goes
+        if (lane == 0 && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_TIMEOUT);
+        dead = true;
+        for (; flying > 0; --flying) {
+          mbar_wait_bounded(wbars + st, parity, kDrainWaitNs);
+          st ^= 1;
+          parity ^= st == 0;
+        }
+        __syncwarp();
+        break;
+      }
+      const uint8_t* blk = ring + st * 2 * kBlock;
+      // S: rows gid and gid + 8 of each page are tokens, columns 2 tig and 2 tig + 1 heads
+      float y[4][2];
+#pragma unroll
+      for (int g2 = 0; g2 < 2; ++g2) {
+        const uint8_t* page = blk + g2 * kBlock;
+        float acc[NGK][4];
+#pragma unroll
+        for (int g = 0; g < NGK; ++g) acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+        uint32_t k0[W], k1[W];
+        lds_n(k0, page + gid * (D / 2) + tig * (4 * W));
+        lds_n(k1, page + (gid + 8) * (D / 2) + tig * (4 * W));
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          mma(acc[w * NGK / W], k0[w] & kLow, k1[w] & kLow, k0[w] & kHigh, k1[w] & kHigh, qb[2 * w][0], qb[2 * w][1]);
+          const uint32_t a = k0[w] >> 8, d = k1[w] >> 8;
+          mma(acc[w * NGK / W], a & kLow, d & kLow, a & kHigh, d & kHigh, qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint8_t* pr = page + kPairs + 4 * NG * (gid + 8 * r);
+          uint32_t kw[NGK];
+          if constexpr (NG % 4 == 0 && NGK % 4 == 0 || NG % 2 == 0 && NGK == 2 || NGK == 1) {
+            lds_n(kw, pr);
+          } else {
+#pragma unroll
+            for (int g = 0; g < NGK; ++g) kw[g] = reinterpret_cast<const uint32_t*>(pr)[g];
+          }
+#pragma unroll
+          for (int g = 0; g < NGK; ++g) {
+            const float2 sz = half2_to_float2(kw[g]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float z = g ? fmaf(sz.y, qs[g][e], y[2 * g2 + r][e]) : sz.y * qs[g][e];
+              y[2 * g2 + r][e] = fmaf(sz.x, acc[g][2 * r + e], z);
+            }
           }
         }
+      }
+      // the values' scales and zeros of tokens 8 i + 2 tig, + 1
+      uint32_t vs[4][NGV], vz[4], smax = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* pp = blk + (i >> 1) * kBlock + kPairs + 4 * NG * (8 * (i & 1) + 2 * tig);
+        uint32_t pr[2 * NG];
+        lds_n(pr, pp);
 #pragma unroll
         for (int g = 0; g < NGV; ++g) {
-          const float2 sz = half2_to_float2(pr[NGK + g]);
-          vp[2 * g2 + r][g][0] = sz.x, vp[2 * g2 + r][g][1] = sz.y;
+          vs[i][g] = prmt(pr[NGK + g], pr[NG + NGK + g], 0x5410);
+          smax = __vmaxu2(smax, vs[i][g]);  // (fp16 values >= 0 order as integers)
+        }
+        if constexpr (NGV == 1) {
+          vz[i] = prmt(pr[NGK], pr[NG + NGK], 0x7632);
+        } else {                            // group gid's, for the row that sums it
+          const uint32_t* zp = reinterpret_cast<const uint32_t*>(pp) + NGK + (gid & (NGV - 1));
+          vz[i] = prmt(zp[0], zp[NG], 0x7632);
         }
       }
-    }
-    if (Formed) {
+      if (Formed) {
+        if (p.s.cap_log2 != 0.f) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) y[r][e] = capped(y[r][e] * unscale[e], p.s);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) y[r][e] *= unscale[e];
+        }
+        if (p.s.slopes) {
+          const float away = float(tok + gid - (cur.len - 1));
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) y[r][e] = fmaf(slope[e], away + float(8 * r), y[r][e]);
+        }
+      }
+      const uint32_t gone = (ring_dead >> (2 * st)) & 3u;
+      if (gone || tok < cur.first || tok + 2 * kInt4Page > cur.len) {
+        // what a stale slot holds is anything
+        smax = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool out_of = (gone >> (i >> 1)) & 1u;
+          const int j = tok + 8 * i + gid, j2 = tok + 8 * i + 2 * tig;
+          if (out_of || j < cur.first || j >= cur.len) y[i][0] = y[i][1] = -INFINITY;
+          uint32_t keep = 0;
+          if (!out_of && j2 >= cur.first && j2 < cur.len) keep |= 0x0000FFFFu;
+          if (!out_of && j2 + 1 >= cur.first && j2 + 1 < cur.len) keep |= 0xFFFF0000u;
+          vz[i] &= keep;
+#pragma unroll
+          for (int g = 0; g < NGV; ++g) {
+            vs[i][g] &= keep;
+            smax = __vmaxu2(smax, vs[i][g]);
+          }
+        }
+      }
+      const float y0 = fmaxf(fmaxf(y[0][0], y[1][0]), fmaxf(y[2][0], y[3][0]));
+      const float y1 = fmaxf(fmaxf(y[0][1], y[1][1]), fmaxf(y[2][1], y[3][1]));
+      if (__any_sync(0xffffffffu, (y0 > thr[0]) | (y1 > thr[1]) | ((smax & 0xFFFFu) > vs_top) | ((smax >> 16) > vs_top))) {
+        const float2 two = half2_to_float2(smax);
+        // 2^e >= top for the exponent e of top plus one
+        const float top = max_over_quad(fmaxf(two.x, two.y));
+        const int ne = min(max(ve, ((__float_as_int(top) >> 23) & 255) - 126), 16);
+        const float fv = pow2i(ve - ne);
+        ve = ne;
+        vs_top = ve < 16 ? uint32_t(ve + 15) << 10 : 0xFFFFu;
+        vs_mul = uint32_t(__half_as_ushort(__float2half_rn(pow2i(-ve)))) * 0x10001u;
+        float f[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x = y[r][e] * unscale[e];
-          y[r][e] = fmaf(slope[e], float(tok + gid + 8 * r - (len - 1)), cap ? capped(x, p.s) : x);
+          const float mn = fmaxf(m[e], max_over_rows(e ? y1 : y0));
+          f[e] = exp2_fast((m[e] - mn) * us[e]);
+          m[e] = mn;
+          off[e] = 7.f - mn * us[e];
+          thr[e] = mn + 8.f / us[e];
+          zl[e] *= f[e];
+          f[e] *= fv;
         }
-    }
-    const uint32_t gone = (ring_dead >> (2 * st)) & 3u;
-    if (gone || tok < first || tok + 2 * kInt4Page > len) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int j = tok + gid + 8 * r;
-        if (j < first || j >= len || ((gone >> (r >> 1)) & 1u)) {
-          y[r][0] = y[r][1] = -INFINITY;
-#pragma unroll
-          for (int g = 0; g < NGV; ++g) vp[r][g][0] = vp[r][g][1] = 0.f;   // a stale slot may hold anything
-        }
-      }
-    }
-    bool grow = false;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      grow = grow | (y[r][0] > thr[0]) | (y[r][1] > thr[1]);
-#pragma unroll
-      for (int g = 0; g < NGV; ++g) grow = grow | (vp[r][g][0] > vs_top);
-    }
-    if (__any_sync(0xffffffffu, grow)) {
-      float top = 0.f;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int g = 0; g < NGV; ++g) top = fmaxf(top, vp[r][g][0]);
-      top = max_over_rows(top);
-      // 2^e >= top for the exponent e of top plus one
-      const int ne = max(ve, ((__float_as_int(top) >> 23) & 255) - 126);
-      const float fv = ne - ve < 126 ? pow2i(ve - ne) : 0.f;
-      ve = ne;
-      vs_top = pow2i(ve);
-      vs_mul = pow2i(7 - ve);
-      float f[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(m[e], max_over_rows(fmaxf(fmaxf(y[0][e], y[1][e]), fmaxf(y[2][e], y[3][e]))));
-        f[e] = exp2_fast((m[e] - mn) * us[e]);
-        m[e] = mn;
-        off[e] = -mn * us[e];
-        thr[e] = mn + 8.f / us[e];
-        l[e] *= f[e];
-#pragma unroll
-        for (int g = 0; g < NGV; ++g) zs[g][e] *= f[e];
-        f[e] *= fv;
+        for (int t = 0; t < 2 * W; ++t) o[t][0] *= f[0], o[t][1] *= f[1], o[t][2] *= f[0], o[t][3] *= f[1];
       }
 #pragma unroll
-      for (int t = 0; t < 2 * W; ++t) o[t][0] *= f[0], o[t][1] *= f[1], o[t][2] *= f[0], o[t][3] *= f[1];
-    }
+      for (int g2 = 0; g2 < 2; ++g2) {
+        uint32_t pw[2];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 2; ++r)
+          pw[r] = movmatrix_trans(pack_half2(exp2_fast(fmaf(y[2 * g2 + r][0], us[0], off[0])),
+                                             exp2_fast(fmaf(y[2 * g2 + r][1], us[1], off[1]))));
+        mma(zl, (vz[2 * g2] & z_keep) | z_one, 0u, (vz[2 * g2 + 1] & z_keep) | z_one, 0u, pw[0], pw[1]);
+        // O: rows are channels; depth = tokens 2 tig, 2 tig + 1 (and + 8)
+        const uint8_t* page = blk + g2 * kBlock;
+        uint32_t v0[W], v1[W];
+        lds_n(v0, page + 8 * D + (8 * tig + gid) * (4 * W));
+        lds_n(v1, page + 8 * D + (8 * (tig + 4) + gid) * (4 * W));
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        y[r][e] = exp2_fast(fmaf(y[r][e], us[e], off[e]));
-        l[e] += y[r][e];
+        for (int g = 0; g < NGV; ++g) {
+          const uint32_t s0 = mul_half2(pw[0], mul_half2(vs[2 * g2][g], vs_mul));
+          const uint32_t s1 = mul_half2(pw[1], mul_half2(vs[2 * g2 + 1][g], vs_mul));
 #pragma unroll
-        for (int g = 0; g < NGV; ++g) zs[g][e] = fmaf(y[r][e], vp[r][g][1], zs[g][e]);
-      }
-    // O: rows are channels; k = tokens 2 tig, 2 tig + 1 (and + 8)
-#pragma unroll
-    for (int g2 = 0; g2 < 2; ++g2) {
-      const uint8_t* page = blk + g2 * kBlock;
-      uint32_t v0[W], v1[W];
-      lds_n(v0, page + 8 * D + (8 * tig + gid) * (4 * W));
-      lds_n(v1, page + 8 * D + (8 * (tig + 4) + gid) * (4 * W));
-#pragma unroll
-      for (int g = 0; g < NGV; ++g) {
-        const float s0 = vp[2 * g2][g][0] * vs_mul, s1 = vp[2 * g2 + 1][g][0] * vs_mul;
-        const uint32_t b0 = movmatrix_trans(pack_half2(y[2 * g2][0] * s0, y[2 * g2][1] * s0));
-        const uint32_t b1 = movmatrix_trans(pack_half2(y[2 * g2 + 1][0] * s1, y[2 * g2 + 1][1] * s1));
-#pragma unroll
-        for (int w = g * W / NGV; w < (g + 1) * W / NGV; ++w) {
-          mma(o[2 * w], v0[w] & kLow, v0[w] & kHigh, v1[w] & kLow, v1[w] & kHigh, b0, b1);
-          const uint32_t a = v0[w] >> 8, d = v1[w] >> 8;
-          mma(o[2 * w + 1], a & kLow, a & kHigh, d & kLow, d & kHigh, b0, b1);
+          for (int w = g * W / NGV; w < (g + 1) * W / NGV; ++w) {
+            mma(o[2 * w], v0[w] & kLow, v0[w] & kHigh, v1[w] & kLow, v1[w] & kHigh, s0, s1);
+            const uint32_t a = v0[w] >> 8, d = v1[w] >> 8;
+            mma(o[2 * w + 1], a & kLow, a & kHigh, d & kLow, d & kHigh, s0, s1);
+          }
         }
       }
+      __syncwarp();                         // the stage has been read
+      --flying;
+      bring();
+      tok += 2 * kWarps * kInt4Page;
+      st ^= 1;
+      parity ^= st == 0;
     }
-    __syncwarp();                         // the stage has been read
-    if (issued < n_it) issue(issued++);
-    tok += 2 * kWarps * kInt4Page;
-    if (++st == kStages) st = 0, parity ^= 1;
-  }
-  if (it < issued) {
-    // a copy did not land in time: nothing more is issued, and what is in
-    // flight is still waited for before its shared memory goes
-    if (lane == 0 && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_TIMEOUT);
-    for (int i = max(it, issued - kStages); i < issued; ++i)
-      mbar_wait_bounded(wbars + i % kStages, (i / kStages) & 1, kDrainWaitNs);
-    __syncwarp();
-  }
 
-  // the warps' states in shared memory, over the rings
-  __syncthreads();
-  float* buf = reinterpret_cast<float*>(smem);
-  const float un = pow2i(17 + ve);        // 2^24 of the codes, 2^(ve - 7) of the scales
+    if (more) ask_q(sm_next[warp]);
+    // The warps' states of this segment, kJoinHeads heads at a time.  (All with
+    // the weights' 2^7; a warp without a token has l = 0, whatever its m.)
+    const float un = pow2i(24 + ve);        // 2^24 of the codes, 2^ve of the scales
+    float z[NGV][2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int h = 2 * tig + e;
-    const float lt = sum_over_rows(l[e]);
-    float z[NGV];
+    for (int e = 0; e < 2; ++e) {
+      const float l = __shfl_sync(0xffffffffu, zl[e], 4 * NGV + tig);
+      if (gid == 0) sm_m[warp][2 * tig + e] = m[e] * us[e], sm_l[warp][2 * tig + e] = l;
 #pragma unroll
-    for (int g = 0; g < NGV; ++g) z[g] = sum_over_rows(zs[g][e]);
-    if (gid == 0) sm_m[warp][h] = lt > 0.f ? m[e] * us[e] : -FLT_MAX, sm_l[warp][h] = lt;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float zg = z[w * NGV / W];
-      float4 v = make_float4(fmaf(o[2 * w][e], un, zg), fmaf(o[2 * w][2 + e], un * 0.0625f, zg),
-                             fmaf(o[2 * w + 1][e], un, zg), fmaf(o[2 * w + 1][2 + e], un * 0.0625f, zg));
-      *reinterpret_cast<float4*>(buf + (warp * kHeads + h) * D + 32 * w + 4 * gid) = v;
+      for (int g = 0; g < NGV; ++g) z[g][e] = __shfl_sync(0xffffffffu, zl[e], 4 * g + tig);
     }
+    const bool whole = cur.off == 0 && cur.hi - cur.lo == cur.pages;
+    uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+    const int slot = 2 * blockIdx.x + (cur.off == 0);
+    uint16_t* out = p.out + (int64_t(cur.b) * c.n_q + hq0) * D;
+    for (int h0 = 0; h0 < heads; h0 += kJoinHeads) {
+      if (h0) __syncthreads();              // the heads before have been read
+      if (2 * tig >= h0 && 2 * tig < h0 + kJoinHeads) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float zg = z[w * NGV / W][e];
+            *reinterpret_cast<float4*>(buf + (warp * kJoinHeads + 2 * tig + e - h0) * D + 32 * w + 4 * gid) =
+                make_float4(fmaf(o[2 * w][e], un, zg), fmaf(o[2 * w][2 + e], un * 0.0625f, zg),
+                            fmaf(o[2 * w + 1][e], un, zg), fmaf(o[2 * w + 1][2 + e], un * 0.0625f, zg));
+          }
+      }
+      __syncthreads();
+      const int i = threadIdx.x, h = h0 + i / (D / 4);      // 4 channels a thread
+      if (i < kJoinHeads * (D / 4) && h < heads) {
+        float mx = -FLT_MAX, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          if (sm_l[w][h] > 0.f) mx = fmaxf(mx, sm_m[w][h]);
+#pragma unroll 4
+        for (int w = 0; w < kWarps; ++w) {
+          const float l = sm_l[w][h], f = l > 0.f ? exp2_fast(sm_m[w][h] - mx) : 0.f;
+          const float4 x = reinterpret_cast<const float4*>(buf)[w * kJoinHeads * (D / 4) + i];
+          sum = fmaf(f, l, sum);
+          v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+        }
+        if (whole) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          reinterpret_cast<uint2*>(out)[h0 * (D / 4) + i] =
+              make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
+        } else {
+          reinterpret_cast<float4*>(ws + kOffO)[(int64_t(slot) * kHeads + h0) * (D / 4) + i] = v;
+          if (i % (D / 4) == 0) reinterpret_cast<float2*>(ws + kOffMl)[slot * kHeads + h] = make_float2(mx, sum);
+        }
+      }
+    }
+    if (!whole && threadIdx.x == 0) sm_part[cur.off == 0] = {cur.at - cur.off, cur.pages, cur.b, hq0, heads};
+    has_part |= whole ? 0 : 1 << (cur.off == 0);
+    if (!more) break;
+    __syncthreads();                        // the joined states have been read
+    cur = sm_next[warp];
+    __syncwarp();
+    more = advance();
+    in_next = false;
+    if (dead) in_n = in_it;
+    if (!dead)
+      while (flying < kStages && bring()) {
+      }
+  }
+  if (!has_part) return;
+
+  // The runs that this CTA has a part of (the first of its share, the last, or
+  // both): the last of a run's CTAs to come here joins its parts.
+  __syncthreads();
+  if (threadIdx.x < 2 && ((has_part >> threadIdx.x) & 1)) {
+    const Part& r = sm_part[threadIdx.x];
+    const int f = r.run / share;          // the run lies in the shares of CTAs f ..
+    uint32_t* ticket = static_cast<uint32_t*>(p.workspace) + f;
+    const bool last = atom_add_acq_rel_gpu(ticket, 1) == uint32_t((r.run + r.pages - 1) / share - f);
+    if (last) *ticket = 0;                // ready for the next call
+    sm_last[threadIdx.x] = last;
   }
   __syncthreads();
-  // (the request, head set) pair's partial states
-  const int64_t pair = (int64_t(b) * c.n_kv + hk) * plan.halves + set;
-  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
-  float2* ml = reinterpret_cast<float2*>(ws + plan.off_ml) + pair * plan.splits * kHeads;
-  float* po = reinterpret_cast<float*>(ws + plan.off_o) + pair * plan.splits * kHeads * D;
-  uint16_t* out = p.out + (int64_t(b) * c.n_q + hq0) * D;
-  for (int i = threadIdx.x; i < heads * D; i += 32 * kWarps) {
-    const int h = i / D, ch = i % D;
-    float mx = sm_m[0][h], sum = 0.f, v = 0.f;
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sm_m[w][h]);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2_fast(sm_m[w][h] - mx);
-      sum = fmaf(f, sm_l[w][h], sum);
-      v = fmaf(f, buf[(w * kHeads + h) * D + ch], v);
+  for (int which = 0; which < 2; ++which)
+    if (((has_part >> which) & 1) && sm_last[which]) {
+      if (which) __syncthreads();
+      join_parts<D>(p, sm_part[which], share, buf, sm_l[0]);
     }
-    if (splits == 1) {
-      out[i] = __bfloat16_as_ushort(__float2bfloat16_rn(sum > 0.f ? v / sum : 0.f));
-    } else {
-      po[(split * kHeads + h) * D + ch] = v;
-      if (ch == 0) ml[split * kHeads + h] = make_float2(mx, sum);
-    }
-  }
-  if (splits == 1) return;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    uint32_t* ticket = reinterpret_cast<uint32_t*>(ws) + pair;
-    sm_last = atom_add_acq_rel_gpu(ticket, 1) == uint32_t(splits - 1);
-    if (sm_last) *ticket = 0;             // ready for the next call
-  }
-  __syncthreads();
-  if (!sm_last) return;
-  // The last CTA: the parts' weights in shared memory, then 4 channels a
-  // thread; where the heads leave threads over, each takes every n-th part.
-  float* wt = reinterpret_cast<float*>(smem);           // [split][head]
-  for (int i = threadIdx.x; i < splits * kHeads; i += 32 * kWarps)
-    wt[i] = (i % kHeads) < heads ? __ldcg(&ml[i]).x : -FLT_MAX;
-  __syncthreads();
-  {                                                     // warp h: head h
-    float mx = -FLT_MAX, sum = 0.f;
-    for (int s = lane; s < splits; s += 32) mx = fmaxf(mx, wt[s * kHeads + warp]);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-    for (int s = lane; s < splits; s += 32) {
-      const float f = exp2_fast(wt[s * kHeads + warp] - mx);
-      wt[s * kHeads + warp] = f;
-      if (warp < heads) sum = fmaf(f, __ldcg(&ml[s * kHeads + warp]).y, sum);
-    }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    if (lane == 0) sm_l[0][warp] = sum;
-  }
-  __syncthreads();
-  const int units = heads * (D / 4), parts = 32 * kWarps / units, part = threadIdx.x / units, unit = threadIdx.x % units;
-  const int h = unit / (D / 4);
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (part < parts) {
-    const float4* from = reinterpret_cast<const float4*>(po) + unit;
-#pragma unroll 8
-    for (int s = part; s < splits; s += parts) {
-      const float f = wt[s * kHeads + h];
-      const float4 x = __ldcg(from + s * (kHeads * D / 4));
-      v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
-    }
-  }
-  float4* sums = reinterpret_cast<float4*>(wt + splits * kHeads);
-  sums[threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.x < units) {
-    for (int i = 1; i < parts; ++i) {
-      const float4 x = sums[i * units + unit];
-      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-    }
-    const float inv = sm_l[0][h] > 0.f ? 1.f / sm_l[0][h] : 0.f;
-    reinterpret_cast<uint2*>(out)[unit] = make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
-  }
 }
 
 template <int D, int NGK, int NGV, bool Formed>
-cudaError_t launch(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
-  constexpr int block = int4_block_bytes(D, NGK, NGV), ring = kWarps * stages_of(block) * 2 * block;
-  constexpr int join = kWarps * kHeads * D * 4, last = kMostSplits * kHeads * 4 + 32 * kWarps * 16;
-  constexpr int bytes = std::max(ring, std::max(join, last));
+cudaError_t launch(const Int4DecodeParams& p, cudaStream_t stream) {
+  constexpr int bytes = kWarps * kStages * 2 * int4_block_bytes(D, NGK, NGV) + join_bytes<D>();
   const cudaError_t e = set_smem_limit<decode_int4_kernel<D, NGK, NGV, Formed>>(bytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid(unsigned(plan.splits), unsigned(p.c.n_kv * plan.halves), unsigned(p.c.batch));
-  return launch_pdl(decode_int4_kernel<D, NGK, NGV, Formed>, grid, dim3(32 * kWarps), bytes, stream, p, plan);
+  const int halves = (p.c.n_q / p.c.n_kv + kHeads - 1) / kHeads;
+  int64_t tokens = p.c.max_len;
+  if (p.s.window) tokens = std::min<int64_t>(tokens, int64_t(p.s.window) + kInt4Page);
+  const int64_t places = ((tokens + kInt4Page - 1) / kInt4Page + kRunCost) * p.c.batch * p.c.n_kv * halves;
+  if (places > INT32_MAX) return cudaErrorNotSupported;
+  const int64_t ctas = std::min<int64_t>(kCtas, std::max<int64_t>(1, (places + kMinShare + kRunCost - 1) / (kMinShare + kRunCost)));
+  return launch_pdl(decode_int4_kernel<D, NGK, NGV, Formed>, dim3(unsigned(ctas)), dim3(kThreads), bytes, stream, p, halves);
 }
 
 template <int D, int NGK, int NGV>
-cudaError_t launch_f(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
-  return p.s.cap_log2 != 0.f || p.s.slopes ? launch<D, NGK, NGV, true>(p, plan, stream)
-                                           : launch<D, NGK, NGV, false>(p, plan, stream);
+cudaError_t launch_f(const Int4DecodeParams& p, cudaStream_t stream) {
+  return p.s.cap_log2 != 0.f || p.s.slopes ? launch<D, NGK, NGV, true>(p, stream) : launch<D, NGK, NGV, false>(p, stream);
 }
 
 template <int D, int NGK>
-cudaError_t launch_v(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
-  if (p.c.ng_v == 1) return launch_f<D, NGK, 1>(p, plan, stream);
-  if (p.c.ng_v == 2) return launch_f<D, NGK, 2>(p, plan, stream);
-  if constexpr (D == 128) return launch_f<D, NGK, 4>(p, plan, stream);
+cudaError_t launch_v(const Int4DecodeParams& p, cudaStream_t stream) {
+  if (p.c.ng_v == 1) return launch_f<D, NGK, 1>(p, stream);
+  if (p.c.ng_v == 2) return launch_f<D, NGK, 2>(p, stream);
+  if constexpr (D == 128) return launch_f<D, NGK, 4>(p, stream);
   return cudaErrorInvalidValue;
 }
 
 template <int D>
-cudaError_t launch_k(const Int4DecodeParams& p, const SplitPlan& plan, cudaStream_t stream) {
-  if (p.c.ng_k == 1) return launch_v<D, 1>(p, plan, stream);
-  if (p.c.ng_k == 2) return launch_v<D, 2>(p, plan, stream);
-  if constexpr (D == 128) return launch_v<D, 4>(p, plan, stream);
+cudaError_t launch_k(const Int4DecodeParams& p, cudaStream_t stream) {
+  if (p.c.ng_k == 1) return launch_v<D, 1>(p, stream);
+  if (p.c.ng_k == 2) return launch_v<D, 2>(p, stream);
+  if constexpr (D == 128) return launch_v<D, 4>(p, stream);
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t int4_decode_workspace_bytes(const Int4Cache& c, const ScoreParams&, cudaError_t* err) {
-  *err = cudaSuccess;
-  return plan_splits(c, ScoreParams{}).bytes;
-}
+size_t int4_decode_workspace_bytes(const Int4Cache& c) { return kOffO + size_t(kCtas) * 2 * kHeads * c.d * 4; }
 
 cudaError_t launch_decode_int4(const Int4DecodeParams& p, cudaStream_t stream) {
-  const SplitPlan plan = plan_splits(p.c, p.s);
-  return p.c.d == 128 ? launch_k<128>(p, plan, stream) : launch_k<64>(p, plan, stream);
+  return p.c.d == 128 ? launch_k<128>(p, stream) : launch_k<64>(p, stream);
 }
 
 }  // namespace oscar

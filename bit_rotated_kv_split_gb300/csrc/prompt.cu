@@ -638,10 +638,7 @@ cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t s
 
 }  // namespace
 
-size_t prompt_workspace_bytes(const PromptParams& p, cudaError_t* err) {
-  *err = cudaSuccess;
-  return plan_prompt(p).bytes;
-}
+size_t prompt_workspace_bytes(const PromptParams& p) { return plan_prompt(p).bytes; }
 
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   const PromptPlan plan = plan_prompt(p);
