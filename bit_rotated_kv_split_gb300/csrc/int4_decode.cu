@@ -4,9 +4,15 @@
 // and each of 304 lasting CTAs (two per SM) takes an equal share of it: a ragged
 // batch is as even as a uniform one, and only the first and the last run of a
 // share can be incomplete.  Those leave their unnormalised sums in the workspace,
-// and the last CTA of a run to finish joins its parts.  (A grid of one CTA for
-// every 16 pages a warp spent a third of its time in the CTAs' first loads and
-// last sums.)
+// and the last CTA of a run to finish joins its parts.  (A grid of short CTAs, each
+// for 16 pages a warp, took 139 us where this takes 95, the ragged batch above: a
+// third of it went into the CTAs' first loads and last sums.)
+//
+// Bound by: HBM within the scan (100k tokens x 8 KV heads: 109 MB at 6.5 TB/s); the
+// rest of that call's 32 us (16 at the measured copy rate) are the first loads one
+// behind the other (lengths, page ids, pages: 4 us), the warps' and the CTAs' joins
+// (6 us) and the launch.  Code outside the scan is kept small on purpose: run once
+// a CTA, its instructions come from far (unrolled joins cost 8 us).
 //
 // A warp takes every 8th pair of a run's pages with an online softmax of its own,
 // so nothing in the scan waits for another warp.  The pages' blocks come by bulk
@@ -47,11 +53,10 @@ constexpr int kStages = 2;            // ring stages of a warp, each two pages
 constexpr int kCtas = 152 * 2;        // CTAs the GPU holds at a time
 constexpr int kMinShare = 4 * kWarps; // pages
 // A run costs its CTA about as much as this many pages besides its own (the
-// query, the warps' join): a run takes up so many more places in the row.
-#ifndef KRUN
-#define KRUN 64
-#endif
-constexpr int kRunCost = KRUN;
+// query, the warps' join): a run takes up so many more places in the row.  (28
+// ragged requests x 8 KV heads: 105 us with 8, 97 with 32, 95 with 64, 100 with 128;
+// 16 short ones: 19, 17, 17, 22.)
+constexpr int kRunCost = 64;
 constexpr int kJoinHeads = 4;         // heads whose states are joined at a time
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
@@ -177,10 +182,21 @@ __device__ __noinline__ void join_parts(const Int4DecodeParams& p, const Part& r
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = r.heads;
   const int f = r.run / share, n = (r.run + r.pages - 1) / share - f + 1;
   auto slot_of = [&](int i) { return 2 * (f + i) + (i == 0); };
+  // the first sums are asked for before their weights are worked out
+  constexpr int kBatch = 10;
+  const int units = heads * (D / 4), ways = kThreads / units, way = threadIdx.x / units, unit = threadIdx.x % units;
+  const int h = unit / (D / 4);
+  const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
+  auto load = [&](float4 (&x)[kBatch], int i) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) x[k] = __ldcg(from + slot_of(min(i + k * ways, n - 1)) * (kHeads * D / 4));
+  };
+  float4 x[kBatch];
+  load(x, way);
   const float2* ml = reinterpret_cast<const float2*>(ws + kOffMl) + warp;
   if (warp < heads) {                     // warp h: head h
     float mx = -FLT_MAX, sum = 0.f;
-#pragma unroll 1
+#pragma unroll 2
     for (int i = lane; i < n; i += 32) {
       const float2 s = __ldcg(&ml[slot_of(i) * kHeads]);
       const float m = s.y > 0.f ? s.x : -FLT_MAX, mn = fmaxf(mx, m);
@@ -199,16 +215,16 @@ __device__ __noinline__ void join_parts(const Int4DecodeParams& p, const Part& r
     if (lane == 0) sum_of[warp] = sum;
   }
   __syncthreads();
-  const int units = heads * (D / 4), ways = kThreads / units, way = threadIdx.x / units, unit = threadIdx.x % units;
-  const int h = unit / (D / 4);
-  const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (way < ways)
-#pragma unroll 8
-    for (int i = way; i < n; i += ways) {
-      const float g = wt[i * kHeads + h];
-      const float4 x = __ldcg(from + slot_of(i) * (kHeads * D / 4));
-      v.x = fmaf(g, x.x, v.x), v.y = fmaf(g, x.y, v.y), v.z = fmaf(g, x.z, v.z), v.w = fmaf(g, x.w, v.w);
+#pragma unroll 1
+    for (int i = way; i < n; i += kBatch * ways) {
+      if (i != way) load(x, i);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float g = i + k * ways < n ? wt[(i + k * ways) * kHeads + h] : 0.f;
+        v.x = fmaf(g, x[k].x, v.x), v.y = fmaf(g, x[k].y, v.y), v.z = fmaf(g, x[k].z, v.z), v.w = fmaf(g, x[k].w, v.w);
+      }
     }
   float4* sums = reinterpret_cast<float4*>(wt + n * kHeads);
   sums[threadIdx.x] = v;
@@ -304,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (!advance()) return;                 // (nothing but places of a run's cost; the same in all warps)
   Segment cur = sm_next[warp];
   __syncwarp();
-  bool more = advance();
+  bool more = false;                      // sm_next holds another
 
   // The ring.  A warp's pairs of a segment begin with another warp each time,
   // so that short segments spread over the warps.  Lane i knows pairs 32 n + i
@@ -377,6 +393,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       uq[w] = gid < min(kHeads, group - set * kHeads) ? *reinterpret_cast<const uint4*>(row + 32 * w) : make_uint4(0, 0, 0, 0);
   };
   ask_q(cur);
+  while (flying < kStages && bring()) {
+  }
+  more = advance();                       // (the first copies do not wait for it)
   while (flying < kStages && bring()) {
   }
 
