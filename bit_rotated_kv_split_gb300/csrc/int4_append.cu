@@ -307,37 +307,81 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
   }
 }
 
-// One warp per (token, kRows KV heads): K, then V.
+// zero + scale * code of the 8 codes of a word, as bf16.  Codes become halves
+// by a mask (1024 + c is 0x6400 | c) and an exact subtraction: an integer
+// conversion for each would keep the special function unit busy for longer than
+// the loads take.
+__device__ __forceinline__ uint4 values8(uint32_t word, uint32_t pair) {
+  const float2 sz = half2_to_float2(pair);
+  const __half2 k1024 = __floats2half2_rn(1024.f, 1024.f);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {           // nibbles i and i + 4
+    uint32_t h;
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(h) : "r"(word >> (4 * i)));
+    const float2 c = __half22float2(__hsub2(*reinterpret_cast<__half2*>(&h), k1024));
+    x[i] = fmaf(c.x, sz.x, sz.y);
+    x[i + 4] = fmaf(c.y, sz.x, sz.y);
+  }
+  return pack_bf16x8(x);
+}
+
+// A warp takes `slots_per_warp` slots (the KV heads that it holds at a time) of
+// one token, the next slot's loads ahead of the present one's work.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) gather_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(kAppendThreads) gather_kernel(const __grid_constant__ GatherParams p, int slots_per_warp) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31, o = lane % kLanes, sub = lane / kLanes;
-  const int per_token = (p.c.n_kv + kRows - 1) / kRows;
+  const int slots = (p.c.n_kv + kRows - 1) / kRows, warps_per_token = (slots + slots_per_warp - 1) / slots_per_warp;
   const int64_t w = (int64_t(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
-  const int64_t i = w / per_token;
+  const int64_t i = w / warps_per_token;
   if (i >= p.n) return;
-  const int head = int(w % per_token) * kRows + sub;
-  const int pos = p.src_pos[i];
-  const uint8_t* base = token_block(p.c, p.src_req[i], pos, lane == 0 && w % per_token == 0);
-  if (!base || head >= p.c.n_kv) return;
-  const int slot = pos % kInt4Page, ng_k = p.c.ng_k, ng_v = p.c.ng_v;
-  const uint8_t* block = base + int64_t(head) * int4_block_bytes(D, ng_k, ng_v);
-  const uint32_t kw = *reinterpret_cast<const uint32_t*>(block + int4_k_word(D, slot, o));
-  const uint32_t vw = uint32_t(*reinterpret_cast<const uint16_t*>(block + int4_v_half(D, slot, 2 * o))) |
-                      (uint32_t(*reinterpret_cast<const uint16_t*>(block + int4_v_half(D, slot, 2 * o + 1))) << 16);
-#pragma unroll
-  for (int kind = 0; kind < 2; ++kind) {
-    const int q = kind == 0 ? o * ng_k / kLanes : ng_k + o * ng_v / kLanes;
-    const float2 sz = half2_to_float2(*reinterpret_cast<const uint32_t*>(block + int4_pair(D, ng_k, ng_v, slot, q)));
-    const uint32_t word = kind == 0 ? kw : vw;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(float((word >> (4 * e)) & 15u), sz.x, sz.y);
-    uint16_t* out = kind == 0 ? p.k_out + i * p.k_stride : p.v_out + i * p.v_stride;
-    *reinterpret_cast<uint4*>(out + int64_t(head) * D + 8 * o) = pack_bf16x8(x);
+  const int part = int(w - i * warps_per_token), pos = p.src_pos[i];
+  const uint8_t* base = token_block(p.c, p.src_req[i], pos, lane == 0 && part == 0);
+  if (!base) return;
+  const int slot = pos % kInt4Page, ng_k = p.c.ng_k, ng_v = p.c.ng_v, block_bytes = int4_block_bytes(D, ng_k, ng_v);
+  const int begin = part * slots_per_warp, end = min(slots, begin + slots_per_warp);
+  const uint8_t* k_at = base + int4_k_word(D, slot, o);
+  const uint8_t* v_at = base + int4_v_half(D, slot, 2 * o);
+  const uint8_t* kp_at = base + int4_pair(D, ng_k, ng_v, slot, o * ng_k / kLanes);
+  const uint8_t* vp_at = base + int4_pair(D, ng_k, ng_v, slot, ng_k + o * ng_v / kLanes);
+  constexpr int kSecond = int4_v_half(D, 0, 1) - int4_v_half(D, 0, 0);   // from quad 2 o to 2 o + 1
+  struct Raw {
+    uint32_t k, v0, v1, kp, vp;
+  };
+  auto load = [&](int s) {
+    Raw r{};
+    const int head = s * kRows + sub;
+    if (s < end && head < p.c.n_kv) {
+      const int64_t at = int64_t(head) * block_bytes;
+      r.k = *reinterpret_cast<const uint32_t*>(k_at + at);
+      r.v0 = *reinterpret_cast<const uint16_t*>(v_at + at);
+      r.v1 = *reinterpret_cast<const uint16_t*>(v_at + kSecond + at);
+      r.kp = *reinterpret_cast<const uint32_t*>(kp_at + at);
+      r.vp = *reinterpret_cast<const uint32_t*>(vp_at + at);
+    }
+    return r;
+  };
+  uint16_t* k_out = p.k_out + i * p.k_stride + 8 * o;
+  uint16_t* v_out = p.v_out + i * p.v_stride + 8 * o;
+  Raw next = load(begin);
+#pragma unroll 2
+  for (int s = begin; s < end; ++s) {
+    const Raw r = next;
+    next = load(s + 1);
+    const int head = s * kRows + sub;
+    if (head >= p.c.n_kv) continue;
+    *reinterpret_cast<uint4*>(k_out + head * D) = values8(r.k, r.kp);
+    *reinterpret_cast<uint4*>(v_out + head * D) = values8(r.v0 | (r.v1 << 16), r.vp);
   }
+}
+
+// Slots of a token for one warp: as many as leave the GPU 24 warps an SM.  A
+// token's place and angles are then read once, not once a slot.
+int slots_of(int n, int slots) {
+  return int(std::min<int64_t>(slots, std::max<int64_t>(1, int64_t(n) * slots / (152 * 24))));
 }
 
 cudaError_t grid_of(int64_t warps, unsigned* blocks) {
@@ -352,9 +396,7 @@ cudaError_t grid_of(int64_t warps, unsigned* blocks) {
 cudaError_t launch_rope_append_int4(const AppendParams& p, cudaStream_t stream) {
   const int rows = 32 / (p.c.d / 8);
   const int slots = (p.q ? (p.c.n_q + rows - 1) / rows : 0) + 2 * ((p.c.n_kv + rows - 1) / rows);
-  // a warp takes as much of a token as leaves the GPU 24 warps an SM: the
-  // angles and places of a token are then read once, not once a slot
-  const int slots_per_warp = int(std::min<int64_t>(slots, std::max<int64_t>(1, int64_t(p.n) * slots / (152 * 24))));
+  const int slots_per_warp = slots_of(p.n, slots);
   unsigned blocks = 0;
   const cudaError_t e = grid_of(int64_t(p.n) * ((slots + slots_per_warp - 1) / slots_per_warp), &blocks);
   if (e != cudaSuccess) return e;
@@ -364,12 +406,13 @@ cudaError_t launch_rope_append_int4(const AppendParams& p, cudaStream_t stream) 
 }
 
 cudaError_t launch_gather_int4(const GatherParams& p, cudaStream_t stream) {
-  const int rows = 32 / (p.c.d / 8);
+  const int rows = 32 / (p.c.d / 8), slots = (p.c.n_kv + rows - 1) / rows;
+  const int slots_per_warp = slots_of(p.n, slots);
   unsigned blocks = 0;
-  const cudaError_t e = grid_of(int64_t(p.n) * ((p.c.n_kv + rows - 1) / rows), &blocks);
+  const cudaError_t e = grid_of(int64_t(p.n) * ((slots + slots_per_warp - 1) / slots_per_warp), &blocks);
   if (e != cudaSuccess) return e;
-  return p.c.d == 128 ? launch_pdl(gather_kernel<128>, dim3(blocks), dim3(kAppendThreads), 0, stream, p)
-                      : launch_pdl(gather_kernel<64>, dim3(blocks), dim3(kAppendThreads), 0, stream, p);
+  return p.c.d == 128 ? launch_pdl(gather_kernel<128>, dim3(blocks), dim3(kAppendThreads), 0, stream, p, slots_per_warp)
+                      : launch_pdl(gather_kernel<64>, dim3(blocks), dim3(kAppendThreads), 0, stream, p, slots_per_warp);
 }
 
 }  // namespace oscar
