@@ -57,6 +57,9 @@ constexpr int kMinShare = 4 * kWarps; // pages
 // ragged requests x 8 KV heads: 105 us with 8, 97 with 32, 95 with 64, 100 with 128;
 // 16 short ones: 19, 17, 17, 22.)
 constexpr int kRunCost = 64;
+// A run of no more pages is not split: it goes whole to the CTA whose share holds
+// its first page.  (Joining parts takes about as long as scanning these.)
+constexpr int kWhole = 64;
 constexpr int kJoinHeads = 4;         // heads whose states are joined at a time
 constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
 
@@ -145,9 +148,10 @@ struct Walk {
   Span span;            // of request b
   __device__ __forceinline__ bool next(const Int4DecodeParams& p, int sets, Segment* s) {
     int pages = span.pages();
-    if (off >= pages && at < end) step(p, sets), pages = span.pages();   // (the share begins behind a run's pages)
+    // the share begins behind a run's pages, or within a run that is another's whole
+    if (at < end && off > 0 && (off >= pages || pages <= kWhole)) step(p, sets), pages = span.pages();
     if (at >= end) return false;
-    const int n = min(pages - off, end - at), lo = span.page0() + off;
+    const int n = pages <= kWhole ? pages : min(pages - off, end - at), lo = span.page0() + off;
     *s = {b, h, lo, lo + n, off, pages, span.len, span.first, at};
     off += n;
     at += n;
