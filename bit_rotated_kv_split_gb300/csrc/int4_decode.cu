@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (w < warp) before += sm_scan[w];
     total += sm_scan[w];
   }
-  const int share = max(kMinShare + kRunCost, int((unsigned(total) + gridDim.x - 1) / gridDim.x));
+  const int share = max(kMinShare, int((unsigned(total) + gridDim.x - 1) / gridDim.x));
   const int64_t start = int64_t(share) * blockIdx.x;
   const bool any = start < total;
   if (any && start >= before && start - before < mine) {
@@ -747,7 +747,7 @@ cudaError_t launch(const Int4DecodeParams& p, cudaStream_t stream) {
   if (p.s.window) tokens = std::min<int64_t>(tokens, int64_t(p.s.window) + kInt4Page);
   const int64_t places = ((tokens + kInt4Page - 1) / kInt4Page + kRunCost) * p.c.batch * p.c.n_kv * halves;
   if (places > INT32_MAX) return cudaErrorNotSupported;
-  const int64_t ctas = std::min<int64_t>(kCtas, std::max<int64_t>(1, (places + kMinShare + kRunCost - 1) / (kMinShare + kRunCost)));
+  const int64_t ctas = std::min<int64_t>(kCtas, (places + kMinShare - 1) / kMinShare);
   return launch_pdl(decode_int4_kernel<D, NGK, NGV, Formed>, dim3(unsigned(ctas)), dim3(kThreads), bytes, stream, p, halves);
 }
 

@@ -76,6 +76,27 @@ def int4_store(pool: np.ndarray, page: int, slot: int, which: int, codes, s, z, 
             block[o:o + 4] = np.array([s[h, g], z[h, g]], np.float16).view(np.uint8)
 
 
+def int4_store_rows(pool: np.ndarray, pages, slots, which: int, codes, s, z, ng_k: int, ng_v: int) -> None:
+    """Tokens at (pages[i], slots[i]), distinct: codes [T][n_kv][d], s and z [T][n_kv][groups]."""
+    t, h, d = codes.shape
+    if t == 0:
+        return
+    pages, slots = np.asarray(pages)[:, None, None], np.asarray(slots)
+    head = np.arange(h)[None, :, None]
+    at, sh = _nibble(d, which, slots[:, None], np.arange(d)[None])
+    sh = np.broadcast_to(sh, (t, d))
+    for low in (True, False):               # a byte's two nibbles one after the other
+        pick = sh[0] == (0 if low else 4)
+        a, c = at[:, None, pick], codes[:, :, pick]
+        old = pool[pages, head, a]
+        pool[pages, head, a] = (old & 0xF0) | c if low else (old & 0x0F) | (c << 4)
+    for g in range(s.shape[2]):
+        o = _pair(d, ng_k, ng_v, which, slots, g)[:, None]
+        raw = np.stack([s[:, :, g], z[:, :, g]], -1).astype(np.float16).view(np.uint8)
+        for i in range(4):
+            pool[pages[:, :, 0], head[:, :, 0], o + i] = raw[..., i]
+
+
 def int4_load(pool: np.ndarray, pages, slots, which: int, d: int, ng_k: int, ng_v: int):
     """(codes [T][n_kv][d], s, z [T][n_kv][groups]) of the tokens at (pages[i], slots[i])."""
     ng = ng_v if which else ng_k

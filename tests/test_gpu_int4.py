@@ -79,8 +79,8 @@ class Layer:
         """Quantises and stores rows [n][hk][d] at positions pos; returns what they stand for."""
         ng = self.ngv if which else self.ngk
         c, s, z = O.int4_quantize(rows, self.d // ng, self.cache.tau_k)
-        for i, p in enumerate(pos):
-            O.int4_store(self.pool, self.table[b, p // 16], p % 16, which, c[i], s[i], z[i], self.ngk, self.ngv)
+        pos = np.asarray(pos, dtype=np.int64)
+        O.int4_store_rows(self.pool, self.table[b, pos // 16], pos % 16, which, c, s, z, self.ngk, self.ngv)
         return O.int4_values(c, s, z)
 
     def gpu_pool(self):
@@ -286,6 +286,35 @@ def test_decode_matches_oracle(lens, hq, hk, d, gk, gv, mods):
     assert (err <= bound).all(), "worst %.3g of its bound" % np.nanmax(err / np.maximum(bound, 1e-30))
     assert bool((out.view(torch.int16) == again.view(torch.int16)).all())
     assert L.status() == 0
+
+
+RAGGED = [
+    # lens of many requests: runs that are whole, split over several CTAs, empty, of one token
+    ([0, 3, 0, 0, 17] * 60 + [900, 0, 1, 2100, 64, 65], 2, 1, 64, 64, 32, {}),          # more requests than threads
+    ([9000, 5, 0, 7000, 1025, 1024, 1023, 1039, 2], 4, 2, 64, 32, 64, {}),
+    ([30000, 1, 12000], 12, 1, 64, 64, 64, dict(softcap=9.0)),                           # two head sets
+    ([40000], 8, 8, 64, 64, 64, dict(window=20001)),
+    ([6000, 6000, 6001, 5999, 1, 6000], 8, 2, 128, 128, 64, dict(window=1500, slopes=True)),
+]
+
+
+@pytest.mark.parametrize("lens,hq,hk,d,gk,gv,mods", RAGGED)
+def test_decode_ragged_batches(lens, hq, hk, d, gk, gv, mods):
+    test_decode_matches_oracle(lens, hq, hk, d, gk, gv, mods)
+
+
+def test_workspace_shared_by_calls_of_different_sizes():
+    """One workspace for layers and batches of all sizes, one call after the other (it is zero-filled once)."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    shapes = [([5000, 300], 8, 2, 128, 128, 128), ([1] * 400, 2, 1, 64, 64, 64), ([2500] * 9, 16, 2, 128, 32, 64),
+              ([20000], 4, 1, 64, 32, 32), ([3000, 0, 700], 24, 8, 128, 64, 128)]
+    Ls = [Layer(60 + i, *s) for i, s in enumerate(shapes)]
+    ws = torch.zeros(max(B.oscar_decode_int4_workspace_bytes(L.desc) for L in Ls), dtype=torch.uint8, device="cuda")
+    qs = [O.bf16(L.g.standard_normal((len(L.lens), L.hq, L.d))) for L in Ls]
+    for L, q in list(zip(Ls, qs)) * 2:
+        ref, bound = decode_ref(L, q)
+        assert (np.abs(host(run_decode(L, dev_bf16(q), ws=ws)) - ref) <= bound).all()
 
 
 def test_decode_peaked_and_far_scores():

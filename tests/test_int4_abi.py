@@ -56,6 +56,9 @@ def test_oracle_layout_covers_each_nibble_once(d, gk, gv):
         np.testing.assert_array_equal(c, c2)
         np.testing.assert_array_equal(s, s2)
         np.testing.assert_array_equal(z, z2)
+        rows = g.integers(0, 256, pool.shape).astype(np.uint8)
+        O.int4_store_rows(rows, [2] * 16, np.arange(16), which, c, s, z, ngk, ngv)
+        np.testing.assert_array_equal(O.int4_load(rows, [2] * 16, np.arange(16), which, d, ngk, ngv)[0], c)
 
 
 BAD_CACHE = [
