@@ -569,7 +569,7 @@ typedef struct oscar_rope_desc {
 /* What becomes of a score before the softmax.  For query position i and key
  * position j: t = scale (q . k); softcap > 0: t = softcap tanh(t / softcap);
  * slopes: t -= slopes[h] |i - j|; window > 0: keys with i - j >= window are
- * masked. */
+ * masked.  Scores may be as large as 2^22 in magnitude. */
 typedef struct oscar_score_desc {
   float scale;                /* > 0 and finite; 0 = 1 / sqrt(head_dim)         */
   float softcap;              /* > 0 and finite; 0 = none                       */
@@ -601,7 +601,7 @@ int64_t oscar_int4_block_bytes(int32_t head_dim, int32_t quant_group_k, int32_t 
  *   k' is rounded from its exact value (codes do not depend on how the
  *   rotation is computed); q' is within one rounding of fp32 sums.  A NaN
  *   is quantised as -tau; other rows are not affected.
- *   dst_req[i] = -1 marks a padding row: nothing of it is read or written.
+ *   dst_req[i] = -1 marks a padding row: nothing of it is written.
  *   Any other request outside the batch, a position beyond the page table
  *   or a rotation row outside cos_sin skips the item and sets
  *   OSCAR_DEV_LENGTH; a page id outside the pool skips it and sets
@@ -611,7 +611,8 @@ int64_t oscar_int4_block_bytes(int32_t head_dim, int32_t quant_group_k, int32_t 
  *   dst_req, dst_pos, rope_pos: device int32 [n].  Rows 16-byte aligned,
  *   strides multiples of 8 elements and at least one row.  seq_len is not
  *   read: the caller advances it.  Items must name distinct (request,
- *   position) pairs.  n = 0 is a no-op.  Async.
+ *   position) pairs.  Outputs may share memory with inputs only as said
+ *   above.  n = 0 is a no-op.  Async.
  */
 oscar_status oscar_rope_append_int4(const oscar_int4_desc* desc, const oscar_rope_desc* rope,
                                     const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
@@ -648,11 +649,15 @@ oscar_status oscar_gather_int4(const oscar_int4_desc* desc, const int32_t* src_r
  *   slots past seq_len may hold anything.  A length above max_len is
  *   clamped and sets OSCAR_DEV_LENGTH, a negative one counts as 0 and sets
  *   it; a page outside the pool is skipped and sets OSCAR_DEV_PAGE_BOUNDS.
+ *   A copy that does not land within 1 s sets OSCAR_DEV_TIMEOUT (the output
+ *   must not be used then).  Groups above 16, or more than 2^31 pages over all
+ *   requests and KV heads at max_len: OSCAR_ERR_UNSUPPORTED.  out must not
+ *   overlap q.  The result does not depend on scheduling.
  *
- *   Workspace as for oscar_decode_attention: NULL asks for the size; 256-byte
+ *   Workspace: NULL asks for the size (it depends on head_dim alone); 256-byte
  *   aligned, zero-filled before its first use; each call leaves it ready for
- *   the next; calls that may overlap (other streams, two graphs replayed at
- *   once) need workspaces of their own.  Async.
+ *   the next, of whatever sizes; calls that may overlap (other streams, two
+ *   graphs replayed at once) need workspaces of their own.  Async.
  */
 oscar_status oscar_decode_attention_int4(const oscar_int4_desc* desc, const oscar_score_desc* score,
                                          const uint16_t* q, int64_t q_stride, uint16_t* out, void* workspace,
@@ -696,10 +701,12 @@ typedef struct oscar_prompt_desc {
  *   were; rows of k and v outside a request never reach it, whatever they
  *   hold.  A request's own rows must be finite.  Lengths above max_q / max_k
  *   or rows outside total_q / total_k are clamped and set OSCAR_DEV_LENGTH.
+ *   A wait within the kernel that runs out (1 s) sets OSCAR_DEV_TIMEOUT (the
+ *   output must not be used then).  out must not overlap q, k or v.  The result
+ *   does not depend on scheduling.
  *
- *   Workspace: NULL asks for the size (which depends on desc and the current
- *   device); otherwise 256-byte aligned, zero-filled before its first use;
- *   each call leaves it ready for the next; calls that may overlap need
+ *   Workspace: NULL asks for the size (it depends on desc); otherwise 256-byte
+ *   aligned device memory, of any content; calls that may overlap need
  *   workspaces of their own.  Async.
  */
 oscar_status oscar_prompt_attention(const oscar_prompt_desc* desc, const oscar_score_desc* score,

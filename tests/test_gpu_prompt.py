@@ -33,9 +33,10 @@ def i32(x):
     return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
 
 
-def run(case_seed, nq, nk, hq, hk, d, causal=True, prefix=None, gap=0, lead=0, packed=False, check=True, **mods):
+def run(case_seed, nq, nk, hq, hk, d, causal=True, prefix=None, gap=0, packed=False, slack=1, **mods):
     """One call over requests of nq[i] queries and nk[i] keys; `gap` rows of NaN keys and values (and untouched query
-    rows) before the first and after the last request.  Returns (out, lse, status) after checking them."""
+    rows) before the first and after the last request; `slack` times the longest request as bounds.  Returns (out,
+    lse) after checking them."""
     import torch
     from bit_rotated_kv_split_gb300 import binding as B
     g = np.random.default_rng(case_seed)
@@ -52,7 +53,7 @@ def run(case_seed, nq, nk, hq, hk, d, causal=True, prefix=None, gap=0, lead=0, p
     out = torch.full((tq, hq, d), -3.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((tq, hq), -3.0, dtype=torch.float32, device="cuda")
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
-    desc = B.prompt_desc(len(nq), hq, hk, d, max(nq), max(nk), tq, tk, causal, st)
+    desc = B.prompt_desc(len(nq), hq, hk, d, slack * max(nq), slack * max(nk), tq, tk, causal, st)
     sl = None
     slopes = np.zeros(hq, np.float32)
     if mods.pop("slopes", False):
@@ -112,6 +113,15 @@ CASES = [
     ([1000], [1000], 2, 1, 128, {}),
     ([3] * 30, [3] * 30, 4, 1, 64, {}),
     ([257], [257], 7, 1, 128, dict(packed=True)),
+    # keys split over several CTAs: alternate tiles for few rows, two row tiles, requests with few keys or none among them
+    ([5, 3, 1], [2500, 90, 0], 8, 2, 128, {}),
+    ([100, 40], [5000, 1300], 8, 2, 64, dict(gap=5)),
+    ([20], [4000], 4, 1, 128, dict(prefix=[700], window=300)),
+    ([33, 1], [2049, 2048], 6, 2, 64, dict(softcap=8.0, slopes=True)),
+    ([2], [1025], 16, 16, 64, dict(causal=False)),
+    ([130], [1500], 1, 1, 128, dict(window=1)),
+    ([12, 70], [1300, 70], 20, 1, 64, dict(slack=3)),            # a group of 20: ten heads to a row set
+    ([60, 200, 9], [60, 200, 9], 5, 1, 128, dict(slack=4, prefix=[5, 0, 100])),
 ]
 
 
@@ -126,7 +136,6 @@ def test_prompt_clamps_and_reports_bad_rows():
     from bit_rotated_kv_split_gb300 import binding as B
     g = np.random.default_rng(4)
     q, k, v = (dev_bf16(g.standard_normal((60, h, 64))) for h in (4, 2, 2))
-    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
 
     def call(cu_q, cu_k, max_q, max_k):
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -143,7 +152,6 @@ def test_prompt_clamps_and_reports_bad_rows():
         out, status = call(cu_q, cu_k, mq, mk)
         assert status == 2
         assert bool((out[:20] == good[:20]).all())
-    del ws
 
 
 def test_prompt_on_another_stream_and_in_a_graph():
@@ -165,3 +173,25 @@ def test_prompt_on_another_stream_and_in_a_graph():
         graph.replay()
     torch.cuda.synchronize()
     assert bool((out[0] == out[1]).all())
+
+
+def test_prompt_scores_far_apart_and_rows_of_one_key():
+    """Scores of thousands (one key takes all), a whole row of equal scores, and caps that bite."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g = np.random.default_rng(8)
+    n, hq, hk, d = 300, 4, 2, 64
+    q, k, v = (O.bf16(g.standard_normal((n, h, d))) for h in (hq, hk, hk))
+    q[:100] *= 512.0
+    q[100:150] = 0.0
+    for softcap in (0.0, 2.0, 4000.0):
+        desc = B.prompt_desc(1, hq, hk, d, n, n, n, n)
+        ws = torch.zeros(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+        out = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda")
+        B.oscar_prompt_attention(desc, dev_bf16(q), dev_bf16(k), dev_bf16(v), i32([0, n]), i32([0, n]), out, ws,
+                                 score=B.score_desc(softcap=softcap))
+        got = host(out)
+        for h in range(hq):
+            r, r_abs, _ = O.masked_attention(O.modified_scores(q[:, h], k[:, h // 2], 0, softcap=softcap), v[:, h // 2])
+            # fp32 scores of up to 2^13 are off by up to 2^-10 each, which their weights repeat
+            assert (np.abs(got[:, h] - r) <= HALF_BF16 * (np.abs(r) + r_abs) + 2.0 ** -9 * r_abs + 2.0 ** -14).all()

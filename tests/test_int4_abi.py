@@ -237,6 +237,13 @@ def test_binding_checks():
         B.oscar_decode_attention_int4(desc, row(1, 8), row(1, 8), torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(ValueError):
         B.oscar_gather_int4(desc, idx, idx, row(3, 2), row(2, 2))
+    # rightly shaped, but not on a GPU: refused before the library sees a pointer
+    with pytest.raises(ValueError, match="CUDA device"):
+        B.oscar_rope_append_int4(desc, None, row(3, 8), row(3, 2), row(3, 2), idx, idx, row(3, 8))
+    with pytest.raises(ValueError, match="CUDA device"):
+        B.oscar_gather_int4(desc, idx, idx, row(3, 2), row(3, 2))
+    with pytest.raises(ValueError, match="CUDA device"):
+        B.oscar_decode_attention_int4(desc, row(2, 8), row(2, 8), torch.zeros(256, dtype=torch.uint8))
     pd = B.prompt_desc(1, 8, 2, 64, 3, 3, 3, 3)
     cu = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
