@@ -42,6 +42,23 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {   // a 
   return d;
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 bf16_pair(uint32_t u) { return make_float2(bf16_lo(u), bf16_hi(u)); }
+
 // Codes of the 8 bf16 values u of this lane (x - zero over scale, to nearest
 // even, 0 .. 15) in a group of `lanes` lanes; *pair = (scale, zero), fp16 bits.
 //
@@ -126,22 +143,28 @@ struct Turn {
   bool on;
 };
 
-// Value i of the turned octet: a c + b s.
-__device__ __forceinline__ void operands(const Turn& t, bool interleaved, const float (&x)[8], const float (&y)[8],
-                                         int i, float* a, float* c, float* b, float* s) {
-  if (!interleaved) {
-    *a = x[i], *c = t.c[i], *b = y[i], *s = t.s[i];
+// Values 2 i, 2 i + 1 of the turned octet are a c + b s.
+template <bool Interleaved>
+__device__ __forceinline__ void operands(const Turn& t, uint32_t x, uint32_t y, int i, float2* a, float2* c, float2* b,
+                                         float2* s) {
+  const float2 u = bf16_pair(x);
+  if (!Interleaved) {
+    *a = u;
+    *b = bf16_pair(y);
+    *c = make_float2(t.c[2 * i], t.c[2 * i + 1]);
+    *s = make_float2(t.s[2 * i], t.s[2 * i + 1]);
   } else {
-    *a = x[i & ~1], *b = x[i | 1];
-    *c = (i & 1) ? t.s[i >> 1] : t.c[i >> 1];
-    *s = (i & 1) ? t.c[i >> 1] : -t.s[i >> 1];
+    *a = twice(u.x);
+    *b = twice(u.y);
+    *c = make_float2(t.c[i], t.s[i]);
+    *s = make_float2(-t.s[i], t.c[i]);
   }
 }
 
 // Rotates the octet held in `raw`; whole warps call it.  Exact: the rounding to
 // bf16 is that of the exact value.  The fp32 result r is within e of it; where
-// r - e and r + e round apart (about one value in 2^13) the octet is formed in
-// 64 bits, whose products are exact and whose sums are rounded at 2^-53.
+// r - e and r + e round apart (about one value in 2^13) the pair is formed in 64
+// bits, whose products are exact and whose sums are rounded at 2^-53.
 template <bool Exact, bool Interleaved>
 __device__ __forceinline__ void rotate8(uint4& raw, const Turn& t) {
   uint4 other = make_uint4(0, 0, 0, 0);
@@ -152,45 +175,31 @@ __device__ __forceinline__ void rotate8(uint4& raw, const Turn& t) {
     other.w = __shfl_sync(0xffffffffu, raw.w, t.partner);
   }
   if (!t.on) return;
-  float x[8], y[8];
-  unpack_bf16x8(raw, x);
-  unpack_bf16x8(other, y);
-  uint32_t out[4], apart = 0;
+  const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w}, y[4] = {other.x, other.y, other.z, other.w};
+  uint32_t out[4], apart[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float r[2], e[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float a, c, b, s;
-      operands(t, Interleaved, x, y, 2 * i + u, &a, &c, &b, &s);
-      const float bs = b * s;
-      r[u] = fmaf(a, c, bs);
-      if (Exact) e[u] = (fabsf(bs) + fabsf(r[u])) * 1.1920929e-7f;
-    }
+    float2 a, b, c, s;
+    operands<Interleaved>(t, x[i], y[i], i, &a, &c, &b, &s);
+    const float2 bs = mul2(b, s), r = fma2(a, c, bs);
     if (Exact) {
-      out[i] = pack_bf162(r[0] - e[0], r[1] - e[1]);
-      apart |= out[i] ^ pack_bf162(r[0] + e[0], r[1] + e[1]);
+      const float2 e = make_float2(fabsf(bs.x) + fabsf(r.x), fabsf(bs.y) + fabsf(r.y));
+      const float2 lo = fma2(e, twice(-1.1920929e-7f), r), hi = fma2(e, twice(1.1920929e-7f), r);
+      out[i] = pack_bf162(lo.x, lo.y);
+      apart[i] = out[i] ^ pack_bf162(hi.x, hi.y);
     } else {
-      out[i] = pack_bf162(r[0], r[1]);
+      out[i] = pack_bf162(r.x, r.y);
     }
   }
-  if (Exact && apart) {
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      float r[2];
+  if (Exact && (apart[0] | apart[1] | apart[2] | apart[3])) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float a = 0.f, c = 0.f, b = 0.f, s = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          if (w == i) operands(t, Interleaved, x, y, 2 * w + u, &a, &c, &b, &s);
-        r[u] = float(fma(double(a), double(c), double(b) * double(s)));
+    for (int i = 0; i < 4; ++i)
+      if (apart[i]) {
+        float2 a, b, c, s;
+        operands<Interleaved>(t, x[i], y[i], i, &a, &c, &b, &s);
+        out[i] = pack_bf162(float(fma(double(a.x), double(c.x), double(b.x) * double(s.x))),
+                            float(fma(double(a.y), double(c.y), double(b.y) * double(s.y))));
       }
-      const uint32_t v = pack_bf162(r[0], r[1]);
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        if (w == i) out[w] = v;
-    }
   }
   raw = make_uint4(out[0], out[1], out[2], out[3]);
 }
@@ -208,7 +217,7 @@ __device__ __forceinline__ void load8(float (&x)[8], const float* p, int n) {
 // a time, whose loads are in flight together, then k and v heads with the next
 // slot's load ahead of the present one's work.
 template <int D, bool Interleaved>
-__global__ void __launch_bounds__(kAppendThreads, 6)
+__global__ void __launch_bounds__(kAppendThreads, 7)
     rope_append_kernel(const __grid_constant__ AppendParams p, int slots_per_warp) {
   pdl_wait();
   pdl_launch_dependents();
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
       if (p.rot) rotate8<true, Interleaved>(raw, turn);
       if (p.k_out && valid) *reinterpret_cast<uint4*>(p.k_out + (i * p.c.n_kv + head) * D + 8 * o) = raw;
     }
-    const int lanes = kLanes / (is_v ? ng_v : ng_k);
+    const int lanes = kLanes >> ((is_v ? ng_v : ng_k) >> 1);   // 1, 2 or 4 groups
     uint32_t pair;
     const uint32_t word = quantise8(raw, is_v ? p.tau_v : p.tau_k, lanes, &pair);   // of the rounded row
     if (!valid) continue;
@@ -302,8 +311,8 @@ __global__ void __launch_bounds__(kAppendThreads, 6)
       *reinterpret_cast<uint16_t*>(block + int4_v_half(D, slot, 2 * o)) = uint16_t(word);
       *reinterpret_cast<uint16_t*>(block + int4_v_half(D, slot, 2 * o + 1)) = uint16_t(word >> 16);
     }
-    if (o % lanes == 0)
-      *reinterpret_cast<uint32_t*>(block + int4_pair(D, ng_k, ng_v, slot, (is_v ? ng_k : 0) + o / lanes)) = pair;
+    if ((o & (lanes - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(block + int4_pair(D, ng_k, ng_v, slot, is_v ? ng_k + o * ng_v / kLanes : o * ng_k / kLanes)) = pair;
   }
 }
 
