@@ -221,6 +221,35 @@ def test_gather_matches_oracle(d, hk, gk, gv):
     assert L.status() == 0
 
 
+def test_many_rows_appended_and_read_back():
+    """Enough rows that a warp takes whole tokens, several of them when they are read back; some rows are padding, some
+    name bad places, and the last warp's are not all there."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    n, hq, hk, d = 15_011, 3, 3, 64
+    L = Layer(77, [n], hq, hk, d, 32, 64, fill=False)
+    q, k, v = (O.bf16(L.g.standard_normal((n, h, d))) for h in (hq, hk, hk))
+    cs = angles(n, d)
+    req, pos = np.zeros(n, np.int64), L.g.permutation(n)
+    req[::7], pos[5::1000], req[11::1001] = -1, -3, 1
+    good = (req == 0) & (pos >= 0)
+    q_out, k_out = (torch.full((n, h, d), 5.0, dtype=torch.bfloat16, device="cuda") for h in (hq, hk))
+    B.oscar_rope_append_int4(L.desc, B.rope_desc(torch.from_numpy(cs).cuda(), d), dev_bf16(q), dev_bf16(k), dev_bf16(v),
+                             i32(req), i32(pos), q_out, k_out)
+    torch.cuda.synchronize()
+    assert L.status() == 2
+    k_ref = O.bf16(O.rope(k[good], cs[pos[good]], False))
+    np.testing.assert_array_equal(host(k_out)[good], k_ref)
+    assert (host(k_out)[~good] == 5.0).all() and (host(q_out)[~good] == 5.0).all()
+    kc, vc = L.put(0, pos[good], 0, k_ref), L.put(0, pos[good], 1, v[good])
+    np.testing.assert_array_equal(L.gpu_pool(), L.pool)
+    ko, vo = (torch.full((n, hk, d), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    B.oscar_gather_int4(L.desc, i32(req), i32(pos), ko, vo)
+    for got, ref in ((host(ko), kc), (host(vo), vc)):
+        np.testing.assert_array_equal(got[good], O.bf16(ref))
+        assert (got[~good] == 5.0).all()
+
+
 def decode_ref(L, q, **mods):
     """(attention, its error bound) of q [B][hq][d] over what the cache stands for."""
     slopes = mods.pop("slopes", None)
