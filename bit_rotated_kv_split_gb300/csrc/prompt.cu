@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // first to the last row's last; n[w]: as far as row tile w goes
   int n_pre = 0, from = 0, n[2];
   const int tiles = (sp.n_k + kTile - 1) / kTile;
-  if (p.s.window) from = min(max(0, shift + tok0 - p.s.window + 1) / kTile, tiles);
+  // (positions may be negative and the window any int: compared before they are subtracted)
+  if (p.s.window && shift + tok0 >= p.s.window) from = min((shift + tok0 - p.s.window + 1) / kTile, tiles);
   n_pre = min((sp.prefix + kTile - 1) / kTile, from);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = tok0 + (dual ? 0 : w * per_tile) + row / pack, head = hq0 + row % pack;
     const bool mine = row < pack * per_tile && tok < sp.n_q;   // (rows to spare hold anything)
     const int pos = shift + tok;
-    const int row_lo = p.s.window ? max(0, pos - p.s.window + 1) : 0;
+    const int row_lo = p.s.window && pos >= p.s.window ? pos - p.s.window + 1 : 0;
     const int row_hi = p.causal ? min(pos + 1, sp.n_k) : sp.n_k;
     const float slope = Formed && p.s.slopes ? p.s.slopes[head] * kLog2e : 0.f;
     const bool cap = Formed && p.s.cap_log2 != 0.f;

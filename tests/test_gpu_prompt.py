@@ -130,6 +130,19 @@ def test_prompt_matches_oracle(nq, nk, hq, hk, d, kw):
     run(sum(nq) + sum(nk) + hq + d, nq, nk, hq, hk, d, **kw)
 
 
+@pytest.mark.parametrize("nq,nk,kw", [
+    ([50], [20], dict(causal=False)),
+    ([50], [20], dict(prefix=[7])),
+    ([300, 4], [40, 900], dict(causal=False, slopes=True)),
+    ([9], [1200], dict()),
+])
+def test_prompt_window_of_any_size(nq, nk, kw):
+    """The largest window masks nothing, for queries before the first key (at negative positions) as well."""
+    wide, _ = run(31, nq, nk, 4, 2, 64, window=2 ** 31 - 1, **kw)
+    none, _ = run(31, nq, nk, 4, 2, 64, **kw)
+    assert bool((wide == none).all())
+
+
 def test_prompt_clamps_and_reports_bad_rows():
     """Lengths above the bounds and rows outside the tensors are clamped and reported; other requests are not affected."""
     import torch
