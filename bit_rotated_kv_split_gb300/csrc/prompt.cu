@@ -503,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l != 0.f ? 1.f / l : 0.f;         // (a row with NaN scores stays NaN)
       uint16_t* out = p.out + ((sp.q0 + tok) * p.n_q + head) * D;
-      if (mine && p.lse) p.lse[(sp.q0 + tok) * p.n_q + head] = l > 0.f ? (m * sc + log2f(l)) * kLn2 : -INFINITY;
+      if (mine && p.lse) p.lse[(sp.q0 + tok) * p.n_q + head] = l != 0.f ? (m * sc + log2f(l)) * kLn2 : -INFINITY;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -575,14 +575,14 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, 
         v[s][0] = u.x, v[s][1] = u.y;
       }
     }
-    float top = x.y > 0.f ? x.x : -INFINITY;
+    float top = x.y != 0.f ? x.x : -INFINITY;   // (a part whose sum is NaN counts)
 #pragma unroll
     for (int i = 8; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
     top = __shfl_sync(0xffffffffu, top, 0);
     if (top == -INFINITY) continue;          // the same in all lanes
     const float mn = fmaxf(mx, top), f = mx == -INFINITY ? 0.f : exp2_fast(mx - mn);
     mx = mn;
-    const float g = x.y > 0.f ? exp2_fast(x.x - mn) : 0.f;
+    const float g = x.y != 0.f ? exp2_fast(x.x - mn) : 0.f;
     sum = fmaf(g, x.y, sum * f);             // of this lane's parts
 #pragma unroll
     for (int e = 0; e < kC; ++e) o[e] *= f;
@@ -595,11 +595,11 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, 
   }
 #pragma unroll
   for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.out + ((sp.q0 + tok) * p.n_q + head) * D + kC * lane);
 #pragma unroll
   for (int e = 0; e < kC / 2; ++e) out[e] = pack_bf162(o[2 * e] * inv, o[2 * e + 1] * inv);
-  if (p.lse && lane == 0) p.lse[(sp.q0 + tok) * p.n_q + head] = sum > 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+  if (p.lse && lane == 0) p.lse[(sp.q0 + tok) * p.n_q + head] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // rows [total][heads][d] bf16, `stride` elements apart, in boxes of 64 channels

@@ -590,7 +590,7 @@ int64_t oscar_int4_block_bytes(int32_t head_dim, int32_t quant_group_k, int32_t 
  *
  *   For item i < n: q row i (q + i * q_stride, H_q heads of d bf16), k row i
  *   and v row i (H_kv heads each).  q' and k' are q and k rotated by row
- *   rope_pos[i] of rope->cos_sin (rope_pos NULL: dst_pos[i]), rounded once to
+ *   rope_pos[i] of rope->cos_sin (rope_pos NULL: dst_pos[i]), rounded to
  *   bf16: (a, b) -> (a cos - b sin, a sin + b cos).  q' goes to q_out and k'
  *   to k_out ([n][heads][d], contiguous; each may be NULL, or q / k itself
  *   where that is contiguous).  k' and v, clamped to [-tau, tau], are
@@ -598,9 +598,9 @@ int64_t oscar_int4_block_bytes(int32_t head_dim, int32_t quant_group_k, int32_t 
  *   code = clamp(rint((x - zero) / scale), 0, 15) (0 if scale is 0), and
  *   stored at position dst_pos[i] of request dst_req[i].
  *
- *   k' is rounded from its exact value (codes do not depend on how the
- *   rotation is computed); q' is within one rounding of fp32 sums.  A NaN
- *   is quantised as -tau; other rows are not affected.
+ *   k' is its exact value rounded to fp32 and that to bf16 (codes do not depend
+ *   on how the rotation is computed); q' is within one rounding of fp32 sums.
+ *   A NaN is quantised as -tau; other rows are not affected.
  *   dst_req[i] = -1 marks a padding row: nothing of it is written.
  *   Any other request outside the batch, a position beyond the page table
  *   or a rotation row outside cos_sin skips the item and sets
@@ -699,11 +699,13 @@ typedef struct oscar_prompt_desc {
  *   output sums are fp32; exp(t - max) is rounded to bf16 for its product
  *   with v.  Rows of out and lse outside every request are left as they
  *   were; rows of k and v outside a request never reach it, whatever they
- *   hold.  A request's own rows must be finite.  Lengths above max_q / max_k
- *   or rows outside total_q / total_k are clamped and set OSCAR_DEV_LENGTH.
- *   A wait within the kernel that runs out (1 s) sets OSCAR_DEV_TIMEOUT (the
- *   output must not be used then).  out must not overlap q, k or v.  The result
- *   does not depend on scheduling.
+ *   hold.  A query row with a NaN has a NaN result and reaches no other row.  A
+ *   request's value rows must be finite (one with a NaN may reach queries that
+ *   it is masked for).  Lengths above max_q /
+ *   max_k or rows outside total_q / total_k are clamped and set
+ *   OSCAR_DEV_LENGTH.  A wait within the kernel that runs out (1 s) sets
+ *   OSCAR_DEV_TIMEOUT (the output must not be used then).  out must not overlap
+ *   q, k or v.  The result does not depend on scheduling.
  *
  *   Workspace: NULL asks for the size (it depends on desc); otherwise 256-byte
  *   aligned device memory, of any content; calls that may overlap need

@@ -143,6 +143,28 @@ def test_prompt_window_of_any_size(nq, nk, kw):
     assert bool((wide == none).all())
 
 
+@pytest.mark.parametrize("nq,nk,bad,d,softcap", [(40, 40, 7, 64, 0.0), (300, 300, 0, 128, 5.0), (9, 4000, 8, 128, 0.0), (200, 3000, 150, 64, 0.0)])
+def test_prompt_query_with_nan_shows_and_stays_alone(nq, nk, bad, d, softcap):
+    """A NaN in a query's row makes that row and its lse NaN, split keys or not; the other rows are bit for bit the same."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g = np.random.default_rng(nq + nk)
+    q, k, v = dev_bf16(g.standard_normal((nq, 4, d))), dev_bf16(g.standard_normal((nk, 2, d))), dev_bf16(g.standard_normal((nk, 2, d)))
+    desc = B.prompt_desc(1, 4, 2, d, nq, nk, nq, nk)
+    ws = torch.empty(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    res = []
+    for x in (1.0, float("nan")):
+        q[bad, 1, 5] = x
+        out, lse = torch.empty_like(q), torch.empty(nq, 4, dtype=torch.float32, device="cuda")
+        B.oscar_prompt_attention(desc, q, k, v, i32([0, nq]), i32([0, nk]), out, ws, score=B.score_desc(0.0, softcap, 0, None), lse=lse)
+        res.append((out, lse))
+    torch.cuda.synchronize()
+    (out, lse), (out_n, lse_n) = res
+    assert bool(out_n[bad, 1].isnan().all()) and bool(lse_n[bad, 1].isnan())
+    out_n[bad, 1], lse_n[bad, 1] = out[bad, 1], lse[bad, 1]
+    assert bool((out == out_n).all()) and bool((lse == lse_n).all())
+
+
 def test_prompt_clamps_and_reports_bad_rows():
     """Lengths above the bounds and rows outside the tensors are clamped and reported; other requests are not affected."""
     import torch
