@@ -168,9 +168,9 @@ __device__ __forceinline__ void operands(const Turn& t, uint32_t x, uint32_t y, 
 }
 
 // Rotates the octet held in `raw`; whole warps call it.  Exact: the rounding to
-// bf16 is that of the exact value.  The fp32 result r is within e of it; where
-// r - e and r + e round apart (about one value in 2^13) the pair is formed in 64
-// bits, whose products are exact and whose sums are rounded at 2^-53.
+// bf16 is that of the exact value's fp32.  The fp32 result r is within e of it;
+// where r - e and r + e round apart (about one value in 2^13) the pair is formed
+// in 64 bits, whose products are exact and whose sums are rounded at 2^-53.
 template <bool Exact, bool Interleaved>
 __device__ __forceinline__ void rotate8(uint4& raw, const Turn& t) {
   uint4 other = make_uint4(0, 0, 0, 0);
