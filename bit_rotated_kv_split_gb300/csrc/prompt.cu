@@ -42,7 +42,7 @@ namespace {
 constexpr int kTile = 128;            // rows of a tile, of queries and of keys
 constexpr int kPanel = kTile * 128;   // bytes of 128 rows of 64 channels
 constexpr int kThreads = 384;         // three warpgroups: two of softmax, one of single warps
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kTailWarp = 10;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kHoleWarp = 10;
 constexpr int kSms = 152;
 // tiles of K and V in flight or in use: a ring in the order K0 V0 K1 V1 ..
 template <int D>
@@ -102,7 +102,7 @@ __device__ __forceinline__ PromptSpan prompt_span(const PromptParams& p, int b, 
 }
 
 struct Barriers {
-  uint64_t q_full, full[10], empty[10], tail, s_full[2], p_full[2], o_done[2], fin;
+  uint64_t q_full, full[10], empty[10], holed[3], s_full[2], p_full[2], o_done[2], fin;
   uint32_t tmem;
   int dead;
 };
@@ -186,10 +186,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // key tiles that some row sees: the prefix's, then those from the window's
   // first to the last row's last; n[w]: as far as row tile w goes
-  int n_pre = 0, from = 0, n[2];
+  int n_pre = 0, from = 0, first = 0, n[2];   // first: the window's first key for the CTA's first row
   const int tiles = (sp.n_k + kTile - 1) / kTile;
   // (positions may be negative and the window any int: compared before they are subtracted)
-  if (p.s.window && shift + tok0 >= p.s.window) from = min((shift + tok0 - p.s.window + 1) / kTile, tiles);
+  if (p.s.window && shift + tok0 >= p.s.window) first = shift + tok0 - p.s.window + 1;
+  from = min(first / kTile, tiles);
   n_pre = min((sp.prefix + kTile - 1) / kTile, from);
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (n_all > 0) {
     if (tid == 0) {
       mbar_init(&bar.q_full, 1);
-      mbar_init(&bar.tail, 1);
+      for (int i = 0; i < 3; ++i) mbar_init(&bar.holed[i], 1);
       mbar_init(&bar.fin, 1);
       for (int i = 0; i < kR; ++i) {
         mbar_init(&bar.full[i], 1);
@@ -244,10 +245,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return true;
   };
-  // The request's last key tile, where the keys end inside it, is the list's
-  // last.  Rows of V behind the last key may hold anything, and 0 times that is
-  // not 0: a warp of its own clears them between the load and the product.
-  const bool tail = n_all > 0 && tile_of(n_all - 1) == tiles - 1 && sp.n_k % kTile != 0;
+  // Rows of V that no row here sees may hold anything, and 0 times that is not
+  // 0: a warp of its own clears them between the load and the product.  They are
+  // the keys from the prefix's end to the window's first, in the list's entries
+  // e_pre and e_win, and those behind the last key, in e_end.
+  const int e_pre = first > sp.prefix && sp.prefix % kTile ? n_pre - 1 - lo : -1;
+  const int e_win = first > sp.prefix && first % kTile ? n_pre - lo : -1;
+  const int e_end = n_all > 0 && tile_of(n_all - 1) == tiles - 1 && sp.n_k % kTile ? n_all - 1 : -1;
+  auto holes = [&](int j) { return j == e_pre || j == e_win || j == e_end; };
 
   // Registers: the launch's 168 a thread, 504 over the three warpgroups.  A
   // softmax thread holds a row's 128 scores; the issuing warp must not spill (at
@@ -260,11 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int w = 0; w < tiles_q; ++w)
         for (int c = 0; c < kPanels; ++c)
           tma_load_3d(sq + w * kTileBytes + c * kPanel, &tq, 64 * c, hq0, int(sp.q0) + tok0 + w * per_tile, &bar.q_full);
-      int t = 0, st = 0, turn = 0;           // t = 2 j is K of step j, 2 j + 1 its V
+      int t = 0, st = 0, turn = 0, n_holed = 0;   // t = 2 j is K of step j, 2 j + 1 its V
       for (; t < 2 * n_all; ++t) {
         if (turn > 0 && !wait(&bar.empty[st], (turn - 1) & 1)) break;
         const int row = int(sp.k0) + tile_of(t >> 1) * kTile;
-        uint64_t* at = tail && t == 2 * n_all - 1 ? &bar.tail : &bar.full[st];
+        uint64_t* at = (t & 1) && holes(t >> 1) ? &bar.holed[n_holed++] : &bar.full[st];
         mbar_arrive_expect_tx(at, kTileBytes);
         for (int c = 0; c < kPanels; ++c)
           tma_load_3d(ring + st * kTileBytes + c * kPanel, (t & 1) ? &tv : &tk, 64 * c, hk, row, at);
@@ -272,21 +277,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // what was issued has landed before the CTA's shared memory goes
       mbar_wait_bounded(&bar.q_full, 0, kDrainWaitNs);
+      for (int i = 0; i < n_holed; ++i) mbar_wait_bounded(&bar.holed[i], 0, kDrainWaitNs);
       for (int i = max(0, t - kR); i < t; ++i)
-        if (tail && i == 2 * n_all - 1)
-          mbar_wait_bounded(&bar.tail, 0, kDrainWaitNs);
-        else
-          mbar_wait_bounded(&bar.full[i % kR], (i / kR) & 1, kDrainWaitNs);
-    } else if (warp == kTailWarp && tail) {
-      const int t = 2 * n_all - 1, valid = sp.n_k % kTile;
-      if (__all_sync(0xffffffffu, wait(&bar.tail, 0))) {
-        uint8_t* v = ring + (t % kR) * kTileBytes;
-        for (int i = valid * 8 + lane; i < kTile * 8; i += 32)
+        if (!((i & 1) && holes(i >> 1))) mbar_wait_bounded(&bar.full[i % kR], (i / kR) & 1, kDrainWaitNs);
+    } else if (warp == kHoleWarp) {
+      int n_holed = 0;
+      for (int j = 0; j < n_all; ++j) {
+        if (!holes(j)) continue;
+        const int k0 = tile_of(j) * kTile, st = (2 * j + 1) % kR;
+        if (!__all_sync(0xffffffffu, wait(&bar.holed[n_holed++], 0))) break;
+        uint8_t* v = ring + st * kTileBytes;
+        auto clear = [&](int a, int b) {     // rows a .. b - 1
+          for (int i = a * 8 + lane; i < b * 8; i += 32)
 #pragma unroll
-          for (int c = 0; c < kPanels; ++c) *reinterpret_cast<uint4*>(v + c * kPanel + 16 * i) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < kPanels; ++c) *reinterpret_cast<uint4*>(v + c * kPanel + 16 * i) = make_uint4(0, 0, 0, 0);
+        };
+        clear(max(sp.prefix - k0, 0), min(first - k0, kTile));
+        clear(max(sp.n_k - k0, 0), kTile);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.full[t % kR]);
+        if (lane == 0) mbar_arrive(&bar.full[st]);
       }
     } else if (warp == kMmaWarp && n_all > 0) {
       // Step i of row tile w uses K and V of the list's entry i (dual: 2 i + w).

@@ -700,8 +700,9 @@ typedef struct oscar_prompt_desc {
  *   with v.  Rows of out and lse outside every request are left as they
  *   were; rows of k and v outside a request never reach it, whatever they
  *   hold.  A query row with a NaN has a NaN result and reaches no other row.  A
- *   request's value rows must be finite (one with a NaN may reach queries that
- *   it is masked for).  Lengths above max_q /
+ *   request's value rows must be finite where one of its queries sees them (one
+ *   with a NaN may reach queries that it is masked for); key and value rows
+ *   that the window hides from all of its queries may hold anything.  Lengths above max_q /
  *   max_k or rows outside total_q / total_k are clamped and set
  *   OSCAR_DEV_LENGTH.  A wait within the kernel that runs out (1 s) sets
  *   OSCAR_DEV_TIMEOUT (the output must not be used then).  out must not overlap

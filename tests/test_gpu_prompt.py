@@ -165,6 +165,41 @@ def test_prompt_query_with_nan_shows_and_stays_alone(nq, nk, bad, d, softcap):
     assert bool((out == out_n).all()) and bool((lse == lse_n).all())
 
 
+@pytest.mark.parametrize("nq,nk,window,prefix,d,kw", [
+    (24, 2000, 300, 0, 128, {}),                       # split keys, alternate tiles
+    (24, 2000, 300, 70, 64, {}),
+    (200, 700, 150, 65, 64, dict(softcap=4.0)),
+    (200, 700, 150, 330, 128, {}),                     # the prefix ends in the window's first tile
+    (200, 700, 150, 256, 128, dict(slopes=True)),
+    (300, 1500, 40, 0, 128, dict(causal=0)),
+    (2, 129, 1, 5, 64, {}),
+    (1, 1025, 1, 0, 128, {}),
+    (513, 513 + 384, 128, 10, 128, {}),
+    (130, 260, 5, 300, 64, {}),                        # the prefix is all keys
+])
+def test_prompt_rows_before_the_window_may_hold_anything(nq, nk, window, prefix, d, kw):
+    """Keys and values that no query sees are NaN or infinite; the result is bit for bit that of zeros there."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g = np.random.default_rng(nq + nk + window)
+    q, k, v = dev_bf16(g.standard_normal((nq, 4, d))), dev_bf16(g.standard_normal((nk, 2, d))), dev_bf16(g.standard_normal((nk, 2, d)))
+    slopes = torch.full((4,), 0.25, device="cuda") if kw.get("slopes") else None
+    desc = B.prompt_desc(1, 4, 2, d, nq, nk, nq, nk, bool(kw.get("causal", 1)))
+    ws = torch.empty(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    lo, hi = min(prefix, nk), max(min(prefix, nk), nk - nq - window + 1)
+    res = []
+    for a, b in ((0.0, 0.0), (float("nan"), float("inf")), (float("-inf"), float("nan"))):
+        k[lo:hi], v[lo:hi] = a, b
+        out, lse = torch.empty_like(q), torch.empty(nq, 4, dtype=torch.float32, device="cuda")
+        B.oscar_prompt_attention(desc, q, k, v, i32([0, nq]), i32([0, nk]), out, ws, prefix_len=i32([prefix]), lse=lse,
+                                 score=B.score_desc(0.0, kw.get("softcap", 0.0), window, slopes))
+        res.append((out, lse))
+    torch.cuda.synchronize()
+    assert bool(res[0][0].isfinite().all())
+    for out, lse in res[1:]:
+        assert bool((out == res[0][0]).all()) and bool((lse == res[0][1]).all())
+
+
 def test_prompt_clamps_and_reports_bad_rows():
     """Lengths above the bounds and rows outside the tensors are clamped and reported; other requests are not affected."""
     import torch
