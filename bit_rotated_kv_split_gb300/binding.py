@@ -47,6 +47,7 @@ class LayerDesc(ctypes.Structure):
 
 class Int4Desc(ctypes.Structure):
     """Mirror of `oscar_int4_desc`."""
+    keep = None   # a tensor whose memory it points to
     _fields_ = [
         ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
         ("max_pages_per_seq", c_int32), ("max_len", c_int32), ("n_pages", c_int64),
@@ -57,17 +58,20 @@ class Int4Desc(ctypes.Structure):
 
 class RopeDesc(ctypes.Structure):
     """Mirror of `oscar_rope_desc`."""
+    keep = None   # a tensor whose memory it points to
     _fields_ = [("cos_sin", c_void_p), ("n_positions", c_int64), ("rot_dim", c_int32), ("interleaved", c_int32)]
 
 
 class ScoreDesc(ctypes.Structure):
     """Mirror of `oscar_score_desc`."""
+    keep = None   # a tensor whose memory it points to
     _fields_ = [("scale", c_float), ("softcap", c_float), ("window", c_int32), ("reserved", c_int32),
                 ("slopes", c_void_p)]
 
 
 class PromptDesc(ctypes.Structure):
     """Mirror of `oscar_prompt_desc`."""
+    keep = None   # a tensor whose memory it points to
     _fields_ = [
         ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
         ("max_q", c_int32), ("max_k", c_int32), ("causal", c_int32), ("reserved", c_int32),
@@ -377,10 +381,22 @@ def prompt_desc(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_
     return d
 
 
+_torch = None
+
+
+def _half(t):
+    """bfloat16 or raw 16-bit integers: fp16 rows have the size of bf16's and would be read as such."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return t.dtype is _torch.bfloat16 or (t.element_size() == 2 and not t.is_floating_point())
+
+
 def _heads(name, t, heads, d):
     """Row stride of bf16 rows t [n][heads][d] (bfloat16, or its bits as uint16) whose heads lie side by side."""
     shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != d or t.element_size() != 2:
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or not _half(t):
         raise ValueError("%s must be bfloat16 [n][%d][%d]" % (name, heads, d))
     if shape[0] == 0:
         return heads * d
@@ -397,17 +413,18 @@ def _index(name, t, n):
 
 
 def _contiguous(name, t, shape, itemsize):
-    if t is not None and (t.shape != shape or t.element_size() != itemsize or not t.is_contiguous()):
-        raise ValueError("%s must be contiguous %s" % (name, list(shape)))
+    if t is not None and (t.shape != shape or not t.is_contiguous() or not (
+            _half(t) if itemsize == 2 else t.element_size() == 4 and t.is_floating_point())):
+        raise ValueError("%s must be contiguous %s %s" % (name, "bfloat16" if itemsize == 2 else "float32", list(shape)))
 
 
-_torch = _raw_stream = None
+_raw_stream = None
 
 
 def _on_device(name, stream, tensors, fn, args):
     """Calls the library with the tensors' device current and, without a stream, on that device's current stream."""
     global _torch, _raw_stream
-    if _torch is None:
+    if _raw_stream is None:
         import torch
         _torch = torch
         # the current stream's handle without a Stream object around it (3 us a call less)
@@ -451,7 +468,7 @@ def oscar_rope_append_int4(desc: Int4Desc, rope, q, k, v, dst_req, dst_pos, q_ou
     _index("dst_req", dst_req, n), _index("dst_pos", dst_pos, n), _index("rope_pos", rope_pos, n)
     _contiguous("q_out", q_out, (n, hq, d), 2)
     _contiguous("k_out", k_out, (n, hk, d), 2)
-    _on_device("oscar_rope_append_int4", stream, (k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos),
+    _on_device("oscar_rope_append_int4", stream, (k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos, desc.keep, rope and rope.keep),
                lib.oscar_rope_append_int4, (
                    ctypes.byref(desc), _ref(rope), _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, dst_req.data_ptr(),
                    dst_pos.data_ptr(), _ptr(rope_pos), n, _ptr(q_out), _ptr(k_out)))
@@ -464,7 +481,7 @@ def oscar_gather_int4(desc: Int4Desc, src_req, src_pos, k_out, v_out, stream=Non
     if v_out.shape[0] != n:
         raise ValueError("k_out and v_out must have one row count")
     _index("src_req", src_req, n), _index("src_pos", src_pos, n)
-    _on_device("oscar_gather_int4", stream, (k_out, v_out, src_req, src_pos), lib.oscar_gather_int4, (
+    _on_device("oscar_gather_int4", stream, (k_out, v_out, src_req, src_pos, desc.keep), lib.oscar_gather_int4, (
         ctypes.byref(desc), src_req.data_ptr(), src_pos.data_ptr(), n, k_out.data_ptr(), ks, v_out.data_ptr(), vs))
 
 
@@ -484,8 +501,10 @@ def oscar_decode_attention_int4(desc: Int4Desc, q, out, workspace, score=None, s
     _contiguous("out", out, (b, hq, d), 2)
     _slopes_ok(score, hq)
     size = c_size_t(workspace.numel() * workspace.element_size())
-    _on_device("oscar_decode_attention_int4", stream, (q, out, workspace), lib.oscar_decode_attention_int4, (
-        ctypes.byref(desc), _ref(score), q.data_ptr(), qs, out.data_ptr(), workspace.data_ptr(), ctypes.byref(size)))
+    _on_device("oscar_decode_attention_int4", stream, (q, out, workspace, desc.keep, score and score.keep),
+               lib.oscar_decode_attention_int4, (
+                   ctypes.byref(desc), _ref(score), q.data_ptr(), qs, out.data_ptr(), workspace.data_ptr(),
+                   ctypes.byref(size)))
 
 
 def oscar_prompt_workspace_bytes(desc: PromptDesc) -> int:
@@ -509,7 +528,8 @@ def oscar_prompt_attention(desc: PromptDesc, q, k, v, cu_q, cu_k, out, workspace
     _contiguous("lse", lse, (desc.total_q, hq), 4)
     _slopes_ok(score, hq)
     size = c_size_t(workspace.numel() * workspace.element_size())
-    _on_device("oscar_prompt_attention", stream, (q, k, v, cu_q, cu_k, out, workspace, prefix_len, lse),
+    _on_device("oscar_prompt_attention", stream, (
+        q, k, v, cu_q, cu_k, out, workspace, prefix_len, lse, desc.keep, score and score.keep),
                lib.oscar_prompt_attention, (
                    ctypes.byref(desc), _ref(score), q.data_ptr(), qs, _ptr(k), ks, _ptr(v), vs, cu_q.data_ptr(),
                    cu_k.data_ptr(), _ptr(prefix_len), out.data_ptr(), _ptr(lse), workspace.data_ptr(),

@@ -103,4 +103,5 @@ class Int4Cache:
         d.quant_group_k, d.quant_group_v = self.quant_group_k, self.quant_group_v
         for name in ("pages", "page_table", "seq_len", "dev_status"):
             setattr(d, name, getattr(self, name).data_ptr())
+        d.keep = self.pages
         return d

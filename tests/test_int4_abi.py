@@ -250,3 +250,58 @@ def test_binding_checks():
         B.oscar_prompt_attention(pd, row(3, 8), row(4, 2), row(4, 2), cu, cu, row(3, 8), torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(ValueError):
         B.oscar_prompt_attention(pd, row(3, 8), row(3, 2), row(3, 2), cu[:1], cu, row(3, 8), torch.zeros(256, dtype=torch.uint8))
+
+
+def test_binding_refuses_rows_of_other_types_and_descriptors_of_the_host():
+    """fp16 has bf16's size; a table, slopes or pages in host memory must not reach a kernel."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    from bit_rotated_kv_split_gb300.cache import Int4Cache
+    cache = Int4Cache(2, 8, 2, 64, 4, 8, device="cpu")
+    desc, idx = cache.desc(), torch.zeros(3, dtype=torch.int32)
+    assert desc.keep is cache.pages
+
+    def row(n, h, t=torch.bfloat16):
+        return torch.zeros(n, h, 64, dtype=t)
+
+    for over in (dict(q=row(3, 8, torch.float16)), dict(k=row(3, 2, torch.float16)), dict(q_out=row(3, 8, torch.float16)),
+                 dict(k_out=row(3, 2, torch.float16))):
+        a = dict(q=row(3, 8), k=row(3, 2), v=row(3, 2), dst_req=idx, dst_pos=idx, q_out=row(3, 8), k_out=None)
+        a.update(over)
+        with pytest.raises(ValueError, match="bfloat16"):
+            B.oscar_rope_append_int4(desc, None, **a)
+    with pytest.raises(ValueError, match="bfloat16"):
+        B.oscar_gather_int4(desc, idx, idx, row(3, 2), row(3, 2, torch.float16))
+    with pytest.raises(ValueError, match="bfloat16"):
+        B.oscar_decode_attention_int4(desc, row(2, 8), row(2, 8, torch.float16), torch.zeros(256, dtype=torch.uint8))
+    pd, cu = B.prompt_desc(1, 8, 2, 64, 3, 3, 3, 3), torch.zeros(2, dtype=torch.int32)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="float32"):
+        B.oscar_prompt_attention(pd, row(3, 8), row(3, 2), row(3, 2), cu, cu, row(3, 8), ws,
+                                 lse=torch.zeros(3, 8, dtype=torch.int32))
+
+    # of the tensors, only those that the descriptors point to are not on the device
+    class OnDevice:
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return 0
+
+    def dev(t):
+        return OnDevice(t)
+
+    a = [dev(row(3, 8)), dev(row(3, 2)), dev(row(3, 2)), dev(idx), dev(idx), dev(row(3, 8))]
+    with pytest.raises(ValueError, match="one CUDA device"):
+        B.oscar_rope_append_int4(desc, None, *a)
+    desc.keep = dev(cache.pages)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        B.oscar_rope_append_int4(desc, B.rope_desc(torch.zeros(4, 32), 32), *a)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        B.oscar_decode_attention_int4(desc, dev(row(2, 8)), dev(row(2, 8)), dev(ws), score=B.score_desc(slopes=torch.zeros(8)))
+    pd = B.prompt_desc(1, 8, 2, 64, 3, 3, 3, 3, dev_status=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="one CUDA device"):
+        B.oscar_prompt_attention(pd, dev(row(3, 8)), dev(row(3, 2)), dev(row(3, 2)), dev(cu), dev(cu), dev(row(3, 8)), dev(ws))
