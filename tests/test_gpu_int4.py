@@ -381,6 +381,22 @@ def test_decode_query_of_zeros_and_of_extreme_size():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("lens,softcap", [([300, 40, 5000], 0.0), ([20000, 1], 7.0)])
+def test_decode_query_with_nan_shows_and_stays_alone(lens, softcap):
+    """A NaN in a head's query makes that head's result NaN, its request's pages split or not, and no other's."""
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(77, lens, 6, 2, 64, 64, 64)
+    q = O.bf16(L.g.standard_normal((len(lens), 6, 64)))
+    ref, bound = decode_ref(L, q, softcap=softcap)
+    for b in range(len(lens)):
+        bad = dev_bf16(q)
+        bad[b, 4, 9] = float("nan")
+        out = host(run_decode(L, bad, B.score_desc(0.0, softcap, 0, None)))
+        assert np.isnan(out[b, 4]).all()
+        out[b, 4] = ref[b, 4]
+        assert (np.abs(out - ref) <= bound).all()
+
+
 @pytest.mark.parametrize("kscale,vscale", [(1e-3, 1e-4), (100.0, 3000.0)])
 def test_decode_small_and_large_values(kscale, vscale):
     """Scales near fp16's ends: keys and values far from 1, and a token with one large channel among small ones."""
