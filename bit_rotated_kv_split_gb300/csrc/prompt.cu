@@ -3,9 +3,9 @@
 // A CTA takes 2 x 128 query rows of one KV head: rows are (token, head) pairs
 // of the query heads that read it (up to 16), so that short
 // prompts fill the tiles and K and V are read once for those heads.  Keys come
-// in tiles of 128.  Ten warps: one brings Q, K and V by TMA, one issues the
-// MMAs, and four for each of the two row tiles do the softmax, one thread a
-// row.  Per key tile and row tile:
+// in tiles of 128.  One warp brings Q, K and V by TMA, one issues the MMAs, one
+// clears what no row sees of V, and four for each of the two row tiles do the
+// softmax, one thread a row.  Per key tile and row tile:
 //   S = Q K^T   A and B in shared memory, the 128 x 128 result in TMEM;
 //   P = 2^(S - m) in the thread's registers, written over S in TMEM as bf16 (the
 //               one rounding below fp32: the tensor cores take 16-bit operands);
@@ -16,14 +16,16 @@
 // first tiles).  Tiles of keys that the mask rules out for all rows are not
 // visited.  A few rows over many keys are split over the keys; the parts'
 // unnormalised sums go to the workspace and a second kernel joins them.  Where the
-// rows fit one tile, the two row tiles take alternate key tiles of a part.
+// rows fit one tile, the two row tiles take alternate key tiles of a part, and
+// are joined in the CTA before they go out (24 tokens on 32,000 keys: 36.7 us, with
+// twice the parts for the second kernel 40.9).
 //
-// Measured: 8,192 causal tokens of 32/8 heads x 128 in 411 us, 1.34 PFLOP/s (69 % of
+// Measured: 8,192 causal tokens of 32/8 heads x 128 in 388 us, 1.42 PFLOP/s (73 % of
 // the burst rate of a large GEMM), bound by shared memory beside the MMAs (S reads
 // 128 bytes a cycle for its two operands) and by the chain S, softmax, P, O: of a
-// step's 3,300 cycles a tile's softmax takes 1,300 and its two products 1,000.  24
-// tokens on 32,000 keys in 41 us (132 MB): 5.2 TB/s within the scan, then 4 us of first
-// loads and 8 of the join.  Slower: P handed over in halves (4 %), a second issuing
+// step's 3,100 cycles a tile's softmax takes 1,300 and its two products 1,000.  24
+// tokens on 32,000 keys in 37 us (132 MB): 5.2 TB/s within the scan, then 4 us of first
+// loads and 4 of the join.  Slower: P handed over in halves (4 %), a second issuing
 // warp (10 %), the maximum taken beside the powers (6 %).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -73,7 +75,7 @@ PromptPlan plan_prompt(const PromptParams& p) {
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   r.dual = r.splits > 1 && p.max_q <= per_tile;
   if (r.splits > 1) {
-    const size_t rows = size_t(ctas) * r.splits * 2 * kTile;
+    const size_t rows = size_t(ctas) * r.splits * (r.dual ? 1 : 2) * kTile;
     r.off_o = up(rows * 8);
     r.bytes = r.off_o + rows * p.d * 4;
   } else {
@@ -160,8 +162,13 @@ __device__ __forceinline__ float row_max(const float (&s)[kTile]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// Formed: the scores have a cap or a distance bias.
-template <int D, bool Formed>
+// What the scores go through before the softmax.  (In a kernel for all forms the
+// loop spills: 8k tokens without any took 406 us against 388, 4096 with a cap
+// 167 against 146.)
+enum Form { kPlain, kCapped, kBiased };   // kBiased: a distance bias, with or without a cap
+
+// Dual: one row tile, its key tiles to the two warpgroups in turn (PromptPlan's dual).
+template <int D, Form kForm, bool Dual>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_kernel(const __grid_constant__ PromptParams p, const PromptPlan plan, const __grid_constant__ CUtensorMap tq,
                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
@@ -180,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b = blockIdx.y, split = blockIdx.z;
   const PromptSpan sp = prompt_span(p, b, tid == 0 && blockIdx.x == 0 && split == 0);
   const int pack = plan.pack, per_tile = kTile / pack;   // tokens of a tile
-  const int dual = plan.dual, tok0 = blk * 2 * per_tile;
+  constexpr bool dual = Dual, kFormed = kForm != kPlain;
+  const int tok0 = blk * 2 * per_tile;
   if (tok0 >= sp.n_q) return;
   const int hq0 = set * pack, hk = hq0 / (p.n_q / p.n_kv), shift = sp.n_k - sp.n_q;   // position = shift + token
 
@@ -385,14 +393,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int w = warp >> 2, row = tid & (kTile - 1);
+    const int steps = w ? n[1] : n[0];     // (n[w] would put n, and with it the kernel, in local memory)
     const int tok = tok0 + (dual ? 0 : w * per_tile) + row / pack, head = hq0 + row % pack;
     const bool mine = row < pack * per_tile && tok < sp.n_q;   // (rows to spare hold anything)
     const int pos = shift + tok;
     const int row_lo = p.s.window && pos >= p.s.window ? pos - p.s.window + 1 : 0;
     const int row_hi = p.causal ? min(pos + 1, sp.n_k) : sp.n_k;
-    const float slope = Formed && p.s.slopes ? p.s.slopes[head] * kLog2e : 0.f;
-    const bool cap = Formed && p.s.cap_log2 != 0.f;
-    const float sc = Formed ? 1.f : p.s.scale_log2;
+    const float slope = kForm == kBiased ? p.s.slopes[head] * kLog2e : 0.f;
+    const bool cap = kForm == kCapped || (kForm == kBiased && p.s.cap_log2 != 0.f);
+    const float sc = kFormed ? 1.f : p.s.scale_log2;
     const float cap_in = p.s.cap_in * (0.5f * kLn2);      // scale / cap
     constexpr float kP[5] = {1.f, -0x1.5554a6p-2f, 0x1.10e47ap-3f, -0x1.b2167ep-5f, 0x1.18d7e8p-6f};
     float near[5];   // P of capped_near
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = tmem + lanes + w * kTile, t_o = tmem + lanes + kColO + w * D;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n[w]; ++j) {
+    for (int j = 0; j < steps; ++j) {
       ok = wait(&bar.s_full[w], j & 1);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kTile; ++i) far = fmaxf(far, fabsf(s[i]));
         // (a NaN is not above either: both ways keep it)
-        if (__any_sync(0xffffffffu, far * cap_in > 0.5f)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, far * cap_in > 0.5f), 0)) {
 #pragma unroll
           for (int i = 0; i < kTile; ++i) s[i] = capped(s[i], p.s);
         } else {
@@ -431,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (Formed && p.s.slopes) {
+      if (kForm == kBiased) {
         const float away = float(pos - k0);
 #pragma unroll
         for (int i = 0; i < kTile; ++i) s[i] = fmaf(-slope, fabsf(away - float(i)), cap ? s[i] : s[i] * p.s.scale_log2);
@@ -488,28 +497,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(&bar.p_full[w]);
     }
-    if (ok && n[w] > 0) {
-      ok = wait(&bar.o_done[w], (n[w] - 1) & 1);
+    if (ok && steps > 0) {
+      ok = wait(&bar.o_done[w], (steps - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
     const int64_t cta = (int64_t(b) * plan.blocks + blk) * plan.sets + set;
     if (plan.splits > 1) {
+      // a part: each row's maximum (log2 units), sum and channels.  One without
+      // keys, or without visible ones: l = 0, its channels are not read.
       uint8_t* ws = static_cast<uint8_t*>(p.workspace);
-      const int64_t at = (cta * plan.splits + split) * 2 * kTile + w * kTile + row;
-      // (a part without keys, or a row without visible ones: l = 0, its sums are not read)
-      if (mine) reinterpret_cast<float2*>(ws + plan.off_ml)[at] = make_float2(m == -INFINITY ? 0.f : m * sc, ok ? l : 0.f);
-      if (ok && n[w] > 0) {
-        float* po = reinterpret_cast<float*>(ws + plan.off_o) + at * D;
+      const int64_t at = (cta * plan.splits + split) * (dual ? 1 : 2) * kTile + (dual ? 0 : w * kTile) + row;
+      float* po = reinterpret_cast<float*>(ws + plan.off_o) + at * D;
+      float2 ml = make_float2(m == -INFINITY ? 0.f : m * sc, ok ? l : 0.f);
+      if (dual) {
+        // Both warpgroups hold the same rows.  Each gives the other its half of
+        // the channels, by way of the queries' place, and joins its own half.
+        float4* xo = reinterpret_cast<float4*>(sq);
+        float2* xml = reinterpret_cast<float2*>(ring);
+        constexpr int kChunks = D / 8;                    // 4 channels each, of half a row
+        auto chunk = [&](int half, int c) { return (half * kTile + row) * kChunks + (c ^ (row & (kChunks - 1))); };
+        named_barrier(1, 2 * kTile);                      // the products are done: their operands' place is free
+        if (ok && steps > 0) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(t_o + 32 * c, o);
-          tc_wait_ld();
-          if (mine)
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_o + (1 - w) * (D / 2) + 32 * c, o);
+            tc_wait_ld();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(po + 32 * c)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              reinterpret_cast<uint4*>(xo)[chunk(1 - w, 8 * c + i)] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        xml[w * kTile + row] = ml;
+        named_barrier(1, 2 * kTile);
+        const float2 other = xml[(1 - w) * kTile + row];
+        const float top = other.y == 0.f ? ml.x : ml.y == 0.f ? other.x : fmaxf(ml.x, other.x);
+        const float f = ml.y != 0.f ? exp2_fast(ml.x - top) : 0.f, g = other.y != 0.f ? exp2_fast(other.x - top) : 0.f;
+        const bool read = ok && steps > 0;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t o[32];
+          if (read) {
+            tmem_ld32(t_o + w * (D / 2) + 32 * c, o);
+            tc_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 x = make_float4(f * __uint_as_float(o[4 * i]), f * __uint_as_float(o[4 * i + 1]),
+                                   f * __uint_as_float(o[4 * i + 2]), f * __uint_as_float(o[4 * i + 3]));
+            if (other.y != 0.f) {
+              const float4 y = xo[chunk(w, 8 * c + i)];
+              x.x = fmaf(g, y.x, x.x), x.y = fmaf(g, y.y, x.y), x.z = fmaf(g, y.z, x.z), x.w = fmaf(g, y.w, x.w);
+            }
+            if (mine) reinterpret_cast<float4*>(po + w * (D / 2) + 32 * c)[i] = x;
+          }
+        }
+        ml = make_float2(top, fmaf(f, ml.y, g * other.y));
+        if (mine && w == 0) reinterpret_cast<float2*>(ws + plan.off_ml)[at] = ml;
+      } else {
+        if (mine) reinterpret_cast<float2*>(ws + plan.off_ml)[at] = ml;
+        if (ok && steps > 0) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_o + 32 * c, o);
+            tc_wait_ld();
+            if (mine)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<uint4*>(po + 32 * c)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
         }
       }
     } else {
@@ -519,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
-        if (ok && n[w] > 0) {
+        if (ok && steps > 0) {
           tmem_ld32(t_o + 32 * c, o);
           tc_wait_ld();
         } else {
@@ -565,8 +626,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptParams p, 
   const int tok = (blk * 2 + row / kTile) * per_tile + in_tile / plan.pack, head = set * plan.pack + in_tile % plan.pack;
   if (in_tile >= plan.pack * per_tile || tok >= sp.n_q) return;
   const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
-  const int parts = plan.splits * (1 + plan.dual);
-  const int64_t first = cta * plan.splits * 2 * kTile + row;    // parts are `rows` rows apart
+  const int parts = plan.splits;
+  const int64_t first = cta * parts * rows + row;    // parts are `rows` rows apart
   const float2* ml = reinterpret_cast<const float2*>(ws + plan.off_ml) + first;
   const float* po = reinterpret_cast<const float*>(ws + plan.off_o) + first * D + lane * kC;
   float mx = -INFINITY, sum = 0.f, o[kC] = {};
@@ -634,7 +695,7 @@ bool encode_rows(CUtensorMap* map, const uint16_t* x, int d, int heads, int64_t 
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool Formed>
+template <int D, Form kForm, bool Dual>
 cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t stream) {
   CUtensorMap tq, tk, tv;
   const uint16_t* k = p.total_k ? p.k : p.q;   // no key, no load: the maps only have to be well-formed
@@ -644,15 +705,22 @@ cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t s
       !encode_rows(&tv, v, D, p.n_kv, p.total_k, p.v_stride, 1, kTile))
     return cudaErrorInvalidValue;
   constexpr int bytes = 1024 + (2 + kRing<D>) * (D / 64) * kPanel;
-  cudaError_t e = set_smem_limit<prompt_kernel<D, Formed>>(bytes);
+  cudaError_t e = set_smem_limit<prompt_kernel<D, kForm, Dual>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t x = int64_t(plan.blocks) * plan.sets;
   if (x > 0x7fffffff || x * p.batch > 0x7fffffff / 32) return cudaErrorInvalidValue;
   const dim3 grid(unsigned(x), unsigned(p.batch), unsigned(plan.splits));
-  e = launch_pdl(prompt_kernel<D, Formed>, grid, dim3(kThreads), bytes, stream, p, plan, tq, tk, tv);
+  e = launch_pdl(prompt_kernel<D, kForm, Dual>, grid, dim3(kThreads), bytes, stream, p, plan, tq, tk, tv);
   if (e != cudaSuccess || plan.splits == 1) return e;
-  const int rows = plan.dual ? kTile : 2 * kTile;
+  const int rows = Dual ? kTile : 2 * kTile;
   return launch_pdl(prompt_join_kernel<D>, dim3(unsigned(x * p.batch * (rows / 8))), dim3(256), 0, stream, p, plan, rows);
+}
+
+template <int D>
+cudaError_t launch_d(const PromptParams& p, const PromptPlan& plan, cudaStream_t stream) {
+  if (p.s.slopes) return plan.dual ? launch<D, kBiased, true>(p, plan, stream) : launch<D, kBiased, false>(p, plan, stream);
+  if (p.s.cap_log2 != 0.f) return plan.dual ? launch<D, kCapped, true>(p, plan, stream) : launch<D, kCapped, false>(p, plan, stream);
+  return plan.dual ? launch<D, kPlain, true>(p, plan, stream) : launch<D, kPlain, false>(p, plan, stream);
 }
 
 }  // namespace
@@ -661,9 +729,7 @@ size_t prompt_workspace_bytes(const PromptParams& p) { return plan_prompt(p).byt
 
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   const PromptPlan plan = plan_prompt(p);
-  const bool formed = p.s.cap_log2 != 0.f || p.s.slopes;
-  if (p.d == 128) return formed ? launch<128, true>(p, plan, stream) : launch<128, false>(p, plan, stream);
-  return formed ? launch<64, true>(p, plan, stream) : launch<64, false>(p, plan, stream);
+  return p.d == 128 ? launch_d<128>(p, plan, stream) : launch_d<64>(p, plan, stream);
 }
 
 }  // namespace oscar
