@@ -395,7 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = warp >> 2, row = tid & (kTile - 1);
     const int steps = w ? n[1] : n[0];     // (n[w] would put n, and with it the kernel, in local memory)
     const int tok = tok0 + (dual ? 0 : w * per_tile) + row / pack, head = hq0 + row % pack;
-    const bool mine = row < pack * per_tile && tok < sp.n_q;   // (rows to spare hold anything)
+    // a query of this request (the rows to spare of a group that does not divide 128
+    // are never written: they hold what an earlier CTA left there)
+    const bool mine = row < pack * per_tile && tok < sp.n_q;
     const int pos = shift + tok;
     const int row_lo = p.s.window && pos >= p.s.window ? pos - p.s.window + 1 : 0;
     const int row_hi = p.causal ? min(pos + 1, sp.n_k) : sp.n_k;
@@ -424,13 +426,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_wait_ld();
       const int k0 = tile_of(dual ? 2 * j + w : j) * kTile;
       if (cap) {
+        // The form is chosen for each score by itself, so that a row's bits are its
+        // own; the vote only says whether any row needs the other one.
         float far = 0.f;
 #pragma unroll
         for (int i = 0; i < kTile; ++i) far = fmaxf(far, fabsf(s[i]));
         // (a NaN is not above either: both ways keep it)
-        if (__builtin_expect(__any_sync(0xffffffffu, far * cap_in > 0.5f), 0)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, mine && far * cap_in > 0.5f), 0)) {
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) s[i] = capped(s[i], p.s);
+          for (int i = 0; i < kTile; ++i) {
+            const float x = s[i];
+            s[i] = fabsf(x) * cap_in > 0.5f ? capped(x, p.s) : capped_near(make_float2(x, x), cap_in, near).x;
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < kTile / 2; ++i) {
@@ -455,11 +462,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (uint32_t(a + i) >= width && i >= pre) s[i] = -INFINITY;
       }
       const float mt = row_max(s);
-      // (nothing seen yet, nothing here: -inf - -inf is no growth)
-      if (__any_sync(0xffffffffu, (mt - m) * sc > 8.f)) {
-        const float mn = fmaxf(m, mt);
-        const float f = m == -INFINITY ? 0.f : exp2_fast((m - mn) * sc);
-        m = mn;
+      // Each row raises its own reference (a factor of 1 changes no bit of the other
+      // rows' O); rows to spare and other requests' rows, which may hold anything, have
+      // no say.  (Nothing seen yet, nothing here: -inf - -inf is no growth.)
+      const bool grows = mine && (mt - m) * sc > 8.f;
+      if (__any_sync(0xffffffffu, grows)) {
+        const float f = !grows ? 1.f : m == -INFINITY ? 0.f : exp2_fast((m - mt) * sc);
+        m = grows ? mt : m;
         l *= f;
         if (j > 0) {
           ok = __all_sync(0xffffffffu, wait(&bar.o_done[w], (j - 1) & 1));

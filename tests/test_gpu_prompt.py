@@ -265,3 +265,65 @@ def test_prompt_scores_far_apart_and_rows_of_one_key():
             r, r_abs, _ = O.masked_attention(O.modified_scores(q[:, h], k[:, h // 2], 0, softcap=softcap), v[:, h // 2])
             # fp32 scores of up to 2^13 are off by up to 2^-10 each, which their weights repeat
             assert (np.abs(got[:, h] - r) <= HALF_BF16 * (np.abs(r) + r_abs) + 2.0 ** -9 * r_abs + 2.0 ** -14).all()
+
+
+def spoil(d, size):
+    """Leaves queries of the given size in every SM's shared memory: all rows of every tile, whatever its head group."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g = torch.Generator(device="cuda").manual_seed(1)
+    b, n = 400, 64
+    q = (torch.randn(b * n, 4, d, generator=g, device="cuda") * size).to(torch.bfloat16)
+    k = torch.randn(b * n, 1, d, generator=g, device="cuda").to(torch.bfloat16)
+    desc = B.prompt_desc(b, 4, 1, d, n, n, b * n, b * n)
+    ws = torch.empty(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    cu = i32(np.arange(b + 1) * n)
+    B.oscar_prompt_attention(desc, q, k, k, cu, cu, torch.empty_like(q), ws)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("softcap", [0.0, 40.0])
+@pytest.mark.parametrize("group,nq,nk", [(3, 200, 700), (5, 300, 1000), (6, 31, 600), (7, 9, 4000), (15, 3, 5000)])
+def test_prompt_bits_do_not_depend_on_the_calls_before(group, nq, nk, softcap, d):
+    """A group that does not divide 128 leaves rows of a query tile over: what an earlier call left there has no say."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g = np.random.default_rng(group + nk)
+    q, k, v = (dev_bf16(g.standard_normal((n, h, d))) for n, h in ((nq, group), (nk, 1), (nk, 1)))
+    desc = B.prompt_desc(1, group, 1, d, nq, nk, nq, nk)
+    ws = torch.empty(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    res = []
+    for size in (0.0, 300.0, 1.0, 1e6):
+        spoil(d, size)
+        out, lse = torch.empty_like(q), torch.empty(nq, group, dtype=torch.float32, device="cuda")
+        B.oscar_prompt_attention(desc, q, k, v, i32([0, nq]), i32([0, nk]), out, ws, score=B.score_desc(softcap=softcap), lse=lse)
+        torch.cuda.synchronize()
+        res.append((out, lse))
+    for out, lse in res[1:]:
+        assert bool((out == res[0][0]).all()) and bool((lse == res[0][1]).all())
+
+
+@pytest.mark.parametrize("hq,softcap", [(4, 0.0), (4, 40.0), (3, 40.0), (8, 0.0)])
+def test_prompt_rows_do_not_reach_one_another(hq, softcap):
+    """Another request's queries and keys, or another query row of one's own, change no bit of a row, whatever their size."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g, d = np.random.default_rng(hq), 64
+    nq, nk = [40, 50], [700, 300]
+    q, k, v = (dev_bf16(g.standard_normal((n, h, d))) for n, h in ((90, hq), (1000, 1), (1000, 1)))
+    desc = B.prompt_desc(2, hq, 1, d, 50, 700, 90, 1000)
+    ws = torch.empty(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    res = []
+    for size in (1.0, 300.0, 2.0 ** -20):
+        a, b = q.clone(), k.clone()
+        a[40:] *= size
+        a[7, 0] *= size
+        b[700:] *= size
+        out, lse = torch.empty_like(q), torch.empty(90, hq, dtype=torch.float32, device="cuda")
+        B.oscar_prompt_attention(desc, a, b, v, i32([0, 40, 90]), i32([0, 700, 1000]), out, ws, score=B.score_desc(softcap=softcap),
+                                 lse=lse)
+        out[7, 0], lse[7, 0] = 0.0, 0.0
+        res.append((out[:40], lse[:40]))
+    torch.cuda.synchronize()
+    for out, lse in res[1:]:
+        assert bool((out == res[0][0]).all()) and bool((lse == res[0][1]).all())
