@@ -45,6 +45,7 @@ struct ScoreParams {
   float scale_log2;    // scale log2 e (no cap)
   float cap_in;        // 2 scale / cap log2 e: e^(2 x scale / cap) = 2^(x cap_in)
   float cap_log2;      // cap log2 e; 0 = no cap
+  float cap_near[5];   // scores up to half the cap are x P((x cap_in)^2): P's coefficients
   int32_t window;      // 0 = none
   const float* slopes; // natural units; NULL = none
 };

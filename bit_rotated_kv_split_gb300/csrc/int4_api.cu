@@ -66,6 +66,10 @@ oscar_status check_score(const oscar_score_desc* d, int32_t head_dim, oscar::Sco
   s->scale_log2 = float(scale * log2e);
   s->cap_in = d->softcap > 0.f ? float(2.0 * scale / double(d->softcap) * log2e) : 0.f;
   s->cap_log2 = float(double(d->softcap) * log2e);
+  // tanh(y) = y P(y^2) for |y| <= 1 / 2, and y = x cap_in ln 2 / 2
+  const double tanh_near[5] = {1., -0x1.5554a6p-2, 0x1.10e47ap-3, -0x1.b2167ep-5, 0x1.18d7e8p-6};
+  double unit = scale * log2e;
+  for (int k = 0; k < 5; ++k, unit /= 4. * log2e * log2e) s->cap_near[k] = float(tanh_near[k] * unit);
   if (!std::isnormal(s->scale_log2) || !std::isfinite(s->cap_in) || !std::isfinite(2.f * s->cap_log2))
     return OSCAR_ERR_INVALID_ARG;
   s->window = d->window;

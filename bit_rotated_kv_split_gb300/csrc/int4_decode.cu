@@ -552,16 +552,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (Formed) {
+        float far = 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) y[r][e] *= unscale[e], far = fmaxf(far, fabsf(y[r][e]));
         if (p.s.cap_log2 != 0.f) {
+          // (the vote skips a form that no score here needs; each score's own is its own)
+          if (__builtin_expect(__any_sync(0xffffffffu, !cap_is_near(far, p.s)), 0)) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) y[r][e] = capped(y[r][e] * unscale[e], p.s);
-        } else {
+              for (int e = 0; e < 2; ++e) y[r][e] = capped(y[r][e], p.s);
+          } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) y[r][e] *= unscale[e];
+              for (int e = 0; e < 2; ++e) y[r][e] = capped_near(y[r][e], p.s);
+          }
         }
         if (p.s.slopes) {
           const float away = float(tok + gid - (cur.len - 1));

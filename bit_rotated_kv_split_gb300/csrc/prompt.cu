@@ -132,17 +132,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
-// The capped score where |x| scale / cap <= 1 / 2: tanh(y) = y P(y^2), P of degree 4
-// fitted at the Chebyshev points of [0, 1 / 4] (6e-8 of the value in fp32); c
-// holds P's coefficients times cap.  By powers and reciprocals (two of the special
-// function unit's instructions a score, besides the softmax's one) a tile of 128
-// x 128 scores took twice as long.
-__device__ __forceinline__ float2 capped_near(float2 x, float cap_in, const float (&c)[5]) {
-  const float2 y = mul2(x, make_float2(cap_in, cap_in)), u = mul2(y, y);
+// capped_near of two scores; c holds its coefficients.  (By powers and reciprocals, two
+// of the special function unit's instructions a score besides the softmax's one, a
+// tile of 128 x 128 scores took twice as long.)
+__device__ __forceinline__ float2 capped_near2(float2 x, float cap_in, const float (&c)[5]) {
+  const float2 w = mul2(x, make_float2(cap_in, cap_in)), u = mul2(w, w);
   float2 r = make_float2(c[4], c[4]);
 #pragma unroll
   for (int k = 3; k >= 0; --k) r = fma2(r, u, make_float2(c[k], c[k]));
-  return mul2(y, r);
+  return mul2(x, r);
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -163,9 +161,9 @@ __device__ __forceinline__ float row_max(const float (&s)[kTile]) {
 }
 
 // What the scores go through before the softmax.  (In a kernel for all forms the
-// loop spills: 8k tokens without any took 406 us against 388, 4096 with a cap
-// 167 against 146.)
-enum Form { kPlain, kCapped, kBiased };   // kBiased: a distance bias, with or without a cap
+// loop spills: 8k tokens without any took 406 us against 388; 4096 with a bias, in one
+// for biases with and without a cap, 155 against 141.)
+enum Form { kPlain, kCapped, kBiased, kBiasedCapped };   // kBiased: a distance bias
 
 // Dual: one row tile, its key tiles to the two warpgroups in turn (PromptPlan's dual).
 template <int D, Form kForm, bool Dual>
@@ -188,6 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PromptSpan sp = prompt_span(p, b, tid == 0 && blockIdx.x == 0 && split == 0);
   const int pack = plan.pack, per_tile = kTile / pack;   // tokens of a tile
   constexpr bool dual = Dual, kFormed = kForm != kPlain;
+  constexpr bool kBias = kForm == kBiased || kForm == kBiasedCapped, kCap = kForm == kCapped || kForm == kBiasedCapped;
   const int tok0 = blk * 2 * per_tile;
   if (tok0 >= sp.n_q) return;
   const int hq0 = set * pack, hk = hq0 / (p.n_q / p.n_kv), shift = sp.n_k - sp.n_q;   // position = shift + token
@@ -401,14 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = shift + tok;
     const int row_lo = p.s.window && pos >= p.s.window ? pos - p.s.window + 1 : 0;
     const int row_hi = p.causal ? min(pos + 1, sp.n_k) : sp.n_k;
-    const float slope = kForm == kBiased ? p.s.slopes[head] * kLog2e : 0.f;
-    const bool cap = kForm == kCapped || (kForm == kBiased && p.s.cap_log2 != 0.f);
+    const float slope = kBias ? p.s.slopes[head] * kLog2e : 0.f;
     const float sc = kFormed ? 1.f : p.s.scale_log2;
-    const float cap_in = p.s.cap_in * (0.5f * kLn2);      // scale / cap
-    constexpr float kP[5] = {1.f, -0x1.5554a6p-2f, 0x1.10e47ap-3f, -0x1.b2167ep-5f, 0x1.18d7e8p-6f};
-    float near[5];   // P of capped_near
+    const float cap_in = p.s.cap_in;
+    float near[5];
 #pragma unroll
-    for (int k = 0; k < 5; ++k) near[k] = kP[k] * p.s.cap_log2;
+    for (int k = 0; k < 5; ++k) near[k] = p.s.cap_near[k];
     const uint32_t lanes = uint32_t(32 * (warp & 3)) << 16;
     const uint32_t t_s = tmem + lanes + w * kTile, t_o = tmem + lanes + kColO + w * D;
     float m = -INFINITY, l = 0.f;
@@ -425,32 +422,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, reinterpret_cast<uint32_t(&)[32]>(s[32 * c]));
       tc_wait_ld();
       const int k0 = tile_of(dual ? 2 * j + w : j) * kTile;
-      if (cap) {
-        // The form is chosen for each score by itself, so that a row's bits are its
-        // own; the vote only says whether any row needs the other one.
-        float far = 0.f;
+      if (kCap) {
+        // The form is chosen for each score by itself, so that a row's bits are its own;
+        // the votes skip the form that no score of theirs needs.
+        auto far = [&](int a, int b) {
+          float x = 0.f;
 #pragma unroll
-        for (int i = 0; i < kTile; ++i) far = fmaxf(far, fabsf(s[i]));
-        // (a NaN is not above either: both ways keep it)
-        if (__builtin_expect(__any_sync(0xffffffffu, mine && far * cap_in > 0.5f), 0)) {
+          for (int i = a; i < b; ++i) x = fmaxf(x, fabsf(s[i]));
+          // (a NaN is not above either: both ways keep it)
+          return __any_sync(0xffffffffu, mine && x * cap_in > kLog2e) != 0;
+        };
+        auto near_all = [&](int a, int b) {
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) {
-            const float x = s[i];
-            s[i] = fabsf(x) * cap_in > 0.5f ? capped(x, p.s) : capped_near(make_float2(x, x), cap_in, near).x;
+          for (int i = a; i < b; i += 2) {
+            const float2 t = capped_near2(make_float2(s[i], s[i + 1]), cap_in, near);
+            s[i] = t.x;
+            s[i + 1] = t.y;
           }
+        };
+        if (__builtin_expect(!far(0, kTile), 1)) {
+          near_all(0, kTile);
         } else {
+          // (32 keys at a time: the code for all of them at once spills)
 #pragma unroll
-          for (int i = 0; i < kTile / 2; ++i) {
-            const float2 t = capped_near(make_float2(s[2 * i], s[2 * i + 1]), cap_in, near);
-            s[2 * i] = t.x;
-            s[2 * i + 1] = t.y;
+          for (int c = 0; c < kTile; c += 32) {
+            if (far(c, c + 32)) {
+#pragma unroll
+              for (int i = c; i < c + 32; i += 2) {
+                const float2 t = capped_near2(make_float2(s[i], s[i + 1]), cap_in, near);
+                s[i] = capped_pick(s[i], t.x, p.s);
+                s[i + 1] = capped_pick(s[i + 1], t.y, p.s);
+              }
+            } else {
+              near_all(c, c + 32);
+            }
           }
         }
       }
-      if (kForm == kBiased) {
+      if (kBias) {
         const float away = float(pos - k0);
 #pragma unroll
-        for (int i = 0; i < kTile; ++i) s[i] = fmaf(-slope, fabsf(away - float(i)), cap ? s[i] : s[i] * p.s.scale_log2);
+        for (int i = 0; i < kTile; ++i) s[i] = fmaf(-slope, fabsf(away - float(i)), kCap ? s[i] : s[i] * p.s.scale_log2);
       }
       const bool full = (k0 >= row_lo && k0 + kTile <= row_hi) || k0 + kTile <= sp.prefix;
       if (!__all_sync(0xffffffffu, full)) {
@@ -725,11 +737,16 @@ cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t s
   return launch_pdl(prompt_join_kernel<D>, dim3(unsigned(x * p.batch * (rows / 8))), dim3(256), 0, stream, p, plan, rows);
 }
 
+template <int D, Form kForm>
+cudaError_t launch_f(const PromptParams& p, const PromptPlan& plan, cudaStream_t stream) {
+  return plan.dual ? launch<D, kForm, true>(p, plan, stream) : launch<D, kForm, false>(p, plan, stream);
+}
+
 template <int D>
 cudaError_t launch_d(const PromptParams& p, const PromptPlan& plan, cudaStream_t stream) {
-  if (p.s.slopes) return plan.dual ? launch<D, kBiased, true>(p, plan, stream) : launch<D, kBiased, false>(p, plan, stream);
-  if (p.s.cap_log2 != 0.f) return plan.dual ? launch<D, kCapped, true>(p, plan, stream) : launch<D, kCapped, false>(p, plan, stream);
-  return plan.dual ? launch<D, kPlain, true>(p, plan, stream) : launch<D, kPlain, false>(p, plan, stream);
+  const bool cap = p.s.cap_log2 != 0.f;
+  if (p.s.slopes) return cap ? launch_f<D, kBiasedCapped>(p, plan, stream) : launch_f<D, kBiased>(p, plan, stream);
+  return cap ? launch_f<D, kCapped>(p, plan, stream) : launch_f<D, kPlain>(p, plan, stream);
 }
 
 }  // namespace

@@ -555,3 +555,64 @@ def test_two_graphs_with_workspaces_of_their_own():
     torch.cuda.synchronize()
     for a, b in zip(want, outs):
         assert bool((a.view(torch.int16) == b.view(torch.int16)).all())
+
+
+def weighted_ref(L, q, **mods):
+    """(attention, its error bound) of q over what the cache stands for, each key's error counted with its weight.
+
+    A weight p (the largest of a row 1, their sum at least 1) is rounded to fp16 for the sums of zeros and weights, and
+    its product with the scale s once more: 2^-11 of p |v - out| and of p |s c|.  Below fp16's normal range (weights
+    are held times 2^7 or more, products times 2^-ve with s 2^-ve >= 2^-14) the steps are 2^-32 of a weight, and 2^-17
+    of s c.  fp32 sums, products and powers: 2^-13 of all terms.  The result is rounded to bf16.
+    """
+    slopes = mods.pop("slopes", None)
+    out, bound = np.zeros(q.shape), np.zeros(q.shape)
+    for b, n in enumerate(L.lens):
+        if n == 0:
+            continue
+        pos = np.arange(n)
+        c, s, z = O.int4_load(L.pool, L.table[b, pos // 16], pos % 16, 1, L.d, L.ngk, L.ngv)
+        sc = np.repeat(s.astype(np.float64), L.d // L.ngv, -1) * c
+        z = np.repeat(z.astype(np.float64), L.d // L.ngv, -1)
+        for h in range(L.hq):
+            kv = h // (L.hq // L.hk)
+            t = O.modified_scores(q[b, h:h + 1], L.k[b][:, kv], n - 1, slope=0.0 if slopes is None else float(slopes[h]), **mods)[0]
+            seen = np.isfinite(t)
+            p = np.exp(t[seen] - t[seen].max())
+            zv, sv = z[seen, kv], sc[seen, kv]
+            v = zv + sv
+            r = p @ v / p.sum()
+            away = np.abs(v - r)
+            near = 2.0 ** -11 * (p @ away + p @ sv) + 2.0 ** -13 * (p @ (np.abs(zv) + sv + away))
+            near += np.minimum(p, 2.0 ** -32) @ away + np.minimum(p, 2.0 ** -17) @ sv
+            out[b, h], bound[b, h] = r, np.abs(r) * HALF_BF16 + near / p.sum()
+    return out, bound
+
+
+@pytest.mark.parametrize("softcap", [1e3, 1e5, 1e7, 1e12, 1e30, 1e38])
+@pytest.mark.parametrize("d,slopes", [(128, False), (64, True)])
+def test_decode_large_caps_leave_ordinary_scores(softcap, d, slopes):
+    """Scores of ordinary size under a cap far above them: the cap's error is one of the score, not of the cap."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(91, [2000, 40, 3000], 8, 2, d, 64, 32)
+    q = O.bf16(L.g.standard_normal((3, 8, d)))
+    mods = dict(softcap=softcap)
+    sl = None
+    if slopes:
+        mods["slopes"] = np.exp2(-8.0 * np.arange(1, 9) / 8).astype(np.float32)
+        sl = torch.from_numpy(mods["slopes"]).cuda()
+    out = host(run_decode(L, dev_bf16(q), B.score_desc(0.0, softcap, 0, sl)))
+    ref, bound = weighted_ref(L, q, **mods)
+    assert (np.abs(out - ref) <= bound).all(), "worst %.3g of its bound" % np.nanmax(np.abs(out - ref) / bound)
+
+
+def test_decode_cap_of_scores_on_both_sides_of_it():
+    """Scores from a hundredth of the cap to a hundred times it in one request, small and large in the same warp."""
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(92, [700, 90], 4, 1, 128, 128, 128)
+    q = O.bf16(L.g.standard_normal((2, 4, 128)) * np.array([0.01, 0.3, 3.0, 60.0])[None, :, None])
+    for softcap in (1.0, 8.0, 300.0):
+        out = host(run_decode(L, dev_bf16(q), B.score_desc(0.0, softcap, 0, None)))
+        ref, bound = weighted_ref(L, q, softcap=softcap)
+        assert (np.abs(out - ref) <= bound).all()

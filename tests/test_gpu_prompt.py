@@ -327,3 +327,26 @@ def test_prompt_rows_do_not_reach_one_another(hq, softcap):
     torch.cuda.synchronize()
     for out, lse in res[1:]:
         assert bool((out == res[0][0]).all()) and bool((lse == res[0][1]).all())
+
+
+@pytest.mark.parametrize("softcap", [1e3, 1e5, 1e7, 1e12, 1e30, 1e38])
+def test_prompt_large_caps_leave_ordinary_scores(softcap):
+    """Scores of ordinary size under a cap far above them, with and without a row at the cap in the same warp: the
+    tolerances are those of the other cases."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    g, n, hq, d = np.random.default_rng(12), 200, 4, 64
+    q, k, v = (O.bf16(g.standard_normal((n, h, d))) for h in (hq, 1, 1))
+    for far in (False, True):
+        if far:
+            q[::9] *= 2.0 ** np.ceil(np.log2(min(softcap, 1e6)))
+        desc = B.prompt_desc(1, hq, 1, d, n, n, n, n)
+        ws = torch.empty(B.oscar_prompt_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+        out = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda")
+        B.oscar_prompt_attention(desc, dev_bf16(q), dev_bf16(k), dev_bf16(v), i32([0, n]), i32([0, n]), out, ws,
+                                 score=B.score_desc(softcap=softcap))
+        got = host(out)
+        rows = np.arange(n) % 9 != 0 if far else np.ones(n, bool)
+        for h in range(hq):
+            r, r_abs, _ = O.masked_attention(O.modified_scores(q[:, h], k[:, 0], 0, softcap=softcap), v[:, 0])
+            assert (np.abs(got[:, h] - r) <= HALF_BF16 * (np.abs(r) + r_abs) + 2.0 ** -14)[rows].all()
