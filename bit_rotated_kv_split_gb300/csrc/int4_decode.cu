@@ -33,7 +33,8 @@
 // native here: 38 us against 32 for 100k tokens.)
 // The weights' reference is raised only when a score exceeds it by 2^8, and
 // the values' scales are taken relative to a power of two above them, raised
-// when a larger one comes: both by one vote for two pages.
+// when a larger one comes: both by one vote for two pages.  Where a warp's scales lie
+// more than 2^14 apart, its segment is scanned anew in fp32 (scan_wide).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -139,6 +140,8 @@ __device__ __forceinline__ Span span_of(const Int4DecodeParams& p, int b, bool r
 // begins at place `at` of the row.
 struct Segment {
   int b, h, lo, hi, off, pages, len, first, at;
+  // a warp's first pair
+  __device__ __forceinline__ int place(int warp) const { return (warp - (at >> 1)) & (kWarps - 1); }
 };
 
 // Walks through a share, run by run.
@@ -170,6 +173,175 @@ struct Walk {
     at = end;
   }
 };
+
+// Joins the warps' states of heads h0 .. of a segment, 4 channels a thread: to `out`, or
+// to the workspace's partial state `slot` if that is not negative.
+template <int D>
+__device__ __forceinline__ void join_warps(const Int4DecodeParams& p, int hq0, int h0, int heads, int slot, int b,
+                                           const float* buf, const float (&sm_m)[kWarps][kHeads],
+                                           const float (&sm_l)[kWarps][kHeads]) {
+  const int i = threadIdx.x, h = h0 + i / (D / 4);
+  if (i >= kJoinHeads * (D / 4) || h >= heads) return;
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  float mx = -FLT_MAX, sum = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (sm_l[w][h] > 0.f) mx = fmaxf(mx, sm_m[w][h]);
+#pragma unroll 4
+  for (int w = 0; w < kWarps; ++w) {
+    const float l = sm_l[w][h], f = l > 0.f ? exp2_fast(sm_m[w][h] - mx) : 0.f;
+    const float4 x = reinterpret_cast<const float4*>(buf)[w * kJoinHeads * (D / 4) + i];
+    sum = fmaf(f, l, sum);
+    v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+  }
+  if (slot < 0) {
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    reinterpret_cast<uint2*>(p.out + (int64_t(b) * p.c.n_q + hq0) * D)[h0 * (D / 4) + i] =
+        make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
+  } else {
+    reinterpret_cast<float4*>(ws + kOffO)[(int64_t(slot) * kHeads + h0) * (D / 4) + i] = v;
+    if (i % (D / 4) == 0) reinterpret_cast<float2*>(ws + kOffMl)[slot * kHeads + h] = make_float2(mx, sum);
+  }
+}
+
+// 2^ve with ve in [-14, 16] is at least a scale of this size (fp16 bits) and any smaller one
+__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+  return min(max(((__float_as_int(half2_to_float2(bits).x) >> 23) & 255) - 126, -14), 16);
+}
+// Scales, relative to 2^ve, that fp16 holds with fewer bits: below 2^(ve - 14).
+// `least`: a lane's least ones that are not 0, less 1, as fp16 bits.  Whole warps.
+__device__ __forceinline__ bool scales_wide(int ve, uint32_t least) {
+  const int e = ve - 14;
+  const uint32_t from = e >= -14 ? uint32_t(e + 15) << 10 : e >= -24 ? 1u << (e + 24) : 1u;
+  return __any_sync(0xffffffffu, (least & 0xFFFFu) < from - 1 || (least >> 16) < from - 1);
+}
+
+// Once more, in fp32 throughout, those segments of the CTA's share whose values' scales
+// lie further apart within a warp's pages than products of fp16 numbers hold.  (A token
+// far above the others may have no weight, and the others are not to lose bits for it.)
+// Rare, and slower: with one such value in each KV head 100k tokens take 181 us, with one
+// in every page 216 (32 without).  Run after all segments, where nothing else is live: a
+// call within the loop over them cost 7 % of every decode, the products in bands of
+// scales there had the loop spill.
+//
+// A warp takes the pages it had, kJoinHeads heads at a time.  Lanes t and t + 16 take
+// half a row each of token t for the scores, then each lane D / 32 channels of all
+// tokens.  States as the scan leaves them, with the weights' 2^7.
+template <int D, int NGK, int NGV>
+__device__ __noinline__ void scan_wide(const Int4DecodeParams& p, Walk walk, int sets, int halves, float* buf_all,
+                                       float (&sm_m)[kWarps][kHeads], float (&sm_l)[kWarps][kHeads]) {
+  constexpr int C = D / 32, kBlock = int4_block_bytes(D, NGK, NGV);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 15, half = lane >> 4, ch = C * lane;
+  const int group = p.c.n_q / p.c.n_kv;
+  float* buf = buf_all + warp * kJoinHeads * D;
+  Segment cur;
+  __syncthreads();                          // the scan's states have been read
+  while (walk.next(p, sets, &cur)) {
+    const int hk = cur.h / halves, set = cur.h % halves, in_set = min(kHeads, group - set * kHeads);
+    const int lo = cur.lo + 2 * cur.place(warp);
+    const int32_t* table = p.c.page_table + int64_t(cur.b) * p.c.max_pages;
+    auto page_of = [&](int i) { return lo + (i >> 1) * 2 * kWarps + (i & 1); };
+    auto block_of = [&](int page) -> const uint8_t* {
+      const int id = page < cur.hi ? table[page] : -1;
+      return id < 0 || id >= p.c.n_pages ? nullptr : p.c.pages + (int64_t(id) * p.c.n_kv + hk) * kBlock;
+    };
+    // the scan's own test, a pair of pages at a time
+    uint32_t top = 0, least = 0xFFFFFFFFu;
+#pragma unroll 1
+    for (int i = 0; page_of(i) < cur.hi; i += 2) {
+      const int j = page_of(i + half) * kInt4Page + t;
+      const uint8_t* block = block_of(page_of(i + half));
+      if (block && j >= cur.first && j < cur.len)
+#pragma unroll
+        for (int g = 0; g < NGV; ++g) {
+          const uint32_t s = *reinterpret_cast<const uint16_t*>(block + int4_pair(D, NGK, NGV, t, NGK + g));
+          top = max(top, s);
+          least = min(least, (s - 1) & 0xFFFFu);
+        }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (!__syncthreads_or(scales_wide(scale_exponent(top), least | 0xFFFF0000u))) continue;
+
+#pragma unroll 1
+    for (int h0 = 0; h0 < in_set; h0 += kJoinHeads) {
+      const int heads = min(kJoinHeads, in_set - h0), hq0 = hk * group + set * kHeads + h0;
+      const uint16_t* q = p.q + cur.b * p.q_stride + int64_t(hq0) * D;
+      float m[kJoinHeads], l[kJoinHeads], o[kJoinHeads][C], slope[kJoinHeads];
+#pragma unroll
+      for (int h = 0; h < kJoinHeads; ++h) {
+        m[h] = -FLT_MAX, l[h] = 0.f;
+        slope[h] = p.s.slopes && h < heads ? p.s.slopes[hq0 + h] * kLog2e : 0.f;
+#pragma unroll
+        for (int n = 0; n < C; ++n) o[h][n] = 0.f;
+      }
+#pragma unroll 1
+      for (int i = 0; page_of(i) < cur.hi; ++i) {
+        const uint8_t* block = block_of(page_of(i));
+        if (!block) continue;
+        uint32_t vc[8], vp[16];
+#pragma unroll
+        for (int a = 0; a < 8; ++a) vc[a] = *reinterpret_cast<const uint32_t*>(block + int4_v_half(D, 2 * a, ch / 4)) >> (4 * (ch % 4));
+#pragma unroll
+        for (int a = 0; a < 16; ++a) vp[a] = *reinterpret_cast<const uint32_t*>(block + int4_pair(D, NGK, NGV, a, NGK + ch * NGV / D));
+        float x[kJoinHeads] = {};
+#pragma unroll 2
+        for (int e = half * (D / 16); e < (half + 1) * (D / 16); ++e) {      // octets
+          const uint32_t kc = *reinterpret_cast<const uint32_t*>(block + int4_k_word(D, t, e));
+          const float2 ks = half2_to_float2(*reinterpret_cast<const uint32_t*>(block + int4_pair(D, NGK, NGV, t, 8 * e * NGK / D)));
+          float k[8];
+#pragma unroll
+          for (int n = 0; n < 8; ++n) k[n] = fmaf(float((kc >> (4 * n)) & 15u), ks.x, ks.y);
+#pragma unroll
+          for (int h = 0; h < kJoinHeads; ++h)
+            if (h < heads) {
+              const uint4 u = *reinterpret_cast<const uint4*>(q + h * D + 8 * e);
+              x[h] = fmaf(bf16_lo(u.x), k[0], fmaf(bf16_hi(u.x), k[1], fmaf(bf16_lo(u.y), k[2], fmaf(bf16_hi(u.y), k[3], x[h]))));
+              x[h] = fmaf(bf16_lo(u.z), k[4], fmaf(bf16_hi(u.z), k[5], fmaf(bf16_lo(u.w), k[6], fmaf(bf16_hi(u.w), k[7], x[h]))));
+            }
+        }
+        const int j = page_of(i) * kInt4Page + t;
+#pragma unroll
+        for (int h = 0; h < kJoinHeads; ++h) {
+          float y = x[h] + __shfl_xor_sync(0xffffffffu, x[h], 16);
+          y = p.s.cap_log2 != 0.f ? capped(y, p.s) : y * p.s.scale_log2;
+          y = j >= cur.first && j < cur.len ? fmaf(slope[h], float(j - (cur.len - 1)), y) : -INFINITY;
+          float mn = fmaxf(m[h], y);
+#pragma unroll
+          for (int n = 8; n; n >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, n));
+          const float f = exp2_fast(m[h] - mn), g = exp2_fast(y - mn);
+          m[h] = mn;
+          float sum = g;
+#pragma unroll
+          for (int n = 8; n; n >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, n);
+          l[h] = fmaf(l[h], f, sum);
+#pragma unroll
+          for (int n = 0; n < C; ++n) o[h][n] *= f;
+#pragma unroll
+          for (int a = 0; a < 16; ++a) {
+            const float w = __shfl_sync(0xffffffffu, g, a);
+            const float2 vs = half2_to_float2(vp[a]);
+#pragma unroll
+            for (int n = 0; n < C; ++n)
+              if (w != 0.f)                     // (a stale slot holds anything; a NaN stays one)
+                o[h][n] = fmaf(w, fmaf(float((vc[a / 2] >> (16 * (a & 1) + 4 * n)) & 15u), vs.x, vs.y), o[h][n]);
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < kJoinHeads; ++h)
+        if (h < heads) {
+#pragma unroll
+          for (int n = 0; n < C; ++n) buf[h * D + ch + n] = 128.f * o[h][n];
+          if (lane == 0) sm_m[warp][h0 + h] = m[h], sm_l[warp][h0 + h] = 128.f * l[h];
+        }
+      __syncthreads();
+      const bool whole = cur.off == 0 && cur.hi - cur.lo == cur.pages;
+      join_warps<D>(p, hk * group + set * kHeads, h0, in_set, whole ? -1 : 2 * int(blockIdx.x) + (cur.off == 0), cur.b, buf_all, sm_m, sm_l);
+      __syncthreads();                      // the states have been read
+    }
+  }
+}
 
 // A run in more than one share: its place in the row, pages, request, first
 // query head and their number.
@@ -257,11 +429,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ Walk sm_walk, sm_walks[kWarps];
   __shared__ Segment sm_next[kWarps];
   __shared__ Part sm_part[2];
-  __shared__ int sm_last[2];
+  __shared__ int sm_last[2], sm_wide;     // (a segment of this CTA has to be scanned by scan_wide)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
   if (lane < kStages) mbar_init(&bars[warp][lane], 1);
   fence_mbar_init();
   __syncwarp();
+  if (threadIdx.x == 0) sm_wide = 0;
   pdl_wait();
   pdl_launch_dependents();
   const Int4Cache& c = p.c;
@@ -332,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* ring = smem + warp * (kStages * 2 * kBlock);
   float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * kBlock);
   uint64_t* wbars = bars[warp];
-  auto place = [&](const Segment& s) { return (warp - (s.at >> 1)) & (kWarps - 1); };
+  auto place = [&](const Segment& s) { return s.place(warp); };
   // the segment being brought in: its pages from this warp's first, KV head, request, and pairs
   int in_lo, in_hi, in_hk, in_b, in_it = 0, in_n;
   auto turn_to = [&](const Segment& s) {
@@ -475,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int t = 0; t < 2 * W; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
     int ve = -14;                           // the V scales seen are at most 2^ve
     uint32_t vs_top = 0x0400u, vs_mul = 0x74007400u;   // 2^ve, and 2^-ve twice, in fp16
+    uint32_t vs_least = 0xFFFFFFFFu;        // one below the least scale seen that is not 0, fp16 bits twice
     const uint32_t z_keep = gid < NGV ? 0xffffffffu : 0u, z_one = gid == NGV ? 0x3C003C00u : 0u;
 
     int tok = lo * kInt4Page;
@@ -533,23 +707,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       // the values' scales and zeros of tokens 8 i + 2 tig, + 1
-      uint32_t vs[4][NGV], vz[4], smax = 0;
+      uint32_t vs[4][NGV], vz[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint8_t* pp = blk + (i >> 1) * kBlock + kPairs + 4 * NG * (8 * (i & 1) + 2 * tig);
         uint32_t pr[2 * NG];
         lds_n(pr, pp);
 #pragma unroll
-        for (int g = 0; g < NGV; ++g) {
-          vs[i][g] = prmt(pr[NGK + g], pr[NG + NGK + g], 0x5410);
-          smax = __vmaxu2(smax, vs[i][g]);  // (fp16 values >= 0 order as integers)
-        }
+        for (int g = 0; g < NGV; ++g) vs[i][g] = prmt(pr[NGK + g], pr[NG + NGK + g], 0x5410);
         if constexpr (NGV == 1) {
           vz[i] = prmt(pr[NGK], pr[NG + NGK], 0x7632);
         } else {                            // group gid's, for the row that sums it
           const uint32_t* zp = reinterpret_cast<const uint32_t*>(pp) + NGK + (gid & (NGV - 1));
           vz[i] = prmt(zp[0], zp[NG], 0x7632);
         }
+      }
+      // lane i: token i's scales, two to a word (fp16 values >= 0 order as integers)
+      uint32_t own[(NGV + 1) / 2];
+      {
+        const uint32_t* pp = reinterpret_cast<const uint32_t*>(blk + (lane >> 4) * kBlock + kPairs + 4 * NG * (lane & 15)) + NGK;
+#pragma unroll
+        for (int g = 0; g < (NGV + 1) / 2; ++g) own[g] = NGV == 1 ? pp[0] & 0xFFFFu : prmt(pp[2 * g], pp[2 * g + 1], 0x5410);
       }
       if (Formed) {
         float far = 0.f;
@@ -582,7 +760,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint32_t gone = (ring_dead >> (2 * st)) & 3u;
       if (gone || tok < cur.first || tok + 2 * kInt4Page > cur.len) {
         // what a stale slot holds is anything
-        smax = 0;
+        const bool here = !((gone >> (lane >> 4)) & 1u) && tok + lane >= cur.first && tok + lane < cur.len;
+#pragma unroll
+        for (int g = 0; g < (NGV + 1) / 2; ++g) own[g] = here ? own[g] : 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool out_of = (gone >> (i >> 1)) & 1u;
@@ -593,19 +773,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (!out_of && j2 + 1 >= cur.first && j2 + 1 < cur.len) keep |= 0xFFFF0000u;
           vz[i] &= keep;
 #pragma unroll
-          for (int g = 0; g < NGV; ++g) {
-            vs[i][g] &= keep;
-            smax = __vmaxu2(smax, vs[i][g]);
-          }
+          for (int g = 0; g < NGV; ++g) vs[i][g] &= keep;
         }
+      }
+      uint32_t smax = own[0];
+      vs_least = __viaddmin_u16x2(own[0], 0xFFFFFFFFu, vs_least);
+      if constexpr (NGV == 4) {
+        smax = __vmaxu2(smax, own[1]);
+        vs_least = __viaddmin_u16x2(own[1], 0xFFFFFFFFu, vs_least);
       }
       const float y0 = fmaxf(fmaxf(y[0][0], y[1][0]), fmaxf(y[2][0], y[3][0]));
       const float y1 = fmaxf(fmaxf(y[0][1], y[1][1]), fmaxf(y[2][1], y[3][1]));
       if (__any_sync(0xffffffffu, (y0 > thr[0]) | (y1 > thr[1]) | ((smax & 0xFFFFu) > vs_top) | ((smax >> 16) > vs_top))) {
-        const float2 two = half2_to_float2(smax);
-        // 2^e >= top for the exponent e of top plus one
-        const float top = max_over_quad(fmaxf(two.x, two.y));
-        const int ne = min(max(ve, ((__float_as_int(top) >> 23) & 255) - 126), 16);
+        const int ne = max(ve, scale_exponent(__reduce_max_sync(0xffffffffu, max(smax & 0xFFFFu, smax >> 16))));
         const float fv = pow2i(ve - ne);
         ve = ne;
         vs_top = ve < 16 ? uint32_t(ve + 15) << 10 : 0xFFFFu;
@@ -669,10 +849,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int g = 0; g < NGV; ++g) z[g][e] = __shfl_sync(0xffffffffu, zl[e], 4 * g + tig);
     }
+    if (scales_wide(ve, vs_least) && !dead) sm_wide = 1;
     const bool whole = cur.off == 0 && cur.hi - cur.lo == cur.pages;
-    uint8_t* ws = static_cast<uint8_t*>(p.workspace);
     const int slot = 2 * blockIdx.x + (cur.off == 0);
-    uint16_t* out = p.out + (int64_t(cur.b) * c.n_q + hq0) * D;
     for (int h0 = 0; h0 < heads; h0 += kJoinHeads) {
       if (h0) __syncthreads();              // the heads before have been read
       if (2 * tig >= h0 && 2 * tig < h0 + kJoinHeads) {
@@ -687,29 +866,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
       }
       __syncthreads();
-      const int i = threadIdx.x, h = h0 + i / (D / 4);      // 4 channels a thread
-      if (i < kJoinHeads * (D / 4) && h < heads) {
-        float mx = -FLT_MAX, sum = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-          if (sm_l[w][h] > 0.f) mx = fmaxf(mx, sm_m[w][h]);
-#pragma unroll 4
-        for (int w = 0; w < kWarps; ++w) {
-          const float l = sm_l[w][h], f = l > 0.f ? exp2_fast(sm_m[w][h] - mx) : 0.f;
-          const float4 x = reinterpret_cast<const float4*>(buf)[w * kJoinHeads * (D / 4) + i];
-          sum = fmaf(f, l, sum);
-          v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
-        }
-        if (whole) {
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
-          reinterpret_cast<uint2*>(out)[h0 * (D / 4) + i] =
-              make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
-        } else {
-          reinterpret_cast<float4*>(ws + kOffO)[(int64_t(slot) * kHeads + h0) * (D / 4) + i] = v;
-          if (i % (D / 4) == 0) reinterpret_cast<float2*>(ws + kOffMl)[slot * kHeads + h] = make_float2(mx, sum);
-        }
-      }
+      join_warps<D>(p, hq0, h0, heads, whole ? -1 : slot, cur.b, buf, sm_m, sm_l);
     }
     if (!whole && threadIdx.x == 0) sm_part[cur.off == 0] = {cur.at - cur.off, cur.pages, cur.b, hq0, heads};
     has_part |= whole ? 0 : 1 << (cur.off == 0);
@@ -724,6 +881,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       while (flying < kStages && bring()) {
       }
   }
+  if (__builtin_expect(sm_wide, 0)) scan_wide<D, NGK, NGV>(p, sm_walk, sets, halves, buf, sm_m, sm_l);
   if (!has_part) return;
 
   // The runs that this CTA has a part of (the first of its share, the last, or

@@ -616,3 +616,81 @@ def test_decode_cap_of_scores_on_both_sides_of_it():
         out = host(run_decode(L, dev_bf16(q), B.score_desc(0.0, softcap, 0, None)))
         ref, bound = weighted_ref(L, q, softcap=softcap)
         assert (np.abs(out - ref) <= bound).all()
+
+
+
+
+@pytest.mark.parametrize("gk,gv,big,lens,hq,d,mods", [
+    (128, 128, 3.0, [900, 2500], 4, 128, {}),
+    (32, 32, 300.0, [900, 2500], 4, 128, {}),
+    (64, 64, 6e4, [900, 2500], 12, 128, {}),
+    (32, 64, 6e4, [3, 17, 1100], 5, 64, dict(softcap=100.0)),
+    (128, 32, 6e4, [2500], 8, 128, dict(window=2000, slopes=True)),
+    (64, 32, 6e4, [9000, 33, 0, 5000], 9, 64, {}),             # split over CTAs
+])
+def test_decode_large_value_of_no_weight_leaves_small_ones(gk, gv, big, lens, hq, d, mods):
+    """One token's values far above all others': a head that gives it no weight keeps its precision, one that gives it all
+    takes it."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(93, lens, hq, 1, d, gk, gv, fill=False)
+    q = np.zeros((len(lens), hq, d))
+    for b, n in enumerate(L.lens):
+        k = O.bf16(L.g.standard_normal((n, 1, d)))
+        v = O.bf16(L.g.standard_normal((n, 1, d)) * 0.003 + 0.01)
+        if n:
+            k[n // 3, 0, 5] = 64.0
+            v[n // 3] = O.bf16(L.g.standard_normal((1, d)).clip(-1, 1) * big)
+        L.k.append(L.put(b, np.arange(n), 0, k)), L.v.append(L.put(b, np.arange(n), 1, v))
+        q[b] = O.bf16(L.g.standard_normal((hq, d)) * 0.1)
+        q[b, :, 5] = np.resize([-16.0, 16.0, -20.0, 0.5], hq)
+    L.cache.pages.copy_(torch.from_numpy(L.pool.reshape(-1)))
+    mods, sl = dict(mods), None
+    if mods.get("slopes"):
+        mods["slopes"] = np.exp2(-8.0 * np.arange(1, hq + 1) / hq).astype(np.float32)
+        sl = torch.from_numpy(mods["slopes"]).cuda()
+    out = host(run_decode(L, dev_bf16(q), B.score_desc(0.0, mods.get("softcap", 0.0), mods.get("window", 0), sl)))
+    ref, bound = weighted_ref(L, q, **mods)
+    err = np.abs(out - ref)
+    assert (err <= bound).all(), "worst %.3g of its bound" % np.nanmax(err / np.maximum(bound, 1e-30))
+    assert L.status() == 0
+
+
+def test_decode_large_value_among_small_ones_on_bad_pages():
+    """The same where a page is not in the pool: it is passed over and reported."""
+    import torch
+    L = Layer(98, [200, 50], 6, 2, 128, 64, 32, fill=False)
+    for b, n in enumerate(L.lens):
+        k, v = O.bf16(L.g.standard_normal((n, 2, 128))), O.bf16(L.g.standard_normal((n, 2, 128)) * 0.003 + 0.01)
+        k[5, :, 5], v[5] = 64.0, 5e4
+        v[5, :, ::2] = -5e4
+        L.k.append(L.put(b, np.arange(n), 0, k)), L.v.append(L.put(b, np.arange(n), 1, v))
+    L.cache.pages.copy_(torch.from_numpy(L.pool.reshape(-1)))
+    L.cache.page_table[1, 1] = 1000                 # tokens 16 .. 31 of request 1 are passed over
+    q = O.bf16(L.g.standard_normal((2, 6, 128)) * 0.1)
+    q[:, :, 5] = -20.0
+    out = host(run_decode(L, dev_bf16(q)))
+    assert L.status() == 1
+    keep = np.r_[0:16, 32:50]
+    L.lens, L.k[1] = [200, 34], L.k[1][keep]
+    first, second = L.table[1, 0], L.table[1, 2]    # tokens 32 .. 49 as 16 .. 33
+    L.table[1, 1], L.table[1, 2], L.table[1, 0] = second, L.table[1, 3], first
+    ref, bound = weighted_ref(L, q)
+    assert (np.abs(out - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("spread", [4, 12, 20])
+def test_decode_values_of_all_sizes(spread):
+    """Tokens and groups of values from 2^-spread to 2^13 (scales down into fp16's subnormal range, some 0)."""
+    import torch
+    L = Layer(94, [1300, 33], 6, 2, 128, 64, 32, fill=False)
+    for b, n in enumerate(L.lens):
+        k = O.bf16(L.g.standard_normal((n, 2, 128)))
+        v = O.bf16(L.g.standard_normal((n, 2, 128)) * 2.0 ** L.g.integers(-spread, 14, (n, 2, 1)) *
+                   np.repeat(2.0 ** -L.g.integers(0, 5, (n, 2, 4)) * (L.g.random((n, 2, 4)) < 0.9), 32, -1))
+        L.k.append(L.put(b, np.arange(n), 0, k)), L.v.append(L.put(b, np.arange(n), 1, v))
+    L.cache.pages.copy_(torch.from_numpy(L.pool.reshape(-1)))
+    q = O.bf16(L.g.standard_normal((2, 6, 128)))
+    out = host(run_decode(L, dev_bf16(q)))
+    ref, bound = weighted_ref(L, q)
+    assert (np.abs(out - ref) <= bound).all(), "worst %.3g of its bound" % np.nanmax(np.abs(out - ref) / bound)
