@@ -694,3 +694,76 @@ def test_decode_values_of_all_sizes(spread):
     out = host(run_decode(L, dev_bf16(q)))
     ref, bound = weighted_ref(L, q)
     assert (np.abs(out - ref) <= bound).all(), "worst %.3g of its bound" % np.nanmax(np.abs(out - ref) / bound)
+
+
+@pytest.mark.parametrize("lens,hq,hk,d,gk,gv,window", [
+    ([777, 64, 65, 1024, 1025], 4, 2, 64, 64, 64, 0),
+    ([5000], 9, 1, 64, 32, 32, 0),
+    ([9000, 5, 0, 7000, 1025, 1024, 1023, 1039, 2], 4, 2, 64, 32, 64, 0),
+    ([30000, 1, 12000], 12, 1, 128, 64, 64, 0),
+    ([40000], 8, 8, 128, 128, 128, 20001),
+    ([0, 3, 0, 0, 17] * 60 + [900, 0, 1, 2100, 64, 65], 2, 1, 64, 64, 32, 0),
+    ([6000, 6000, 6001, 5999, 1, 6000], 8, 2, 128, 128, 64, 1500),
+    ([2000] * 33, 2, 2, 64, 64, 64, 0),
+])
+def test_decode_counts_each_page_once(lens, hq, hk, d, gk, gv, window):
+    """Equal weights, and values that are 1 in one channel for the pages of one remainder mod d: a page left out or taken
+    twice, at the ends of a run or of a CTA's share or within them, moves that channel by several times its bound."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(sum(lens) + d, lens, hq, hk, d, gk, gv, fill=False)
+    for b, n in enumerate(lens):
+        v = np.zeros((n, hk, d))
+        v[np.arange(n), :, np.arange(n) // 16 % d] = 1.0
+        L.k.append(L.put(b, np.arange(n), 0, O.bf16(L.g.standard_normal((n, hk, d))))), L.v.append(L.put(b, np.arange(n), 1, v))
+    L.cache.pages.copy_(torch.from_numpy(L.pool.reshape(-1)))
+    q = np.zeros((len(lens), hq, d))
+    out = host(run_decode(L, dev_bf16(q), B.score_desc(0.0, 0.0, window, None)))
+    ref, bound = weighted_ref(L, q, window=window)
+    assert (np.abs(out - ref) <= bound).all(), "worst %.3g of its bound" % np.nanmax(np.abs(out - ref) / np.maximum(bound, 1e-30))
+    for b, n in enumerate(lens):
+        if n > 16:
+            assert bound[b].max() < 0.5 * 16 / min(n, window or n)
+
+
+@pytest.mark.parametrize("lens", [[1000, 40], [6000, 3]])
+def test_decode_queries_of_all_sizes_with_keys_apart(lens):
+    """Queries of 2^-100 to 2^16 with, for each head, one key whose score is several times all others': the small ones take
+    the mean, the large ones that key's value, each within the weighted bound."""
+    import torch
+    L = Layer(99, lens, 4, 1, 64, 64, 32, fill=False)
+    sizes = 2.0 ** np.array([-100.0, 3.0, 12.0, 16.0])
+    q = np.zeros((len(lens), 4, 64))
+    for b, n in enumerate(lens):
+        unit = O.bf16(L.g.standard_normal((4, 64)))
+        k, v = O.bf16(L.g.standard_normal((n, 1, 64))), O.bf16(L.g.standard_normal((n, 1, 64)))
+        for h in range(4):
+            k[(h + 1) * n // 5, 0] = 4.0 * np.sign(unit[h])
+        L.k.append(L.put(b, np.arange(n), 0, k)), L.v.append(L.put(b, np.arange(n), 1, v))
+        q[b] = unit * sizes[:, None]
+    L.cache.pages.copy_(torch.from_numpy(L.pool.reshape(-1)))
+    out = host(run_decode(L, dev_bf16(q)))
+    ref, bound = weighted_ref(L, q)
+    assert (np.abs(out - ref) <= bound).all(), "worst %.3g of its bound" % np.nanmax(np.abs(out - ref) / bound)
+    for b, n in enumerate(lens):
+        if n > 4:
+            for h in (2, 3):
+                np.testing.assert_allclose(out[b, h], L.v[b][(h + 1) * n // 5, 0], rtol=2.0 ** -8 + 2.0 ** -10, atol=2.0 ** -9)
+
+
+@pytest.mark.parametrize("lens,hq,hk,d,gk,gv,mods", RAGGED + DECODES)
+def test_decode_within_the_weighted_bound(lens, hq, hk, d, gk, gv, mods):
+    """The batches above with each key's error counted with its weight, which for long requests is a small part of what the
+    largest value would allow."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(sum(lens) + hq, lens, hq, hk, d, gk, gv)
+    mods, sl = dict(mods), None
+    if mods.get("slopes"):
+        mods["slopes"] = np.exp2(-8.0 * np.arange(1, hq + 1) / hq).astype(np.float32)
+        sl = torch.from_numpy(mods["slopes"]).cuda()
+    q = O.bf16(L.g.standard_normal((len(lens), hq, d)))
+    score = B.score_desc(mods.get("scale", 0.0), mods.get("softcap", 0.0), mods.get("window", 0), sl)
+    out = host(run_decode(L, dev_bf16(q), score))
+    ref, bound = weighted_ref(L, q, **mods)
+    assert (np.abs(out - ref) <= bound).all(), "worst %.3g of its bound" % np.nanmax(np.abs(out - ref) / np.maximum(bound, 1e-30))
