@@ -65,14 +65,22 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 bf16_pair(uint32_t u) { return make_float2(bf16_lo(u), bf16_hi(u)); }
 
+// a - b >= 0, to odd: where 24 bits do not hold it, the last one is set.  A quotient of it
+// is then not taken for a tie of fewer bits that the exact one only comes near to.
+__device__ __forceinline__ float sub_odd(float a, float b) {
+  const float lo = __fsub_rz(a, b), hi = __fsub_ru(a, b);   // (a - a is +0 in both)
+  return __uint_as_float(__float_as_uint(lo) | (lo != hi ? 1u : 0u));
+}
+
 // Codes of the 8 bf16 values u of this lane (x - zero over scale, to nearest
 // even, 0 .. 15) in a group of `lanes` lanes; *pair = (scale, zero), fp16 bits.
+// Scales and codes are those of exact differences.
 //
 // The group's extremes are taken on packed bf16 (max x, max -x).  rint(t / s)
 // is taken as rint(t / s by an approximate reciprocal) and checked: where the
-// remainder t - k s (one fma) comes within 2^-19 of half a step, the quotients
-// are divided out.  (With a division for every value the kernel had a third
-// more instructions.)
+// remainder t - k s (one fma) comes within 1e-6 of half a step (t's own rounding, 2^-24
+// of at most 15.5 steps, is below that), the quotients are divided out.
+// (With a division for every value the kernel had a third more instructions.)
 __device__ __forceinline__ uint32_t quantise8(const uint4& u, float tau, int lanes, uint32_t* pair) {
   uint32_t hi2 = max_bf16x2(max_bf16x2(u.x, u.y), max_bf16x2(u.z, u.w));
   uint32_t lo2 = max_bf16x2(max_bf16x2(u.x ^ 0x80008000u, u.y ^ 0x80008000u),
@@ -82,7 +90,8 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& u, float tau, int lan
   float hi = bf16_lo(ends), lo = -bf16_hi(ends);
   float x[8];
   unpack_bf16x8(u, x);
-  if (!(hi <= tau && lo >= -tau)) {       // clamped values, or a NaN, which becomes -tau
+  const bool clamped = !(hi <= tau && lo >= -tau);
+  if (clamped) {                          // or a NaN, which becomes -tau
     hi = -tau, lo = tau;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -97,7 +106,10 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& u, float tau, int lan
       lo = fminf(lo, __shfl_xor_sync(group, lo, m));
     }
   }
-  const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f)), zh = __float2half_rn(lo);
+  // (a range of two bf16 numbers comes near a tie of a normal scale only where 24 bits hold it)
+  float range = hi - lo;
+  if (clamped || range < 1e-3f) range = sub_odd(hi, lo);
+  const __half sh = __float2half_rn(__fdiv_rn(range, 15.f)), zh = __float2half_rn(lo);
   const float s = __half2float(sh), z = __half2float(zh);
   *pair = uint32_t(__half_as_ushort(sh)) | (uint32_t(__half_as_ushort(zh)) << 16);
   const float inv = rcp_fast(s), top = 15.f * s, half = s * 0.499999f;
@@ -106,16 +118,18 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& u, float tau, int lan
   bool near = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[i] = fminf(fmaxf(x[i] - z, 0.f), top);
-    const float k = fmaf(x[i], inv, kRound);
-    near = near | (fabsf(fmaf(kRound - k, s, x[i])) >= half);
+    const float t = fminf(fmaxf(x[i] - z, 0.f), top), k = fmaf(t, inv, kRound);
+    near = near | (fabsf(fmaf(kRound - k, s, t)) >= half);
     word += (__float_as_uint(k) - 0x4B400000u) << (4 * i);
   }
   if (!(s > 0.f)) return 0;
   if (near) {
     word = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) word |= uint32_t(rintf(__fdiv_rn(x[i], s))) << (4 * i);
+    for (int i = 0; i < 8; ++i) {
+      const float t = fminf(fmaxf(sub_odd(x[i], z), 0.f), top);
+      word |= uint32_t(rintf(__fdiv_rn(t, s))) << (4 * i);
+    }
   }
   return word;
 }

@@ -767,3 +767,47 @@ def test_decode_within_the_weighted_bound(lens, hq, hk, d, gk, gv, mods):
     out = host(run_decode(L, dev_bf16(q), score))
     ref, bound = weighted_ref(L, q, **mods)
     assert (np.abs(out - ref) <= bound).all(), "worst %.3g of its bound" % np.nanmax(np.abs(out - ref) / np.maximum(bound, 1e-30))
+
+
+def test_append_codes_where_differences_need_more_than_fp32():
+    """Quotients next to a half, on the side that a difference rounded to fp32 loses: a zero 2^-25 of the values beside it."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    n, hk, d = 60, 2, 64
+    L = Layer(95, [n], hk, hk, d, 32, 64, fill=False)
+    g = L.g
+    v = np.zeros((n, hk, d))
+    for i in range(n):
+        s = 2.0 ** int(g.integers(-6, 4))                       # every group: 15 s at most, halves of s, the least 2^-24 ..
+        for h in range(hk):
+            x = (g.integers(0, 31, d) * 0.5) * s
+            x[::32] = 15.0 * s
+            x[7::32] = 2.0 ** float(g.integers(-40, -20)) * (1 if g.random() < 0.5 else -1)
+            v[i, h] = np.where(x == 0, s, x)
+    v = O.bf16(v)
+    k = O.bf16(v[::-1] * 1.0)
+    B.oscar_rope_append_int4(L.desc, None, None, dev_bf16(k), dev_bf16(v), i32([0] * n), i32(np.arange(n)), None)
+    torch.cuda.synchronize()
+    L.put(0, np.arange(n), 0, k), L.put(0, np.arange(n), 1, v)
+    np.testing.assert_array_equal(L.gpu_pool(), L.pool)
+
+
+def test_append_scales_where_the_range_needs_more_than_fp32():
+    """Ranges of 15 (2 m + 1) 2^-25, halfway between two subnormal scales, less or more by a least value of 2^-50."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    n, d = 40, 64
+    L = Layer(96, [n], 1, 1, d, 64, 64, fill=False)
+    v = np.zeros((n, 1, d))
+    for i in range(n):
+        m = i % 8
+        v[i, 0] = 15.0 * (2 * m + 1) * 2.0 ** -25 * (np.arange(d) % 4) / 4 + 2.0 ** -30
+        v[i, 0, 3] = 15.0 * (2 * m + 1) * 2.0 ** -25
+        v[i, 0, 8] = (1.0, -1.0)[i // 8 % 2] * 2.0 ** -(50 + i % 3)
+        if i // 16 % 2:
+            v[i] = -v[i]
+    v = O.bf16(v)
+    B.oscar_rope_append_int4(L.desc, None, None, dev_bf16(v), dev_bf16(v), i32([0] * n), i32(np.arange(n)), None)
+    torch.cuda.synchronize()
+    L.put(0, np.arange(n), 0, v), L.put(0, np.arange(n), 1, v)
+    np.testing.assert_array_equal(L.gpu_pool(), L.pool)
