@@ -18,6 +18,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "int4.h"
 #include "kernels.h"
@@ -58,6 +59,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
       : "=l"(reinterpret_cast<uint64_t&>(d))
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return d;
@@ -203,7 +211,8 @@ __device__ __forceinline__ void rotate8(uint4& raw, const Turn& t) {
     operands<Interleaved>(t, x[i], y[i], i, &a, &c, &b, &s);
     const float2 bs = mul2(b, s), r = fma2(a, c, bs);
     if (Exact) {
-      const float2 e = make_float2(fabsf(bs.x) + fabsf(r.x), fabsf(bs.y) + fabsf(r.y));
+      // (twice the two roundings: 2^-23 of each, and at least the last place of a subnormal sum)
+      const float2 e = add2(make_float2(fabsf(bs.x) + fabsf(r.x), fabsf(bs.y) + fabsf(r.y)), twice(FLT_MIN));
       const float2 lo = fma2(e, twice(-1.1920929e-7f), r), hi = fma2(e, twice(1.1920929e-7f), r);
       out[i] = pack_bf162(lo.x, lo.y);
       apart[i] = out[i] ^ pack_bf162(hi.x, hi.y);

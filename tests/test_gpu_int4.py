@@ -811,3 +811,20 @@ def test_append_scales_where_the_range_needs_more_than_fp32():
     torch.cuda.synchronize()
     L.put(0, np.arange(n), 0, v), L.put(0, np.arange(n), 1, v)
     np.testing.assert_array_equal(L.gpu_pool(), L.pool)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_rotates_the_smallest_keys_exactly(inter):
+    """Keys at and below fp32's least normal number: k' is the rounding of its exact value there as well."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    n, d = 3000, 64
+    L = Layer(97, [n], 2, 2, d, 64, 64, fill=False)
+    k = O.bf16(L.g.standard_normal((n, 2, d)) * 2.0 ** L.g.integers(-132, -118, (n, 2, 1)))
+    cs = angles(n, d)
+    tk = dev_bf16(k)
+    np.testing.assert_array_equal(host(tk), k)
+    B.oscar_rope_append_int4(L.desc, B.rope_desc(torch.from_numpy(cs).cuda(), d, inter), None, tk, tk.clone(), i32([0] * n),
+                             i32(np.arange(n)), None, tk)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(host(tk), O.bf16(O.rope(k, cs, inter)))
