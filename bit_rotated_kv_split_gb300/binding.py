@@ -48,6 +48,7 @@ class LayerDesc(ctypes.Structure):
 class Int4Desc(ctypes.Structure):
     """Mirror of `oscar_int4_desc`."""
     keep = None   # a tensor whose memory it points to
+    keep_others = ()   # the others
     _fields_ = [
         ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
         ("max_pages_per_seq", c_int32), ("max_len", c_int32), ("n_pages", c_int64),

@@ -94,7 +94,10 @@ class Int4Cache:
         self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
 
     def desc(self, max_len: int = None) -> Int4Desc:
-        """The descriptor; max_len bounds every seq_len of the decodes it is used for (default: the page table's)."""
+        """The descriptor; max_len bounds every seq_len of the decodes it is used for (default: the page table's).
+
+        It keeps the tensors that it points to alive, those of the cache at this moment.
+        """
         d = Int4Desc()
         d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim = self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim
         d.max_pages_per_seq, d.n_pages = self.max_pages_per_seq, self.n_pages
@@ -104,4 +107,5 @@ class Int4Cache:
         for name in ("pages", "page_table", "seq_len", "dev_status"):
             setattr(d, name, getattr(self, name).data_ptr())
         d.keep = self.pages
+        d.keep_others = (self.page_table, self.seq_len, self.dev_status)
         return d

@@ -305,3 +305,23 @@ def test_binding_refuses_rows_of_other_types_and_descriptors_of_the_host():
     pd = B.prompt_desc(1, 8, 2, 64, 3, 3, 3, 3, dev_status=torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError, match="one CUDA device"):
         B.oscar_prompt_attention(pd, dev(row(3, 8)), dev(row(3, 2)), dev(row(3, 2)), dev(cu), dev(cu), dev(row(3, 8)), dev(ws))
+
+
+def test_cache_descriptor_keeps_its_tensors():
+    """A descriptor that outlives its cache still points to live tables, lengths and status words."""
+    import gc
+    import weakref
+
+    from bit_rotated_kv_split_gb300.cache import Int4Cache
+    cache = Int4Cache(2, 8, 2, 64, 4, 8, device="cpu")
+    desc = cache.desc()
+    refs = {name: weakref.ref(getattr(cache, name)) for name in ("pages", "page_table", "seq_len", "dev_status")}
+    at = {name: getattr(cache, name).data_ptr() for name in refs}
+    del cache
+    gc.collect()
+    for name, ref in refs.items():
+        assert ref() is not None, name
+        assert getattr(desc, name) == at[name] == ref().data_ptr()
+    del desc
+    gc.collect()
+    assert all(ref() is None for ref in refs.values())
