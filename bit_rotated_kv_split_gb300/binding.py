@@ -469,7 +469,8 @@ def oscar_rope_append_int4(desc: Int4Desc, rope, q, k, v, dst_req, dst_pos, q_ou
     _index("dst_req", dst_req, n), _index("dst_pos", dst_pos, n), _index("rope_pos", rope_pos, n)
     _contiguous("q_out", q_out, (n, hq, d), 2)
     _contiguous("k_out", k_out, (n, hk, d), 2)
-    _on_device("oscar_rope_append_int4", stream, (k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos, desc.keep, rope and rope.keep),
+    _on_device("oscar_rope_append_int4", stream, (k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos, desc.keep, rope and rope.keep,
+                                                  *desc.keep_others),
                lib.oscar_rope_append_int4, (
                    ctypes.byref(desc), _ref(rope), _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, dst_req.data_ptr(),
                    dst_pos.data_ptr(), _ptr(rope_pos), n, _ptr(q_out), _ptr(k_out)))
@@ -482,7 +483,7 @@ def oscar_gather_int4(desc: Int4Desc, src_req, src_pos, k_out, v_out, stream=Non
     if v_out.shape[0] != n:
         raise ValueError("k_out and v_out must have one row count")
     _index("src_req", src_req, n), _index("src_pos", src_pos, n)
-    _on_device("oscar_gather_int4", stream, (k_out, v_out, src_req, src_pos, desc.keep), lib.oscar_gather_int4, (
+    _on_device("oscar_gather_int4", stream, (k_out, v_out, src_req, src_pos, desc.keep, *desc.keep_others), lib.oscar_gather_int4, (
         ctypes.byref(desc), src_req.data_ptr(), src_pos.data_ptr(), n, k_out.data_ptr(), ks, v_out.data_ptr(), vs))
 
 
@@ -502,7 +503,7 @@ def oscar_decode_attention_int4(desc: Int4Desc, q, out, workspace, score=None, s
     _contiguous("out", out, (b, hq, d), 2)
     _slopes_ok(score, hq)
     size = c_size_t(workspace.numel() * workspace.element_size())
-    _on_device("oscar_decode_attention_int4", stream, (q, out, workspace, desc.keep, score and score.keep),
+    _on_device("oscar_decode_attention_int4", stream, (q, out, workspace, desc.keep, score and score.keep, *desc.keep_others),
                lib.oscar_decode_attention_int4, (
                    ctypes.byref(desc), _ref(score), q.data_ptr(), qs, out.data_ptr(), workspace.data_ptr(),
                    ctypes.byref(size)))

@@ -325,3 +325,33 @@ def test_cache_descriptor_keeps_its_tensors():
     del desc
     gc.collect()
     assert all(ref() is None for ref in refs.values())
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_cache_descriptor_refuses_a_host_table(which):
+    """A page table, lengths or a status word in host memory is refused before the library sees the pointer."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    from bit_rotated_kv_split_gb300.cache import Int4Cache
+
+    class OnDevice:
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
+            return 0
+
+    cache = Int4Cache(2, 8, 2, 64, 4, 8, device="cpu")
+    desc, idx = cache.desc(), OnDevice(torch.zeros(3, dtype=torch.int32))
+    rows = [OnDevice(torch.zeros(n, h, 64, dtype=torch.bfloat16)) for n, h in ((3, 8), (3, 2), (3, 2), (2, 8), (2, 8))]
+    desc.keep = OnDevice(cache.pages)
+    desc.keep_others = tuple(t if i == which else OnDevice(t) for i, t in enumerate(desc.keep_others))
+    with pytest.raises(ValueError, match="one CUDA device"):
+        B.oscar_rope_append_int4(desc, None, None, rows[1], rows[2], idx, idx, None)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        B.oscar_gather_int4(desc, idx, idx, rows[1], rows[2])
+    with pytest.raises(ValueError, match="one CUDA device"):
+        B.oscar_decode_attention_int4(desc, rows[3], rows[4], OnDevice(torch.zeros(256, dtype=torch.uint8)))
