@@ -179,6 +179,8 @@ extern "C" oscar_status oscar_decode_attention_int4(const oscar_int4_desc* desc,
   if (st != OSCAR_OK) return st;
   if (!desc->seq_len || !workspace_bytes) return OSCAR_ERR_INVALID_ARG;
   if (desc->n_q_heads / desc->n_kv_heads > 16) return OSCAR_ERR_UNSUPPORTED;
+  // positions up to a few pages past the end are 32-bit numbers
+  if (desc->max_len >= INT32_MAX - 511) return OSCAR_ERR_UNSUPPORTED;
   st = check_score(score, desc->head_dim, &p.s);
   if (st != OSCAR_OK) return st;
   const size_t need = oscar::int4_decode_workspace_bytes(p.c);

@@ -650,9 +650,10 @@ oscar_status oscar_gather_int4(const oscar_int4_desc* desc, const int32_t* src_r
  *   clamped and sets OSCAR_DEV_LENGTH, a negative one counts as 0 and sets
  *   it; a page outside the pool is skipped and sets OSCAR_DEV_PAGE_BOUNDS.
  *   A copy that does not land within 1 s sets OSCAR_DEV_TIMEOUT (the output
- *   must not be used then).  Groups above 16, or more than 2^31 pages over all
- *   requests and KV heads at max_len: OSCAR_ERR_UNSUPPORTED.  out must not
- *   overlap q.  The result does not depend on scheduling.
+ *   must not be used then).  OSCAR_ERR_UNSUPPORTED: groups above 16; max_len
+ *   above 2^31 - 513; 2^31 or more of (pages of max_len, or of the window if that
+ *   is less, + 64) x B x H_kv x (2 for groups above 8).  out must not overlap q.
+ *   The result does not depend on scheduling.
  *
  *   Workspace: NULL asks for the size (it depends on head_dim alone); 256-byte
  *   aligned, zero-filled before its first use; each call leaves it ready for

@@ -355,3 +355,13 @@ def test_cache_descriptor_refuses_a_host_table(which):
         B.oscar_gather_int4(desc, idx, idx, rows[1], rows[2])
     with pytest.raises(ValueError, match="one CUDA device"):
         B.oscar_decode_attention_int4(desc, rows[3], rows[4], OnDevice(torch.zeros(256, dtype=torch.uint8)))
+
+
+def test_decode_refuses_lengths_whose_positions_pass_32_bits(built_lib):
+    """Positions and page counts are 32-bit integers: max_len near 2^31 is refused, by the size query as well."""
+    from bit_rotated_kv_split_gb300 import binding as B
+    for n in (2 ** 31 - 1, 2 ** 31 - 16, 2 ** 31 - 512):
+        d = _desc(max_pages_per_seq=1 << 27, max_len=n, batch=1, n_q_heads=1, n_kv_heads=1)
+        assert _decode(B, d) == 6 and _decode(B, d, ws=None) == 6
+    d = _desc(max_pages_per_seq=1 << 27, max_len=2 ** 31 - 513, batch=1, n_q_heads=1, n_kv_heads=1)
+    assert _decode(B, d, ws=None) == 0
