@@ -419,6 +419,12 @@ def _contiguous(name, t, shape, itemsize):
         raise ValueError("%s must be contiguous %s %s" % (name, "bfloat16" if itemsize == 2 else "float32", list(shape)))
 
 
+def _workspace_size(t):
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return c_size_t(t.numel() * t.element_size())
+
+
 _raw_stream = None
 
 
@@ -502,7 +508,7 @@ def oscar_decode_attention_int4(desc: Int4Desc, q, out, workspace, score=None, s
         raise ValueError("q must have one row per request")
     _contiguous("out", out, (b, hq, d), 2)
     _slopes_ok(score, hq)
-    size = c_size_t(workspace.numel() * workspace.element_size())
+    size = _workspace_size(workspace)
     _on_device("oscar_decode_attention_int4", stream, (q, out, workspace, desc.keep, score and score.keep, *desc.keep_others),
                lib.oscar_decode_attention_int4, (
                    ctypes.byref(desc), _ref(score), q.data_ptr(), qs, out.data_ptr(), workspace.data_ptr(),
@@ -529,7 +535,7 @@ def oscar_prompt_attention(desc: PromptDesc, q, k, v, cu_q, cu_k, out, workspace
     _contiguous("out", out, (desc.total_q, hq, d), 2)
     _contiguous("lse", lse, (desc.total_q, hq), 4)
     _slopes_ok(score, hq)
-    size = c_size_t(workspace.numel() * workspace.element_size())
+    size = _workspace_size(workspace)
     _on_device("oscar_prompt_attention", stream, (
         q, k, v, cu_q, cu_k, out, workspace, prefix_len, lse, desc.keep, score and score.keep),
                lib.oscar_prompt_attention, (

@@ -365,3 +365,18 @@ def test_decode_refuses_lengths_whose_positions_pass_32_bits(built_lib):
         assert _decode(B, d) == 6 and _decode(B, d, ws=None) == 6
     d = _desc(max_pages_per_seq=1 << 27, max_len=2 ** 31 - 513, batch=1, n_q_heads=1, n_kv_heads=1)
     assert _decode(B, d, ws=None) == 0
+
+
+def test_binding_refuses_workspaces_that_are_not_contiguous():
+    """numel of an expanded or strided view is not the memory behind it."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    from bit_rotated_kv_split_gb300.cache import Int4Cache
+    desc = Int4Cache(2, 8, 2, 64, 4, 8, device="cpu").desc()
+    row = lambda n, h: torch.zeros(n, h, 64, dtype=torch.bfloat16)   # noqa: E731
+    pd, cu = B.prompt_desc(1, 8, 2, 64, 3, 3, 3, 3), torch.zeros(2, dtype=torch.int32)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 24), torch.zeros(1 << 24, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            B.oscar_decode_attention_int4(desc, row(2, 8), row(2, 8), ws)
+        with pytest.raises(ValueError, match="workspace"):
+            B.oscar_prompt_attention(pd, row(3, 8), row(3, 2), row(3, 2), cu, cu, row(3, 8), ws)
