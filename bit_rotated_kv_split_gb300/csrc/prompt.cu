@@ -729,7 +729,6 @@ cudaError_t launch(const PromptParams& p, const PromptPlan& plan, cudaStream_t s
   cudaError_t e = set_smem_limit<prompt_kernel<D, kForm, Dual>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t x = int64_t(plan.blocks) * plan.sets;
-  if (x > 0x7fffffff || x * p.batch > 0x7fffffff / 32) return cudaErrorInvalidValue;
   const dim3 grid(unsigned(x), unsigned(p.batch), unsigned(plan.splits));
   e = launch_pdl(prompt_kernel<D, kForm, Dual>, grid, dim3(kThreads), bytes, stream, p, plan, tq, tk, tv);
   if (e != cudaSuccess || plan.splits == 1) return e;
@@ -755,6 +754,8 @@ size_t prompt_workspace_bytes(const PromptParams& p) { return plan_prompt(p).byt
 
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   const PromptPlan plan = plan_prompt(p);
+  // grid limits, of the join's grid too (32 CTAs for each of this one's)
+  if (int64_t(plan.blocks) * plan.sets * p.batch > 0x7fffffff / 32) return cudaErrorNotSupported;
   return p.d == 128 ? launch_d<128>(p, plan, stream) : launch_d<64>(p, plan, stream);
 }
 

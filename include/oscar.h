@@ -706,8 +706,10 @@ typedef struct oscar_prompt_desc {
  *   that the window hides from all of its queries may hold anything.  Lengths above max_q /
  *   max_k or rows outside total_q / total_k are clamped and set
  *   OSCAR_DEV_LENGTH.  A wait within the kernel that runs out (1 s) sets
- *   OSCAR_DEV_TIMEOUT (the output must not be used then).  out must not overlap
- *   q, k or v.  The result does not depend on scheduling.
+ *   OSCAR_DEV_TIMEOUT (the output must not be used then).  2^26 or more row
+ *   blocks over B x max_q and the head sets (256 rows of (query, head) pairs each):
+ *   OSCAR_ERR_UNSUPPORTED.  out must not overlap q, k or v.  The result does not
+ *   depend on scheduling.
  *
  *   Workspace: NULL asks for the size (it depends on desc); otherwise 256-byte
  *   aligned device memory, of any content; calls that may overlap need

@@ -380,3 +380,11 @@ def test_binding_refuses_workspaces_that_are_not_contiguous():
             B.oscar_decode_attention_int4(desc, row(2, 8), row(2, 8), ws)
         with pytest.raises(ValueError, match="workspace"):
             B.oscar_prompt_attention(pd, row(3, 8), row(3, 2), row(3, 2), cu, cu, row(3, 8), ws)
+
+
+@pytest.mark.parametrize("over", [dict(batch=65535, max_q=2 ** 31 - 1, total_q=2 ** 31 - 1), dict(max_q=2 ** 31 - 1, n_q_heads=64, n_kv_heads=64)])
+def test_prompt_refuses_grids_beyond_the_launch_limit(built_lib, over):
+    """A valid description whose row blocks over all requests and heads are too many: unsupported, no CUDA error."""
+    from bit_rotated_kv_split_gb300 import binding as B
+    d = _pdesc(**over)
+    assert _prompt(B, d, qs=64 * 128, ks=64 * 128, vs=64 * 128) == 6
