@@ -338,6 +338,13 @@ def oscar_int4_block_bytes(head_dim: int, quant_group_k: int = 0, quant_group_v:
     return lib.oscar_int4_block_bytes(int(head_dim), int(quant_group_k), int(quant_group_v))
 
 
+def _int32(name, n) -> int:
+    n = int(n)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError("%s: %d is no 32-bit integer" % (name, n))
+    return n
+
+
 def rope_desc(cos_sin, rot_dim: int, interleaved: bool = False) -> RopeDesc:
     """Position rotation by cos_sin [n_positions][rot_dim] fp32 (device): rot_dim / 2 cosines, then the sines.
 
@@ -350,7 +357,7 @@ def rope_desc(cos_sin, rot_dim: int, interleaved: bool = False) -> RopeDesc:
             raise ValueError("cos_sin must be contiguous float32 [n_positions][rot_dim]")
         d.cos_sin, d.n_positions = cos_sin.data_ptr(), cos_sin.shape[0]
         d.keep = cos_sin
-    d.rot_dim, d.interleaved = int(rot_dim), int(bool(interleaved))
+    d.rot_dim, d.interleaved = _int32("rot_dim", rot_dim), int(bool(interleaved))
     return d
 
 
@@ -360,7 +367,7 @@ def score_desc(scale: float = 0.0, softcap: float = 0.0, window: int = 0, slopes
     The descriptor keeps the slopes alive.
     """
     d = ScoreDesc()
-    d.scale, d.softcap, d.window = float(scale), float(softcap), int(window)
+    d.scale, d.softcap, d.window = float(scale), float(softcap), _int32("window", window)
     if slopes is not None:
         if str(slopes.dtype) != "torch.float32" or slopes.dim() != 1 or not slopes.is_contiguous():
             raise ValueError("slopes must be contiguous float32 [n_q_heads]")
@@ -373,8 +380,10 @@ def prompt_desc(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_
                 total_k: int, causal: bool = True, dev_status=None) -> PromptDesc:
     """A batch of packed prompts: bounds on one request's queries and keys, rows in all."""
     d = PromptDesc()
-    d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim = int(batch), int(n_q_heads), int(n_kv_heads), int(head_dim)
-    d.max_q, d.max_k, d.total_q, d.total_k = int(max_q), int(max_k), int(total_q), int(total_k)
+    for name, n in (("batch", batch), ("n_q_heads", n_q_heads), ("n_kv_heads", n_kv_heads), ("head_dim", head_dim),
+                    ("max_q", max_q), ("max_k", max_k)):
+        setattr(d, name, _int32(name, n))
+    d.total_q, d.total_k = int(total_q), int(total_k)
     d.causal = int(bool(causal))
     if dev_status is not None:
         d.dev_status = dev_status.data_ptr()

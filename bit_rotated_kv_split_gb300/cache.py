@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from .binding import Int4Desc, LayerDesc, oscar_block_bytes, oscar_int4_block_bytes
+from .binding import Int4Desc, LayerDesc, _int32, oscar_block_bytes, oscar_int4_block_bytes
 
 HEAD_DIM = 128
 PAGE_TOKENS = 16
@@ -101,7 +101,7 @@ class Int4Cache:
         d = Int4Desc()
         d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim = self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim
         d.max_pages_per_seq, d.n_pages = self.max_pages_per_seq, self.n_pages
-        d.max_len = self.max_pages_per_seq * PAGE_TOKENS if max_len is None else int(max_len)
+        d.max_len = _int32("max_len", self.max_pages_per_seq * PAGE_TOKENS if max_len is None else max_len)
         d.tau_k, d.tau_v = self.tau_k, self.tau_v
         d.quant_group_k, d.quant_group_v = self.quant_group_k, self.quant_group_v
         for name in ("pages", "page_table", "seq_len", "dev_status"):

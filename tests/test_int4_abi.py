@@ -388,3 +388,23 @@ def test_prompt_refuses_grids_beyond_the_launch_limit(built_lib, over):
     from bit_rotated_kv_split_gb300 import binding as B
     d = _pdesc(**over)
     assert _prompt(B, d, qs=64 * 128, ks=64 * 128, vs=64 * 128) == 6
+
+
+def test_descriptors_refuse_numbers_beyond_32_bits():
+    """ctypes cuts an integer to its field: a window of 2^32 + 5 would be one of 5."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    from bit_rotated_kv_split_gb300.cache import Int4Cache
+    for n in (2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="32-bit"):
+            B.score_desc(window=n)
+        with pytest.raises(ValueError, match="32-bit"):
+            Int4Cache(1, 2, 1, 64, 4, 4, device="cpu").desc(n)
+        for at in range(6):
+            a = [1, 8, 2, 64, 3, 3]
+            a[at] = n
+            with pytest.raises(ValueError, match="32-bit"):
+                B.prompt_desc(*a, 3, 3)
+        with pytest.raises(ValueError):
+            B.rope_desc(torch.zeros(4, 32), n)
+    assert B.score_desc(window=2 ** 31 - 1).window == 2 ** 31 - 1
