@@ -386,6 +386,8 @@ def prompt_desc(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_
     d.total_q, d.total_k = int(total_q), int(total_k)
     d.causal = int(bool(causal))
     if dev_status is not None:
+        if dev_status.numel() < 1 or dev_status.element_size() != 4:
+            raise ValueError("dev_status must be an int32 word")
         d.dev_status = dev_status.data_ptr()
         d.keep = dev_status
     return d

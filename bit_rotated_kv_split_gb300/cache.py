@@ -104,8 +104,15 @@ class Int4Cache:
         d.max_len = _int32("max_len", self.max_pages_per_seq * PAGE_TOKENS if max_len is None else max_len)
         d.tau_k, d.tau_v = self.tau_k, self.tau_v
         d.quant_group_k, d.quant_group_v = self.quant_group_k, self.quant_group_v
-        for name in ("pages", "page_table", "seq_len", "dev_status"):
-            setattr(d, name, getattr(self, name).data_ptr())
+        for name, n, dtype in (("pages", self.n_pages * self.n_kv_heads * self.block_bytes, torch.uint8),
+                               ("page_table", self.batch * self.max_pages_per_seq, torch.int32),
+                               ("seq_len", self.batch, torch.int32), ("dev_status", 1, torch.int32)):
+            t = getattr(self, name)
+            if t.numel() < n or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError("%s must be contiguous %s with at least %d entries" % (name, dtype, n))
+            setattr(d, name, t.data_ptr())
+        if self.page_table.shape[-1] != self.max_pages_per_seq:
+            raise ValueError("page_table must have rows of max_pages_per_seq entries")
         d.keep = self.pages
         d.keep_others = (self.page_table, self.seq_len, self.dev_status)
         return d

@@ -408,3 +408,27 @@ def test_descriptors_refuse_numbers_beyond_32_bits():
         with pytest.raises(ValueError):
             B.rope_desc(torch.zeros(4, 32), n)
     assert B.score_desc(window=2 ** 31 - 1).window == 2 ** 31 - 1
+
+
+def test_cache_descriptor_refuses_tensors_that_do_not_fit():
+    """A table, lengths, pages or a status word put in place of the cache's own have to be of its sizes and types."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    from bit_rotated_kv_split_gb300.cache import Int4Cache
+    bad = dict(page_table=[torch.zeros(2, 3, dtype=torch.int32), torch.zeros(8, 1, dtype=torch.int32), torch.zeros(1, 4, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int64),
+                           torch.zeros(4, 2, dtype=torch.int32).t(), torch.zeros(1, 1, dtype=torch.int32).expand(2, 4)],
+               seq_len=[torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int64), torch.zeros(4, dtype=torch.int32)[::2]],
+               pages=[torch.zeros(100, dtype=torch.uint8)],
+               dev_status=[torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int8)])
+    for name, tensors in bad.items():
+        for t in tensors:
+            cache = Int4Cache(2, 8, 2, 64, 4, 8, device="cpu")
+            setattr(cache, name, t)
+            with pytest.raises(ValueError, match=name):
+                cache.desc()
+    cache = Int4Cache(2, 8, 2, 64, 4, 8, device="cpu")
+    cache.seq_len = torch.zeros(9, dtype=torch.int32)[3:5]
+    assert cache.desc().seq_len == cache.seq_len.data_ptr()
+    for t in bad["dev_status"]:
+        with pytest.raises(ValueError, match="dev_status"):
+            B.prompt_desc(1, 8, 2, 64, 3, 3, 3, 3, dev_status=t)
