@@ -10,7 +10,7 @@
 // once: q heads, then k heads, then v heads of one token.
 //
 // Measured: 30,186 tokens of 32/8 heads x 128 appended in 136 us (710 MB read and
-// written: 5.2 TB/s, 78 % of a plain copy's rate), bound by instruction issue (65 %)
+// written: 5.2 TB/s, 78 % of a plain copy's rate), bound by instruction issue (67 %)
 // and by the latency of each token's place and angles; without the rotation it
 // takes 32 us less, without the quantisation 13.  65,521 tokens read back in 57 us
 // (5.9 TB/s, 89 %).

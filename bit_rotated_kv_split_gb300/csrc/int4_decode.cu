@@ -5,14 +5,20 @@
 // batch is as even as a uniform one, and only the first and the last run of a
 // share can be incomplete.  Those leave their unnormalised sums in the workspace,
 // and the last CTA of a run to finish joins its parts.  (A grid of short CTAs, each
-// for 16 pages a warp, took 139 us where this takes 95, the ragged batch above: a
-// third of it went into the CTAs' first loads and last sums.)
+// for 16 pages a warp, took 139 us where this takes 97, 28 ragged requests: a third
+// of it went into the CTAs' first loads and last sums.)
 //
-// Bound by: HBM within the scan (100k tokens x 8 KV heads: 109 MB at 6.5 TB/s); the
-// rest of that call's 32 us (16 at the measured copy rate) are the first loads one
-// behind the other (lengths, page ids, pages: 4 us), the warps' and the CTAs' joins
-// (6 us) and the launch.  Code outside the scan is kept small on purpose: run once
-// a CTA, its instructions come from far (unrolled joins cost 8 us).
+// Bound by: chains before and after the scan.  Of 100k tokens x 8 KV heads (32 us; 109
+// MB, 16 us at the measured copy rate), cold: shares 1.5 us, a warp's first page at
+// 6 (11 at the latest), scans done at 24 to 28, the warps' joins at 26 to 29, the
+// runs' last parts joined at 34.  16 short windowed requests (16 us): shares 1.3, first
+// pages 5 to 10, scans 10 to 12, warps' joins 11 to 14, parts joined 17.  Within the
+// scan no unit is full (ragged batch with a cap: issue 54 %, ALU 46 %, DRAM 51 %): a
+// warp's step is one chain, with four warps a scheduler.  At 128 registers the kernels
+// for 128 channels spill 160 to 330 bytes a thread.  Code outside the scan is kept small
+// on purpose: run once a CTA, its instructions come from far (unrolled joins cost 8 us).
+// Groups of 9 to 16 query heads copy and unpack every page twice (100k tokens: group 8
+// 35 us, group 16 52).
 //
 // A warp takes every 8th pair of a run's pages with an online softmax of its own,
 // so nothing in the scan waits for another warp.  The pages' blocks come by bulk

@@ -20,13 +20,14 @@
 // are joined in the CTA before they go out (24 tokens on 32,000 keys: 36.7 us, with
 // twice the parts for the second kernel 40.9).
 //
-// Measured: 8,192 causal tokens of 32/8 heads x 128 in 388 us, 1.42 PFLOP/s (73 % of
-// the burst rate of a large GEMM), bound by shared memory beside the MMAs (S reads
-// 128 bytes a cycle for its two operands) and by the chain S, softmax, P, O: of a
-// step's 3,100 cycles a tile's softmax takes 1,300 and its two products 1,000.  24
+// Measured: 8,192 causal tokens of 32/8 heads x 128 in 380 to 400 us, 1.37 to 1.45
+// PFLOP/s (71 to 75 % of the burst rate of a large GEMM), bound by the chain S, softmax,
+// P, O, which two row tiles cover only in part: of a step's 3,100 cycles the tensor
+// cores work 2,000 (S 484 and P V 512 for each tile), a tile's softmax takes 1,300.  24
 // tokens on 32,000 keys in 37 us (132 MB): 5.2 TB/s within the scan, then 4 us of first
-// loads and 4 of the join.  Slower: P handed over in halves (4 %), a second issuing
-// warp (10 %), the maximum taken beside the powers (6 %).
+// loads and 4 of the join.  The dual kernels spill 32 to 40 bytes a thread (with bias and
+// cap at 64 channels 124), of the others one 12.  Slower: P handed over in halves (4 %), a second issuing warp
+// (10 %), the maximum taken beside the powers (6 %).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

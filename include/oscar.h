@@ -569,7 +569,8 @@ typedef struct oscar_rope_desc {
 /* What becomes of a score before the softmax.  For query position i and key
  * position j: t = scale (q . k); softcap > 0: t = softcap tanh(t / softcap);
  * slopes: t -= slopes[h] |i - j|; window > 0: keys with i - j >= window are
- * masked.  Scores may be as large as 2^22 in magnitude. */
+ * masked.  Scores may be as large as 2^22 in magnitude; a capped one is as exact as
+ * an uncapped one, whatever the cap. */
 typedef struct oscar_score_desc {
   float scale;                /* > 0 and finite; 0 = 1 / sqrt(head_dim)         */
   float softcap;              /* > 0 and finite; 0 = none                       */
@@ -624,7 +625,7 @@ oscar_status oscar_rope_append_int4(const oscar_int4_desc* desc, const oscar_rop
  * oscar_gather_int4 - reads cached rows of a 4-bit layer back as bf16, for
  * instance to go on with a prompt behind a cached prefix.
  *
- *   For item i < n: zero + scale * code, rounded to bf16, of position
+ *   For item i < n: zero + scale * code, rounded to bf16 by way of fp32, of position
  *   src_pos[i] of request src_req[i], to row i of k_out and v_out
  *   (k_out + i * k_stride, H_kv heads of d).  src_req[i] = -1 and the skips
  *   are those of oscar_rope_append_int4: a skipped row is left as it was.
@@ -644,9 +645,11 @@ oscar_status oscar_gather_int4(const oscar_int4_desc* desc, const int32_t* src_r
  *   query sits at position seq_len[b] - 1 (its token has been appended) and
  *   attends positions 0 .. seq_len[b] - 1; query head j reads KV head
  *   j / (H_q / H_kv), a group of 1 .. 16.  score may be NULL (all defaults).
- *   Sums, softmax statistics and the output are fp32 until the one rounding
- *   of out.  A request with no token gets zeros.  Codes, scales and zeros of
- *   slots past seq_len may hold anything.  A length above max_len is
+ *   Scores, sums and softmax statistics are fp32.  exp(t - max), and its product
+ *   with a value's scale, are rounded to fp16 for the tensor cores (2^-11 each of a
+ *   key's part in the result; where the scales of one scan lie more than 2^14 apart
+ *   they stay fp32), and out to bf16.  A request with no token gets zeros.  Codes,
+ *   scales and zeros of slots past seq_len may hold anything.  A length above max_len is
  *   clamped and sets OSCAR_DEV_LENGTH, a negative one counts as 0 and sets
  *   it; a page outside the pool is skipped and sets OSCAR_DEV_PAGE_BOUNDS.
  *   A copy that does not land within 1 s sets OSCAR_DEV_TIMEOUT (the output
