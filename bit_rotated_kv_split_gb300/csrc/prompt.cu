@@ -25,9 +25,9 @@
 // P, O, which two row tiles cover only in part: of a step's 3,100 cycles the tensor
 // cores work 2,000 (S 484 and P V 512 for each tile), a tile's softmax takes 1,300.  24
 // tokens on 32,000 keys in 37 us (132 MB): 5.2 TB/s within the scan, then 4 us of first
-// loads and 4 of the join.  The dual kernels spill 32 to 40 bytes a thread (with bias and
-// cap at 64 channels 124), of the others one 12.  Slower: P handed over in halves (4 %), a second issuing warp
-// (10 %), the maximum taken beside the powers (6 %).
+// loads and 4 of the join.  The dual kernels spill 32 to 40 bytes a thread (with bias
+// and cap at 64 channels 124), of the others one 12.  Slower: P handed over in halves
+// (4 %), a second issuing warp (10 %), the maximum taken beside the powers (6 %).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
