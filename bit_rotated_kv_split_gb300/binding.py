@@ -57,6 +57,31 @@ class Int4Desc(ctypes.Structure):
     ]
 
 
+class Int8Desc(ctypes.Structure):
+    """Mirror of `oscar_int8_desc`."""
+    keep = None   # a tensor whose memory it points to
+    keep_others = ()   # the others
+    _fields_ = [
+        ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+        ("max_pages_per_seq", c_int32), ("max_len", c_int32), ("n_pages", c_int64),
+        ("tau_k", c_float), ("tau_v", c_float), ("pages", c_void_p), ("page_table", c_void_p),
+        ("seq_len", c_void_p), ("dev_status", c_void_p),
+    ]
+
+
+class RopeScaling(ctypes.Structure):
+    """Mirror of `oscar_rope_scaling`."""
+    _fields_ = [("kind", c_int32), ("reserved", c_int32), ("factor", c_double), ("original_len", c_double),
+                ("turns_low", c_double), ("turns_high", c_double)]
+
+
+class HeadNorm(ctypes.Structure):
+    """Mirror of `oscar_head_norm`."""
+    keep = None   # a tensor whose memory it points to
+    keep_others = ()   # the other
+    _fields_ = [("q_weight", c_void_p), ("k_weight", c_void_p), ("eps", c_float), ("reserved", c_int32)]
+
+
 class RopeDesc(ctypes.Structure):
     """Mirror of `oscar_rope_desc`."""
     keep = None   # a tensor whose memory it points to
@@ -116,6 +141,14 @@ def _load():
         "oscar_gather_int4": (c_int32, [P, P, P, c_int32, P, c_int64, P, c_int64, P]),
         "oscar_decode_attention_int4": (c_int32, [P, P, P, c_int64, P, P, P, P]),
         "oscar_prompt_attention": (c_int32, [P, P, P, c_int64, P, c_int64, P, c_int64, P, P, P, P, P, P, P, P]),
+        "oscar_rope_frequencies": (c_int32, [c_int32, c_double, P, P, P]),
+        "oscar_rope_table": (c_int32, [P, c_int32, c_double, c_int64, c_int64, P, P]),
+        "oscar_norm_rope": (c_int32, [c_int32, c_int32, c_int32, P, P, P, c_int64, P, c_int64, P, c_int32, P, c_int64,
+                                      P, c_int64, P, P]),
+        "oscar_int8_block_bytes": (c_int64, [c_int32]),
+        "oscar_rope_append_int8": (c_int32, [P, P, P, P, c_int64, P, c_int64, P, c_int64, P, P, P, c_int32, P, P, P, P, P]),
+        "oscar_gather_int8": (c_int32, [P, P, P, c_int32, P, c_int64, P, c_int64, P]),
+        "oscar_decode_attention_int8": (c_int32, [P, P, P, c_int64, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -552,4 +585,154 @@ def oscar_prompt_attention(desc: PromptDesc, q, k, v, cu_q, cu_k, out, workspace
                lib.oscar_prompt_attention, (
                    ctypes.byref(desc), _ref(score), q.data_ptr(), qs, _ptr(k), ks, _ptr(v), vs, cu_q.data_ptr(),
                    cu_k.data_ptr(), _ptr(prefix_len), out.data_ptr(), _ptr(lse), workspace.data_ptr(),
+                   ctypes.byref(size)))
+
+
+# ---------------------------------------------------------------- rotary positions
+
+ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "by_index": 3, "by_turns": 4}
+
+
+def oscar_rope_frequencies(rot_dim: int, theta: float, kind: str = "plain", factor: float = 1.0, original_len: float = 0.0,
+                           turns_low: float = 0.0, turns_high: float = 0.0):
+    """(radians per position of each pair [rot_dim / 2] float64, the factor on cosines and sines)."""
+    if kind not in ROPE_KINDS:
+        raise ValueError("kind must be one of %s" % ", ".join(ROPE_KINDS))
+    s = RopeScaling(ROPE_KINDS[kind], 0, float(factor), float(original_len), float(turns_low), float(turns_high))
+    rot_dim = _int32("rot_dim", rot_dim)
+    freq = np.empty(max(rot_dim // 2, 0), dtype=np.float64)
+    magnitude = c_double(0.0)
+    _check("oscar_rope_frequencies", lib.oscar_rope_frequencies(rot_dim, float(theta), ctypes.byref(s), freq.ctypes.data,
+                                                                ctypes.byref(magnitude)))
+    return freq, magnitude.value
+
+
+def oscar_rope_table(freq, cos_sin, magnitude: float = 1.0, first: int = 0, stream=None) -> None:
+    """Fills cos_sin [n][rot_dim] fp32 (device): cosines, then sines, of (first + j) freq, times magnitude."""
+    freq = _f64(freq)
+    if freq.ndim != 1 or cos_sin.dim() != 2 or cos_sin.shape[1] != 2 * freq.shape[0]:
+        raise ValueError("freq must be [rot_dim / 2] and cos_sin [n][rot_dim]")
+    _contiguous("cos_sin", cos_sin, cos_sin.shape, 4)
+    _on_device("oscar_rope_table", stream, (cos_sin,), lib.oscar_rope_table, (
+        freq.ctypes.data, 2 * freq.shape[0], float(magnitude), int(first), cos_sin.shape[0], cos_sin.data_ptr()))
+
+
+def norm_desc(q_weight=None, k_weight=None, eps: float = 1e-6) -> HeadNorm:
+    """Norm of the query and key heads by weights [head_dim] bf16 (device); None: those heads have none.
+
+    The descriptor keeps the weights alive.
+    """
+    d = HeadNorm()
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if w.dim() != 1 or not w.is_contiguous() or not _half(w):
+                raise ValueError("%s must be contiguous bfloat16 [head_dim]" % name)
+            setattr(d, name, w.data_ptr())
+    d.eps = float(eps)
+    d.sizes = tuple(w.shape[0] for w in (q_weight, k_weight) if w is not None)
+    d.keep, d.keep_others = q_weight, (k_weight,)
+    return d
+
+
+def _norm_ok(norm, d):
+    if norm is not None and any(n != d for n in getattr(norm, "sizes", ())):
+        raise ValueError("norm: weights of another head size than %d" % d)
+
+
+def _kept(norm, rope):
+    """The tensors that the two descriptors (each may be None) point to."""
+    return (rope and rope.keep, *((norm.keep, *norm.keep_others) if norm is not None else ()))
+
+
+def oscar_norm_rope(norm, rope, q, k, pos, q_out, k_out, dev_status=None, stream=None) -> None:
+    """Norms and rotates q [n][H_q][d] and k [n][H_kv][d] (bf16) by position pos [n] int32 into q_out and k_out.
+
+    norm and rope may be None, and so may q and q_out, or k and k_out.  Rows may be strided (slices of one
+    projection's output), and outputs may be their inputs.
+    """
+    shape = (q if q is not None else k).shape
+    if len(shape) != 3 or (q is not None and k is not None and (k.dim() != 3 or k.shape[0] != shape[0] or k.shape[2] != shape[2])):
+        raise ValueError("q and k must be [n][heads][d] with one row count and head size")
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q_out must be given with q, k_out with k")
+    n, d = int(shape[0]), int(shape[2])
+    hq, hk = (1 if x is None else int(x.shape[1]) for x in (q, k))
+    strides = []
+    for name, x, heads in (("q", q, hq), ("k", k, hk), ("q_out", q_out, hq), ("k_out", k_out, hk)):
+        if x is not None and x.shape[0] != n:
+            raise ValueError("%s must have %d rows" % (name, n))
+        strides.append(0 if x is None else _heads(name, x, heads, d))
+    if dev_status is not None and (dev_status.numel() < 1 or dev_status.element_size() != 4):
+        raise ValueError("dev_status must be an int32 word")
+    _index("pos", pos, n)
+    _norm_ok(norm, d)
+    _on_device("oscar_norm_rope", stream, ((q if q is not None else k), k, q_out, k_out, pos, dev_status, *_kept(norm, rope)),
+               lib.oscar_norm_rope, (
+                   hq, hk, d, _ref(norm), _ref(rope), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(pos), n, _ptr(q_out),
+                   strides[2], _ptr(k_out), strides[3], _ptr(dev_status)))
+
+
+# ---------------------------------------------------------------- 8-bit layers
+
+def oscar_int8_block_bytes(head_dim: int) -> int:
+    """Bytes of one (page, KV head) block of an 8-bit layer; 0 for an invalid head size."""
+    return lib.oscar_int8_block_bytes(int(head_dim))
+
+
+def oscar_rope_append_int8(desc: Int8Desc, norm, rope, q, k, v, dst_req, dst_pos, q_out, k_out=None, rope_pos=None,
+                           k_held=None, v_held=None, stream=None) -> None:
+    """Norms and rotates q [n][H_q][d] and k [n][H_kv][d] (bf16) into q_out, k_out and appends k, v to the pages.
+
+    norm, rope and k_out may be None, q and q_out both.  Rows may be strided (slices of one projection's output).
+    k_held, v_held [n][H_kv][d]: the rows as the cache holds them from now on.
+    """
+    hq, hk, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, int(k.shape[0])
+    qs = _heads("q", q, hq, d) if q is not None else 0
+    ks, vs = _heads("k", k, hk, d), _heads("v", v, hk, d)
+    if v.shape[0] != n or (q is not None and q.shape[0] != n):
+        raise ValueError("q, k and v must have one row count")
+    _index("dst_req", dst_req, n), _index("dst_pos", dst_pos, n), _index("rope_pos", rope_pos, n)
+    _contiguous("q_out", q_out, (n, hq, d), 2)
+    rows = (n, hk, d)
+    _contiguous("k_out", k_out, rows, 2), _contiguous("k_held", k_held, rows, 2), _contiguous("v_held", v_held, rows, 2)
+    _norm_ok(norm, d)
+    _on_device("oscar_rope_append_int8", stream, (
+        k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos, k_held, v_held, desc.keep, *desc.keep_others, *_kept(norm, rope)),
+               lib.oscar_rope_append_int8, (
+                   ctypes.byref(desc), _ref(norm), _ref(rope), _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                   dst_req.data_ptr(), dst_pos.data_ptr(), _ptr(rope_pos), n, _ptr(q_out), _ptr(k_out), _ptr(k_held),
+                   _ptr(v_held)))
+
+
+def oscar_gather_int8(desc: Int8Desc, src_req, src_pos, k_out, v_out, stream=None) -> None:
+    """Cached rows (src_req[i], src_pos[i]) as bf16 into k_out, v_out [n][H_kv][d] (rows may be strided)."""
+    hk, d, n = desc.n_kv_heads, desc.head_dim, int(k_out.shape[0])
+    ks, vs = _heads("k_out", k_out, hk, d), _heads("v_out", v_out, hk, d)
+    if v_out.shape[0] != n:
+        raise ValueError("k_out and v_out must have one row count")
+    _index("src_req", src_req, n), _index("src_pos", src_pos, n)
+    _on_device("oscar_gather_int8", stream, (k_out, v_out, src_req, src_pos, desc.keep, *desc.keep_others), lib.oscar_gather_int8, (
+        ctypes.byref(desc), src_req.data_ptr(), src_pos.data_ptr(), n, k_out.data_ptr(), ks, v_out.data_ptr(), vs))
+
+
+def oscar_decode_int8_workspace_bytes(desc: Int8Desc) -> int:
+    size = c_size_t(0)
+    _check("oscar_decode_attention_int8", lib.oscar_decode_attention_int8(
+        ctypes.byref(desc), None, None, 0, None, None, None, ctypes.byref(size), None))
+    return size.value
+
+
+def oscar_decode_attention_int8(desc: Int8Desc, q, out, workspace, score=None, lse=None, stream=None) -> None:
+    """out [B][H_q][d] bf16 (and lse [B][H_q] fp32) = attention of one query per request q [B][H_q][d] over the 8-bit cache."""
+    hq, d, b = desc.n_q_heads, desc.head_dim, desc.batch
+    qs = _heads("q", q, hq, d)
+    if q.shape[0] != b:
+        raise ValueError("q must have one row per request")
+    _contiguous("out", out, (b, hq, d), 2)
+    _contiguous("lse", lse, (b, hq), 4)
+    _slopes_ok(score, hq)
+    size = _workspace_size(workspace)
+    _on_device("oscar_decode_attention_int8", stream, (q, out, workspace, lse, desc.keep, score and score.keep, *desc.keep_others),
+               lib.oscar_decode_attention_int8, (
+                   ctypes.byref(desc), _ref(score), q.data_ptr(), qs, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
                    ctypes.byref(size)))

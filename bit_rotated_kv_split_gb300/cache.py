@@ -1,8 +1,9 @@
 """Device storage of one attention layer: the three-segment token pool of a
-two-bit layer (LayerCache) or the pages of a 4-bit layer (Int4Cache).
+two-bit layer (LayerCache) or the pages of a 4-bit (Int4Cache) or 8-bit layer
+(Int8Cache).
 
-Host-side plumbing only: it allocates the tensors that `oscar_layer_desc` or
-`oscar_int4_desc` points at (page pool, page table, lengths, BF16 sink and
+Host-side plumbing only: it allocates the tensors that `oscar_layer_desc`,
+`oscar_int4_desc` or `oscar_int8_desc` points at (page pool, page table, lengths, BF16 sink and
 recent ring, rotations, device status word) and fills the descriptor.  All
 computation on them happens in liboscar.so.
 """
@@ -10,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from .binding import Int4Desc, LayerDesc, _int32, oscar_block_bytes, oscar_int4_block_bytes
+from .binding import Int4Desc, Int8Desc, LayerDesc, _int32, oscar_block_bytes, oscar_int4_block_bytes, oscar_int8_block_bytes
 
 HEAD_DIM = 128
 PAGE_TOKENS = 16
@@ -98,21 +99,48 @@ class Int4Cache:
 
         It keeps the tensors that it points to alive, those of the cache at this moment.
         """
-        d = Int4Desc()
-        d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim = self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim
-        d.max_pages_per_seq, d.n_pages = self.max_pages_per_seq, self.n_pages
-        d.max_len = _int32("max_len", self.max_pages_per_seq * PAGE_TOKENS if max_len is None else max_len)
-        d.tau_k, d.tau_v = self.tau_k, self.tau_v
+        d = _fill_paged(self, Int4Desc(), max_len)
         d.quant_group_k, d.quant_group_v = self.quant_group_k, self.quant_group_v
-        for name, n, dtype in (("pages", self.n_pages * self.n_kv_heads * self.block_bytes, torch.uint8),
-                               ("page_table", self.batch * self.max_pages_per_seq, torch.int32),
-                               ("seq_len", self.batch, torch.int32), ("dev_status", 1, torch.int32)):
-            t = getattr(self, name)
-            if t.numel() < n or t.dtype != dtype or not t.is_contiguous():
-                raise ValueError("%s must be contiguous %s with at least %d entries" % (name, dtype, n))
-            setattr(d, name, t.data_ptr())
-        if self.page_table.shape[-1] != self.max_pages_per_seq:
-            raise ValueError("page_table must have rows of max_pages_per_seq entries")
-        d.keep = self.pages
-        d.keep_others = (self.page_table, self.seq_len, self.dev_status)
         return d
+
+
+class Int8Cache:
+    """Pages, page table and lengths of one 8-bit layer for `batch` requests."""
+
+    def __init__(self, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_pages_per_seq: int,
+                 n_pages: int, tau_k: float = 65504.0, tau_v: float = 65504.0, device="cuda"):
+        self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim = batch, n_q_heads, n_kv_heads, head_dim
+        self.block_bytes = oscar_int8_block_bytes(head_dim)
+        if self.block_bytes <= 0:
+            raise ValueError("head_dim must be 64 or 128")
+        self.max_pages_per_seq, self.n_pages = max_pages_per_seq, n_pages
+        self.tau_k, self.tau_v = float(tau_k), float(tau_v)
+        dev = torch.device(device)
+        self.pages = torch.zeros(n_pages * n_kv_heads * self.block_bytes, dtype=torch.uint8, device=dev)
+        self.page_table = torch.full((batch, max_pages_per_seq), -1, dtype=torch.int32, device=dev)
+        self.seq_len = torch.zeros(batch, dtype=torch.int32, device=dev)
+        self.dev_status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def desc(self, max_len: int = None) -> Int8Desc:
+        """The descriptor; max_len and what it keeps alive are as for Int4Cache."""
+        return _fill_paged(self, Int8Desc(), max_len)
+
+
+def _fill_paged(cache, d, max_len):
+    """The fields that the descriptors of 4-bit and 8-bit layers share."""
+    d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim = cache.batch, cache.n_q_heads, cache.n_kv_heads, cache.head_dim
+    d.max_pages_per_seq, d.n_pages = cache.max_pages_per_seq, cache.n_pages
+    d.max_len = _int32("max_len", cache.max_pages_per_seq * PAGE_TOKENS if max_len is None else max_len)
+    d.tau_k, d.tau_v = cache.tau_k, cache.tau_v
+    for name, n, dtype in (("pages", cache.n_pages * cache.n_kv_heads * cache.block_bytes, torch.uint8),
+                           ("page_table", cache.batch * cache.max_pages_per_seq, torch.int32),
+                           ("seq_len", cache.batch, torch.int32), ("dev_status", 1, torch.int32)):
+        t = getattr(cache, name)
+        if t.numel() < n or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError("%s must be contiguous %s with at least %d entries" % (name, dtype, n))
+        setattr(d, name, t.data_ptr())
+    if cache.page_table.shape[-1] != cache.max_pages_per_seq:
+        raise ValueError("page_table must have rows of max_pages_per_seq entries")
+    d.keep = cache.pages
+    d.keep_others = (cache.page_table, cache.seq_len, cache.dev_status)
+    return d

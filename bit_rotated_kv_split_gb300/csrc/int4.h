@@ -8,7 +8,7 @@
 
 namespace oscar {
 
-constexpr int kInt4Page = 16;
+constexpr int kPageTokens = 16;
 
 // Page block of one (page, KV head), d channels, ng_k / ng_v groups:
 //   [0, 8 d)      K: slot t's d / 2 code bytes at t d / 2; channel 32 w + 8 u
@@ -29,14 +29,24 @@ __host__ __device__ constexpr int int4_pair(int d, int ng_k, int ng_v, int t, in
   return 16 * d + 4 * ((ng_k + ng_v) * t + q);
 }
 
-struct Int4Cache {
+// The pages of a layer, whatever its codes' width.
+struct PagedCache {
   uint8_t* pages;
   const int32_t* page_table;
   const int32_t* seq_len;
   int32_t* dev_status;
   int32_t batch, n_q, n_kv, d, max_pages, max_len;
   int64_t n_pages;
+};
+
+struct Int4Cache : PagedCache {
   int32_t ng_k, ng_v;
+};
+
+struct RopeParams {
+  const float* cos_sin;
+  int64_t n_positions;
+  int32_t rot, interleaved;
 };
 
 // The score's form: log2 units throughout (t log2 e), so that the softmax is
@@ -52,9 +62,7 @@ struct ScoreParams {
 
 struct AppendParams {
   Int4Cache c;
-  const float* cos_sin;
-  int64_t n_positions;
-  int32_t rot, interleaved;
+  RopeParams rope;
   const uint16_t *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;
   const int32_t *dst_req, *dst_pos, *rope_pos;

@@ -1,16 +1,20 @@
 // C-ABI entry points of the 4-bit layers and of prompt attention: host
 // validation, then the launch.  A rejected call launches nothing.
-#include <cmath>
 #include <cstdint>
 
+#include "api_checks.h"
 #include "int4.h"
 #include "kernels.h"
 #include "oscar.h"
 #include "trace.h"
 
-namespace {
+using oscar::aligned;
+using oscar::check_heads;
+using oscar::check_score;
+using oscar::done;
+using oscar::row_stride_ok;
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+namespace {
 
 // groups per vector of d channels for a quantisation group size (0 = d); 0 if invalid
 int groups(int32_t d, int32_t g) {
@@ -19,69 +23,10 @@ int groups(int32_t d, int32_t g) {
   return (g == 32 || g == 64 || g == 128) && g <= d ? d / g : 0;
 }
 
-oscar_status check_heads(int32_t batch, int32_t n_q, int32_t n_kv, int32_t d) {
-  if (batch < 1 || n_q < 1 || n_kv < 1 || n_q % n_kv || (d != 64 && d != 128)) return OSCAR_ERR_INVALID_ARG;
-  // grid dimensions
-  return batch > 65535 || n_q > 65535 ? OSCAR_ERR_UNSUPPORTED : OSCAR_OK;
-}
-
 oscar_status check_cache(const oscar_int4_desc* d, oscar::Int4Cache* c) {
-  if (!d) return OSCAR_ERR_INVALID_ARG;
-  const oscar_status st = check_heads(d->batch, d->n_q_heads, d->n_kv_heads, d->head_dim);
-  if (st != OSCAR_OK) return st;
-  if (d->max_pages_per_seq < 1 || d->n_pages < 1 || d->n_pages > INT32_MAX) return OSCAR_ERR_INVALID_ARG;
-  if (d->max_len < 0 || int64_t(d->max_len) > int64_t(d->max_pages_per_seq) * oscar::kInt4Page)
-    return OSCAR_ERR_INVALID_ARG;
-  if (!(d->tau_k > 0.f) || !(d->tau_v > 0.f) || !(d->tau_k <= 65504.f) || !(d->tau_v <= 65504.f))
-    return OSCAR_ERR_INVALID_ARG;
-  const int gk = groups(d->head_dim, d->quant_group_k), gv = groups(d->head_dim, d->quant_group_v);
-  if (!gk || !gv || !d->pages || !d->page_table) return OSCAR_ERR_INVALID_ARG;
-  if (!aligned(d->pages, 128) || !aligned(d->page_table, 4) || !aligned(d->seq_len, 4) || !aligned(d->dev_status, 4))
-    return OSCAR_ERR_ALIGNMENT;
-  c->pages = d->pages;
-  c->page_table = d->page_table;
-  c->seq_len = d->seq_len;
-  c->dev_status = d->dev_status;
-  c->batch = d->batch;
-  c->n_q = d->n_q_heads;
-  c->n_kv = d->n_kv_heads;
-  c->d = d->head_dim;
-  c->max_pages = d->max_pages_per_seq;
-  c->max_len = d->max_len;
-  c->n_pages = d->n_pages;
-  c->ng_k = gk;
-  c->ng_v = gv;
-  return OSCAR_OK;
-}
-
-oscar_status check_score(const oscar_score_desc* d, int32_t head_dim, oscar::ScoreParams* s) {
-  const oscar_score_desc none{};
-  if (!d) d = &none;
-  if (!(d->scale >= 0.f) || !std::isfinite(d->scale) || !(d->softcap >= 0.f) || !std::isfinite(d->softcap) ||
-      d->window < 0 || d->reserved != 0)
-    return OSCAR_ERR_INVALID_ARG;
-  if (!aligned(d->slopes, 4)) return OSCAR_ERR_ALIGNMENT;
-  const double log2e = 1.4426950408889634;
-  const double scale = d->scale > 0.f ? double(d->scale) : 1.0 / std::sqrt(double(head_dim));
-  s->scale_log2 = float(scale * log2e);
-  s->cap_in = d->softcap > 0.f ? float(2.0 * scale / double(d->softcap) * log2e) : 0.f;
-  s->cap_log2 = float(double(d->softcap) * log2e);
-  // tanh(y) = y P(y^2) for |y| <= 1 / 2, and y = x cap_in ln 2 / 2
-  const double tanh_near[5] = {1., -0x1.5554a6p-2, 0x1.10e47ap-3, -0x1.b2167ep-5, 0x1.18d7e8p-6};
-  double unit = scale * log2e;
-  for (int k = 0; k < 5; ++k, unit /= 4. * log2e * log2e) s->cap_near[k] = float(tanh_near[k] * unit);
-  if (!std::isnormal(s->scale_log2) || !std::isfinite(s->cap_in) || !std::isfinite(2.f * s->cap_log2))
-    return OSCAR_ERR_INVALID_ARG;
-  s->window = d->window;
-  s->slopes = d->slopes;
-  return OSCAR_OK;
-}
-
-// rows of `heads` heads of d bf16, `stride` elements apart
-bool row_stride_ok(int64_t stride, int64_t heads, int32_t d) { return stride >= heads * d && stride % 8 == 0; }
-
-oscar_status done(cudaError_t e) {
-  return e == cudaSuccess ? OSCAR_OK : e == cudaErrorNotSupported ? OSCAR_ERR_UNSUPPORTED : OSCAR_ERR_CUDA;
+  c->ng_k = d ? groups(d->head_dim, d->quant_group_k) : 0;
+  c->ng_v = d ? groups(d->head_dim, d->quant_group_v) : 0;
+  return oscar::check_pages(d, c->ng_k && c->ng_v, c);
 }
 
 }  // namespace
@@ -101,19 +46,8 @@ extern "C" oscar_status oscar_rope_append_int4(const oscar_int4_desc* desc, cons
   oscar::AppendParams p{};
   const oscar_status st = check_cache(desc, &p.c);
   if (st != OSCAR_OK) return st;
-  if (rope) {
-    if (rope->rot_dim < 0 || rope->rot_dim > desc->head_dim || rope->rot_dim % 16 ||
-        (rope->interleaved != 0 && rope->interleaved != 1))
-      return OSCAR_ERR_INVALID_ARG;
-    if (rope->rot_dim > 0) {
-      if (!rope->cos_sin || rope->n_positions < 1) return OSCAR_ERR_INVALID_ARG;
-      if (!aligned(rope->cos_sin, 16)) return OSCAR_ERR_ALIGNMENT;
-    }
-    p.cos_sin = rope->cos_sin;
-    p.n_positions = rope->n_positions;
-    p.rot = rope->rot_dim;
-    p.interleaved = rope->interleaved;
-  }
+  const oscar_status rs = oscar::check_rope(rope, desc->head_dim, &p.rope);
+  if (rs != OSCAR_OK) return rs;
   if (n < 0) return OSCAR_ERR_INVALID_ARG;
   if (n == 0) return OSCAR_OK;
   if (!k || !v || !dst_req || !dst_pos || (q == nullptr) != (q_out == nullptr)) return OSCAR_ERR_INVALID_ARG;

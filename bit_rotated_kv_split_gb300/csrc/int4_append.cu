@@ -24,61 +24,10 @@
 #include "kernels.h"
 #include "oscar.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace oscar {
 namespace {
-
-constexpr int kAppendThreads = 128;
-
-__device__ __forceinline__ void unpack_bf16x8(const uint4& u, float (&x)[8]) {
-  x[0] = bf16_lo(u.x), x[1] = bf16_hi(u.x), x[2] = bf16_lo(u.y), x[3] = bf16_hi(u.y);
-  x[4] = bf16_lo(u.z), x[5] = bf16_hi(u.z), x[6] = bf16_lo(u.w), x[7] = bf16_hi(u.w);
-}
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
-  return make_uint4(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]), pack_bf162(x[4], x[5]), pack_bf162(x[6], x[7]));
-}
-
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {   // a NaN wins
-  uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(d))
-      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
-  return d;
-}
-__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float2 bf16_pair(uint32_t u) { return make_float2(bf16_lo(u), bf16_hi(u)); }
-
-// a - b >= 0, to odd: where 24 bits do not hold it, the last one is set.  A quotient of it
-// is then not taken for a tie of fewer bits that the exact one only comes near to.
-__device__ __forceinline__ float sub_odd(float a, float b) {
-  const float lo = __fsub_rz(a, b), hi = __fsub_ru(a, b);   // (a - a is +0 in both)
-  return __uint_as_float(__float_as_uint(lo) | (lo != hi ? 1u : 0u));
-}
 
 // Codes of the 8 bf16 values u of this lane (x - zero over scale, to nearest
 // even, 0 .. 15) in a group of `lanes` lanes; *pair = (scale, zero), fp16 bits.
@@ -142,19 +91,15 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& u, float tau, int lan
   return word;
 }
 
-__device__ __forceinline__ void flag(int32_t* dev_status, int bit) {
-  if (dev_status) atomicOr(dev_status, bit);
-}
-
 // The block of (req, pos), KV head 0, or nullptr (skip) for a padding row, a
 // place outside the table or a page outside the pool.
 __device__ __forceinline__ uint8_t* token_block(const Int4Cache& c, int req, int pos, bool report) {
   if (req == -1) return nullptr;
-  if (req < 0 || req >= c.batch || pos < 0 || pos / kInt4Page >= c.max_pages) {
+  if (req < 0 || req >= c.batch || pos < 0 || pos / kPageTokens >= c.max_pages) {
     if (report) flag(c.dev_status, OSCAR_DEV_LENGTH);
     return nullptr;
   }
-  const int page = c.page_table[int64_t(req) * c.max_pages + pos / kInt4Page];
+  const int page = c.page_table[int64_t(req) * c.max_pages + pos / kPageTokens];
   if (page < 0 || page >= c.n_pages) {
     if (report) flag(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
     return nullptr;
@@ -233,20 +178,11 @@ __device__ __forceinline__ void rotate8(uint4& raw, const Turn& t) {
   raw = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-__device__ __forceinline__ void load8(float (&x)[8], const float* p, int n) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (4 * i < n) {
-      const float4 v = *reinterpret_cast<const float4*>(p + 4 * i);
-      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
-}
-
 // One warp takes `slots_per_warp` slots of one token: its q heads four slots at
 // a time, whose loads are in flight together, then k and v heads with the next
 // slot's load ahead of the present one's work.
 template <int D, bool Interleaved>
-__global__ void __launch_bounds__(kAppendThreads, 7)
+__global__ void __launch_bounds__(kRowThreads, 7)
     rope_append_kernel(const __grid_constant__ AppendParams p, int slots_per_warp) {
   pdl_wait();
   pdl_launch_dependents();
@@ -254,7 +190,7 @@ __global__ void __launch_bounds__(kAppendThreads, 7)
   const int lane = threadIdx.x & 31, o = lane % kLanes, sub = lane / kLanes;
   const int sq = p.q ? (p.c.n_q + kRows - 1) / kRows : 0, sk = (p.c.n_kv + kRows - 1) / kRows;
   const int slots = sq + 2 * sk, warps_per_token = (slots + slots_per_warp - 1) / slots_per_warp;
-  const int64_t w = (int64_t(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
+  const int64_t w = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   const int64_t i = w / warps_per_token;
   if (i >= p.n) return;
   const int part = int(w - i * warps_per_token);
@@ -262,18 +198,18 @@ __global__ void __launch_bounds__(kAppendThreads, 7)
   const bool report = part == 0 && lane == 0;
   uint8_t* base = token_block(p.c, p.dst_req[i], pos, report);
   if (!base) return;
-  const int slot = pos % kInt4Page;
+  const int slot = pos % kPageTokens;
   Turn turn;
-  const int h = p.rot / 16;
+  const int h = p.rope.rot / 16;
   turn.on = o < 2 * h;
   turn.partner = lane;
-  if (p.rot) {
+  if (p.rope.rot) {
     const int64_t at = p.rope_pos ? p.rope_pos[i] : pos;
-    if (at < 0 || at >= p.n_positions) {
+    if (at < 0 || at >= p.rope.n_positions) {
       if (report) flag(p.c.dev_status, OSCAR_DEV_LENGTH);
       return;
     }
-    const float* row = p.cos_sin + at * p.rot;
+    const float* row = p.rope.cos_sin + at * p.rope.rot;
     if (turn.on && !Interleaved) {
       const int j = o < h ? o : o - h;
       turn.partner = o < h ? lane + h : lane - h;
@@ -302,7 +238,7 @@ __global__ void __launch_bounds__(kAppendThreads, 7)
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (s0 + u >= end_q) break;
-      if (p.rot) rotate8<false, Interleaved>(raw[u], turn);
+      if (p.rope.rot) rotate8<false, Interleaved>(raw[u], turn);
       if ((s0 + u) * kRows + sub < p.c.n_q) *reinterpret_cast<uint4*>(dst + (s0 + u) * (kRows * D)) = raw[u];
     }
   }
@@ -326,7 +262,7 @@ __global__ void __launch_bounds__(kAppendThreads, 7)
     const int head = (is_v ? s - sk : s) * kRows + sub;
     const bool valid = head < p.c.n_kv;
     if (!is_v) {
-      if (p.rot) rotate8<true, Interleaved>(raw, turn);
+      if (p.rope.rot) rotate8<true, Interleaved>(raw, turn);
       if (p.k_out && valid) *reinterpret_cast<uint4*>(p.k_out + (i * p.c.n_kv + head) * D + 8 * o) = raw;
     }
     const int lanes = kLanes >> ((is_v ? ng_v : ng_k) >> 1);   // 1, 2 or 4 groups
@@ -369,14 +305,14 @@ __device__ __forceinline__ uint4 values8(uint32_t word, uint32_t pair) {
 // once (position, page, block: one behind the other, they take longer than a
 // token's rows do); the next slot's loads are ahead of the present one's work.
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kRowThreads)
     gather_kernel(const __grid_constant__ GatherParams p, int slots_per_warp, int tokens) {
   pdl_wait();
   pdl_launch_dependents();
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   const int lane = threadIdx.x & 31, o = lane % kLanes, sub = lane / kLanes;
   const int slots = (p.c.n_kv + kRows - 1) / kRows, warps_per_token = (slots + slots_per_warp - 1) / slots_per_warp;
-  const int64_t w = (int64_t(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
+  const int64_t w = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   const int64_t i0 = w / warps_per_token * tokens;
   if (i0 >= p.n) return;
   const int part = int(w % warps_per_token), count = int(min(int64_t(tokens), p.n - i0));
@@ -384,7 +320,7 @@ __global__ void __launch_bounds__(kAppendThreads)
   if (lane < count) {
     const int pos = p.src_pos[i0 + lane];
     const uint8_t* base = token_block(p.c, p.src_req[i0 + lane], pos, part == 0);
-    if (base) mine = reinterpret_cast<uint64_t>(base) | uint64_t(pos % kInt4Page);
+    if (base) mine = reinterpret_cast<uint64_t>(base) | uint64_t(pos % kPageTokens);
   }
   const int ng_k = p.c.ng_k, ng_v = p.c.ng_v, block_bytes = int4_block_bytes(D, ng_k, ng_v);
   const int begin = part * slots_per_warp, end = min(slots, begin + slots_per_warp);
@@ -429,19 +365,6 @@ __global__ void __launch_bounds__(kAppendThreads)
   }
 }
 
-// Slots of a token for one warp: as many as leave the GPU 24 warps an SM.  A
-// token's place and angles are then read once, not once a slot.
-int slots_of(int n, int slots) {
-  return int(std::min<int64_t>(slots, std::max<int64_t>(1, int64_t(n) * slots / (152 * 24))));
-}
-
-cudaError_t grid_of(int64_t warps, unsigned* blocks) {
-  const int64_t b = (warps + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
-  if (b < 1 || b > 0x7fffffff) return cudaErrorInvalidValue;
-  *blocks = unsigned(b);
-  return cudaSuccess;
-}
-
 }  // namespace
 
 cudaError_t launch_rope_append_int4(const AppendParams& p, cudaStream_t stream) {
@@ -451,9 +374,9 @@ cudaError_t launch_rope_append_int4(const AppendParams& p, cudaStream_t stream) 
   unsigned blocks = 0;
   const cudaError_t e = grid_of(int64_t(p.n) * ((slots + slots_per_warp - 1) / slots_per_warp), &blocks);
   if (e != cudaSuccess) return e;
-  auto* kernel = p.c.d == 128 ? (p.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
-                              : (p.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
-  return launch_pdl(kernel, dim3(blocks), dim3(kAppendThreads), 0, stream, p, slots_per_warp);
+  auto* kernel = p.c.d == 128 ? (p.rope.interleaved ? rope_append_kernel<128, true> : rope_append_kernel<128, false>)
+                              : (p.rope.interleaved ? rope_append_kernel<64, true> : rope_append_kernel<64, false>);
+  return launch_pdl(kernel, dim3(blocks), dim3(kRowThreads), 0, stream, p, slots_per_warp);
 }
 
 cudaError_t launch_gather_int4(const GatherParams& p, cudaStream_t stream) {
@@ -466,7 +389,7 @@ cudaError_t launch_gather_int4(const GatherParams& p, cudaStream_t stream) {
   const cudaError_t e = grid_of((int64_t(p.n) + tokens - 1) / tokens * ((slots + slots_per_warp - 1) / slots_per_warp), &blocks);
   if (e != cudaSuccess) return e;
   auto* kernel = p.c.d == 128 ? gather_kernel<128> : gather_kernel<64>;
-  return launch_pdl(kernel, dim3(blocks), dim3(kAppendThreads), 0, stream, p, slots_per_warp, tokens);
+  return launch_pdl(kernel, dim3(blocks), dim3(kRowThreads), 0, stream, p, slots_per_warp, tokens);
 }
 
 }  // namespace oscar

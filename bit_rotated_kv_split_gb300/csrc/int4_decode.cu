@@ -48,6 +48,7 @@
 
 #include "kernels.h"
 #include "oscar.h"
+#include "page_walk.cuh"
 #include "ptx.cuh"
 #include "score.cuh"
 
@@ -126,59 +127,9 @@ __device__ __forceinline__ float max_over_quad(float v) {   // over the 4 lanes 
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
-// The tokens of a request that its query sees, and their pages.
-struct Span {
-  int len, first;
-  __device__ __forceinline__ int page0() const { return first / kInt4Page; }
-  __device__ __forceinline__ int pages() const { return (len + kInt4Page - 1) / kInt4Page - page0(); }
-};
-__device__ __forceinline__ Span span_of(const Int4DecodeParams& p, int b, bool report) {
-  int len = p.c.seq_len[b];
-  if (len < 0 || len > p.c.max_len) {
-    if (report && p.c.dev_status) atomicOr(p.c.dev_status, OSCAR_DEV_LENGTH);
-    len = min(max(len, 0), p.c.max_len);
-  }
-  return {len, p.s.window ? max(0, len - p.s.window) : 0};
-}
-
-// A run's pages, or the part of them in this CTA's share: pages lo .. hi - 1 of
-// request b, head set h; `off` pages of the run lie before it, `pages` in all; it
-// begins at place `at` of the row.
-struct Segment {
-  int b, h, lo, hi, off, pages, len, first, at;
-  // a warp's first pair
-  __device__ __forceinline__ int place(int warp) const { return (warp - (at >> 1)) & (kWarps - 1); }
-};
-
-// Walks through a share, run by run.
-struct Walk {
-  int b, h, off;        // where the next segment begins: `off` pages into the run
-  int at, end;          // its place, and the share's end
-  Span span;            // of request b
-  __device__ __forceinline__ bool next(const Int4DecodeParams& p, int sets, Segment* s) {
-    int pages = span.pages();
-    // the share begins behind a run's pages, or within a run that is another's whole
-    if (at < end && off > 0 && (off >= pages || pages <= kWhole)) step(p, sets), pages = span.pages();
-    if (at >= end) return false;
-    const int n = pages <= kWhole ? pages : min(pages - off, end - at), lo = span.page0() + off;
-    *s = {b, h, lo, lo + n, off, pages, span.len, span.first, at};
-    off += n;
-    at += n;
-    if (off == pages) step(p, sets);
-    return true;
-  }
-  __device__ __forceinline__ void step(const Int4DecodeParams& p, int sets) {   // to the next run's first page
-    at += span.pages() + kRunCost - off;
-    off = 0;
-    if (++h < sets) return;
-    h = 0;
-    while (at < end && ++b < p.c.batch) {
-      span = span_of(p, b, false);
-      if (span.pages() > 0) return;
-    }
-    at = end;
-  }
-};
+using Walk = PageWalk<kRunCost, kWhole>;
+// a warp's first pair of a segment
+__device__ __forceinline__ int place_of(const Segment& s, int warp) { return (warp - (s.at >> 1)) & (kWarps - 1); }
 
 // Joins the warps' states of heads h0 .. of a segment, 4 channels a thread: to `out`, or
 // to the workspace's partial state `slot` if that is not negative.
@@ -245,7 +196,7 @@ __device__ __noinline__ void scan_wide(const Int4DecodeParams& p, Walk walk, int
   __syncthreads();                          // the scan's states have been read
   while (walk.next(p, sets, &cur)) {
     const int hk = cur.h / halves, set = cur.h % halves, in_set = min(kHeads, group - set * kHeads);
-    const int lo = cur.lo + 2 * cur.place(warp);
+    const int lo = cur.lo + 2 * place_of(cur, warp);
     const int32_t* table = p.c.page_table + int64_t(cur.b) * p.c.max_pages;
     auto page_of = [&](int i) { return lo + (i >> 1) * 2 * kWarps + (i & 1); };
     auto block_of = [&](int page) -> const uint8_t* {
@@ -256,7 +207,7 @@ __device__ __noinline__ void scan_wide(const Int4DecodeParams& p, Walk walk, int
     uint32_t top = 0, least = 0xFFFFFFFFu;
 #pragma unroll 1
     for (int i = 0; page_of(i) < cur.hi; i += 2) {
-      const int j = page_of(i + half) * kInt4Page + t;
+      const int j = page_of(i + half) * kPageTokens + t;
       const uint8_t* block = block_of(page_of(i + half));
       if (block && j >= cur.first && j < cur.len)
 #pragma unroll
@@ -306,7 +257,7 @@ __device__ __noinline__ void scan_wide(const Int4DecodeParams& p, Walk walk, int
               x[h] = fmaf(bf16_lo(u.z), k[4], fmaf(bf16_hi(u.z), k[5], fmaf(bf16_lo(u.w), k[6], fmaf(bf16_hi(u.w), k[7], x[h]))));
             }
         }
-        const int j = page_of(i) * kInt4Page + t;
+        const int j = page_of(i) * kPageTokens + t;
 #pragma unroll
         for (int h = 0; h < kJoinHeads; ++h) {
           float y = x[h] + __shfl_xor_sync(0xffffffffu, x[h], 16);
@@ -446,44 +397,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   const Int4Cache& c = p.c;
   const int sets = c.n_kv * halves, group = c.n_q / c.n_kv;
 
-  // this CTA's share: a prefix sum over the places of the requests' runs, a
-  // thread taking batch / 256 of them
-  const int per = (c.batch + kThreads - 1) / kThreads, b0 = min(c.batch, int(threadIdx.x) * per), b1 = min(c.batch, b0 + per);
-  int mine = 0;
-#pragma unroll 1
-  for (int b = b0; b < b1; ++b) {
-    const int n = span_of(p, b, blockIdx.x == 0).pages();
-    mine += n ? (n + kRunCost) * sets : 0;
-  }
-  int before = mine;
-#pragma unroll
-  for (int x = 1; x < 32; x <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, before, x);
-    if (lane >= x) before += v;
-  }
-  if (lane == 31) sm_scan[warp] = before;
-  __syncthreads();
-  int total = 0;
-  before -= mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm_scan[w];
-    total += sm_scan[w];
-  }
-  const int share = max(kMinShare, int((unsigned(total) + gridDim.x - 1) / gridDim.x));
-  const int64_t start = int64_t(share) * blockIdx.x;
-  const bool any = start < total;
-  if (any && start >= before && start - before < mine) {
-    int b = b0, at = int(start) - before;
-    Span s = span_of(p, b, false);
-#pragma unroll 1
-    while (s.pages() == 0 || at >= (s.pages() + kRunCost) * sets) {
-      at -= s.pages() ? (s.pages() + kRunCost) * sets : 0;
-      s = span_of(p, ++b, false);
-    }
-    const int run = s.pages() + kRunCost;
-    sm_walk = {b, at / run, at % run, int(start), int(min(int64_t(total), start + share)), s};
-  }
+  int share = 0;
+  const bool any = begin_share<kThreads>(p, sets, kMinShare, sm_scan, &sm_walk, &share);
   // requests without a token
   for (int b = blockIdx.x; b < c.batch; b += gridDim.x)
     if (c.seq_len[b] <= 0 || c.max_len == 0)
@@ -511,11 +426,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint8_t* ring = smem + warp * (kStages * 2 * kBlock);
   float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * kBlock);
   uint64_t* wbars = bars[warp];
-  auto place = [&](const Segment& s) { return s.place(warp); };
   // the segment being brought in: its pages from this warp's first, KV head, request, and pairs
   int in_lo, in_hi, in_hk, in_b, in_it = 0, in_n;
   auto turn_to = [&](const Segment& s) {
-    in_lo = s.lo + 2 * place(s);
+    in_lo = s.lo + 2 * place_of(s, warp);
     in_hi = s.hi;
     in_hk = s.h / halves;
     in_b = s.b;
@@ -587,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   int has_part = 0;                       // bits: of a run that began before this share, of one that goes on behind it
   while (true) {
     const int hk = cur.h / halves, set = cur.h % halves, heads = min(kHeads, group - set * kHeads);
-    const int hq0 = hk * group + set * kHeads, lo = cur.lo + 2 * place(cur);
+    const int hq0 = hk * group + set * kHeads, lo = cur.lo + 2 * place_of(cur, warp);
     const int n_it = max(0, (cur.hi - lo + 2 * kWarps - 1) / (2 * kWarps));
 
     // Query operands of column gid: head hq0 + gid, scaled by 2^(141 - ex) so
@@ -657,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint32_t vs_least = 0xFFFFFFFFu;        // one below the least scale seen that is not 0, fp16 bits twice
     const uint32_t z_keep = gid < NGV ? 0xffffffffu : 0u, z_one = gid == NGV ? 0x3C003C00u : 0u;
 
-    int tok = lo * kInt4Page;
+    int tok = lo * kPageTokens;
     for (int it = 0; it < n_it && !dead; ++it) {
       if (!__all_sync(0xffffffffu, mbar_try_wait(wbars + st, parity)) &&
           !__all_sync(0xffffffffu, mbar_wait_bounded(wbars + st, parity, kDefaultWaitNs))) {
@@ -764,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       const uint32_t gone = (ring_dead >> (2 * st)) & 3u;
-      if (gone || tok < cur.first || tok + 2 * kInt4Page > cur.len) {
+      if (gone || tok < cur.first || tok + 2 * kPageTokens > cur.len) {
         // what a stale slot holds is anything
         const bool here = !((gone >> (lane >> 4)) & 1u) && tok + lane >= cur.first && tok + lane < cur.len;
 #pragma unroll
@@ -838,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();                         // the stage has been read
       --flying;
       bring();
-      tok += 2 * kWarps * kInt4Page;
+      tok += 2 * kWarps * kPageTokens;
       st ^= 1;
       parity ^= st == 0;
     }
@@ -916,8 +830,8 @@ cudaError_t launch(const Int4DecodeParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int halves = (p.c.n_q / p.c.n_kv + kHeads - 1) / kHeads;
   int64_t tokens = p.c.max_len;
-  if (p.s.window) tokens = std::min<int64_t>(tokens, int64_t(p.s.window) + kInt4Page);
-  const int64_t places = ((tokens + kInt4Page - 1) / kInt4Page + kRunCost) * p.c.batch * p.c.n_kv * halves;
+  if (p.s.window) tokens = std::min<int64_t>(tokens, int64_t(p.s.window) + kPageTokens);
+  const int64_t places = ((tokens + kPageTokens - 1) / kPageTokens + kRunCost) * p.c.batch * p.c.n_kv * halves;
   if (places > INT32_MAX) return cudaErrorNotSupported;
   const int64_t ctas = std::min<int64_t>(kCtas, (places + kMinShare - 1) / kMinShare);
   return launch_pdl(decode_int4_kernel<D, NGK, NGV, Formed>, dim3(unsigned(ctas)), dim3(kThreads), bytes, stream, p, halves);

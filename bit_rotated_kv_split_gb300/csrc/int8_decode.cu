@@ -1,0 +1,666 @@
+// Decode attention over an 8-bit layer: one query token per request.
+//
+// The pages of all (request, KV head) runs stand in one row, and each of 152
+// lasting CTAs (one per SM) takes an equal share of it.  Only the first and the last
+// run of a share can be incomplete: they leave their unnormalised sums in the
+// workspace, and the last CTA of a run to finish joins its parts.
+//
+// A warp takes every 12th page of a run with an online softmax of its own, so
+// nothing in the scan waits for another warp.  The pages' blocks come by bulk copies
+// into a ring of the warp's own, the next run's ahead of the present one's end.
+//
+// Per page, on the tensor cores with the query heads as the rows:
+//   S = q K^T:  B = the K codes: ldmatrix gives a lane 4 channels' bytes of a token,
+//               two operand registers of one operation each: a byte c alone in an fp16
+//               is the subnormal c 2^-24, exactly.  q is scaled by a power of two per
+//               head to just below fp16's end, exact for bf16.
+//               x = scale (sum c q) + zero (sum q).
+//   O += P V:   A = P scale_V; B = the V codes, by ldmatrix with transposition.
+// S's accumulators are P's operands lane by lane, so nothing is moved between the two.
+// P scale_V is formed in fp32 and split into two fp16 parts (the second in rows 8 to
+// 15 where a group has at most 8 heads, else in products of its own), so that it
+// keeps 22 bits: a byte's range is a value's range, and an error of 2^-11 of it would
+// show in the bf16 output where values cancel.  The weights' sum and the zeros' share
+// of O are summed in fp32 beside it.
+// The weights' reference is raised only when a score exceeds it by 2^8, and the
+// values' scales are taken relative to a power of two above them, raised when a larger
+// one comes: both by one vote a page.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "int8.h"
+#include "kernels.h"
+#include "oscar.h"
+#include "page_walk.cuh"
+#include "ptx.cuh"
+#include "score.cuh"
+
+namespace oscar {
+namespace {
+
+constexpr int kWarps = 12, kThreads = 32 * kWarps;
+constexpr int kStages = 4;            // pages of a warp's ring
+constexpr int kCtas = 152;            // CTAs the GPU holds at a time
+constexpr int kHeads = 16;            // most query heads of a KV head
+constexpr int kMinShare = 2 * kWarps; // pages
+constexpr int kRunCost = 32;          // a run costs its CTA about as much as this many pages besides its own
+constexpr int kWhole = 48;            // a run of no more pages is not split
+constexpr int kJoinHeads = 4;         // heads whose states are joined at a time
+constexpr uint32_t kLow = 0x00FF00FFu;
+
+using Walk = PageWalk<kRunCost, kWhole>;
+// a warp's first page of a segment
+__device__ __forceinline__ int place_of(const Segment& s, int warp) {
+  const int i = warp - s.at % kWarps;
+  return i < 0 ? i + kWarps : i;
+}
+
+// Workspace: a ticket for each CTA (of the run that goes on behind its share),
+// then two partial states for each, of a run that began before its share and of one
+// that begins in it: (m, l) and the sums.
+constexpr size_t kOffMl = 4096, kOffO = kOffMl + size_t(kCtas) * 2 * kHeads * 8;
+
+template <int D>
+constexpr int join_bytes() {
+  // the warps' states of kJoinHeads heads; or the parts' weights and partial sums
+  return std::max(kWarps * kJoinHeads * D * 4, (kCtas + 1) * kHeads * 4 + kThreads * 16);
+}
+
+// D += A (16x16 f16, row) * B (16x8 f16, col); free for the compiler to move.
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&d)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_t(uint32_t (&d)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// bytes 0 and 2, bytes 1 and 3 of a word as two fp16 subnormals
+__device__ __forceinline__ uint32_t even(uint32_t w) { return w & kLow; }
+__device__ __forceinline__ uint32_t odd(uint32_t w) { return prmt(w, 0u, 0x4341); }
+
+__device__ __forceinline__ float max_over_quad(float v) {   // over the 4 lanes of a row
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float sum_over_quad(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+// The logarithm of the sum, from the reference in log2 units and the sum of 2^(7 + x - m).
+__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + (log2f(l) - 7.f)) * kLn2 : l == 0.f ? -INFINITY : l; }
+
+// Joins the warps' states of heads h0 .. of a segment, 4 channels a thread: to `out`, or
+// to the workspace's partial state `slot` if that is not negative.
+template <int D>
+__device__ __forceinline__ void join_warps(const Int8DecodeParams& p, int hq0, int h0, int heads, int slot, int b,
+                                           const float* buf, const float (&sm_m)[kWarps][kHeads],
+                                           const float (&sm_l)[kWarps][kHeads]) {
+  const int i = threadIdx.x, h = h0 + i / (D / 4);
+  if (i >= kJoinHeads * (D / 4) || h >= heads) return;
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  float mx = -FLT_MAX, sum = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    if (sm_l[w][h] > 0.f) mx = fmaxf(mx, sm_m[w][h]);
+#pragma unroll 4
+  for (int w = 0; w < kWarps; ++w) {
+    const float l = sm_l[w][h], f = l == 0.f ? 0.f : exp2_fast(sm_m[w][h] - mx);   // (a NaN stays one)
+    const float4 x = reinterpret_cast<const float4*>(buf)[w * kJoinHeads * (D / 4) + i];
+    sum = fmaf(f, l, sum);
+    v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+  }
+  if (slot < 0) {
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    reinterpret_cast<uint2*>(p.out + (int64_t(b) * p.c.n_q + hq0) * D)[h0 * (D / 4) + i] =
+        make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
+    if (p.lse && i % (D / 4) == 0) p.lse[int64_t(b) * p.c.n_q + hq0 + h] = lse_of(mx, sum);
+  } else {
+    reinterpret_cast<float4*>(ws + kOffO)[(int64_t(slot) * kHeads + h0) * (D / 4) + i] = v;
+    if (i % (D / 4) == 0) reinterpret_cast<float2*>(ws + kOffMl)[slot * kHeads + h] = make_float2(mx, sum);
+  }
+}
+
+// 2^ve with ve in [-14, 16] is at least a scale of this size (fp16 bits) and any smaller one
+__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+  return min(max(((__float_as_int(half2_to_float2(bits).x) >> 23) & 255) - 126, -14), 16);
+}
+
+// A run in more than one share: its place in the row, pages, request, first
+// query head and their number.
+struct Part {
+  int run, pages, b, hq0, heads;
+};
+
+// Joins the parts of a run; the whole CTA, 4 channels a thread.  Where the heads
+// leave threads over, each takes every n-th part; where there are more heads than
+// threads for them, they come in turns.  (Small code: it runs once a CTA, when its
+// instructions have to come from far.)
+template <int D>
+__device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r, int share, float* wt, float* sum_of) {
+  const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = r.heads;
+  const int f = r.run / share, n = (r.run + r.pages - 1) / share - f + 1;
+  auto slot_of = [&](int i) { return 2 * (f + i) + (i == 0); };
+  const float2* ml = reinterpret_cast<const float2*>(ws + kOffMl);
+  for (int h = warp; h < heads; h += kWarps) {
+    float mx = -FLT_MAX, sum = 0.f;
+#pragma unroll 2
+    for (int i = lane; i < n; i += 32) {
+      const float2 s = __ldcg(&ml[slot_of(i) * kHeads + h]);
+      const float m = s.y == 0.f ? -FLT_MAX : s.x, mn = fmaxf(mx, m);
+      sum = fmaf(exp2_fast(m - mn), s.y, sum * exp2_fast(mx - mn));
+      mx = mn;
+      wt[i * kHeads + h] = m;
+    }
+    float all = mx;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, i));
+    sum *= exp2_fast(mx - all);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) wt[i * kHeads + h] = exp2_fast(wt[i * kHeads + h] - all);
+    if (lane == 0) {
+      sum_of[h] = sum;
+      if (p.lse) p.lse[int64_t(r.b) * p.c.n_q + r.hq0 + h] = lse_of(all, sum);
+    }
+  }
+  __syncthreads();
+  constexpr int kBatch = 8;
+  const int units = heads * (D / 4), ways = max(1, kThreads / units);
+  float4* sums = reinterpret_cast<float4*>(wt + n * kHeads);
+  for (int u0 = 0; u0 < units; u0 += kThreads) {
+    const int left = min(units - u0, kThreads), way = threadIdx.x / left, unit = u0 + threadIdx.x % left, h = unit / (D / 4);
+    const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (way < ways)
+#pragma unroll 1
+      for (int i = way; i < n; i += kBatch * ways) {
+        float4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) x[k] = __ldcg(from + slot_of(min(i + k * ways, n - 1)) * (kHeads * D / 4));
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float g = i + k * ways < n ? wt[(i + k * ways) * kHeads + h] : 0.f;
+          v.x = fmaf(g, x[k].x, v.x), v.y = fmaf(g, x[k].y, v.y), v.z = fmaf(g, x[k].z, v.z), v.w = fmaf(g, x[k].w, v.w);
+        }
+      }
+    if (ways > 1) {
+      sums[threadIdx.x] = v;
+      __syncthreads();
+    }
+    if (way == 0) {
+#pragma unroll 1
+      for (int i = 1; i < ways; ++i) {
+        const float4 y = sums[i * units + unit];
+        v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+      }
+      const float inv = sum_of[h] != 0.f ? 1.f / sum_of[h] : 0.f;
+      reinterpret_cast<uint2*>(p.out + (int64_t(r.b) * p.c.n_q + r.hq0) * D)[unit] =
+          make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
+    }
+  }
+}
+
+// R: rows of heads a lane has (1: groups of up to 8 heads, 2: of up to 16).
+// Formed: the scores have a cap or a distance bias.
+template <int D, int R, bool Formed>
+__global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_constant__ Int8DecodeParams p) {
+  constexpr int kBlock = int8_block_bytes(D), C = D / 16;   // chunks of 16 channels
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
+  __shared__ int sm_scan[kWarps];
+  __shared__ Walk sm_walk, sm_walks[kWarps];
+  __shared__ Segment sm_next[kWarps];
+  __shared__ Part sm_part[2];
+  __shared__ int sm_last[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
+  if (lane < kStages) mbar_init(&bars[warp][lane], 1);
+  fence_mbar_init();
+  __syncwarp();
+  pdl_wait();
+  pdl_launch_dependents();
+  const PagedCache& c = p.c;
+  const int group = c.n_q / c.n_kv;
+
+  int share = 0;
+  const bool any = begin_share<kThreads>(p, c.n_kv, kMinShare, sm_scan, &sm_walk, &share);
+  // requests without a token
+  for (int b = blockIdx.x; b < c.batch; b += gridDim.x)
+    if (c.seq_len[b] <= 0 || c.max_len == 0) {
+      for (int i = threadIdx.x; i < c.n_q * D / 8; i += kThreads)
+        reinterpret_cast<uint4*>(p.out + int64_t(b) * c.n_q * D)[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse)
+        for (int i = threadIdx.x; i < c.n_q; i += kThreads) p.lse[int64_t(b) * c.n_q + i] = -INFINITY;
+    }
+  __syncthreads();
+  if (!any) return;
+
+  // Each warp walks by itself; the next segment waits in shared memory.
+  auto advance = [&]() {
+    bool ok = false;
+    if (lane == 0) ok = sm_walks[warp].next(p, c.n_kv, &sm_next[warp]);
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+  };
+  if (lane == 0) sm_walks[warp] = sm_walk;
+  if (!advance()) return;                 // (nothing but places of a run's cost; the same in all warps)
+  Segment cur = sm_next[warp];
+  __syncwarp();
+  bool more = false;                      // sm_next holds another
+
+  // The ring.  A warp's pages of a segment begin with another warp each time, so
+  // that short segments spread over the warps.  Lane i knows pages 32 n + i of the
+  // segment that is being brought in.
+  uint8_t* ring = smem + warp * (kStages * kBlock);
+  float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * kBlock);
+  uint64_t* wbars = bars[warp];
+  // the segment being brought in: its pages from this warp's first, KV head, request, and number
+  int in_lo, in_hi, in_hk, in_b, in_it = 0, in_n;
+  auto turn_to = [&](const Segment& s) {
+    in_lo = s.lo + place_of(s, warp);
+    in_hi = s.hi;
+    in_hk = s.h;
+    in_b = s.b;
+    in_it = 0;
+    in_n = max(0, (in_hi - in_lo + kWarps - 1) / kWarps);
+  };
+  turn_to(cur);
+  bool in_next = false, dead = false;     // it is the next one, not cur
+  int id = -1, st_in = 0, flying = 0;
+  uint32_t ring_dead = 0;                 // bit i: stage i's page is not there
+  auto bring = [&]() {                    // one more page; false if there is none to bring yet
+    if (in_it == in_n) {
+      if (in_next || !more || dead) return false;
+      in_next = true;
+      turn_to(sm_next[warp]);
+      if (in_n == 0) return false;
+    }
+    if ((in_it & 31) == 0) {
+      const int page = in_lo + kWarps * (in_it + lane);
+      id = page < in_hi ? c.page_table[int64_t(in_b) * c.max_pages + page] : -1;
+      if (page < in_hi && (id < 0 || id >= c.n_pages)) {
+        if (c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+        id = -1;
+      }
+    }
+    const int owner = in_it & 31;
+    const uint32_t none = __shfl_sync(0xffffffffu, id < 0 ? 1u : 0u, owner);
+    ring_dead = (ring_dead & ~(1u << st_in)) | (none << st_in);
+    if (lane == owner) {
+      uint64_t* bar = wbars + st_in;
+      if (none) {
+        mbar_arrive(bar);
+      } else {
+        mbar_arrive_expect_tx(bar, kBlock);
+        bulk_copy_g2s(ring + st_in * kBlock, c.pages + (int64_t(id) * c.n_kv + in_hk) * kBlock, kBlock, bar);
+      }
+    }
+    st_in = st_in + 1 == kStages ? 0 : st_in + 1;
+    ++in_it;
+    ++flying;
+    return true;
+  };
+  // The queries of rows gid and gid + 8, channels 16 i + 4 tig .. + 3, asked for
+  // before the copies.
+  uint2 uq[R][C];
+  auto ask_q = [&](const Segment& s) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint16_t* row = p.q + s.b * p.q_stride + int64_t(s.h * group + gid + 8 * r) * D + 4 * tig;
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        uq[r][i] = gid + 8 * r < group ? *reinterpret_cast<const uint2*>(row + 16 * i) : make_uint2(0, 0);
+    }
+  };
+  ask_q(cur);
+  while (flying < kStages && bring()) {
+  }
+  more = advance();                       // (the first copies do not wait for it)
+  while (flying < kStages && bring()) {
+  }
+
+  // Where this lane's rows of the ldmatrix loads lie in a page: matrices 0 .. 3 are
+  // tokens 0 - 7 and 8 - 15 of chunk 2 i, then of chunk 2 i + 1; chunks 2 i further
+  // on are an exclusive or with 32 i.
+  const int lm_t = (lane & 7) + 8 * ((lane >> 3) & 1);
+  const uint32_t lm = uint32_t(lm_t * D + 16 * ((lane >> 4) ^ int8_swizzle(D, lm_t)));
+
+  int st = 0;
+  uint32_t parity = 0;
+  int has_part = 0;                       // bits: of a run that began before this share, of one that goes on behind it
+  while (true) {
+    const int hq0 = cur.h * group, lo = cur.lo + place_of(cur, warp);
+    const int n_it = max(0, (cur.hi - lo + kWarps - 1) / kWarps);
+
+    // Query operands, scaled by 2^(141 - ex) so that a head's largest channel is in [2^14, 2^15).
+    uint32_t qa[R][C][2];
+    float qs[R], unscale[R], slope[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float top = 0.f, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        top = fmaxf(top, fmaxf(fabsf(bf16_lo(uq[r][i].x)), fabsf(bf16_hi(uq[r][i].x))));
+        top = fmaxf(top, fmaxf(fabsf(bf16_lo(uq[r][i].y)), fabsf(bf16_hi(uq[r][i].y))));
+      }
+      top = max_over_quad(top);
+      const int ex = min(max((__float_as_int(top) >> 23) & 255, 14), 243);
+      const float up = pow2i(141 - ex);
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const float q0 = bf16_lo(uq[r][i].x) * up, q1 = bf16_hi(uq[r][i].x) * up;
+        const float q2 = bf16_lo(uq[r][i].y) * up, q3 = bf16_hi(uq[r][i].y) * up;
+        sum += (q0 + q1) + (q2 + q3);
+        qa[r][i][0] = pack_half2(q0, q2);
+        qa[r][i][1] = pack_half2(q1, q3);
+      }
+      qs[r] = sum_over_quad(sum) * 5.9604644775390625e-8f;   // 2^-24, as the codes carry
+      unscale[r] = pow2i(ex - 117);                          // 2^24 / up
+      if (p.s.cap_log2 == 0.f) unscale[r] *= p.s.scale_log2; // (with a cap, capped() takes the scale)
+      slope[r] = Formed && p.s.slopes && gid + 8 * r < group ? p.s.slopes[hq0 + gid + 8 * r] * kLog2e : 0.f;
+    }
+
+    // x is in the dot product's own scale, or in log2 units where the score has a
+    // form of its own; us takes it to log2 units, thr is m + 8 / us.  The weights are
+    // 2^(7 + (x - m) us) <= 2^15 (the difference first: exact where it matters, however
+    // far the scores).
+    float us[R], thr[R], m[R], l[R], zs[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      us[r] = Formed ? 1.f : fmaxf(unscale[r], FLT_MIN);
+      m[r] = thr[r] = -FLT_MAX;
+      l[r] = zs[r] = 0.f;
+    }
+    // o[4 i + 2 k + e]: chunk 2 i + k, its even (e = 0) or odd channels.  Rows: R = 1: head
+    // gid by the two parts of the weights; R = 2: heads gid, gid + 8.
+    float o[2 * C][4];
+#pragma unroll
+    for (int t = 0; t < 2 * C; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    int ve = -14;                           // the V scales seen are at most 2^ve
+    uint32_t vs_top = 0x0400u;              // 2^ve in fp16
+    float vs_mul = 16384.f;                 // 2^-ve
+
+    int tok = lo * kPageTokens;
+    for (int it = 0; it < n_it && !dead; ++it) {
+      if (!__all_sync(0xffffffffu, mbar_try_wait(wbars + st, parity)) &&
+          !__all_sync(0xffffffffu, mbar_wait_bounded(wbars + st, parity, kDefaultWaitNs))) {
+        // a copy did not land in time: nothing more is brought in, and what is in
+        // flight is still waited for before its shared memory goes
+        if (lane == 0 && c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_TIMEOUT);
+        dead = true;
+        for (; flying > 0; --flying) {
+          mbar_wait_bounded(wbars + st, parity, kDrainWaitNs);
+          st = st + 1 == kStages ? 0 : st + 1;
+          parity ^= st == 0;
+        }
+        __syncwarp();
+        break;
+      }
+      const uint32_t blk = smem_addr(ring + st * kBlock), at = blk + lm;
+      // S: rows are heads, columns tokens: two products over the even, two over the odd pairs of chunks
+      float acc[2][2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) acc[t][u][0] = acc[t][u][1] = acc[t][u][2] = acc[t][u][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        uint32_t k[4];
+        ldmatrix_x4(k, at ^ (32 * i));
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            mma(acc[t][u], qa[0][2 * i + u][0], R == 2 ? qa[R - 1][2 * i + u][0] : 0u, qa[0][2 * i + u][1],
+                R == 2 ? qa[R - 1][2 * i + u][1] : 0u, even(k[2 * u + t]), odd(k[2 * u + t]));
+      }
+      // tokens 2 tig, + 1, 8 + 2 tig, + 1: scales and zeros
+      float ks[4], kz[4], vs[4], vz[4];
+      uint32_t vbits[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const uint4 w = lds128(blk + 32 * D + 64 * t + 16 * tig);
+        const float2 k0 = half2_to_float2(w.x), v0 = half2_to_float2(w.y), k1 = half2_to_float2(w.z), v1 = half2_to_float2(w.w);
+        ks[2 * t] = k0.x, kz[2 * t] = k0.y, ks[2 * t + 1] = k1.x, kz[2 * t + 1] = k1.y;
+        vs[2 * t] = v0.x, vz[2 * t] = v0.y, vs[2 * t + 1] = v1.x, vz[2 * t + 1] = v1.y;
+        vbits[2 * t] = w.y & 0xFFFFu, vbits[2 * t + 1] = w.w & 0xFFFFu;
+      }
+      float y[R][4];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          y[r][j] = fmaf(ks[j], acc[j >> 1][0][2 * r + (j & 1)] + acc[j >> 1][1][2 * r + (j & 1)], kz[j] * qs[r]);
+      if (Formed) {
+        float far = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[r][j] *= unscale[r], far = fmaxf(far, fabsf(y[r][j]));
+        if (p.s.cap_log2 != 0.f) {
+          // (the vote skips a form that no score here needs; each score's own is its own)
+          if (__builtin_expect(__any_sync(0xffffffffu, !cap_is_near(far, p.s)), 0)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[r][j] = capped(y[r][j], p.s);
+          } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[r][j] = capped_near(y[r][j], p.s);
+          }
+        }
+        if (p.s.slopes) {
+          const int away = tok + 2 * tig - (cur.len - 1);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[r][j] = fmaf(slope[r], float(away + 8 * (j >> 1) + (j & 1)), y[r][j]);
+        }
+      }
+      const bool gone = (ring_dead >> st) & 1u;
+      if (gone || tok < cur.first || tok + kPageTokens > cur.len) {
+        // what a stale slot holds is anything
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at_tok = tok + 8 * (j >> 1) + 2 * tig + (j & 1);
+          if (gone || at_tok < cur.first || at_tok >= cur.len) {
+            vs[j] = vz[j] = 0.f;
+            vbits[j] = 0;
+#pragma unroll
+            for (int r = 0; r < R; ++r) y[r][j] = -INFINITY;
+          }
+        }
+      }
+      const uint32_t smax = max(max(vbits[0], vbits[1]), max(vbits[2], vbits[3]));   // (fp16 values >= 0 order as integers)
+      bool raise = smax > vs_top;
+      float top[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        top[r] = fmaxf(fmaxf(y[r][0], y[r][1]), fmaxf(y[r][2], y[r][3]));
+        raise = raise | (top[r] > thr[r]);
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+        const int ne = max(ve, scale_exponent(__reduce_max_sync(0xffffffffu, smax)));
+        const float fv = pow2i(ve - ne);
+        ve = ne;
+        vs_top = ve < 16 ? uint32_t(ve + 15) << 10 : 0xFFFFu;
+        vs_mul = pow2i(-ve);
+        float f[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float mn = fmaxf(m[r], max_over_quad(top[r]));
+          f[r] = exp2_fast((m[r] - mn) * us[r]);
+          m[r] = mn;
+          thr[r] = mn + 8.f / us[r];
+          l[r] *= f[r];
+          zs[r] *= f[r];
+          f[r] *= fv;
+        }
+#pragma unroll
+        for (int t = 0; t < 2 * C; ++t)
+          o[t][0] *= f[0], o[t][1] *= f[0], o[t][2] *= f[R - 1], o[t][3] *= f[R - 1];
+      }
+      uint32_t hi[R][2], part[R][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = exp2_fast(fmaf(y[r][2 * t] - m[r], us[r], 7.f)), p1 = exp2_fast(fmaf(y[r][2 * t + 1] - m[r], us[r], 7.f));
+          l[r] += p0 + p1;
+          zs[r] = fmaf(p0, vz[2 * t], fmaf(p1, vz[2 * t + 1], zs[r]));
+          const float w0 = p0 * (vs[2 * t] * vs_mul), w1 = p1 * (vs[2 * t + 1] * vs_mul);
+          hi[r][t] = pack_half2(w0, w1);
+          const float2 h = half2_to_float2(hi[r][t]);
+          part[r][t] = pack_half2(w0 - h.x, w1 - h.y);
+        }
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        uint32_t v[4];
+        ldmatrix_x4_t(v, (at + 16 * D) ^ (32 * i));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t b0 = even(v[2 * u]), b1 = even(v[2 * u + 1]), d0 = odd(v[2 * u]), d1 = odd(v[2 * u + 1]);
+          float(&oe)[4] = o[4 * i + 2 * u], (&oo)[4] = o[4 * i + 2 * u + 1];
+          if (R == 1) {
+            mma(oe, hi[0][0], part[0][0], hi[0][1], part[0][1], b0, b1);
+            mma(oo, hi[0][0], part[0][0], hi[0][1], part[0][1], d0, d1);
+          } else {
+            mma(oe, hi[0][0], hi[R - 1][0], hi[0][1], hi[R - 1][1], b0, b1);
+            mma(oo, hi[0][0], hi[R - 1][0], hi[0][1], hi[R - 1][1], d0, d1);
+            mma(oe, part[0][0], part[R - 1][0], part[0][1], part[R - 1][1], b0, b1);
+            mma(oo, part[0][0], part[R - 1][0], part[0][1], part[R - 1][1], d0, d1);
+          }
+        }
+      }
+      __syncwarp();                         // the stage has been read
+      --flying;
+      bring();
+      tok += kWarps * kPageTokens;
+      st = st + 1 == kStages ? 0 : st + 1;
+      parity ^= st == 0;
+    }
+
+    if (more) ask_q(sm_next[warp]);
+    // The warps' states of this segment, kJoinHeads heads at a time.  (All with
+    // the weights' 2^7; a warp without a token has l = 0, whatever its m.)
+    const float un = pow2i(24 + ve);        // 2^24 of the codes, 2^ve of the scales
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] = sum_over_quad(l[r]);
+      zs[r] = sum_over_quad(zs[r]);
+      if (tig == 0) sm_m[warp][gid + 8 * r] = m[r] * us[r], sm_l[warp][gid + 8 * r] = l[r];
+    }
+    const bool whole = cur.off == 0 && cur.hi - cur.lo == cur.pages;
+    const int slot = 2 * blockIdx.x + (cur.off == 0);
+    for (int h0 = 0; h0 < group; h0 += kJoinHeads) {
+      if (h0) __syncthreads();              // the heads before have been read
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int h = gid + 8 * r - h0;
+        if (h >= 0 && h < kJoinHeads) {
+          float4* to = reinterpret_cast<float4*>(buf + (warp * kJoinHeads + h) * D + 4 * tig);
+#pragma unroll
+          for (int i = 0; i < C; ++i) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+                x[2 * n + e] = fmaf(R == 1 ? o[2 * i + e][n] + o[2 * i + e][2 + n] : o[2 * i + e][2 * r + n], un, zs[r]);
+            to[4 * i] = make_float4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+      __syncthreads();
+      join_warps<D>(p, hq0, h0, group, whole ? -1 : slot, cur.b, buf, sm_m, sm_l);
+    }
+    if (!whole && threadIdx.x == 0) sm_part[cur.off == 0] = {cur.at - cur.off, cur.pages, cur.b, hq0, group};
+    has_part |= whole ? 0 : 1 << (cur.off == 0);
+    if (!more) break;
+    __syncthreads();                        // the joined states have been read
+    cur = sm_next[warp];
+    __syncwarp();
+    more = advance();
+    in_next = false;
+    if (dead) in_n = in_it;
+    if (!dead)
+      while (flying < kStages && bring()) {
+      }
+  }
+  if (!has_part) return;
+
+  // The runs that this CTA has a part of (the first of its share, the last, or
+  // both): the last of a run's CTAs to come here joins its parts.
+  __syncthreads();
+  if (threadIdx.x < 2 && ((has_part >> threadIdx.x) & 1)) {
+    const Part& r = sm_part[threadIdx.x];
+    const int f = r.run / share;          // the run lies in the shares of CTAs f ..
+    uint32_t* ticket = static_cast<uint32_t*>(p.workspace) + f;
+    const bool last = atom_add_acq_rel_gpu(ticket, 1) == uint32_t((r.run + r.pages - 1) / share - f);
+    if (last) *ticket = 0;                // ready for the next call
+    sm_last[threadIdx.x] = last;
+  }
+  __syncthreads();
+  for (int which = 0; which < 2; ++which)
+    if (((has_part >> which) & 1) && sm_last[which]) {
+      if (which) __syncthreads();
+      join_parts<D>(p, sm_part[which], share, buf, sm_l[0]);
+    }
+}
+
+template <int D, int R, bool Formed>
+cudaError_t launch(const Int8DecodeParams& p, cudaStream_t stream) {
+  constexpr int bytes = kWarps * kStages * int8_block_bytes(D) + join_bytes<D>();
+  const cudaError_t e = set_smem_limit<decode_int8_kernel<D, R, Formed>>(bytes);
+  if (e != cudaSuccess) return e;
+  int64_t tokens = p.c.max_len;
+  if (p.s.window) tokens = std::min<int64_t>(tokens, int64_t(p.s.window) + kPageTokens);
+  const int64_t places = ((tokens + kPageTokens - 1) / kPageTokens + kRunCost) * p.c.batch * p.c.n_kv;
+  if (places > INT32_MAX) return cudaErrorNotSupported;
+  const int64_t ctas = std::min<int64_t>(kCtas, (places + kMinShare - 1) / kMinShare);
+  return launch_pdl(decode_int8_kernel<D, R, Formed>, dim3(unsigned(ctas)), dim3(kThreads), bytes, stream, p);
+}
+
+template <int D, int R>
+cudaError_t launch_f(const Int8DecodeParams& p, cudaStream_t stream) {
+  return p.s.cap_log2 != 0.f || p.s.slopes ? launch<D, R, true>(p, stream) : launch<D, R, false>(p, stream);
+}
+template <int D>
+cudaError_t launch_r(const Int8DecodeParams& p, cudaStream_t stream) {
+  return p.c.n_q / p.c.n_kv > 8 ? launch_f<D, 2>(p, stream) : launch_f<D, 1>(p, stream);
+}
+
+}  // namespace
+
+size_t int8_decode_workspace_bytes(const PagedCache& c) { return kOffO + size_t(kCtas) * 2 * kHeads * c.d * 4; }
+
+cudaError_t launch_decode_int8(const Int8DecodeParams& p, cudaStream_t stream) {
+  return p.c.d == 128 ? launch_r<128>(p, stream) : launch_r<64>(p, stream);
+}
+
+}  // namespace oscar

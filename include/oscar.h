@@ -724,6 +724,210 @@ oscar_status oscar_prompt_attention(const oscar_prompt_desc* desc, const oscar_s
                                     const int32_t* prefix_len, uint16_t* out, float* lse, void* workspace,
                                     size_t* workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------- rotary positions
+ *
+ * What serves every kind of layer before its cache: the tables that
+ * oscar_rope_desc points to, and norm and rotation of query and key rows.  (The
+ * pages take keys as given, after both.)
+ */
+
+/* How the frequencies theta^(-2 i / rot_dim) of the pairs i are scaled for contexts
+ * longer than the trained one. */
+enum {
+  OSCAR_ROPE_PLAIN = 0,     /* not at all                                         */
+  OSCAR_ROPE_LINEAR = 1,    /* all divided by the factor                          */
+  OSCAR_ROPE_BASE = 2,      /* theta times factor^(rot_dim / (rot_dim - 2)): the  */
+                            /* fastest pair stays, the slowest is divided         */
+  OSCAR_ROPE_BY_INDEX = 3,  /* pairs that make turns_high turns or more over the  */
+                            /* trained context stay, those of turns_low or fewer  */
+                            /* are divided; between, a ramp over the pair's index */
+                            /* (its ends rounded outwards to whole indices)       */
+  OSCAR_ROPE_BY_TURNS = 4   /* the same with the ramp over the pair's turns       */
+};
+typedef struct oscar_rope_scaling {
+  int32_t kind;               /* OSCAR_ROPE_*                                   */
+  int32_t reserved;           /* 0                                              */
+  double factor;              /* >= 1 (not read for PLAIN)                      */
+  double original_len;        /* positions of the trained context (BY_*)        */
+  double turns_low;           /* BY_*: 0 < low < high; both 0: 1 and 32         */
+  double turns_high;          /* (BY_INDEX), 1 and 4 (BY_TURNS)                 */
+} oscar_rope_scaling;
+
+/*
+ * oscar_rope_frequencies - the frequencies of a rotation, in radians per
+ * position: freq_out (host, [rot_dim / 2] float64).  scaling may be NULL
+ * (PLAIN).  *magnitude_out (nullable): the factor on cosines and sines that goes
+ * with the scaling (BY_INDEX: 0.1 ln(factor) + 1; else 1).  rot_dim a multiple of 16,
+ * 16 .. 128; theta > 1.  Host-only, synchronous.
+ */
+oscar_status oscar_rope_frequencies(int32_t rot_dim, double theta, const oscar_rope_scaling* scaling,
+                                    double* freq_out, double* magnitude_out);
+
+/*
+ * oscar_rope_table - the table of an oscar_rope_desc: cos_sin (device, [n][rot_dim]
+ * fp32, 16-byte aligned), row j = the rot_dim / 2 cosines of the angles (first + j) freq[i],
+ * then their sines, all times magnitude.
+ *
+ *   freq: host [rot_dim / 2], 0 <= freq <= 6 radians (of oscar_rope_frequencies, or any
+ *   others; read during the call).  Angles are reduced exactly: an entry is off by
+ *   2^-23 of its own size and (first + j) 2^-64 of a turn at the most, at any position.  rot_dim a
+ *   multiple of 16, 16 .. 128; 0 <= first, n <= 2^40.  n = 0 is a no-op.  Async.
+ */
+oscar_status oscar_rope_table(const double* freq, int32_t rot_dim, double magnitude, int64_t first, int64_t n,
+                              float* cos_sin, void* stream);
+
+/* Norm of each head before its rotation: x / sqrt(mean of x^2 + eps), times the weights. */
+typedef struct oscar_head_norm {
+  const uint16_t* q_weight;   /* device [head_dim] bf16, 16-byte aligned; NULL: */
+  const uint16_t* k_weight;   /* query (key) heads have no norm                 */
+  float eps;                  /* >= 0 and finite                                */
+  int32_t reserved;           /* 0                                              */
+} oscar_head_norm;
+
+/*
+ * oscar_norm_rope - norm and rotation of the query and key rows of n tokens, for
+ * layers whose cache is filled by another call (oscar_quantize_append and
+ * oscar_decode_step take keys as they come out of this one).
+ *
+ *   For item i < n: every head of q row i (q + i * q_stride, n_q_heads heads of
+ *   head_dim bf16) and of k row i is normed (norm NULL, or without that weight: not)
+ *   and then rotated by row pos[i] of rope->cos_sin as in oscar_rope_append_int4
+ *   (rope NULL: not), to row i of q_out and k_out.  fp32 arithmetic, one rounding to
+ *   bf16 at the end.  The mean of the squares is fp32: rows above 2^63 in magnitude
+ *   are the caller's to scale.
+ *   pos: device int32 [n]; may be NULL without a rotation.  pos[i] = -1 marks a padding
+ *   row: it is left as it was.  Any other position outside cos_sin skips the item and
+ *   sets OSCAR_DEV_LENGTH in *dev_status (device int32, nullable).
+ *   q and q_out may be NULL together, and so may k and k_out.  Rows 16-byte aligned, strides
+ *   multiples of 8 elements and at least a row.  q_out may be q where the strides are
+ *   equal, and k_out k; no other overlap.  head_dim 64 or 128.  n = 0 is a no-op.  Async.
+ */
+oscar_status oscar_norm_rope(int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, const oscar_head_norm* norm,
+                             const oscar_rope_desc* rope, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                             int64_t k_stride, const int32_t* pos, int32_t n, uint16_t* q_out, int64_t q_out_stride,
+                             uint16_t* k_out, int64_t k_out_stride, int32_t* dev_status, void* stream);
+
+/*
+ * ---------------------------------------------------------------- 8-bit layers
+ *
+ * A layer that four bits do not carry keeps its whole KV cache at 8: the paged
+ * cache of the 4-bit layers with 256 codes and one (scale, zero) for each vector
+ * of a (token, KV head, K|V).
+ *
+ * Codec: zero = the vector's least channel rounded down to fp16, scale =
+ * (greatest - zero) / 255 rounded up to fp16, code = (x - zero) / scale to the nearest
+ * integer (ties to even), 0 where scale is 0: no channel lies outside the codes, and
+ * every one is within half a scale of zero + scale * code.  Scales and codes are those
+ * of exact differences and quotients.
+ *
+ * Page pool layout: head_dim d is 64 or 128, 16 tokens per page.  A block of one
+ * (page p, KV head h) has 32 d + 128 bytes (oscar_int8_block_bytes) and sits at
+ * byte (p * n_kv_heads + h) * block:
+ *   [0, 16 d)     K codes: channel 16 c + i of token slot t is byte t d +
+ *                 16 (c ^ x) + i, x = t % 8 (d = 128) or (t / 2) % 4 (d = 64);
+ *   [16 d, 32 d)  V codes the same way;
+ *   [32 d, ...)   slot t: K scale, K zero, V scale, V zero (fp16) at 32 d + 8 t.
+ * (The order of a slot's 16-byte chunks lets eight slots' chunks of the same
+ * channels be read from different shared-memory banks at once.)
+ */
+typedef struct oscar_int8_desc {
+  int32_t batch;              /* B >= 1                                         */
+  int32_t n_q_heads;          /* H_q, a multiple of n_kv_heads                  */
+  int32_t n_kv_heads;         /* H_kv >= 1                                      */
+  int32_t head_dim;           /* 64 or 128                                      */
+  int32_t max_pages_per_seq;  /* row length of page_table                       */
+  int32_t max_len;            /* host upper bound on every seq_len[b] (decode)  */
+  int64_t n_pages;            /* physical pages in the pool                     */
+  float tau_k;                /* keys are clamped to [-tau_k, tau_k]; 0 < tau <= 65504 */
+  float tau_v;                /* the same for values                            */
+  uint8_t* pages;             /* pool, 128-byte aligned (layout above)          */
+  const int32_t* page_table;  /* [B][max_pages_per_seq] physical page ids       */
+  const int32_t* seq_len;     /* [B] cached tokens of each request (decode)     */
+  int32_t* dev_status;        /* optional device word for OSCAR_DEV_* bits      */
+} oscar_int8_desc;
+
+/* Bytes of one (page, KV head) block of an 8-bit layer; 0 for an invalid head size.  Host-only. */
+int64_t oscar_int8_block_bytes(int32_t head_dim);
+
+/*
+ * oscar_rope_append_int8 - norms and rotates the queries and keys of n tokens
+ * and appends their keys and values to an 8-bit layer's pages.
+ *
+ *   For item i < n: q row i and k row i are normed (norm) and rotated by row rope_pos[i]
+ *   of rope->cos_sin (rope_pos NULL: dst_pos[i]) as in oscar_norm_rope, rounded to bf16:
+ *   q' and k'.  q' goes to q_out and k' to k_out ([n][heads][d], contiguous; each may be
+ *   NULL, or q / k itself where that is contiguous).  k' and v row i, clamped to
+ *   [-tau, tau], are quantised by the codec above and stored at position dst_pos[i] of
+ *   request dst_req[i].  k_held and v_held ([n][H_kv][d] contiguous, each may be NULL, or
+ *   k / v itself where that is contiguous) receive what the cache stands for from now on,
+ *   the rows that oscar_gather_int8 would read: a prompt's attention over them sees the
+ *   values that later decodes see.
+ *
+ *   A NaN is quantised as -tau; other rows are not affected.
+ *   dst_req[i] = -1 marks a padding row: nothing of it is written.  Any other request
+ *   outside the batch, a position beyond the page table or a rotation row outside cos_sin
+ *   skips the item and sets OSCAR_DEV_LENGTH; a page id outside the pool skips it and
+ *   sets OSCAR_DEV_PAGE_BOUNDS.  A skipped item writes nothing.
+ *
+ *   norm and rope may be NULL.  q and q_out may be NULL together.  dst_req, dst_pos,
+ *   rope_pos: device int32 [n].  Rows 16-byte aligned, strides multiples of 8 elements and
+ *   at least one row.  seq_len is not read: the caller advances it.  Items must name
+ *   distinct (request, position) pairs.  Outputs may share memory with inputs only as said
+ *   above, and with one another not at all.  n = 0 is a no-op.  Async.
+ */
+oscar_status oscar_rope_append_int8(const oscar_int8_desc* desc, const oscar_head_norm* norm,
+                                    const oscar_rope_desc* rope, const uint16_t* q, int64_t q_stride,
+                                    const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                    const int32_t* dst_req, const int32_t* dst_pos, const int32_t* rope_pos, int32_t n,
+                                    uint16_t* q_out, uint16_t* k_out, uint16_t* k_held, uint16_t* v_held, void* stream);
+
+/*
+ * oscar_gather_int8 - reads cached rows of an 8-bit layer back as bf16.
+ *
+ *   For item i < n: zero + scale * code, rounded to bf16 by way of fp32, of position
+ *   src_pos[i] of request src_req[i], to row i of k_out and v_out (k_out + i * k_stride,
+ *   H_kv heads of d).  src_req[i] = -1 and the skips are those of
+ *   oscar_rope_append_int8: a skipped row is left as it was.  src_req, src_pos: device
+ *   int32 [n].  Rows 16-byte aligned, strides multiples of 8.  seq_len is not read.  n = 0 is
+ *   a no-op.  Async.
+ */
+oscar_status oscar_gather_int8(const oscar_int8_desc* desc, const int32_t* src_req, const int32_t* src_pos, int32_t n,
+                               uint16_t* k_out, int64_t k_stride, uint16_t* v_out, int64_t v_stride, void* stream);
+
+/*
+ * oscar_decode_attention_int8 - one decode step of attention for every request
+ * of the batch over an 8-bit layer.
+ *
+ *   q: row b at q + b * q_stride, H_q heads of d bf16 (16-byte aligned, stride a multiple
+ *   of 8); out: [B][H_q][d] bf16 (16-byte aligned); lse: optional [B][H_q] fp32, the natural
+ *   logarithm of the sum of exp(t), by which results over other tokens can be joined.
+ *   Request b's query sits at position seq_len[b] - 1 and attends positions 0 ..
+ *   seq_len[b] - 1; query head j reads KV head j / (H_q / H_kv), a group of 1 .. 16.  (With
+ *   seq_len the length of an encoder's states this is cross attention.)  score may be NULL
+ *   (all defaults).
+ *   Scores, sums and softmax statistics are fp32; a weight's product with a value's scale
+ *   keeps 22 bits (two fp16 parts), as long as the scale is within 2^20 of the largest in
+ *   its scan: below that, 2^-32 of the largest scale are lost for each unit of weight and
+ *   code.  out is rounded to bf16.  A request with no token gets zeros and lse -inf.
+ *   Codes, scales and zeros of slots past seq_len may hold anything.  A query head with a
+ *   NaN has a NaN result and reaches no other.  A length above max_len is clamped and
+ *   sets OSCAR_DEV_LENGTH, a negative one counts as 0 and sets it; a page outside the pool
+ *   is skipped and sets OSCAR_DEV_PAGE_BOUNDS.  A copy that does not land within 1 s sets
+ *   OSCAR_DEV_TIMEOUT (the output must not be used then).  OSCAR_ERR_UNSUPPORTED: groups
+ *   above 16; max_len above 2^31 - 513; 2^31 or more of (pages of max_len, or of the window
+ *   if that is less, + 64) x B x H_kv.  out and lse must not overlap q.  The result does not
+ *   depend on scheduling.
+ *
+ *   Workspace: NULL asks for the size (it depends on head_dim alone); 256-byte aligned,
+ *   zero-filled before its first use; each call leaves it ready for the next, of whatever
+ *   sizes; calls that may overlap (other streams, two graphs replayed at once) need
+ *   workspaces of their own.  Async.
+ */
+oscar_status oscar_decode_attention_int8(const oscar_int8_desc* desc, const oscar_score_desc* score,
+                                         const uint16_t* q, int64_t q_stride, uint16_t* out, float* lse,
+                                         void* workspace, size_t* workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

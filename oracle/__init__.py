@@ -7,4 +7,5 @@ library: it is plain numpy, written from the pages' description of the
 method, and serves as the checker the CUDA path is compared against.
 """
 from .int4_oracle import *  # noqa: F401,F403
+from .int8_oracle import *  # noqa: F401,F403
 from .oscar_oracle import *  # noqa: F401,F403
