@@ -1,27 +1,37 @@
 // Decode attention over an 8-bit layer: one query token per request.
 //
-// The pages of all (request, KV head) runs stand in one row, and each of 152
-// lasting CTAs (one per SM) takes an equal share of it.  Only the first and the last
-// run of a share can be incomplete: they leave their unnormalised sums in the
-// workspace, and the last CTA of a run to finish joins its parts.
+// The pages of all (request, KV head) runs stand in one row, and each of 304 lasting
+// CTAs (two per SM) takes an equal share of it.  Only the first and the last run of a
+// share can be incomplete: they leave their unnormalised sums in the workspace, and the
+// last CTA of a run to finish joins its parts.
 //
-// A warp takes every 12th page of a run with an online softmax of its own, so
+// Bound by HBM where it is long: 8 requests of 100k tokens (8 KV heads x 128, 1.69 GB)
+// take 247 us, 6.85 TB/s, the rate of a plain copy.  One of them (211 MB, 31 us at that
+// rate) takes 41.6, cold: shares 1.2 us, first pages at 3 to 6.5, scans done at 37 to 44
+// (the memory serves SMs unevenly by some 8 %), warps' joins 1, tickets 1, last parts
+// joined 2 to 4 after that.  28 ragged requests of 2k to 32k (654 MB, 96 us): 109 us.
+//
+// A warp takes every 6th page of a run with an online softmax of its own, so
 // nothing in the scan waits for another warp.  The pages' blocks come by bulk copies
 // into a ring of the warp's own, the next run's ahead of the present one's end.
 //
-// Per page, on the tensor cores with the query heads as the rows:
-//   S = q K^T:  B = the K codes: ldmatrix gives a lane 4 channels' bytes of a token,
-//               two operand registers of one operation each: a byte c alone in an fp16
-//               is the subnormal c 2^-24, exactly.  q is scaled by a power of two per
-//               head to just below fp16's end, exact for bf16.
-//               x = scale (sum c q) + zero (sum q).
-//   O += P V:   A = P scale_V; B = the V codes, by ldmatrix with transposition.
-// S's accumulators are P's operands lane by lane, so nothing is moved between the two.
-// P scale_V is formed in fp32 and split into two fp16 parts (the second in rows 8 to
-// 15 where a group has at most 8 heads, else in products of its own), so that it
-// keeps 22 bits: a byte's range is a value's range, and an error of 2^-11 of it would
-// show in the bf16 output where values cancel.  The weights' sum and the zeros' share
-// of O are summed in fp32 beside it.
+// Per page, on the tensor cores with 16 tokens or 16 channels as the rows and 8 query
+// heads as the columns (heads as the rows took twice the products and accumulators):
+//   S = K q:     A = the K codes: ldmatrix gives a lane 4 channels' bytes of a token, two
+//                operand registers of one operation each: a byte c alone in an fp16 is
+//                the subnormal c 2^-24, exactly.  q is scaled by a power of two per head
+//                to just below fp16's end, exact for bf16.
+//                x = scale (sum c q) + zero (sum q).
+//   O += V^T P:  A = the V codes less 128, by ldmatrix with transposition; B = P scale_V.
+//                (Without the subtraction, one operation more per operand, the sums
+//                grow with the tokens and the tensor cores' truncated additions with
+//                them: 100k tokens that cancel came out with a third of bf16's own error
+//                on top.)  The zeros' share of O takes zero + 128 scale.
+// P scale_V is formed in fp32 and split into two fp16 parts, in columns 4 to 7 where a
+// group has at most 4 heads, else in products of its own, so that it keeps 22 bits: a
+// code's range is a value's range, and an error of 2^-11 of it would show in the bf16
+// output where values cancel.  The weights' sum and the zeros' share of O are summed in
+// fp32 beside it.
 // The weights' reference is raised only when a score exceeds it by 2^8, and the
 // values' scales are taken relative to a power of two above them, raised when a larger
 // one comes: both by one vote a page.
@@ -40,18 +50,28 @@
 namespace oscar {
 namespace {
 
-constexpr int kWarps = 12, kThreads = 32 * kWarps;
-constexpr int kStages = 4;            // pages of a warp's ring
-constexpr int kCtas = 152;            // CTAs the GPU holds at a time
+// Warps of a CTA and pages of a warp's ring, by the most query heads of a group.  Up to 8
+// heads: 6 warps (168 registers, none spilled; a count that does not divide over the 4
+// schedulers costs 10 %).  Two pages each, 101 KB in flight on an SM: with three or four
+// 8 requests of 100k tokens took 262 and 269 us where two take 247.  16 heads: 4 warps,
+// which spill nothing.
+constexpr int warps_of(int G) { return G <= 8 ? 6 : 4; }
+constexpr int stages_of(int G) { return G <= 8 ? 2 : 3; }
+constexpr int kPerSm = 2;
+constexpr int kCtas = 152 * kPerSm;   // CTAs the GPU holds at a time
 constexpr int kHeads = 16;            // most query heads of a KV head
-constexpr int kMinShare = 2 * kWarps; // pages
-constexpr int kRunCost = 32;          // a run costs its CTA about as much as this many pages besides its own
-constexpr int kWhole = 48;            // a run of no more pages is not split
+constexpr int kMinShare = 6;          // pages
+// A run costs its CTA about as much as this many pages besides its own (the query, the
+// warps' join).  (28 ragged requests x 8 KV heads: 115 us with 8, 112 with 16, 111 with 32;
+// 64 of 1000 tokens: 33, 33, 32.)
+constexpr int kRunCost = 32;
+constexpr int kWhole = 18;            // a run of no more pages is not split
 constexpr int kJoinHeads = 4;         // heads whose states are joined at a time
 constexpr uint32_t kLow = 0x00FF00FFu;
 
 using Walk = PageWalk<kRunCost, kWhole>;
 // a warp's first page of a segment
+template <int kWarps>
 __device__ __forceinline__ int place_of(const Segment& s, int warp) {
   const int i = warp - s.at % kWarps;
   return i < 0 ? i + kWarps : i;
@@ -61,12 +81,6 @@ __device__ __forceinline__ int place_of(const Segment& s, int warp) {
 // then two partial states for each, of a run that began before its share and of one
 // that begins in it: (m, l) and the sums.
 constexpr size_t kOffMl = 4096, kOffO = kOffMl + size_t(kCtas) * 2 * kHeads * 8;
-
-template <int D>
-constexpr int join_bytes() {
-  // the warps' states of kJoinHeads heads; or the parts' weights and partial sums
-  return std::max(kWarps * kJoinHeads * D * 4, (kCtas + 1) * kHeads * 4 + kThreads * 16);
-}
 
 // D += A (16x16 f16, row) * B (16x8 f16, col); free for the compiler to move.
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -87,14 +101,22 @@ __device__ __forceinline__ void ldmatrix_x4_t(uint32_t (&d)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-// bytes 0 and 2, bytes 1 and 3 of a word as two fp16 subnormals
+// bytes 0 and 2, bytes 1 and 3 of a word as two fp16 subnormals: c 2^-24
 __device__ __forceinline__ uint32_t even(uint32_t w) { return w & kLow; }
 __device__ __forceinline__ uint32_t odd(uint32_t w) { return prmt(w, 0u, 0x4341); }
+// the same as signed integers, c - 128 (a byte under the exponent of 1024 is 1024 + c)
+__device__ __forceinline__ uint32_t minus_1152(uint32_t w) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(0x64806480u));
+  return d;
+}
+__device__ __forceinline__ uint32_t even_signed(uint32_t w) { return minus_1152((w & kLow) | 0x64006400u); }
+__device__ __forceinline__ uint32_t odd_signed(uint32_t w) { return minus_1152(prmt(w, 0x64646464u, 0x4341)); }
 
 __device__ __forceinline__ float max_over_quad(float v) {   // over the 4 lanes of a row
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
@@ -104,6 +126,16 @@ __device__ __forceinline__ float sum_over_quad(float v) {
   v += __shfl_xor_sync(0xffffffffu, v, 1);
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
+__device__ __forceinline__ float max_over_rows(float v) {   // over the 8 lanes of a column pair
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float sum_over_rows(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
 // The logarithm of the sum, from the reference in log2 units and the sum of 2^(7 + x - m).
@@ -111,11 +143,12 @@ __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m 
 
 // Joins the warps' states of heads h0 .. of a segment, 4 channels a thread: to `out`, or
 // to the workspace's partial state `slot` if that is not negative.
-template <int D>
+template <int D, int kWarps>
 __device__ __forceinline__ void join_warps(const Int8DecodeParams& p, int hq0, int h0, int heads, int slot, int b,
                                            const float* buf, const float (&sm_m)[kWarps][kHeads],
                                            const float (&sm_l)[kWarps][kHeads]) {
   const int i = threadIdx.x, h = h0 + i / (D / 4);
+  static_assert(kJoinHeads * (D / 4) <= 32 * kWarps);
   if (i >= kJoinHeads * (D / 4) || h >= heads) return;
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
   float mx = -FLT_MAX, sum = 0.f;
@@ -154,14 +187,26 @@ struct Part {
 
 // Joins the parts of a run; the whole CTA, 4 channels a thread.  Where the heads
 // leave threads over, each takes every n-th part; where there are more heads than
-// threads for them, they come in turns.  (Small code: it runs once a CTA, when its
-// instructions have to come from far.)
-template <int D>
+// threads for them, they come in turns.  Each round trip to L2 costs as much as ten
+// pages, so the first sums are asked for before their weights are known.  (Small code:
+// it runs once a CTA, when its instructions have to come from far.)
+template <int D, int kWarps>
 __device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r, int share, float* wt, float* sum_of) {
+  constexpr int kThreads = 32 * kWarps, kBatch = 10;
   const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = r.heads;
   const int f = r.run / share, n = (r.run + r.pages - 1) / share - f + 1;
   auto slot_of = [&](int i) { return 2 * (f + i) + (i == 0); };
+  const int units = heads * (D / 4), ways = max(1, kThreads / units);
+  const int left = min(units, kThreads), way = threadIdx.x / left;
+  int unit = threadIdx.x % left;
+  float4 x[kBatch];
+  auto load = [&](int i) {
+    const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) x[k] = __ldcg(from + slot_of(min(i + k * ways, n - 1)) * (kHeads * D / 4));
+  };
+  load(way);
   const float2* ml = reinterpret_cast<const float2*>(ws + kOffMl);
   for (int h = warp; h < heads; h += kWarps) {
     float mx = -FLT_MAX, sum = 0.f;
@@ -187,19 +232,16 @@ __device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r
     }
   }
   __syncthreads();
-  constexpr int kBatch = 8;
-  const int units = heads * (D / 4), ways = max(1, kThreads / units);
   float4* sums = reinterpret_cast<float4*>(wt + n * kHeads);
-  for (int u0 = 0; u0 < units; u0 += kThreads) {
-    const int left = min(units - u0, kThreads), way = threadIdx.x / left, unit = u0 + threadIdx.x % left, h = unit / (D / 4);
-    const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
+#pragma unroll 1
+  for (; unit < units; unit += kThreads) {   // (more than once only where ways is 1)
+    const int h = unit / (D / 4);
+    if (unit >= kThreads) load(0);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (way < ways)
 #pragma unroll 1
       for (int i = way; i < n; i += kBatch * ways) {
-        float4 x[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) x[k] = __ldcg(from + slot_of(min(i + k * ways, n - 1)) * (kHeads * D / 4));
+        if (i != way) load(i);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const float g = i + k * ways < n ? wt[(i + k * ways) * kHeads + h] : 0.f;
@@ -223,11 +265,13 @@ __device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r
   }
 }
 
-// R: rows of heads a lane has (1: groups of up to 8 heads, 2: of up to 16).
-// Formed: the scores have a cap or a distance bias.
-template <int D, int R, bool Formed>
-__global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_constant__ Int8DecodeParams p) {
+// G: the most query heads of a group (4, 8 or 16).  Formed: the scores have a cap or a
+// distance bias.
+template <int D, int G, bool Formed>
+__global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(const __grid_constant__ Int8DecodeParams p) {
+  constexpr int kWarps = warps_of(G), kThreads = 32 * kWarps, kStages = stages_of(G);
   constexpr int kBlock = int8_block_bytes(D), C = D / 16;   // chunks of 16 channels
+  constexpr int R = G == 16 ? 2 : 1;                        // sets of 8 columns
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
@@ -272,15 +316,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
   bool more = false;                      // sm_next holds another
 
   // The ring.  A warp's pages of a segment begin with another warp each time, so
-  // that short segments spread over the warps.  Lane i knows pages 32 n + i of the
-  // segment that is being brought in.
+  // that short segments spread over the warps.  Lane i knows the address of page
+  // 32 n + i of the segment that is being brought in (0: the page is not there).
   uint8_t* ring = smem + warp * (kStages * kBlock);
   float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * kBlock);
   uint64_t* wbars = bars[warp];
   // the segment being brought in: its pages from this warp's first, KV head, request, and number
   int in_lo, in_hi, in_hk, in_b, in_it = 0, in_n;
   auto turn_to = [&](const Segment& s) {
-    in_lo = s.lo + place_of(s, warp);
+    in_lo = s.lo + place_of<kWarps>(s, warp);
     in_hi = s.hi;
     in_hk = s.h;
     in_b = s.b;
@@ -289,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
   };
   turn_to(cur);
   bool in_next = false, dead = false;     // it is the next one, not cur
-  int id = -1, st_in = 0, flying = 0;
+  const uint8_t* src = nullptr;
+  int st_in = 0, flying = 0;
   uint32_t ring_dead = 0;                 // bit i: stage i's page is not there
   auto bring = [&]() {                    // one more page; false if there is none to bring yet
     if (in_it == in_n) {
@@ -300,22 +345,25 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
     }
     if ((in_it & 31) == 0) {
       const int page = in_lo + kWarps * (in_it + lane);
-      id = page < in_hi ? c.page_table[int64_t(in_b) * c.max_pages + page] : -1;
-      if (page < in_hi && (id < 0 || id >= c.n_pages)) {
-        if (c.dev_status) atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
-        id = -1;
+      src = nullptr;
+      if (page < in_hi) {
+        const int id = c.page_table[int64_t(in_b) * c.max_pages + page];
+        if (id >= 0 && id < c.n_pages)
+          src = c.pages + (int64_t(id) * c.n_kv + in_hk) * kBlock;
+        else if (c.dev_status)
+          atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
       }
     }
     const int owner = in_it & 31;
-    const uint32_t none = __shfl_sync(0xffffffffu, id < 0 ? 1u : 0u, owner);
-    ring_dead = (ring_dead & ~(1u << st_in)) | (none << st_in);
+    const bool there = (__ballot_sync(0xffffffffu, src != nullptr) >> owner) & 1u;
+    ring_dead = there ? ring_dead & ~(1u << st_in) : ring_dead | (1u << st_in);
     if (lane == owner) {
       uint64_t* bar = wbars + st_in;
-      if (none) {
-        mbar_arrive(bar);
-      } else {
+      if (there) {
         mbar_arrive_expect_tx(bar, kBlock);
-        bulk_copy_g2s(ring + st_in * kBlock, c.pages + (int64_t(id) * c.n_kv + in_hk) * kBlock, kBlock, bar);
+        bulk_copy_g2s(ring + st_in * kBlock, src, kBlock, bar);
+      } else {
+        mbar_arrive(bar);
       }
     }
     st_in = st_in + 1 == kStages ? 0 : st_in + 1;
@@ -323,16 +371,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
     ++flying;
     return true;
   };
-  // The queries of rows gid and gid + 8, channels 16 i + 4 tig .. + 3, asked for
-  // before the copies.
+  // The query of column gid of each set, channels 16 i + 4 tig .. + 3, asked for before
+  // the copies.  G = 4: columns 4 to 7 repeat columns 0 to 3.
   uint2 uq[R][C];
   auto ask_q = [&](const Segment& s) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint16_t* row = p.q + s.b * p.q_stride + int64_t(s.h * group + gid + 8 * r) * D + 4 * tig;
+      const int h = G == 4 ? gid & 3 : gid + 8 * r;
+      const uint16_t* row = p.q + s.b * p.q_stride + int64_t(s.h * group + h) * D + 4 * tig;
 #pragma unroll
-      for (int i = 0; i < C; ++i)
-        uq[r][i] = gid + 8 * r < group ? *reinterpret_cast<const uint2*>(row + 16 * i) : make_uint2(0, 0);
+      for (int i = 0; i < C; ++i) uq[r][i] = h < group ? *reinterpret_cast<const uint2*>(row + 16 * i) : make_uint2(0, 0);
     }
   };
   ask_q(cur);
@@ -347,17 +395,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
   // on are an exclusive or with 32 i.
   const int lm_t = (lane & 7) + 8 * ((lane >> 3) & 1);
   const uint32_t lm = uint32_t(lm_t * D + 16 * ((lane >> 4) ^ int8_swizzle(D, lm_t)));
+  const bool low_part = G == 4 && tig >= 2;
 
   int st = 0;
   uint32_t parity = 0;
   int has_part = 0;                       // bits: of a run that began before this share, of one that goes on behind it
   while (true) {
-    const int hq0 = cur.h * group, lo = cur.lo + place_of(cur, warp);
+    const int hq0 = cur.h * group, lo = cur.lo + place_of<kWarps>(cur, warp);
     const int n_it = max(0, (cur.hi - lo + kWarps - 1) / kWarps);
 
     // Query operands, scaled by 2^(141 - ex) so that a head's largest channel is in [2^14, 2^15).
-    uint32_t qa[R][C][2];
-    float qs[R], unscale[R], slope[R];
+    uint32_t qb[R][C][2];
+    float qs[R][2], unscale[R][2], slope[R][2];   // of columns 2 tig, 2 tig + 1
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float top = 0.f, sum = 0.f;
@@ -374,31 +423,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
         const float q0 = bf16_lo(uq[r][i].x) * up, q1 = bf16_hi(uq[r][i].x) * up;
         const float q2 = bf16_lo(uq[r][i].y) * up, q3 = bf16_hi(uq[r][i].y) * up;
         sum += (q0 + q1) + (q2 + q3);
-        qa[r][i][0] = pack_half2(q0, q2);
-        qa[r][i][1] = pack_half2(q1, q3);
+        qb[r][i][0] = pack_half2(q0, q2);
+        qb[r][i][1] = pack_half2(q1, q3);
       }
-      qs[r] = sum_over_quad(sum) * 5.9604644775390625e-8f;   // 2^-24, as the codes carry
-      unscale[r] = pow2i(ex - 117);                          // 2^24 / up
-      if (p.s.cap_log2 == 0.f) unscale[r] *= p.s.scale_log2; // (with a cap, capped() takes the scale)
-      slope[r] = Formed && p.s.slopes && gid + 8 * r < group ? p.s.slopes[hq0 + gid + 8 * r] * kLog2e : 0.f;
+      sum = sum_over_quad(sum) * 5.9604644775390625e-8f;     // 2^-24, as the codes carry
+      const float un = pow2i(ex - 117);                      // 2^24 / up
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 2 * tig + e, h = G == 4 ? col & 3 : col + 8 * r;
+        qs[r][e] = __shfl_sync(0xffffffffu, sum, 4 * col);
+        unscale[r][e] = __shfl_sync(0xffffffffu, un, 4 * col);
+        if (p.s.cap_log2 == 0.f) unscale[r][e] *= p.s.scale_log2;   // (with a cap, capped() takes the scale)
+        slope[r][e] = Formed && p.s.slopes && h < group ? p.s.slopes[hq0 + h] * kLog2e : 0.f;
+      }
     }
 
     // x is in the dot product's own scale, or in log2 units where the score has a
     // form of its own; us takes it to log2 units, thr is m + 8 / us.  The weights are
     // 2^(7 + (x - m) us) <= 2^15 (the difference first: exact where it matters, however
     // far the scores).
-    float us[R], thr[R], m[R], l[R], zs[R];
+    float us[R][2], thr[R][2], m[R][2], l[R][2], zs[R][2];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      us[r] = Formed ? 1.f : fmaxf(unscale[r], FLT_MIN);
-      m[r] = thr[r] = -FLT_MAX;
-      l[r] = zs[r] = 0.f;
-    }
-    // o[4 i + 2 k + e]: chunk 2 i + k, its even (e = 0) or odd channels.  Rows: R = 1: head
-    // gid by the two parts of the weights; R = 2: heads gid, gid + 8.
-    float o[2 * C][4];
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int t = 0; t < 2 * C; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        us[r][e] = Formed ? 1.f : fmaxf(unscale[r][e], FLT_MIN);
+        m[r][e] = thr[r][e] = -FLT_MAX;
+        l[r][e] = zs[r][e] = 0.f;
+      }
+    // rows: channels 16 i + 2 gid (0, 1), + 1 (2, 3); columns 2 tig, 2 tig + 1
+    float o[R][C][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.f;
     int ve = -14;                           // the V scales seen are at most 2^ve
     uint32_t vs_top = 0x0400u;              // 2^ve in fp16
     float vs_mul = 16384.f;                 // 2^-ve
@@ -420,140 +478,153 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
         break;
       }
       const uint32_t blk = smem_addr(ring + st * kBlock), at = blk + lm;
-      // S: rows are heads, columns tokens: two products over the even, two over the odd pairs of chunks
-      float acc[2][2][4];
+      // S: rows gid and gid + 8 are tokens, columns heads; two chains of products
+      float acc[R][2][4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) acc[t][u][0] = acc[t][u][1] = acc[t][u][2] = acc[t][u][3] = 0.f;
+        for (int u = 0; u < 2; ++u) acc[r][u][0] = acc[r][u][1] = acc[r][u][2] = acc[r][u][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < C / 2; ++i) {
         uint32_t k[4];
         ldmatrix_x4(k, at ^ (32 * i));
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t a0 = even(k[2 * u]), a1 = even(k[2 * u + 1]), a2 = odd(k[2 * u]), a3 = odd(k[2 * u + 1]);
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            mma(acc[t][u], qa[0][2 * i + u][0], R == 2 ? qa[R - 1][2 * i + u][0] : 0u, qa[0][2 * i + u][1],
-                R == 2 ? qa[R - 1][2 * i + u][1] : 0u, even(k[2 * u + t]), odd(k[2 * u + t]));
+          for (int r = 0; r < R; ++r) mma(acc[r][u], a0, a1, a2, a3, qb[r][2 * i + u][0], qb[r][2 * i + u][1]);
+        }
       }
-      // tokens 2 tig, + 1, 8 + 2 tig, + 1: scales and zeros
-      float ks[4], kz[4], vs[4], vz[4];
-      uint32_t vbits[4];
+      // scales and zeros of tokens gid and gid + 8
+      float vs[2], vz[2], y[R][2][2];
+      uint32_t vbits[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const uint4 w = lds128(blk + 32 * D + 64 * t + 16 * tig);
-        const float2 k0 = half2_to_float2(w.x), v0 = half2_to_float2(w.y), k1 = half2_to_float2(w.z), v1 = half2_to_float2(w.w);
-        ks[2 * t] = k0.x, kz[2 * t] = k0.y, ks[2 * t + 1] = k1.x, kz[2 * t + 1] = k1.y;
-        vs[2 * t] = v0.x, vz[2 * t] = v0.y, vs[2 * t + 1] = v1.x, vz[2 * t + 1] = v1.y;
-        vbits[2 * t] = w.y & 0xFFFFu, vbits[2 * t + 1] = w.w & 0xFFFFu;
+        const uint2 w = lds64(blk + 32 * D + 8 * gid + 64 * t);
+        const float2 k = half2_to_float2(w.x), v = half2_to_float2(w.y);
+        vs[t] = v.x;
+        vz[t] = fmaf(128.f, v.x, v.y);
+        vbits[t] = w.y & 0xFFFFu;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            y[r][t][e] = fmaf(k.x, acc[r][0][2 * t + e] + acc[r][1][2 * t + e], k.y * qs[r][e]);
       }
-      float y[R][4];
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          y[r][j] = fmaf(ks[j], acc[j >> 1][0][2 * r + (j & 1)] + acc[j >> 1][1][2 * r + (j & 1)], kz[j] * qs[r]);
       if (Formed) {
         float far = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[r][j] *= unscale[r], far = fmaxf(far, fabsf(y[r][j]));
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) y[r][t][e] *= unscale[r][e], far = fmaxf(far, fabsf(y[r][t][e]));
         if (p.s.cap_log2 != 0.f) {
           // (the vote skips a form that no score here needs; each score's own is its own)
           if (__builtin_expect(__any_sync(0xffffffffu, !cap_is_near(far, p.s)), 0)) {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) y[r][j] = capped(y[r][j], p.s);
+            for (int j = 0; j < 4 * R; ++j) y[j >> 2][(j >> 1) & 1][j & 1] = capped(y[j >> 2][(j >> 1) & 1][j & 1], p.s);
           } else {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) y[r][j] = capped_near(y[r][j], p.s);
+            for (int j = 0; j < 4 * R; ++j) y[j >> 2][(j >> 1) & 1][j & 1] = capped_near(y[j >> 2][(j >> 1) & 1][j & 1], p.s);
           }
         }
         if (p.s.slopes) {
-          const int away = tok + 2 * tig - (cur.len - 1);
+          const float away = float(tok + gid - (cur.len - 1));
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[r][j] = fmaf(slope[r], float(away + 8 * (j >> 1) + (j & 1)), y[r][j]);
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) y[r][t][e] = fmaf(slope[r][e], away + 8.f * t, y[r][t][e]);
         }
       }
       const bool gone = (ring_dead >> st) & 1u;
       if (gone || tok < cur.first || tok + kPageTokens > cur.len) {
         // what a stale slot holds is anything
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int at_tok = tok + 8 * (j >> 1) + 2 * tig + (j & 1);
+        for (int t = 0; t < 2; ++t) {
+          const int at_tok = tok + 8 * t + gid;
           if (gone || at_tok < cur.first || at_tok >= cur.len) {
-            vs[j] = vz[j] = 0.f;
-            vbits[j] = 0;
+            vs[t] = vz[t] = 0.f;
+            vbits[t] = 0;
 #pragma unroll
-            for (int r = 0; r < R; ++r) y[r][j] = -INFINITY;
+            for (int r = 0; r < R; ++r) y[r][t][0] = y[r][t][1] = -INFINITY;
           }
         }
       }
-      const uint32_t smax = max(max(vbits[0], vbits[1]), max(vbits[2], vbits[3]));   // (fp16 values >= 0 order as integers)
+      const uint32_t smax = max(vbits[0], vbits[1]);   // (fp16 values >= 0 order as integers)
       bool raise = smax > vs_top;
-      float top[R];
+      float top[R][2];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        top[r] = fmaxf(fmaxf(y[r][0], y[r][1]), fmaxf(y[r][2], y[r][3]));
-        raise = raise | (top[r] > thr[r]);
-      }
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[r][e] = fmaxf(y[r][0][e], y[r][1][e]);
+          raise = raise | (top[r][e] > thr[r][e]);
+        }
       if (__any_sync(0xffffffffu, raise)) {
         const int ne = max(ve, scale_exponent(__reduce_max_sync(0xffffffffu, smax)));
         const float fv = pow2i(ve - ne);
         ve = ne;
         vs_top = ve < 16 ? uint32_t(ve + 15) << 10 : 0xFFFFu;
         vs_mul = pow2i(-ve);
-        float f[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float mn = fmaxf(m[r], max_over_quad(top[r]));
-          f[r] = exp2_fast((m[r] - mn) * us[r]);
-          m[r] = mn;
-          thr[r] = mn + 8.f / us[r];
-          l[r] *= f[r];
-          zs[r] *= f[r];
-          f[r] *= fv;
-        }
+          float f[2];
 #pragma unroll
-        for (int t = 0; t < 2 * C; ++t)
-          o[t][0] *= f[0], o[t][1] *= f[0], o[t][2] *= f[R - 1], o[t][3] *= f[R - 1];
+          for (int e = 0; e < 2; ++e) {
+            const float mn = fmaxf(m[r][e], max_over_rows(top[r][e]));
+            f[e] = exp2_fast((m[r][e] - mn) * us[r][e]);
+            m[r][e] = mn;
+            thr[r][e] = mn + 8.f / us[r][e];
+            l[r][e] *= f[e];
+            zs[r][e] *= f[e];
+            f[e] *= fv;
+          }
+#pragma unroll
+          for (int i = 0; i < C; ++i) o[r][i][0] *= f[0], o[r][i][1] *= f[1], o[r][i][2] *= f[0], o[r][i][3] *= f[1];
+        }
       }
+      // P's operands: the weights times the values' scales, in two parts
       uint32_t hi[R][2], part[R][2];
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+      for (int t = 0; t < 2; ++t) {
+        const float s = vs[t] * vs_mul;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float p0 = exp2_fast(fmaf(y[r][2 * t] - m[r], us[r], 7.f)), p1 = exp2_fast(fmaf(y[r][2 * t + 1] - m[r], us[r], 7.f));
-          l[r] += p0 + p1;
-          zs[r] = fmaf(p0, vz[2 * t], fmaf(p1, vz[2 * t + 1], zs[r]));
-          const float w0 = p0 * (vs[2 * t] * vs_mul), w1 = p1 * (vs[2 * t + 1] * vs_mul);
-          hi[r][t] = pack_half2(w0, w1);
-          const float2 h = half2_to_float2(hi[r][t]);
-          part[r][t] = pack_half2(w0 - h.x, w1 - h.y);
+        for (int r = 0; r < R; ++r) {
+          float w[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float g = exp2_fast(fmaf(y[r][t][e] - m[r][e], us[r][e], 7.f));
+            l[r][e] += g;
+            zs[r][e] = fmaf(g, vz[t], zs[r][e]);
+            w[e] = g * s;
+          }
+          const uint32_t h = pack_half2(w[0], w[1]);
+          const float2 hf = half2_to_float2(h);
+          const uint32_t rest = pack_half2(w[0] - hf.x, w[1] - hf.y);
+          if (G == 4) {                     // (columns 4 to 7 take the second parts)
+            hi[r][t] = movmatrix_trans(low_part ? rest : h);
+          } else {
+            hi[r][t] = movmatrix_trans(h);
+            part[r][t] = movmatrix_trans(rest);
+          }
         }
+      }
+      // O: rows are channels
 #pragma unroll
       for (int i = 0; i < C / 2; ++i) {
         uint32_t v[4];
         ldmatrix_x4_t(v, (at + 16 * D) ^ (32 * i));
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t b0 = even(v[2 * u]), b1 = even(v[2 * u + 1]), d0 = odd(v[2 * u]), d1 = odd(v[2 * u + 1]);
-          float(&oe)[4] = o[4 * i + 2 * u], (&oo)[4] = o[4 * i + 2 * u + 1];
-          if (R == 1) {
-            mma(oe, hi[0][0], part[0][0], hi[0][1], part[0][1], b0, b1);
-            mma(oo, hi[0][0], part[0][0], hi[0][1], part[0][1], d0, d1);
-          } else {
-            mma(oe, hi[0][0], hi[R - 1][0], hi[0][1], hi[R - 1][1], b0, b1);
-            mma(oo, hi[0][0], hi[R - 1][0], hi[0][1], hi[R - 1][1], d0, d1);
-            mma(oe, part[0][0], part[R - 1][0], part[0][1], part[R - 1][1], b0, b1);
-            mma(oo, part[0][0], part[R - 1][0], part[0][1], part[R - 1][1], d0, d1);
+          const uint32_t a0 = even_signed(v[2 * u]), a1 = odd_signed(v[2 * u]);
+          const uint32_t a2 = even_signed(v[2 * u + 1]), a3 = odd_signed(v[2 * u + 1]);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            mma(o[r][2 * i + u], a0, a1, a2, a3, hi[r][0], hi[r][1]);
+            if (G > 4) mma(o[r][2 * i + u], a0, a1, a2, a3, part[r][0], part[r][1]);
           }
         }
       }
@@ -568,12 +639,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
     if (more) ask_q(sm_next[warp]);
     // The warps' states of this segment, kJoinHeads heads at a time.  (All with
     // the weights' 2^7; a warp without a token has l = 0, whatever its m.)
-    const float un = pow2i(24 + ve);        // 2^24 of the codes, 2^ve of the scales
+    const float un = pow2i(ve);             // of the scales
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      l[r] = sum_over_quad(l[r]);
-      zs[r] = sum_over_quad(zs[r]);
-      if (tig == 0) sm_m[warp][gid + 8 * r] = m[r] * us[r], sm_l[warp][gid + 8 * r] = l[r];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[r][e] = sum_over_rows(l[r][e]);
+        zs[r][e] = sum_over_rows(zs[r][e]);
+        if (gid == 0 && !low_part) sm_m[warp][8 * r + 2 * tig + e] = m[r][e] * us[r][e], sm_l[warp][8 * r + 2 * tig + e] = l[r][e];
+      }
+      if (G == 4)
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[r][i][j] += __shfl_xor_sync(0xffffffffu, o[r][i][j], 2);
     }
     const bool whole = cur.off == 0 && cur.hi - cur.lo == cur.pages;
     const int slot = 2 * blockIdx.x + (cur.off == 0);
@@ -581,23 +660,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
       if (h0) __syncthreads();              // the heads before have been read
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int h = gid + 8 * r - h0;
-        if (h >= 0 && h < kJoinHeads) {
-          float4* to = reinterpret_cast<float4*>(buf + (warp * kJoinHeads + h) * D + 4 * tig);
+        const int h = 8 * r + 2 * tig - h0;
+        if (h >= 0 && h < kJoinHeads && !low_part) {
+          float2* to = reinterpret_cast<float2*>(buf + (warp * kJoinHeads + h) * D + 2 * gid);
 #pragma unroll
           for (int i = 0; i < C; ++i) {
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int n = 0; n < 2; ++n)
-                x[2 * n + e] = fmaf(R == 1 ? o[2 * i + e][n] + o[2 * i + e][2 + n] : o[2 * i + e][2 * r + n], un, zs[r]);
-            to[4 * i] = make_float4(x[0], x[1], x[2], x[3]);
+            to[8 * i] = make_float2(fmaf(o[r][i][0], un, zs[r][0]), fmaf(o[r][i][2], un, zs[r][0]));
+            to[8 * i + D / 2] = make_float2(fmaf(o[r][i][1], un, zs[r][1]), fmaf(o[r][i][3], un, zs[r][1]));
           }
         }
       }
       __syncthreads();
-      join_warps<D>(p, hq0, h0, group, whole ? -1 : slot, cur.b, buf, sm_m, sm_l);
+      join_warps<D, kWarps>(p, hq0, h0, group, whole ? -1 : slot, cur.b, buf, sm_m, sm_l);
     }
     if (!whole && threadIdx.x == 0) sm_part[cur.off == 0] = {cur.at - cur.off, cur.pages, cur.b, hq0, group};
     has_part |= whole ? 0 : 1 << (cur.off == 0);
@@ -629,30 +703,33 @@ __global__ void __launch_bounds__(kThreads, 1) decode_int8_kernel(const __grid_c
   for (int which = 0; which < 2; ++which)
     if (((has_part >> which) & 1) && sm_last[which]) {
       if (which) __syncthreads();
-      join_parts<D>(p, sm_part[which], share, buf, sm_l[0]);
+      join_parts<D, kWarps>(p, sm_part[which], share, reinterpret_cast<float*>(smem), sm_l[0]);   // (the ring is free)
     }
 }
 
-template <int D, int R, bool Formed>
+template <int D, int G, bool Formed>
 cudaError_t launch(const Int8DecodeParams& p, cudaStream_t stream) {
-  constexpr int bytes = kWarps * kStages * int8_block_bytes(D) + join_bytes<D>();
-  const cudaError_t e = set_smem_limit<decode_int8_kernel<D, R, Formed>>(bytes);
+  // the ring, and the warps' states of kJoinHeads heads
+  constexpr int kRing = warps_of(G) * stages_of(G) * int8_block_bytes(D), bytes = kRing + warps_of(G) * kJoinHeads * D * 4;
+  static_assert((kCtas + 1) * kHeads * 4 + 32 * warps_of(G) * 16 <= bytes);   // the parts' weights and partial sums
+  const cudaError_t e = set_smem_limit<decode_int8_kernel<D, G, Formed>>(bytes);
   if (e != cudaSuccess) return e;
   int64_t tokens = p.c.max_len;
   if (p.s.window) tokens = std::min<int64_t>(tokens, int64_t(p.s.window) + kPageTokens);
   const int64_t places = ((tokens + kPageTokens - 1) / kPageTokens + kRunCost) * p.c.batch * p.c.n_kv;
   if (places > INT32_MAX) return cudaErrorNotSupported;
   const int64_t ctas = std::min<int64_t>(kCtas, (places + kMinShare - 1) / kMinShare);
-  return launch_pdl(decode_int8_kernel<D, R, Formed>, dim3(unsigned(ctas)), dim3(kThreads), bytes, stream, p);
+  return launch_pdl(decode_int8_kernel<D, G, Formed>, dim3(unsigned(ctas)), dim3(32 * warps_of(G)), bytes, stream, p);
 }
 
-template <int D, int R>
+template <int D, int G>
 cudaError_t launch_f(const Int8DecodeParams& p, cudaStream_t stream) {
-  return p.s.cap_log2 != 0.f || p.s.slopes ? launch<D, R, true>(p, stream) : launch<D, R, false>(p, stream);
+  return p.s.cap_log2 != 0.f || p.s.slopes ? launch<D, G, true>(p, stream) : launch<D, G, false>(p, stream);
 }
 template <int D>
-cudaError_t launch_r(const Int8DecodeParams& p, cudaStream_t stream) {
-  return p.c.n_q / p.c.n_kv > 8 ? launch_f<D, 2>(p, stream) : launch_f<D, 1>(p, stream);
+cudaError_t launch_g(const Int8DecodeParams& p, cudaStream_t stream) {
+  const int group = p.c.n_q / p.c.n_kv;
+  return group <= 4 ? launch_f<D, 4>(p, stream) : group <= 8 ? launch_f<D, 8>(p, stream) : launch_f<D, 16>(p, stream);
 }
 
 }  // namespace
@@ -660,7 +737,7 @@ cudaError_t launch_r(const Int8DecodeParams& p, cudaStream_t stream) {
 size_t int8_decode_workspace_bytes(const PagedCache& c) { return kOffO + size_t(kCtas) * 2 * kHeads * c.d * 4; }
 
 cudaError_t launch_decode_int8(const Int8DecodeParams& p, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_r<128>(p, stream) : launch_r<64>(p, stream);
+  return p.c.d == 128 ? launch_g<128>(p, stream) : launch_g<64>(p, stream);
 }
 
 }  // namespace oscar
