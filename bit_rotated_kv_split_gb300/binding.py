@@ -49,6 +49,7 @@ class Int4Desc(ctypes.Structure):
     """Mirror of `oscar_int4_desc`."""
     keep = None   # a tensor whose memory it points to
     keep_others = ()   # the others
+    device = None   # their device
     _fields_ = [
         ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
         ("max_pages_per_seq", c_int32), ("max_len", c_int32), ("n_pages", c_int64),
@@ -61,6 +62,7 @@ class Int8Desc(ctypes.Structure):
     """Mirror of `oscar_int8_desc`."""
     keep = None   # a tensor whose memory it points to
     keep_others = ()   # the others
+    device = None   # their device
     _fields_ = [
         ("batch", c_int32), ("n_q_heads", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
         ("max_pages_per_seq", c_int32), ("max_len", c_int32), ("n_pages", c_int64),
@@ -79,18 +81,21 @@ class HeadNorm(ctypes.Structure):
     """Mirror of `oscar_head_norm`."""
     keep = None   # a tensor whose memory it points to
     keep_others = ()   # the other
+    device = None   # their device
     _fields_ = [("q_weight", c_void_p), ("k_weight", c_void_p), ("eps", c_float), ("reserved", c_int32)]
 
 
 class RopeDesc(ctypes.Structure):
     """Mirror of `oscar_rope_desc`."""
     keep = None   # a tensor whose memory it points to
+    device = None   # their device
     _fields_ = [("cos_sin", c_void_p), ("n_positions", c_int64), ("rot_dim", c_int32), ("interleaved", c_int32)]
 
 
 class ScoreDesc(ctypes.Structure):
     """Mirror of `oscar_score_desc`."""
     keep = None   # a tensor whose memory it points to
+    device = None   # their device
     _fields_ = [("scale", c_float), ("softcap", c_float), ("window", c_int32), ("reserved", c_int32),
                 ("slopes", c_void_p)]
 
@@ -389,7 +394,7 @@ def rope_desc(cos_sin, rot_dim: int, interleaved: bool = False) -> RopeDesc:
                 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be contiguous float32 [n_positions][rot_dim]")
         d.cos_sin, d.n_positions = cos_sin.data_ptr(), cos_sin.shape[0]
-        d.keep = cos_sin
+        d.keep, d.device = cos_sin, cos_sin.get_device()
     d.rot_dim, d.interleaved = _int32("rot_dim", rot_dim), int(bool(interleaved))
     return d
 
@@ -405,7 +410,7 @@ def score_desc(scale: float = 0.0, softcap: float = 0.0, window: int = 0, slopes
         if str(slopes.dtype) != "torch.float32" or slopes.dim() != 1 or not slopes.is_contiguous():
             raise ValueError("slopes must be contiguous float32 [n_q_heads]")
         d.slopes = slopes.data_ptr()
-        d.n_slopes, d.keep = slopes.shape[0], slopes
+        d.n_slopes, d.keep, d.device = slopes.shape[0], slopes, slopes.get_device()
     return d
 
 
@@ -426,15 +431,15 @@ def prompt_desc(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_
     return d
 
 
-_torch = None
+_torch = _bf16 = _i32 = None
 
 
 def _half(t):
     """bfloat16 or raw 16-bit integers: fp16 rows have the size of bf16's and would be read as such."""
-    global _torch
+    global _torch, _bf16, _i32
     if _torch is None:
         import torch
-        _torch = torch
+        _torch, _bf16, _i32 = torch, torch.bfloat16, torch.int32
     return t.dtype is _torch.bfloat16 or (t.element_size() == 2 and not t.is_floating_point())
 
 
@@ -469,26 +474,56 @@ def _workspace_size(t):
     return c_size_t(t.numel() * t.element_size())
 
 
-_raw_stream = None
+# The same checks where a tensor is as most are: contiguous, with the exact type (a step that is one token long
+# is bound by them; the others take the checks above).
+
+def _rows(name, t, heads, d):
+    shape = t.shape
+    if t.dtype is _bf16 and len(shape) == 3 and shape[1] == heads and shape[2] == d and t.is_contiguous():
+        return heads * d
+    return _heads(name, t, heads, d)
 
 
-def _on_device(name, stream, tensors, fn, args):
-    """Calls the library with the tensors' device current and, without a stream, on that device's current stream."""
-    global _torch, _raw_stream
+def _whole(name, t, shape):
+    if t is not None and not (t.dtype is _bf16 and t.shape == shape and t.is_contiguous()):
+        _contiguous(name, t, shape, 2)
+
+
+def _places(name, t, n):
+    if t is not None:
+        shape = t.shape
+        if not (t.dtype is _i32 and len(shape) == 1 and shape[0] >= n and t.is_contiguous()):
+            _index(name, t, n)
+
+
+_raw_stream = _current_device = None
+
+
+def _on_device(name, stream, tensors, fn, args, descs=()):
+    """Calls the library with the tensors' device current and, without a stream, on that device's current stream.
+
+    descs: descriptors (or None) whose tensors' device is known.
+    """
+    global _torch, _raw_stream, _current_device
     if _raw_stream is None:
         import torch
         _torch = torch
         # the current stream's handle without a Stream object around it (3 us a call less)
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
-    cuda = _torch.cuda
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     index = tensors[0].get_device()
+    if index < 0:
+        raise ValueError("%s: every tensor must be on one CUDA device" % name)
     for t in tensors:
-        if t is not None and (t.get_device() != index or index < 0):
+        if t is not None and t.get_device() != index:
+            raise ValueError("%s: every tensor must be on one CUDA device" % name)
+    for d in descs:
+        if d is not None and d.device is not None and d.device != index:
             raise ValueError("%s: every tensor must be on one CUDA device" % name)
     handle = _raw_stream(index) if stream is None else _stream(stream)
-    if index != cuda.current_device():
-        with cuda.device(index):
+    if index != _current_device():
+        with _torch.cuda.device(index):
             status = fn(*args, handle)
     else:
         status = fn(*args, handle)
@@ -609,12 +644,14 @@ def oscar_rope_frequencies(rot_dim: int, theta: float, kind: str = "plain", fact
 
 def oscar_rope_table(freq, cos_sin, magnitude: float = 1.0, first: int = 0, stream=None) -> None:
     """Fills cos_sin [n][rot_dim] fp32 (device): cosines, then sines, of (first + j) freq, times magnitude."""
-    freq = _f64(freq)
-    if freq.ndim != 1 or cos_sin.dim() != 2 or cos_sin.shape[1] != 2 * freq.shape[0]:
+    if not (isinstance(freq, np.ndarray) and freq.dtype == np.float64 and freq.flags.c_contiguous):
+        freq = _f64(freq)
+    shape, pairs = cos_sin.shape, freq.shape[0] if freq.ndim == 1 else -1
+    if len(shape) != 2 or shape[1] != 2 * pairs:
         raise ValueError("freq must be [rot_dim / 2] and cos_sin [n][rot_dim]")
-    _contiguous("cos_sin", cos_sin, cos_sin.shape, 4)
+    _contiguous("cos_sin", cos_sin, shape, 4)
     _on_device("oscar_rope_table", stream, (cos_sin,), lib.oscar_rope_table, (
-        freq.ctypes.data, 2 * freq.shape[0], float(magnitude), int(first), cos_sin.shape[0], cos_sin.data_ptr()))
+        freq.ctypes.data, 2 * pairs, magnitude, first, shape[0], cos_sin.data_ptr()))
 
 
 def norm_desc(q_weight=None, k_weight=None, eps: float = 1e-6) -> HeadNorm:
@@ -629,8 +666,12 @@ def norm_desc(q_weight=None, k_weight=None, eps: float = 1e-6) -> HeadNorm:
                 raise ValueError("%s must be contiguous bfloat16 [head_dim]" % name)
             setattr(d, name, w.data_ptr())
     d.eps = float(eps)
-    d.sizes = tuple(w.shape[0] for w in (q_weight, k_weight) if w is not None)
+    given = [w for w in (q_weight, k_weight) if w is not None]
+    if len({w.get_device() for w in given}) > 1:
+        raise ValueError("both weights must be on one device")
+    d.sizes = tuple(w.shape[0] for w in given)
     d.keep, d.keep_others = q_weight, (k_weight,)
+    d.device = given[0].get_device() if given else None
     return d
 
 
@@ -639,37 +680,40 @@ def _norm_ok(norm, d):
         raise ValueError("norm: weights of another head size than %d" % d)
 
 
-def _kept(norm, rope):
-    """The tensors that the two descriptors (each may be None) point to."""
-    return (rope and rope.keep, *((norm.keep, *norm.keep_others) if norm is not None else ()))
-
-
 def oscar_norm_rope(norm, rope, q, k, pos, q_out, k_out, dev_status=None, stream=None) -> None:
     """Norms and rotates q [n][H_q][d] and k [n][H_kv][d] (bf16) by position pos [n] int32 into q_out and k_out.
 
     norm and rope may be None, and so may q and q_out, or k and k_out.  Rows may be strided (slices of one
     projection's output), and outputs may be their inputs.
     """
-    shape = (q if q is not None else k).shape
-    if len(shape) != 3 or (q is not None and k is not None and (k.dim() != 3 or k.shape[0] != shape[0] or k.shape[2] != shape[2])):
-        raise ValueError("q and k must be [n][heads][d] with one row count and head size")
-    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
-        raise ValueError("q_out must be given with q, k_out with k")
-    n, d = int(shape[0]), int(shape[2])
-    hq, hk = (1 if x is None else int(x.shape[1]) for x in (q, k))
-    strides = []
-    for name, x, heads in (("q", q, hq), ("k", k, hk), ("q_out", q_out, hq), ("k_out", k_out, hk)):
-        if x is not None and x.shape[0] != n:
-            raise ValueError("%s must have %d rows" % (name, n))
-        strides.append(0 if x is None else _heads(name, x, heads, d))
+    one = q if q is not None else k
+    if one is None or (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q or k must be given, q_out with q and k_out with k")
+    shape = one.shape
+    if len(shape) != 3:
+        raise ValueError("q and k must be [n][heads][d]")
+    n, hq, d = shape
+    hk = 1
+    qs = ks = qos = kos = 0
+    q_ptr = k_ptr = q_out_ptr = k_out_ptr = None
+    if q is not None:
+        qs, qos = _rows("q", q, hq, d), _rows("q_out", q_out, hq, d)
+        if q_out.shape[0] != n:
+            raise ValueError("q_out must have the rows of q")
+        q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != n or k_out.shape[0] != n:
+            raise ValueError("q, k and k_out must have one row count")
+        hk = k.shape[1]
+        ks, kos = _rows("k", k, hk, d), _rows("k_out", k_out, hk, d)
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
     if dev_status is not None and (dev_status.numel() < 1 or dev_status.element_size() != 4):
         raise ValueError("dev_status must be an int32 word")
-    _index("pos", pos, n)
+    _places("pos", pos, n)
     _norm_ok(norm, d)
-    _on_device("oscar_norm_rope", stream, ((q if q is not None else k), k, q_out, k_out, pos, dev_status, *_kept(norm, rope)),
-               lib.oscar_norm_rope, (
-                   hq, hk, d, _ref(norm), _ref(rope), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(pos), n, _ptr(q_out),
-                   strides[2], _ptr(k_out), strides[3], _ptr(dev_status)))
+    _on_device("oscar_norm_rope", stream, (one, k, q_out, k_out, pos, dev_status), lib.oscar_norm_rope, (
+        hq, hk, d, _ref(norm), _ref(rope), q_ptr, qs, k_ptr, ks, _ptr(pos), n, q_out_ptr, qos, k_out_ptr, kos, _ptr(dev_status)),
+               (norm, rope))
 
 
 # ---------------------------------------------------------------- 8-bit layers
@@ -686,33 +730,39 @@ def oscar_rope_append_int8(desc: Int8Desc, norm, rope, q, k, v, dst_req, dst_pos
     norm, rope and k_out may be None, q and q_out both.  Rows may be strided (slices of one projection's output).
     k_held, v_held [n][H_kv][d]: the rows as the cache holds them from now on.
     """
-    hq, hk, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, int(k.shape[0])
-    qs = _heads("q", q, hq, d) if q is not None else 0
-    ks, vs = _heads("k", k, hk, d), _heads("v", v, hk, d)
-    if v.shape[0] != n or (q is not None and q.shape[0] != n):
+    hq, hk, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, k.shape[0]
+    ks, vs = _rows("k", k, hk, d), _rows("v", v, hk, d)
+    qs = 0
+    q_ptr = q_out_ptr = None
+    if q is not None:
+        qs, q_ptr = _rows("q", q, hq, d), q.data_ptr()
+        if q.shape[0] != n:
+            raise ValueError("q, k and v must have one row count")
+    if v.shape[0] != n:
         raise ValueError("q, k and v must have one row count")
-    _index("dst_req", dst_req, n), _index("dst_pos", dst_pos, n), _index("rope_pos", rope_pos, n)
-    _contiguous("q_out", q_out, (n, hq, d), 2)
+    if q_out is not None:
+        _whole("q_out", q_out, (n, hq, d))
+        q_out_ptr = q_out.data_ptr()
     rows = (n, hk, d)
-    _contiguous("k_out", k_out, rows, 2), _contiguous("k_held", k_held, rows, 2), _contiguous("v_held", v_held, rows, 2)
+    _whole("k_out", k_out, rows), _whole("k_held", k_held, rows), _whole("v_held", v_held, rows)
+    _places("dst_req", dst_req, n), _places("dst_pos", dst_pos, n), _places("rope_pos", rope_pos, n)
     _norm_ok(norm, d)
-    _on_device("oscar_rope_append_int8", stream, (
-        k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos, k_held, v_held, desc.keep, *desc.keep_others, *_kept(norm, rope)),
+    _on_device("oscar_rope_append_int8", stream, (k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos, k_held, v_held),
                lib.oscar_rope_append_int8, (
-                   ctypes.byref(desc), _ref(norm), _ref(rope), _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                   dst_req.data_ptr(), dst_pos.data_ptr(), _ptr(rope_pos), n, _ptr(q_out), _ptr(k_out), _ptr(k_held),
-                   _ptr(v_held)))
+                   ctypes.byref(desc), _ref(norm), _ref(rope), q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                   dst_req.data_ptr(), dst_pos.data_ptr(), _ptr(rope_pos), n, q_out_ptr, _ptr(k_out), _ptr(k_held),
+                   _ptr(v_held)), (desc, norm, rope))
 
 
 def oscar_gather_int8(desc: Int8Desc, src_req, src_pos, k_out, v_out, stream=None) -> None:
     """Cached rows (src_req[i], src_pos[i]) as bf16 into k_out, v_out [n][H_kv][d] (rows may be strided)."""
-    hk, d, n = desc.n_kv_heads, desc.head_dim, int(k_out.shape[0])
-    ks, vs = _heads("k_out", k_out, hk, d), _heads("v_out", v_out, hk, d)
+    hk, d, n = desc.n_kv_heads, desc.head_dim, k_out.shape[0]
+    ks, vs = _rows("k_out", k_out, hk, d), _rows("v_out", v_out, hk, d)
     if v_out.shape[0] != n:
         raise ValueError("k_out and v_out must have one row count")
-    _index("src_req", src_req, n), _index("src_pos", src_pos, n)
-    _on_device("oscar_gather_int8", stream, (k_out, v_out, src_req, src_pos, desc.keep, *desc.keep_others), lib.oscar_gather_int8, (
-        ctypes.byref(desc), src_req.data_ptr(), src_pos.data_ptr(), n, k_out.data_ptr(), ks, v_out.data_ptr(), vs))
+    _places("src_req", src_req, n), _places("src_pos", src_pos, n)
+    _on_device("oscar_gather_int8", stream, (k_out, v_out, src_req, src_pos), lib.oscar_gather_int8, (
+        ctypes.byref(desc), src_req.data_ptr(), src_pos.data_ptr(), n, k_out.data_ptr(), ks, v_out.data_ptr(), vs), (desc,))
 
 
 def oscar_decode_int8_workspace_bytes(desc: Int8Desc) -> int:
@@ -725,14 +775,14 @@ def oscar_decode_int8_workspace_bytes(desc: Int8Desc) -> int:
 def oscar_decode_attention_int8(desc: Int8Desc, q, out, workspace, score=None, lse=None, stream=None) -> None:
     """out [B][H_q][d] bf16 (and lse [B][H_q] fp32) = attention of one query per request q [B][H_q][d] over the 8-bit cache."""
     hq, d, b = desc.n_q_heads, desc.head_dim, desc.batch
-    qs = _heads("q", q, hq, d)
+    qs = _rows("q", q, hq, d)
     if q.shape[0] != b:
         raise ValueError("q must have one row per request")
-    _contiguous("out", out, (b, hq, d), 2)
-    _contiguous("lse", lse, (b, hq), 4)
+    _whole("out", out, (b, hq, d))
+    if lse is not None:
+        _contiguous("lse", lse, (b, hq), 4)
     _slopes_ok(score, hq)
     size = _workspace_size(workspace)
-    _on_device("oscar_decode_attention_int8", stream, (q, out, workspace, lse, desc.keep, score and score.keep, *desc.keep_others),
-               lib.oscar_decode_attention_int8, (
-                   ctypes.byref(desc), _ref(score), q.data_ptr(), qs, out.data_ptr(), _ptr(lse), workspace.data_ptr(),
-                   ctypes.byref(size)))
+    _on_device("oscar_decode_attention_int8", stream, (q, out, workspace, lse), lib.oscar_decode_attention_int8, (
+        ctypes.byref(desc), _ref(score), q.data_ptr(), qs, out.data_ptr(), _ptr(lse), workspace.data_ptr(), ctypes.byref(size)),
+               (desc, score))

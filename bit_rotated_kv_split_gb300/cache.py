@@ -143,4 +143,6 @@ def _fill_paged(cache, d, max_len):
         raise ValueError("page_table must have rows of max_pages_per_seq entries")
     d.keep = cache.pages
     d.keep_others = (cache.page_table, cache.seq_len, cache.dev_status)
+    devices = {t.get_device() for t in (d.keep, *d.keep_others)}
+    d.device = devices.pop() if len(devices) == 1 else -2    # (of no tensor: the calls refuse it)
     return d

@@ -2,12 +2,14 @@
 // with k and v quantised to 8 bits into pages (rope_append_int8), and cached rows
 // back as bf16 (gather_int8).
 //
-// One lane holds an octet of adjacent channels (16 bytes of bf16), d / 8 lanes a
-// row, so a warp holds 32 / (d / 8) rows at a time (a slot).  With r the row's
-// 1 / sqrt(mean x^2 + eps), w the weights and (c, s) a pair's angle, a rotated
-// channel is r (own C + other S): C = c w_own, S = -+ s w_other.  C and S belong to
-// a lane and a token, so every head of the token takes two products a channel;
-// `other` is the partner octet (by shuffle) or the octet's own pairs swapped.
+// Norm, rotation, quantisation: a lane holds two octets of channels (16 bytes of bf16
+// each) that turn with one another, d / 16 lanes a row, so a warp holds 32 / (d / 16)
+// rows at a time (a slot).  With r the row's 1 / sqrt(mean x^2 + eps), w the weights and
+// (c, s) a pair's angle, a rotated channel is r (own C + other S): C = c w_own, S = -+ s
+// w_other.  C and S belong to a lane and a token, so every head of the token takes two
+// products a channel.  (With an octet a lane and its partner by shuffle, every channel
+// was unpacked twice and every row reduced by twice the lanes: 30k tokens appended in 157
+// us where this takes 148.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,134 +41,145 @@ __device__ __forceinline__ uint8_t* token_block(const PagedCache& c, int req, in
   return c.pages + int64_t(page) * c.n_kv * int8_block_bytes(D);
 }
 
-// A lane's share of a token's angles: its octet turns (or is not part of a
-// rotated pair), with its partner's channels from lane `partner`.
-struct Angles {
-  const float* row;   // of cos_sin, at this octet's first angle
-  int half;           // to the sines
-  int partner;
-  bool on, first;     // rotated; the first of the two halves
-};
-
+// A lane's octets of a row, e0 and e1, and their angles.
 template <bool Interleaved>
-__device__ __forceinline__ Angles angles_of(const RopeParams& r, int64_t at, int o, int lane) {
-  const int h = r.rot / 16;                 // octets of a half
-  Angles a;
-  a.on = o < 2 * h;
-  a.first = o < h;
-  a.partner = Interleaved || !a.on ? lane : a.first ? lane + h : lane - h;
-  a.half = r.rot / 2;
-  a.row = r.cos_sin + at * r.rot + (Interleaved ? 4 * o : 8 * (a.first ? o : o - h));
-  return a;
-}
-
-// C and S of the lane's octet; w: the norm's weights or NULL.
-struct Factors {
-  float2 c[4], s[4];
+struct Angles {
+  int e0, e1;
+  bool on0, on1;      // they turn (in halves: with one another)
+  const float* row;   // of cos_sin, at the first angle of e0
+  int half;           // to the sines
+  __device__ __forceinline__ Angles(const RopeParams& r, int64_t at, int i) {
+    const int h = r.rot / 16;               // octets of a half
+    on0 = Interleaved ? 2 * i < 2 * h : i < h;
+    on1 = Interleaved ? 2 * i + 1 < 2 * h : on0;
+    e0 = Interleaved || !on0 ? 2 * i : i;
+    e1 = Interleaved || !on0 ? 2 * i + 1 : i + h;
+    half = r.rot / 2;
+    row = r.cos_sin + at * r.rot + (Interleaved ? 4 : 8) * e0;
+  }
 };
-template <int D, bool Interleaved>
-__device__ __forceinline__ Factors factors_of(const Angles& a, const uint16_t* w, int o, int lane) {
-  float own[8], other[8], c[8], s[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) own[e] = other[e] = c[e] = 1.f, s[e] = 0.f;
-  if (w) {
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(w + 8 * o), own);
-    if (Interleaved) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) other[e] = own[e ^ 1];
-    } else {
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(w + 8 * (o + a.partner - lane)), other);
-    }
-  }
-  if (a.on) {
-    if (Interleaved) {
-      float c4[8], s4[8];
-      load8(c4, a.row, 4);
-      load8(s4, a.row + a.half, 4);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = c4[e / 2], s[e] = e & 1 ? s4[e / 2] : -s4[e / 2];
-    } else {
-      load8(c, a.row, 8);
-      load8(s, a.row + a.half, 8);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = a.first ? -s[e] : s[e];
-    }
-  }
-  Factors f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f.c[i] = make_float2(c[2 * i] * own[2 * i], c[2 * i + 1] * own[2 * i + 1]);
-    f.s[i] = make_float2(s[2 * i] * other[2 * i], s[2 * i + 1] * other[2 * i + 1]);
-  }
-  return f;
-}
 
-// Norms (where `norm`) and rotates the octet held in `raw`; whole warps call it.
-// fp32 throughout: the sum of squares in a fixed order, one rounding to bf16.
-template <int D, bool Interleaved>
-__device__ __forceinline__ void turn8(uint4& raw, const Factors& f, const Angles& a, bool rotate, bool norm, float eps) {
-  const uint32_t x[4] = {raw.x, raw.y, raw.z, raw.w};
-  uint32_t y[4];
-  if (rotate) {
+// C and S of the lane's octets; w: the norm's weights or NULL.
+struct Factors {
+  float2 c0[4], s0[4], c1[4], s1[4];
+};
+template <bool Interleaved>
+__device__ __forceinline__ void factors_of(Factors* f, const Angles<Interleaved>& a, const uint16_t* w) {
+  float w0[8], w1[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      y[i] = Interleaved ? __funnelshift_l(x[i], x[i], 16) : __shfl_sync(0xffffffffu, x[i], a.partner);
+  for (int e = 0; e < 8; ++e) w0[e] = w1[e] = 1.f;
+  if (w) {
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(w + 8 * a.e0), w0);
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(w + 8 * a.e1), w1);
   }
-  float r = 1.f;
-  if (norm) {
-    float2 sum = make_float2(0.f, 0.f);
+  float c[8], s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) c[e] = 1.f, s[e] = 0.f;
+  if (Interleaved) {                        // pairs 0 .. 3 of e0, then of e1
+    if (a.on0) load8(c, a.row, 4), load8(s, a.row + a.half, 4);
+    if (a.on1) {
+      const float4 u = *reinterpret_cast<const float4*>(a.row + 4), v = *reinterpret_cast<const float4*>(a.row + a.half + 4);
+      c[4] = u.x, c[5] = u.y, c[6] = u.z, c[7] = u.w;
+      s[4] = v.x, s[5] = v.y, s[6] = v.z, s[7] = v.w;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 v = bf16_pair(x[i]);
-      sum = fma2(v, v, sum);
+      f->c0[i] = make_float2(c[i] * w0[2 * i], c[i] * w0[2 * i + 1]);
+      f->s0[i] = make_float2(-s[i] * w0[2 * i + 1], s[i] * w0[2 * i]);
+      f->c1[i] = make_float2(c[4 + i] * w1[2 * i], c[4 + i] * w1[2 * i + 1]);
+      f->s1[i] = make_float2(-s[4 + i] * w1[2 * i + 1], s[4 + i] * w1[2 * i]);
     }
-    float all = sum.x + sum.y;
+  } else {
+    if (a.on0) load8(c, a.row, 8), load8(s, a.row + a.half, 8);
 #pragma unroll
-    for (int m = 1; m < D / 8; m <<= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
-    r = rsqrtf(fmaf(all, 1.f / D, eps));
+    for (int i = 0; i < 4; ++i) {
+      f->c0[i] = make_float2(c[2 * i] * w0[2 * i], c[2 * i + 1] * w0[2 * i + 1]);
+      f->s0[i] = make_float2(-s[2 * i] * w1[2 * i], -s[2 * i + 1] * w1[2 * i + 1]);
+      f->c1[i] = make_float2(c[2 * i] * w1[2 * i], c[2 * i + 1] * w1[2 * i + 1]);
+      f->s1[i] = make_float2(s[2 * i] * w0[2 * i], s[2 * i + 1] * w0[2 * i + 1]);
+    }
   }
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 v = mul2(bf16_pair(x[i]), f.c[i]);
-    if (rotate && a.on) v = fma2(bf16_pair(y[i]), f.s[i], v);   // (an infinite partner is none of an octet that stays)
-    if (norm) v = mul2(v, twice(r));
-    out[i] = pack_bf162(v.x, v.y);
-  }
-  raw = make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Quantises the row of which this lane holds the 8 bf16 values u, over `Lanes`
-// lanes: zero = the least value, rounded down to fp16; scale = (greatest - zero) /
-// 255, rounded up, so that no value lies outside the codes; code = (x - zero) /
-// scale to nearest even, of exact differences and quotients.  *pair = (scale, zero);
-// held: zero + scale code, rounded to fp32 and that to bf16.
-//
-// The extremes are taken on packed bf16 (max x, max -x).  The scale is a product with
-// 1/255 rounded up, and one fp16 less where that still reaches the greatest value (255 s
-// has 19 bits, exact in fp32).  A quotient is taken by an approximate reciprocal
-// and checked: its error is below 255 (2^-22 + 2^-24) < 1e-4 of a step, and where the
-// remainder t - k s (one fma) comes within 2e-4 of half a step it is divided out.
-template <int Lanes, bool Held>
-__device__ __forceinline__ uint2 quantise8(const uint4& u, float tau, uint32_t* pair, uint4* held) {
+struct Octets {
+  uint4 u0, u1;
+};
+
+// Norms (where `norm`) and rotates the octets held in x; whole warps call it.
+// fp32 throughout: the sum of squares in a fixed order, one rounding to bf16.
+template <int D, bool Interleaved>
+__device__ __forceinline__ void turn16(Octets& x, const Factors& f, const Angles<Interleaved>& a, bool norm, float eps) {
+  const uint32_t u[4] = {x.u0.x, x.u0.y, x.u0.z, x.u0.w}, v[4] = {x.u1.x, x.u1.y, x.u1.z, x.u1.w};
+  float r = 1.f;
+  if (norm) {
+    float2 sum = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 p = bf16_pair(u[i]), q = bf16_pair(v[i]);
+      sum = fma2(p, p, sum);
+      sum1 = fma2(q, q, sum1);
+    }
+    sum = add2(sum, sum1);
+    float all = sum.x + sum.y;
+#pragma unroll
+    for (int m = 1; m < D / 16; m <<= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
+    r = rsqrtf(fmaf(all, 1.f / D, eps));
+  }
+  uint32_t out0[4], out1[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = bf16_pair(u[i]), q = bf16_pair(v[i]);
+    float2 y = mul2(p, f.c0[i]), z = mul2(q, f.c1[i]);
+    // (a channel that stays takes nothing of a partner that may be infinite)
+    if (a.on0) y = fma2(Interleaved ? make_float2(p.y, p.x) : q, f.s0[i], y);
+    if (a.on1) z = fma2(Interleaved ? make_float2(q.y, q.x) : p, f.s1[i], z);
+    if (norm) y = mul2(y, twice(r)), z = mul2(z, twice(r));
+    out0[i] = pack_bf162(y.x, y.y);
+    out1[i] = pack_bf162(z.x, z.y);
+  }
+  x.u0 = make_uint4(out0[0], out0[1], out0[2], out0[3]);
+  x.u1 = make_uint4(out1[0], out1[1], out1[2], out1[3]);
+}
+
+// (max x, max -x) of the 8 bf16 values of u
+__device__ __forceinline__ uint32_t ends8(const uint4& u) {
   const uint32_t hi2 = max_bf16x2(max_bf16x2(u.x, u.y), max_bf16x2(u.z, u.w));
   const uint32_t lo2 = max_bf16x2(max_bf16x2(u.x ^ 0x80008000u, u.y ^ 0x80008000u),
                                   max_bf16x2(u.z ^ 0x80008000u, u.w ^ 0x80008000u));
-  uint32_t ends = max_bf16x2(prmt(hi2, lo2, 0x5410), prmt(hi2, lo2, 0x7632));   // (max x, max -x)
+  return max_bf16x2(prmt(hi2, lo2, 0x5410), prmt(hi2, lo2, 0x7632));
+}
+
+// Quantises the row of which this lane holds the 16 bf16 values u, over `Lanes`
+// lanes: zero = the least value, rounded down to fp16; scale = (greatest - zero) /
+// 255, rounded up, so that no value lies outside the codes; code = (x - zero) /
+// scale to nearest even, of exact differences and quotients.  *pair = (scale, zero);
+// *held: zero + scale code, rounded to fp32 and that to bf16.  Returns the codes of the
+// two octets.
+//
+// The extremes are taken on packed bf16.  The scale is a product with 1/255 rounded up,
+// and one fp16 less where that still reaches the greatest value (255 s has 19 bits,
+// exact in fp32).  A quotient is taken by an approximate reciprocal and checked: its
+// error is below 255 (2^-22 + 2^-24) < 1e-4 of a step, and where the remainder t - k s
+// (one fma) comes within 2e-4 of half a step it is divided out.
+template <int Lanes>
+__device__ __forceinline__ uint4 quantise16(const Octets& u, float tau, uint32_t* pair, Octets* held) {
+  uint32_t ends = max_bf16x2(ends8(u.u0), ends8(u.u1));
 #pragma unroll
   for (int m = 1; m < Lanes; m <<= 1) ends = max_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
   float hi = bf16_lo(ends), lo = -bf16_hi(ends);
-  float x[8];
-  unpack_bf16x8(u, x);
+  const uint32_t w[8] = {u.u0.x, u.u0.y, u.u0.z, u.u0.w, u.u1.x, u.u1.y, u.u1.z, u.u1.w};
+  float2 x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = bf16_pair(w[i]);
   if (!(hi <= tau && lo >= -tau)) {       // beyond tau, or a NaN, which becomes -tau; the test is the row's
     hi = -tau, lo = tau;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      x[i] = fminf(fmaxf(x[i], -tau), tau);
-      hi = fmaxf(hi, x[i]);
-      lo = fminf(lo, x[i]);
+      x[i] = make_float2(fminf(fmaxf(x[i].x, -tau), tau), fminf(fmaxf(x[i].y, -tau), tau));
+      hi = fmaxf(hi, fmaxf(x[i].x, x[i].y));
+      lo = fminf(lo, fminf(x[i].x, x[i].y));
     }
-    const uint32_t row = Lanes == 32 ? 0xffffffffu : ((1u << Lanes) - 1) << (threadIdx.x & 31 & ~(Lanes - 1));
+    const uint32_t row = ((1u << Lanes) - 1) << (threadIdx.x & 31 & ~(Lanes - 1));
 #pragma unroll
     for (int m = 1; m < Lanes; m <<= 1) {
       hi = fmaxf(hi, __shfl_xor_sync(row, hi, m));
@@ -179,51 +192,87 @@ __device__ __forceinline__ uint2 quantise8(const uint4& u, float tau, uint32_t* 
   if (sh && 255.f * __half2float(__ushort_as_half(uint16_t(sh - 1))) >= range) --sh;
   const float s = __half2float(__ushort_as_half(uint16_t(sh)));
   *pair = sh | (uint32_t(__half_as_ushort(zh)) << 16);
-  const float inv = rcp_fast(s), half = s * 0.4998f;
   constexpr float kRound = 12582912.f;   // 1.5 2^23: the sum's low byte is the rounded integer
-  float k[8];
-  bool near = false;
+  const float2 inv = twice(rcp_fast(s));
+  float2 k[8];
+  float off = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = x[i] - z;
-    k[i] = fmaf(t, inv, kRound);
-    near = near | (fabsf(fmaf(kRound - k[i], s, t)) >= half);
+    const float2 t = add2(x[i], twice(-z));
+    k[i] = fma2(t, inv, twice(kRound));
+    const float2 rest = fma2(fma2(k[i], twice(-1.f), twice(kRound)), twice(s), t);
+    off = fmaxf(off, fmaxf(fabsf(rest.x), fabsf(rest.y)));
   }
   if (!(s > 0.f)) {                       // a constant row that fp16 holds
 #pragma unroll
-    for (int i = 0; i < 8; ++i) k[i] = kRound;
-  } else if (near) {
+    for (int i = 0; i < 8; ++i) k[i] = twice(kRound);
+  } else if (off >= s * 0.4998f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) k[i] = kRound + rintf(__fdiv_rn(sub_odd(x[i], z), s));
+    for (int i = 0; i < 8; ++i)
+      k[i] = make_float2(kRound + rintf(__fdiv_rn(sub_odd(x[i].x, z), s)), kRound + rintf(__fdiv_rn(sub_odd(x[i].y, z), s)));
   }
-  if (Held) {
-    float v[8];
+  uint32_t b[8], v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fmaf(k[i] - kRound, s, z);
-    *held = pack_bf16x8(v);
+  for (int i = 0; i < 8; ++i) {
+    const float2 y = fma2(fma2(k[i], twice(-1.f), twice(kRound)), twice(-s), twice(z));
+    v[i] = pack_bf162(y.x, y.y);
+    b[i] = prmt(__float_as_uint(k[i].x), __float_as_uint(k[i].y), 0x0040);
   }
-  uint32_t b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(k[i]);
-  return make_uint2(prmt(prmt(b[0], b[1], 0x0040), prmt(b[2], b[3], 0x0040), 0x5410),
-                    prmt(prmt(b[4], b[5], 0x0040), prmt(b[6], b[7], 0x0040), 0x5410));
+  held->u0 = make_uint4(v[0], v[1], v[2], v[3]);
+  held->u1 = make_uint4(v[4], v[5], v[6], v[7]);
+  return make_uint4(prmt(b[0], b[1], 0x5410), prmt(b[2], b[3], 0x5410), prmt(b[4], b[5], 0x5410), prmt(b[6], b[7], 0x5410));
 }
 
-// One warp takes `slots_per_warp` slots of one token: its q heads four slots at a
-// time, whose loads are in flight together, then its k and v heads.
+// One warp takes `slots_per_warp` slots of one token: its q heads two slots at a
+// time, then its k and v heads, the next loads ahead of the present work and the first
+// ones ahead of the token's place.
+//
+// Bound by the bytes that the warps keep in flight and by issue (30k tokens appended, 821
+// MB: 148 us, 5.5 TB/s, 81 % of a plain copy's rate; normed and rotated only, 634 MB: 101
+// us, 92 %).  Set aside, each measured on the append: rows by bulk copies into rings that
+// run ahead over several tokens (176 us: more instructions a row), k and v rows side by
+// side (151, spilled), q and k, v rows in CTAs of their own (157), four or six CTAs an SM
+// (153, 161).
 template <int D, bool Interleaved, bool Append>
-__global__ void __launch_bounds__(kRowThreads, 7)
+__global__ void __launch_bounds__(kRowThreads, 5)
     head_rows_kernel(const __grid_constant__ HeadRowsParams p, int slots_per_warp) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 4;
-  const int lane = threadIdx.x & 31, o = lane % kLanes, sub = lane / kLanes;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes, kBatch = 2;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, li = lane % kLanes;
   const int sq = p.q ? (p.c.n_q + kRows - 1) / kRows : 0, sk = p.k ? (p.c.n_kv + kRows - 1) / kRows : 0;
   const int slots = sq + sk * (Append ? 2 : 1), warps_per_token = (slots + slots_per_warp - 1) / slots_per_warp;
   const int64_t w = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   const int64_t i = w / warps_per_token;
   if (i >= p.n) return;
-  const int part = int(w - i * warps_per_token);
+  const int part = int(w - i * warps_per_token), begin = part * slots_per_warp, end = min(slots, begin + slots_per_warp);
+  const int h = p.rope.rot / 16;
+  const bool halves = !Interleaved && li < h;
+  const int e0 = halves ? li : 2 * li, e1 = halves ? li + h : 2 * li + 1;
+
+  // the lane's octets of slot s (zeros from slot `to` and past the last head)
+  auto load = [&](const uint16_t* row, int s, int to, int heads) {
+    Octets x;
+    x.u0 = x.u1 = make_uint4(0, 0, 0, 0);
+    const int head = s * kRows + sub;
+    if (s < to && head < heads) {
+      x.u0 = *reinterpret_cast<const uint4*>(row + head * D + 8 * e0);
+      x.u1 = *reinterpret_cast<const uint4*>(row + head * D + 8 * e1);
+    }
+    return x;
+  };
+  auto store = [&](uint16_t* row, int head, const Octets& x) {
+    *reinterpret_cast<uint4*>(row + head * D + 8 * e0) = x.u0;
+    *reinterpret_cast<uint4*>(row + head * D + 8 * e1) = x.u1;
+  };
+  const uint16_t* q_row = p.q + i * p.q_stride;
+  const uint16_t* k_row = p.k + i * p.k_stride;
+  const int end_q = min(end, sq);
+  Octets first[kBatch];
+  if (begin < sq)
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) first[u] = load(q_row, begin + u, end_q, p.c.n_q);
+
   const bool report = part == 0 && lane == 0;
   uint8_t* base = nullptr;
   int64_t at = 0;
@@ -235,8 +284,7 @@ __global__ void __launch_bounds__(kRowThreads, 7)
     slot = pos % kPageTokens;
     at = pos;
   }
-  const bool rotate = p.rope.rot != 0;
-  if (rotate) {
+  if (p.rope.rot != 0) {
     if (p.rope_pos) at = p.rope_pos[i];
     if (!Append && at == -1) return;       // a padding row
     if (at < 0 || at >= p.rope.n_positions) {
@@ -244,69 +292,62 @@ __global__ void __launch_bounds__(kRowThreads, 7)
       return;
     }
   }
-  const Angles a = angles_of<Interleaved>(p.rope, at, o, lane);
-  const int begin = part * slots_per_warp, end = min(slots, begin + slots_per_warp);
+  const Angles<Interleaved> a(p.rope, at, li);
 
-  auto rows = [&](int from, int to, int heads, const uint16_t* src, uint16_t* dst, const uint16_t* weight) {
-    const Factors f = factors_of<D, Interleaved>(a, weight, o, lane);
-    src += sub * D + 8 * o;
-    dst += sub * D + 8 * o;
+  auto rows = [&](int from, int to, int heads, const uint16_t* src, uint16_t* dst, const uint16_t* weight, Octets (&next)[kBatch]) {
+    Factors f;
+    factors_of<Interleaved>(&f, a, weight);
 #pragma unroll 1
     for (int s0 = from; s0 < to; s0 += kBatch) {
-      uint4 raw[kBatch];
+      Octets x[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (s0 + u < to && (s0 + u) * kRows + sub < heads)
-          raw[u] = *reinterpret_cast<const uint4*>(src + (s0 + u) * (kRows * D));
-      }
+      for (int u = 0; u < kBatch; ++u) x[u] = next[u], next[u] = load(src, s0 + kBatch + u, to, heads);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (s0 + u >= to) break;
-        turn8<D, Interleaved>(raw[u], f, a, rotate, weight != nullptr, p.eps);
-        if ((s0 + u) * kRows + sub < heads) *reinterpret_cast<uint4*>(dst + (s0 + u) * (kRows * D)) = raw[u];
+        turn16<D, Interleaved>(x[u], f, a, weight != nullptr, p.eps);
+        const int head = (s0 + u) * kRows + sub;
+        if (head < heads) store(dst, head, x[u]);
       }
     }
   };
-  if (begin < sq) rows(begin, min(end, sq), p.c.n_q, p.q + i * p.q_stride, p.q_out + i * p.q_out_stride, p.q_weight);
+  if (begin < sq) rows(begin, end_q, p.c.n_q, q_row, p.q_out + i * p.q_out_stride, p.q_weight, first);
   if (end <= sq) return;
+  const int begin_k = max(begin - sq, 0), end_k = end - sq;   // among the slots of k (and v)
   if (!Append) {
-    rows(max(begin - sq, 0), end - sq, p.c.n_kv, p.k + i * p.k_stride, p.k_out + i * p.k_out_stride, p.k_weight);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) first[u] = load(k_row, begin_k + u, end_k, p.c.n_kv);
+    rows(begin_k, end_k, p.c.n_kv, k_row, p.k_out + i * p.k_out_stride, p.k_weight, first);
     return;
   }
-  // k, then v, with the next slot's load ahead of the present one's work
-  const Factors f = factors_of<D, Interleaved>(a, p.k_weight, o, lane);
-  auto load = [&](int s) {
-    uint4 r = make_uint4(0, 0, 0, 0);
-    const bool is_v = s >= sk;
-    const int head = (is_v ? s - sk : s) * kRows + sub;
-    const uint16_t* x = is_v ? p.v + i * p.v_stride : p.k + i * p.k_stride;
-    if (s < end - sq && head < p.c.n_kv) r = *reinterpret_cast<const uint4*>(x + head * D + 8 * o);
-    return r;
-  };
-  int s = max(0, begin - sq);
-  uint4 next = load(s);
+  const uint16_t* v_row = p.v + i * p.v_stride;
+  auto load_kv = [&](int s) { return s < sk ? load(k_row, s, end_k, p.c.n_kv) : load(v_row, s - sk, end_k - sk, p.c.n_kv); };
+  Octets next = load_kv(begin_k);
+  Factors f;
+  factors_of<Interleaved>(&f, a, p.k_weight);
+  const int at0 = int8_octet(D, slot, e0), at1 = int8_octet(D, slot, e1);
 #pragma unroll 1
-  for (; s < end - sq; ++s) {
-    uint4 raw = next;
-    next = load(s + 1);
+  for (int s = begin_k; s < end_k; ++s) {
+    Octets x = next;
+    next = load_kv(s + 1);
     const bool is_v = s >= sk;
     const int head = (is_v ? s - sk : s) * kRows + sub;
     const bool valid = head < p.c.n_kv;
-    const int64_t row = (i * p.c.n_kv + head) * D + 8 * o;
+    const int64_t row = i * p.c.n_kv * D;
     if (!is_v) {
-      turn8<D, Interleaved>(raw, f, a, rotate, p.k_weight != nullptr, p.eps);
-      if (p.k_out && valid) *reinterpret_cast<uint4*>(p.k_out + row) = raw;
+      turn16<D, Interleaved>(x, f, a, p.k_weight != nullptr, p.eps);
+      if (p.k_out && valid) store(p.k_out + row, head, x);
     }
     uint32_t pair;
-    uint4 held;
-    const uint2 codes = quantise8<kLanes, true>(raw, is_v ? p.tau_v : p.tau_k, &pair, &held);   // of the rounded row
+    Octets held;
+    const uint4 codes = quantise16<kLanes>(x, is_v ? p.tau_v : p.tau_k, &pair, &held);   // of the rounded row
     if (!valid) continue;
-    uint8_t* block = base + int64_t(head) * int8_block_bytes(D);
-    *reinterpret_cast<uint2*>(block + (is_v ? 16 * D : 0) + int8_octet(D, slot, o)) = codes;
-    if (o == 0) *reinterpret_cast<uint32_t*>(block + int8_pairs(D, slot) + (is_v ? 4 : 0)) = pair;
+    uint8_t* block = base + int64_t(head) * int8_block_bytes(D) + (is_v ? 16 * D : 0);
+    *reinterpret_cast<uint2*>(block + at0) = make_uint2(codes.x, codes.y);
+    *reinterpret_cast<uint2*>(block + at1) = make_uint2(codes.z, codes.w);
+    if (li == 0) *reinterpret_cast<uint32_t*>(block + int8_pairs(D, slot) + (is_v ? 4 - 16 * D : 0)) = pair;
     uint16_t* out = is_v ? p.v_held : p.k_held;
-    if (out) *reinterpret_cast<uint4*>(out + row) = held;
+    if (out) store(out + row, head, held);
   }
 }
 
@@ -387,7 +428,7 @@ __global__ void __launch_bounds__(kRowThreads)
 
 template <bool Append>
 cudaError_t launch_head_rows(const HeadRowsParams& p, cudaStream_t stream) {
-  const int rows = 32 / (p.c.d / 8);
+  const int rows = 512 / p.c.d;           // of a slot
   const int slots = (p.q ? (p.c.n_q + rows - 1) / rows : 0) + (p.k ? (Append ? 2 : 1) * ((p.c.n_kv + rows - 1) / rows) : 0);
   const int slots_per_warp = slots_of(p.n, slots);
   unsigned blocks = 0;

@@ -35,9 +35,8 @@ bool in_place_ok(const uint16_t* x, int64_t stride, const uint16_t* out, int64_t
 uint64_t turn_of(double w) {
   const double inv = 0.15915494309189535, rest = -9.839338337591243e-18;   // 1 / 2 pi
   const double t = w * inv, e = std::fma(w, inv, -t) + w * rest;
-  const double whole = std::floor(t);
-  const uint64_t high = uint64_t(std::ldexp(t - whole, 64));               // (t - whole is exact and below 1)
-  return high + uint64_t(int64_t(std::nearbyint(std::ldexp(e, 64))));
+  // t < 1 (w <= 6), and e is below 2^-53: both times 2^64 fit, and the products are exact
+  return uint64_t(t * 0x1p64) + uint64_t(int64_t(e * 0x1p64));
 }
 
 }  // namespace
