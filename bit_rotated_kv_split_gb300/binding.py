@@ -650,8 +650,9 @@ def oscar_rope_table(freq, cos_sin, magnitude: float = 1.0, first: int = 0, stre
     if len(shape) != 2 or shape[1] != 2 * pairs:
         raise ValueError("freq must be [rot_dim / 2] and cos_sin [n][rot_dim]")
     _contiguous("cos_sin", cos_sin, shape, 4)
+    # (a copy of the few numbers: the array's own address costs more to ask for)
     _on_device("oscar_rope_table", stream, (cos_sin,), lib.oscar_rope_table, (
-        freq.ctypes.data, 2 * pairs, magnitude, first, shape[0], cos_sin.data_ptr()))
+        freq.tobytes(), 2 * pairs, magnitude, first, shape[0], cos_sin.data_ptr()))
 
 
 def norm_desc(q_weight=None, k_weight=None, eps: float = 1e-6) -> HeadNorm:
@@ -731,27 +732,47 @@ def oscar_rope_append_int8(desc: Int8Desc, norm, rope, q, k, v, dst_req, dst_pos
     k_held, v_held [n][H_kv][d]: the rows as the cache holds them from now on.
     """
     hq, hk, d, n = desc.n_q_heads, desc.n_kv_heads, desc.head_dim, k.shape[0]
-    ks, vs = _rows("k", k, hk, d), _rows("v", v, hk, d)
+    rows = (n, hk, d)
+    ks = vs = hk * d
+    if not (k.dtype is _bf16 and v.dtype is _bf16 and k.shape == rows and v.shape == rows and k.is_contiguous() and v.is_contiguous()):
+        ks, vs = _heads("k", k, hk, d), _heads("v", v, hk, d)
+        if v.shape[0] != n:
+            raise ValueError("q, k and v must have one row count")
     qs = 0
     q_ptr = q_out_ptr = None
     if q is not None:
         qs, q_ptr = _rows("q", q, hq, d), q.data_ptr()
         if q.shape[0] != n:
             raise ValueError("q, k and v must have one row count")
-    if v.shape[0] != n:
-        raise ValueError("q, k and v must have one row count")
     if q_out is not None:
         _whole("q_out", q_out, (n, hq, d))
         q_out_ptr = q_out.data_ptr()
-    rows = (n, hk, d)
-    _whole("k_out", k_out, rows), _whole("k_held", k_held, rows), _whole("v_held", v_held, rows)
-    _places("dst_req", dst_req, n), _places("dst_pos", dst_pos, n), _places("rope_pos", rope_pos, n)
-    _norm_ok(norm, d)
+    k_out_ptr = k_held_ptr = v_held_ptr = None
+    if k_out is not None:
+        _whole("k_out", k_out, rows)
+        k_out_ptr = k_out.data_ptr()
+    if k_held is not None:
+        _whole("k_held", k_held, rows)
+        k_held_ptr = k_held.data_ptr()
+    if v_held is not None:
+        _whole("v_held", v_held, rows)
+        v_held_ptr = v_held.data_ptr()
+    _places("dst_req", dst_req, n)
+    _places("dst_pos", dst_pos, n)
+    rope_pos_ptr = None
+    if rope_pos is not None:
+        _places("rope_pos", rope_pos, n)
+        rope_pos_ptr = rope_pos.data_ptr()
+    norm_ref = rope_ref = None
+    if norm is not None:
+        _norm_ok(norm, d)
+        norm_ref = ctypes.byref(norm)
+    if rope is not None:
+        rope_ref = ctypes.byref(rope)
     _on_device("oscar_rope_append_int8", stream, (k, v, dst_req, dst_pos, q, q_out, k_out, rope_pos, k_held, v_held),
                lib.oscar_rope_append_int8, (
-                   ctypes.byref(desc), _ref(norm), _ref(rope), q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                   dst_req.data_ptr(), dst_pos.data_ptr(), _ptr(rope_pos), n, q_out_ptr, _ptr(k_out), _ptr(k_held),
-                   _ptr(v_held)), (desc, norm, rope))
+                   ctypes.byref(desc), norm_ref, rope_ref, q_ptr, qs, k.data_ptr(), ks, v.data_ptr(), vs, dst_req.data_ptr(),
+                   dst_pos.data_ptr(), rope_pos_ptr, n, q_out_ptr, k_out_ptr, k_held_ptr, v_held_ptr), (desc, norm, rope))
 
 
 def oscar_gather_int8(desc: Int8Desc, src_req, src_pos, k_out, v_out, stream=None) -> None:

@@ -187,12 +187,13 @@ struct Part {
 
 // Joins the parts of a run; the whole CTA, 4 channels a thread.  Where the heads
 // leave threads over, each takes every n-th part; where there are more heads than
-// threads for them, they come in turns.  Each round trip to L2 costs as much as ten
-// pages, so the first sums are asked for before their weights are known.  (Small code:
-// it runs once a CTA, when its instructions have to come from far.)
+// threads for them, they come in turns.  Each round trip to L2 costs as much as five
+// pages, so up to twenty parts are asked for at once, the first before their weights are
+// known.  (100k tokens, 39 parts: 41.3 us; 41.8 with ten at once, 42.6 with asynchronous
+// copies of all of them to shared memory.)
 template <int D, int kWarps>
 __device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r, int share, float* wt, float* sum_of) {
-  constexpr int kThreads = 32 * kWarps, kBatch = 10;
+  constexpr int kThreads = 32 * kWarps, kBatch = 20;
   const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = r.heads;
   const int f = r.run / share, n = (r.run + r.pages - 1) / share - f + 1;
@@ -204,7 +205,10 @@ __device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r
   auto load = [&](int i) {
     const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) x[k] = __ldcg(from + slot_of(min(i + k * ways, n - 1)) * (kHeads * D / 4));
+    for (int k = 0; k < kBatch; ++k) {
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i + k * ways < n) x[k] = __ldcg(from + slot_of(i + k * ways) * (kHeads * D / 4));
+    }
   };
   load(way);
   const float2* ml = reinterpret_cast<const float2*>(ws + kOffMl);
@@ -244,7 +248,8 @@ __device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r
         if (i != way) load(i);
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-          const float g = i + k * ways < n ? wt[(i + k * ways) * kHeads + h] : 0.f;
+          if (i + k * ways >= n) break;
+          const float g = wt[(i + k * ways) * kHeads + h];
           v.x = fmaf(g, x[k].x, v.x), v.y = fmaf(g, x[k].y, v.y), v.z = fmaf(g, x[k].z, v.z), v.w = fmaf(g, x[k].w, v.w);
         }
       }
