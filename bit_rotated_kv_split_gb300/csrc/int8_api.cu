@@ -83,7 +83,8 @@ extern "C" oscar_status oscar_norm_rope(int32_t n_q_heads, int32_t n_kv_heads, i
   if ((q && (!row_stride_ok(q_stride, n_q_heads, head_dim) || !row_stride_ok(q_out_stride, n_q_heads, head_dim))) ||
       (k && (!row_stride_ok(k_stride, n_kv_heads, head_dim) || !row_stride_ok(k_out_stride, n_kv_heads, head_dim))))
     return OSCAR_ERR_INVALID_ARG;
-  if ((q && !in_place_ok(q, q_stride, q_out, q_out_stride)) || (k && !in_place_ok(k, k_stride, k_out, k_out_stride)))
+  if ((q && !in_place_ok(q, q_stride, q_out, q_out_stride)) || (k && !in_place_ok(k, k_stride, k_out, k_out_stride)) ||
+      (q && k && (q_out == k || k_out == q || q_out == k_out)))
     return OSCAR_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(pos, 4) ||
       !aligned(dev_status, 4))
@@ -132,8 +133,15 @@ extern "C" oscar_status oscar_rope_append_int8(const oscar_int8_desc* desc, cons
       !row_stride_ok(v_stride, desc->n_kv_heads, desc->head_dim))
     return OSCAR_ERR_INVALID_ARG;
   if ((q && !in_place_ok(q, q_stride, q_out, q_row)) || !in_place_ok(k, k_stride, k_out, k_row) ||
-      !in_place_ok(k, k_stride, k_held, k_row) || !in_place_ok(v, v_stride, v_held, k_row) || (k_out && k_out == k_held))
+      !in_place_ok(k, k_stride, k_held, k_row) || !in_place_ok(v, v_stride, v_held, k_row))
     return OSCAR_ERR_INVALID_ARG;
+  // no other two rows in one place: a row would be written before it is read, or twice
+  const uint16_t *rows_in[3] = {q, k, v}, *rows_out[4] = {q_out, k_out, k_held, v_held};
+  const bool may_share[4][3] = {{true, false, false}, {false, true, false}, {false, true, false}, {false, false, true}};
+  for (int o = 0; o < 4; ++o)
+    for (int x = 0; rows_out[o] && x < 4; ++x)
+      if ((x < 3 && rows_out[o] == rows_in[x] && !may_share[o][x]) || (x != o && rows_out[o] == rows_out[x]))
+        return OSCAR_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) ||
       !aligned(k_held, 16) || !aligned(v_held, 16) || !aligned(dst_req, 4) || !aligned(dst_pos, 4) || !aligned(rope_pos, 4))
     return OSCAR_ERR_ALIGNMENT;

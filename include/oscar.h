@@ -916,7 +916,7 @@ oscar_status oscar_gather_int8(const oscar_int8_desc* desc, const int32_t* src_r
  *   is skipped and sets OSCAR_DEV_PAGE_BOUNDS.  A copy that does not land within 1 s sets
  *   OSCAR_DEV_TIMEOUT (the output must not be used then).  OSCAR_ERR_UNSUPPORTED: groups
  *   above 16; max_len above 2^31 - 513; 2^31 or more of (pages of max_len, or of the window
- *   if that is less, + 64) x B x H_kv.  out and lse must not overlap q.  The result does not
+ *   if that is less, + 32) x B x H_kv.  out and lse must not overlap q.  The result does not
  *   depend on scheduling.
  *
  *   Workspace: NULL asks for the size (it depends on head_dim alone); 256-byte aligned,

@@ -650,6 +650,105 @@ def test_decode_strided_query_other_stream_and_graph():
     assert (out == want).all()
 
 
+@pytest.mark.parametrize("hq,lens", [(4, [700, 33]), (16, [1500, 1])])
+def test_decode_halves_join_by_their_logarithms(hq, lens):
+    """The first and the last tokens decoded apart, and joined by the logarithms of the sums, are the whole."""
+    d = 128
+    L = Layer(31, lens, hq, 1, d)
+    q = O.bf16(L.g.standard_normal((2, hq, d)))
+    parts = []
+    for cut in (0, 1):
+        M = Layer(32, [max(0, n // 2 if cut == 0 else n - n // 2) for n in lens], hq, 1, d, fill=False)
+        for b, n in enumerate(lens):
+            rows = slice(0, n // 2) if cut == 0 else slice(n // 2, n)
+            for which, x in ((0, L.k[b][rows]), (1, L.v[b][rows])):
+                pos = np.arange(n)[rows]
+                c, s, z = O.int8_load(L.pool, L.table[b, pos // 16], pos % 16, which, d)
+                to = np.arange(len(pos))
+                O.int8_store_rows(M.pool, M.table[b, to // 16], to % 16, which, c, s, z)
+        M.upload()
+        parts.append([host(x) for x in decode(M, q)])
+    (o0, l0), (o1, l1) = parts
+    top = np.maximum(l0, l1)
+    w0, w1 = np.exp(l0 - top), np.exp(l1 - top)
+    joined = (o0 * w0[..., None] + o1 * w1[..., None]) / (w0 + w1)[..., None]
+    out, lse = decode(L, q)
+    most = max(np.abs(v).max() for v in L.v)
+    # three bf16 roundings and the bound of each decode
+    assert (np.abs(joined - host(out)) <= HALF_BF16 * (np.abs(o0) + np.abs(o1) + np.abs(joined)) + 3 * 2.0 ** -12 * most).all()
+    assert (np.abs(top + np.log(w0 + w1) - host(lse)) <= 2.0 ** -11).all()
+
+
+def test_decodes_on_two_streams_at_once():
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    layers = [Layer(41, [4000, 20, 900], 8, 2, 128), Layer(42, [2500, 1, 0, 3100], 20, 4, 64)]
+    qs = [dev_bf16(L.g.standard_normal((len(L.lens), L.hq, L.d))) for L in layers]
+    want = [decode(L, q)[0] for L, q in zip(layers, qs)]
+    outs = [torch.zeros_like(w) for w in want]
+    ws = [torch.zeros(B.oscar_decode_int8_workspace_bytes(L.desc), dtype=torch.uint8, device="cuda") for L in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for L, q, o, w, s in zip(layers, qs, outs, ws, streams):
+            B.oscar_decode_attention_int8(L.desc, q, o, w, stream=s)
+    torch.cuda.synchronize()
+    assert all((o == w).all() for o, w in zip(outs, want))
+
+
+# ---------------------------------------------------------------- offsets beyond 32 bits
+
+def test_pool_beyond_four_gigabytes():
+    """Pages whose blocks lie beyond 2^32 bytes: appended, read back and decoded."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    from bit_rotated_kv_split_gb300.cache import Int8Cache
+    d, hq, hk, n = 128, 4, 2, 100
+    n_pages = (2 ** 32 + 2 ** 28) // (hk * O.int8_block_bytes(d))
+    cache = Int8Cache(1, hq, hk, d, 7, n_pages)
+    cache.page_table.copy_(i32([[n_pages - 1, 3, n_pages - 2, n_pages // 2 + 1, n_pages - 9, n_pages - 4, n_pages - 5]]))
+    cache.seq_len.fill_(n)
+    g = np.random.default_rng(1)
+    q, k, v = (O.bf16(g.standard_normal((n, h, d))) for h in (hq, hk, hk))
+    req, pos = i32(np.zeros(n)), i32(np.arange(n))
+    B.oscar_rope_append_int8(cache.desc(), None, None, None, dev_bf16(k), dev_bf16(v), req, pos, None)
+    back = [torch.empty(n, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    B.oscar_gather_int8(cache.desc(), req, pos, *back)
+    out = torch.empty(1, hq, d, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(B.oscar_decode_int8_workspace_bytes(cache.desc()), dtype=torch.uint8, device="cuda")
+    B.oscar_decode_attention_int8(cache.desc(), dev_bf16(q[-1:]), out, ws)
+    torch.cuda.synchronize()
+    assert int(cache.dev_status.item()) == 0
+    kv = [O.int8_values(*O.int8_quantize(x)) for x in (k, v)]
+    for x, y in zip(back, kv):
+        np.testing.assert_array_equal(host(x), O.bf16(y))
+    for h in range(hq):
+        want, _, _ = O.masked_attention(O.modified_scores(q[-1:, h], kv[0][:, h // 2], n - 1), kv[1][:, h // 2])
+        assert (np.abs(host(out)[0, h] - want[0]) <= HALF_BF16 * np.abs(want[0]) + 2.0 ** -12 * np.abs(kv[1]).max()).all()
+
+
+def test_rows_and_tables_beyond_two_billion_elements():
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    d, n_pos = 128, 2 ** 24 + 70
+    freq, _ = B.oscar_rope_frequencies(d, 1e6)
+    table = torch.empty(n_pos, d, dtype=torch.float32, device="cuda")     # 2^31 entries and more
+    B.oscar_rope_table(freq, table)
+    rows = torch.empty(2 ** 31 + 4096, dtype=torch.bfloat16, device="cuda")
+    x = torch.as_strided(rows, (2, 3, d), (2 ** 31, d, 1))
+    g = np.random.default_rng(2)
+    data = O.bf16(g.standard_normal((2, 3, d)))
+    x.copy_(dev_bf16(data))
+    pos = np.array([n_pos - 1, 2 ** 24 + 1])
+    B.oscar_norm_rope(None, B.rope_desc(table, d), x, None, i32(pos), x, None)
+    torch.cuda.synchronize()
+    cs = host(table[torch.from_numpy(pos).cuda()])
+    want_cs = np.concatenate([O.rope_table(freq, int(p), 1) for p in pos])
+    assert (np.abs(cs - want_cs) <= 2.0 ** -21 * np.abs(want_cs) + 2.0 ** -35).all()
+    want, terms = rotated(data, None, cs, False)
+    assert (np.abs(host(x) - want) <= HALF_BF16 * np.abs(want) + 2.0 ** -19 * terms).all()
+
+
 # ---------------------------------------------------------------- a run of them
 
 def test_layer_run_prompt_then_tokens():

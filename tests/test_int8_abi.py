@@ -190,6 +190,8 @@ def test_cache_descriptor_refusals(built_lib, over, status):
     (dict(q=FAKE + 8), 2), (dict(k=FAKE + 2), 2), (dict(ko=FAKE + 4), 2), (dict(pos=FAKE + 1), 2), (dict(rp=FAKE + 2), 2),
     (dict(kh=FAKE + 8), 2), (dict(vh=FAKE + 2), 2), (dict(qo=FAKE, qs=2048), 1), (dict(ko=FAKE, ks=512), 1),
     (dict(kh=FAKE, ks=512), 1), (dict(vh=FAKE, vs=512), 1), (dict(ko=FAKE * 5, kh=FAKE * 5), 1),
+    (dict(kh=FAKE * 5, vh=FAKE * 5), 1), (dict(qo=FAKE * 5, vh=FAKE * 5), 1), (dict(v=FAKE * 3, kh=FAKE * 3), 1),
+    (dict(k=FAKE * 3, vh=FAKE * 3), 1), (dict(k=FAKE * 3, qo=FAKE * 3), 1),
 ])
 def test_append_refusals(built_lib, over, status):
     from bit_rotated_kv_split_gb300 import binding as B
@@ -202,6 +204,7 @@ def test_append_refusals(built_lib, over, status):
     (dict(pos=None), 1), (dict(qs=1016), 1), (dict(qs=1028), 1), (dict(qos=1016), 1), (dict(ks=128), 1), (dict(kos=252), 1),
     (dict(q=FAKE + 8), 2), (dict(qo=FAKE + 4), 2), (dict(k=FAKE + 2), 2), (dict(ko=FAKE + 8), 2), (dict(pos=FAKE + 2), 2),
     (dict(st=FAKE + 1), 2), (dict(qo=FAKE, qos=2048), 1), (dict(ko=FAKE * 3, kos=512), 1),
+    (dict(qo=FAKE * 3), 1), (dict(ko=FAKE), 1), (dict(ko=FAKE * 2), 1),
 ])
 def test_norm_rope_refusals(built_lib, over, status):
     from bit_rotated_kv_split_gb300 import binding as B
