@@ -7,11 +7,12 @@
 //
 // Bound by HBM where it is long: 8 requests of 100k tokens (8 KV heads x 128, 1.69 GB)
 // take 247 us, 6.85 TB/s, the rate of a plain copy.  One of them (211 MB, 31 us at that
-// rate) takes 41.6, cold: shares 1.2 us, first pages at 3 to 6.5, scans done at 37 to 44
-// (the memory serves SMs unevenly by some 8 %), warps' joins 1, tickets 1, last parts
-// joined 2 to 4 after that.  28 ragged requests of 2k to 32k (654 MB, 96 us): 109 us.
+// rate) takes 41.0: shares 1.2 us, first pages at 3 to 5, scans done at 31 to 34, warps'
+// joins by 34.7, tickets by 35.6, last parts joined at 39 to 40.  28 ragged requests of
+// 2k to 32k (654 MB, 96 us): 109 us, their scans done over 20 us (the memory serves SMs
+// unevenly by some 8 %, and the work is dealt out beforehand).
 //
-// A warp takes every 6th page of a run with an online softmax of its own, so
+// A warp takes every 6th page (or pair of pages) of a run with an online softmax of its own, so
 // nothing in the scan waits for another warp.  The pages' blocks come by bulk copies
 // into a ring of the warp's own, the next run's ahead of the present one's end.
 //
@@ -57,6 +58,9 @@ namespace {
 // which spill nothing.
 constexpr int warps_of(int G) { return G <= 8 ? 6 : 4; }
 constexpr int stages_of(int G) { return G <= 8 ? 2 : 3; }
+// Pages of a step of the scan (and of a ring's stage): about 4 KB.  (Heads of 64 with one
+// page a step: 8 x 100k tokens 151 us, with two 135, 6.4 TB/s.)
+constexpr int pages_of(int D) { return D == 64 ? 2 : 1; }
 constexpr int kPerSm = 2;
 constexpr int kCtas = 152 * kPerSm;   // CTAs the GPU holds at a time
 constexpr int kHeads = 16;            // most query heads of a KV head
@@ -66,14 +70,14 @@ constexpr int kMinShare = 6;          // pages
 // 64 of 1000 tokens: 33, 33, 32.)
 constexpr int kRunCost = 32;
 constexpr int kWhole = 18;            // a run of no more pages is not split
-constexpr int kJoinHeads = 4;         // heads whose states are joined at a time
+constexpr int join_heads(int G) { return G == 4 ? 4 : 8; }   // heads whose states are joined at a time
 constexpr uint32_t kLow = 0x00FF00FFu;
 
 using Walk = PageWalk<kRunCost, kWhole>;
-// a warp's first page of a segment
-template <int kWarps>
+// a warp's first step in a segment
+template <int kWarps, int P>
 __device__ __forceinline__ int place_of(const Segment& s, int warp) {
-  const int i = warp - s.at % kWarps;
+  const int i = warp - s.at / P % kWarps;
   return i < 0 ? i + kWarps : i;
 }
 
@@ -141,36 +145,36 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 // The logarithm of the sum, from the reference in log2 units and the sum of 2^(7 + x - m).
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + (log2f(l) - 7.f)) * kLn2 : l == 0.f ? -INFINITY : l; }
 
-// Joins the warps' states of heads h0 .. of a segment, 4 channels a thread: to `out`, or
-// to the workspace's partial state `slot` if that is not negative.
-template <int D, int kWarps>
+// Joins the warps' states of heads h0 .. of a segment, kJoin at the most, 4 channels a
+// thread: to `out`, or to the workspace's partial state `slot` if that is not negative.
+template <int D, int kWarps, int kJoin>
 __device__ __forceinline__ void join_warps(const Int8DecodeParams& p, int hq0, int h0, int heads, int slot, int b,
                                            const float* buf, const float (&sm_m)[kWarps][kHeads],
                                            const float (&sm_l)[kWarps][kHeads]) {
-  const int i = threadIdx.x, h = h0 + i / (D / 4);
-  static_assert(kJoinHeads * (D / 4) <= 32 * kWarps);
-  if (i >= kJoinHeads * (D / 4) || h >= heads) return;
   uint8_t* ws = static_cast<uint8_t*>(p.workspace);
-  float mx = -FLT_MAX, sum = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = threadIdx.x; i < min(kJoin, heads - h0) * (D / 4); i += 32 * kWarps) {
+    const int h = h0 + i / (D / 4);
+    float mx = -FLT_MAX, sum = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w)
-    if (sm_l[w][h] > 0.f) mx = fmaxf(mx, sm_m[w][h]);
-#pragma unroll 4
-  for (int w = 0; w < kWarps; ++w) {
-    const float l = sm_l[w][h], f = l == 0.f ? 0.f : exp2_fast(sm_m[w][h] - mx);   // (a NaN stays one)
-    const float4 x = reinterpret_cast<const float4*>(buf)[w * kJoinHeads * (D / 4) + i];
-    sum = fmaf(f, l, sum);
-    v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
-  }
-  if (slot < 0) {
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
-    reinterpret_cast<uint2*>(p.out + (int64_t(b) * p.c.n_q + hq0) * D)[h0 * (D / 4) + i] =
-        make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
-    if (p.lse && i % (D / 4) == 0) p.lse[int64_t(b) * p.c.n_q + hq0 + h] = lse_of(mx, sum);
-  } else {
-    reinterpret_cast<float4*>(ws + kOffO)[(int64_t(slot) * kHeads + h0) * (D / 4) + i] = v;
-    if (i % (D / 4) == 0) reinterpret_cast<float2*>(ws + kOffMl)[slot * kHeads + h] = make_float2(mx, sum);
+    for (int w = 0; w < kWarps; ++w)
+      if (sm_l[w][h] > 0.f) mx = fmaxf(mx, sm_m[w][h]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float l = sm_l[w][h], f = l == 0.f ? 0.f : exp2_fast(sm_m[w][h] - mx);   // (a NaN stays one)
+      const float4 x = reinterpret_cast<const float4*>(buf)[w * kJoin * (D / 4) + i];
+      sum = fmaf(f, l, sum);
+      v.x = fmaf(f, x.x, v.x), v.y = fmaf(f, x.y, v.y), v.z = fmaf(f, x.z, v.z), v.w = fmaf(f, x.w, v.w);
+    }
+    if (slot < 0) {
+      const float inv = sum != 0.f ? __fdividef(1.f, sum) : 0.f;
+      reinterpret_cast<uint2*>(p.out + (int64_t(b) * p.c.n_q + hq0) * D)[h0 * (D / 4) + i] =
+          make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
+      if (p.lse && i % (D / 4) == 0) p.lse[int64_t(b) * p.c.n_q + hq0 + h] = lse_of(mx, sum);
+    } else {
+      reinterpret_cast<float4*>(ws + kOffO)[(int64_t(slot) * kHeads + h0) * (D / 4) + i] = v;
+      if (i % (D / 4) == 0) reinterpret_cast<float2*>(ws + kOffMl)[slot * kHeads + h] = make_float2(mx, sum);
+    }
   }
 }
 
@@ -189,8 +193,9 @@ struct Part {
 // leave threads over, each takes every n-th part; where there are more heads than
 // threads for them, they come in turns.  Each round trip to L2 costs as much as five
 // pages, so up to twenty parts are asked for at once, the first before their weights are
-// known.  (100k tokens, 39 parts: 41.3 us; 41.8 with ten at once, 42.6 with asynchronous
-// copies of all of them to shared memory.)
+// known.  (100k tokens, 39 parts: 41.0 us; 41.8 with ten at once, 41.3 and 42.6 with bulk
+// and with asynchronous copies of all of them to shared memory.)  The loads stand in the
+// code once, which runs once a CTA and comes from far: three copies of them took 41.4.
 template <int D, int kWarps>
 __device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r, int share, float* wt, float* sum_of) {
   constexpr int kThreads = 32 * kWarps, kBatch = 20;
@@ -201,73 +206,75 @@ __device__ __noinline__ void join_parts(const Int8DecodeParams& p, const Part& r
   const int units = heads * (D / 4), ways = max(1, kThreads / units);
   const int left = min(units, kThreads), way = threadIdx.x / left;
   int unit = threadIdx.x % left;
-  float4 x[kBatch];
-  auto load = [&](int i) {
-    const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i + k * ways < n) x[k] = __ldcg(from + slot_of(i + k * ways) * (kHeads * D / 4));
-    }
-  };
-  load(way);
-  const float2* ml = reinterpret_cast<const float2*>(ws + kOffMl);
-  for (int h = warp; h < heads; h += kWarps) {
-    float mx = -FLT_MAX, sum = 0.f;
-#pragma unroll 2
-    for (int i = lane; i < n; i += 32) {
-      const float2 s = __ldcg(&ml[slot_of(i) * kHeads + h]);
-      const float m = s.y == 0.f ? -FLT_MAX : s.x, mn = fmaxf(mx, m);
-      sum = fmaf(exp2_fast(m - mn), s.y, sum * exp2_fast(mx - mn));
-      mx = mn;
-      wt[i * kHeads + h] = m;
-    }
-    float all = mx;
-#pragma unroll
-    for (int i = 16; i; i >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, i));
-    sum *= exp2_fast(mx - all);
-#pragma unroll
-    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-#pragma unroll 1
-    for (int i = lane; i < n; i += 32) wt[i * kHeads + h] = exp2_fast(wt[i * kHeads + h] - all);
-    if (lane == 0) {
-      sum_of[h] = sum;
-      if (p.lse) p.lse[int64_t(r.b) * p.c.n_q + r.hq0 + h] = lse_of(all, sum);
-    }
-  }
-  __syncthreads();
   float4* sums = reinterpret_cast<float4*>(wt + n * kHeads);
+  bool ready = false;                       // the weights are there
 #pragma unroll 1
-  for (; unit < units; unit += kThreads) {   // (more than once only where ways is 1)
-    const int h = unit / (D / 4);
-    if (unit >= kThreads) load(0);
+  do {                                      // (more than one unit only where ways is 1)
+    const float4* from = reinterpret_cast<const float4*>(ws + kOffO) + unit;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (way < ways)
+    int i = way;
 #pragma unroll 1
-      for (int i = way; i < n; i += kBatch * ways) {
-        if (i != way) load(i);
+    do {
+      const int stop = way < ways ? n : 0;
+      float4 x[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          if (i + k * ways >= n) break;
-          const float g = wt[(i + k * ways) * kHeads + h];
-          v.x = fmaf(g, x[k].x, v.x), v.y = fmaf(g, x[k].y, v.y), v.z = fmaf(g, x[k].z, v.z), v.w = fmaf(g, x[k].w, v.w);
-        }
+      for (int k = 0; k < kBatch; ++k) {
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + k * ways < stop) x[k] = __ldcg(from + slot_of(i + k * ways) * (kHeads * D / 4));
       }
+      if (!ready) {
+        const float2* ml = reinterpret_cast<const float2*>(ws + kOffMl);
+#pragma unroll 1
+        for (int h = warp; h < heads; h += kWarps) {
+          float mx = -FLT_MAX, sum = 0.f;
+#pragma unroll 1
+          for (int j = lane; j < n; j += 32) {
+            const float2 s = __ldcg(&ml[slot_of(j) * kHeads + h]);
+            const float m = s.y == 0.f ? -FLT_MAX : s.x, mn = fmaxf(mx, m);
+            sum = fmaf(exp2_fast(m - mn), s.y, sum * exp2_fast(mx - mn));
+            mx = mn;
+            wt[j * kHeads + h] = m;
+          }
+          float all = mx;
+#pragma unroll
+          for (int j = 16; j; j >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, j));
+          sum *= exp2_fast(mx - all);
+#pragma unroll
+          for (int j = 16; j; j >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, j);
+#pragma unroll 1
+          for (int j = lane; j < n; j += 32) wt[j * kHeads + h] = exp2_fast(wt[j * kHeads + h] - all);
+          if (lane == 0) {
+            sum_of[h] = sum;
+            if (p.lse) p.lse[int64_t(r.b) * p.c.n_q + r.hq0 + h] = lse_of(all, sum);
+          }
+        }
+        __syncthreads();
+        ready = true;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (i + k * ways >= stop) break;
+        const float g = wt[(i + k * ways) * kHeads + unit / (D / 4)];
+        v.x = fmaf(g, x[k].x, v.x), v.y = fmaf(g, x[k].y, v.y), v.z = fmaf(g, x[k].z, v.z), v.w = fmaf(g, x[k].w, v.w);
+      }
+      i += kBatch * ways;
+    } while (i < n);
     if (ways > 1) {
       sums[threadIdx.x] = v;
       __syncthreads();
     }
     if (way == 0) {
 #pragma unroll 1
-      for (int i = 1; i < ways; ++i) {
-        const float4 y = sums[i * units + unit];
+      for (int j = 1; j < ways; ++j) {
+        const float4 y = sums[j * units + unit];
         v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
       }
-      const float inv = sum_of[h] != 0.f ? 1.f / sum_of[h] : 0.f;
+      const float sum = sum_of[unit / (D / 4)], inv = sum != 0.f ? __fdividef(1.f, sum) : 0.f;
       reinterpret_cast<uint2*>(p.out + (int64_t(r.b) * p.c.n_q + r.hq0) * D)[unit] =
           make_uint2(pack_bf162(v.x * inv, v.y * inv), pack_bf162(v.z * inv, v.w * inv));
     }
-  }
+    unit += kThreads;
+  } while (unit < units);
 }
 
 // G: the most query heads of a group (4, 8 or 16).  Formed: the scores have a cap or a
@@ -276,6 +283,7 @@ template <int D, int G, bool Formed>
 __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(const __grid_constant__ Int8DecodeParams p) {
   constexpr int kWarps = warps_of(G), kThreads = 32 * kWarps, kStages = stages_of(G);
   constexpr int kBlock = int8_block_bytes(D), C = D / 16;   // chunks of 16 channels
+  constexpr int P = pages_of(D), kJoin = join_heads(G);
   constexpr int R = G == 16 ? 2 : 1;                        // sets of 8 columns
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
@@ -320,28 +328,28 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
   __syncwarp();
   bool more = false;                      // sm_next holds another
 
-  // The ring.  A warp's pages of a segment begin with another warp each time, so
-  // that short segments spread over the warps.  Lane i knows the address of page
-  // 32 n + i of the segment that is being brought in (0: the page is not there).
-  uint8_t* ring = smem + warp * (kStages * kBlock);
-  float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * kBlock);
+  // The ring.  A warp's steps of a segment begin with another warp each time, so
+  // that short segments spread over the warps.  Lane i knows the addresses of the pages of
+  // step 32 n + i of the segment that is being brought in (0: the page is not there).
+  uint8_t* ring = smem + warp * (kStages * P * kBlock);
+  float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * P * kBlock);
   uint64_t* wbars = bars[warp];
-  // the segment being brought in: its pages from this warp's first, KV head, request, and number
+  // the segment being brought in: its pages from this warp's first, KV head, request, and steps
   int in_lo, in_hi, in_hk, in_b, in_it = 0, in_n;
   auto turn_to = [&](const Segment& s) {
-    in_lo = s.lo + place_of<kWarps>(s, warp);
+    in_lo = s.lo + P * place_of<kWarps, P>(s, warp);
     in_hi = s.hi;
     in_hk = s.h;
     in_b = s.b;
     in_it = 0;
-    in_n = max(0, (in_hi - in_lo + kWarps - 1) / kWarps);
+    in_n = max(0, (in_hi - in_lo + P * kWarps - 1) / (P * kWarps));
   };
   turn_to(cur);
   bool in_next = false, dead = false;     // it is the next one, not cur
-  const uint8_t* src = nullptr;
+  const uint8_t* src[P];
   int st_in = 0, flying = 0;
-  uint32_t ring_dead = 0;                 // bit i: stage i's page is not there
-  auto bring = [&]() {                    // one more page; false if there is none to bring yet
+  uint32_t ring_dead = 0;                 // bits P i ..: stage i's pages that are not there
+  auto bring = [&]() {                    // one more step's; false if there is none to bring yet
     if (in_it == in_n) {
       if (in_next || !more || dead) return false;
       in_next = true;
@@ -349,27 +357,33 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
       if (in_n == 0) return false;
     }
     if ((in_it & 31) == 0) {
-      const int page = in_lo + kWarps * (in_it + lane);
-      src = nullptr;
-      if (page < in_hi) {
-        const int id = c.page_table[int64_t(in_b) * c.max_pages + page];
-        if (id >= 0 && id < c.n_pages)
-          src = c.pages + (int64_t(id) * c.n_kv + in_hk) * kBlock;
-        else if (c.dev_status)
-          atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+#pragma unroll
+      for (int g = 0; g < P; ++g) {
+        const int page = in_lo + P * kWarps * (in_it + lane) + g;
+        src[g] = nullptr;
+        if (page < in_hi) {
+          const int id = c.page_table[int64_t(in_b) * c.max_pages + page];
+          if (id >= 0 && id < c.n_pages)
+            src[g] = c.pages + (int64_t(id) * c.n_kv + in_hk) * kBlock;
+          else if (c.dev_status)
+            atomicOr(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+        }
       }
     }
     const int owner = in_it & 31;
-    const bool there = (__ballot_sync(0xffffffffu, src != nullptr) >> owner) & 1u;
-    ring_dead = there ? ring_dead & ~(1u << st_in) : ring_dead | (1u << st_in);
+    uint32_t there = 0;
+#pragma unroll
+    for (int g = 0; g < P; ++g) there |= ((__ballot_sync(0xffffffffu, src[g] != nullptr) >> owner) & 1u) << g;
+    ring_dead = (ring_dead & ~(((1u << P) - 1) << (P * st_in))) | ((~there & ((1u << P) - 1)) << (P * st_in));
     if (lane == owner) {
       uint64_t* bar = wbars + st_in;
-      if (there) {
-        mbar_arrive_expect_tx(bar, kBlock);
-        bulk_copy_g2s(ring + st_in * kBlock, src, kBlock, bar);
-      } else {
+      if (there)
+        mbar_arrive_expect_tx(bar, __popc(there) * kBlock);
+      else
         mbar_arrive(bar);
-      }
+#pragma unroll
+      for (int g = 0; g < P; ++g)
+        if (src[g]) bulk_copy_g2s(ring + (st_in * P + g) * kBlock, src[g], kBlock, bar);
     }
     st_in = st_in + 1 == kStages ? 0 : st_in + 1;
     ++in_it;
@@ -406,8 +420,8 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
   uint32_t parity = 0;
   int has_part = 0;                       // bits: of a run that began before this share, of one that goes on behind it
   while (true) {
-    const int hq0 = cur.h * group, lo = cur.lo + place_of<kWarps>(cur, warp);
-    const int n_it = max(0, (cur.hi - lo + kWarps - 1) / kWarps);
+    const int hq0 = cur.h * group, lo = cur.lo + P * place_of<kWarps, P>(cur, warp);
+    const int n_it = max(0, (cur.hi - lo + P * kWarps - 1) / (P * kWarps));
 
     // Query operands, scaled by 2^(141 - ex) so that a head's largest channel is in [2^14, 2^15).
     uint32_t qb[R][C][2];
@@ -482,56 +496,66 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
         __syncwarp();
         break;
       }
-      const uint32_t blk = smem_addr(ring + st * kBlock), at = blk + lm;
-      // S: rows gid and gid + 8 are tokens, columns heads; two chains of products
-      float acc[R][2][4];
+      const uint32_t blk0 = smem_addr(ring + st * P * kBlock);
+      // tokens 8 t + gid of the step: their values' scales and zeros, and the scores
+      float vs[2 * P], vz[2 * P], y[R][2 * P][2];
+      uint32_t vbits[2 * P];
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) acc[r][u][0] = acc[r][u][1] = acc[r][u][2] = acc[r][u][3] = 0.f;
-#pragma unroll
-      for (int i = 0; i < C / 2; ++i) {
-        uint32_t k[4];
-        ldmatrix_x4(k, at ^ (32 * i));
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t a0 = even(k[2 * u]), a1 = even(k[2 * u + 1]), a2 = odd(k[2 * u]), a3 = odd(k[2 * u + 1]);
-#pragma unroll
-          for (int r = 0; r < R; ++r) mma(acc[r][u], a0, a1, a2, a3, qb[r][2 * i + u][0], qb[r][2 * i + u][1]);
-        }
-      }
-      // scales and zeros of tokens gid and gid + 8
-      float vs[2], vz[2], y[R][2][2];
-      uint32_t vbits[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const uint2 w = lds64(blk + 32 * D + 8 * gid + 64 * t);
-        const float2 k = half2_to_float2(w.x), v = half2_to_float2(w.y);
-        vs[t] = v.x;
-        vz[t] = fmaf(128.f, v.x, v.y);
-        vbits[t] = w.y & 0xFFFFu;
+      for (int g = 0; g < P; ++g) {
+        const uint32_t blk = blk0 + g * kBlock, at = blk + lm;
+        // S: rows gid and gid + 8 are tokens, columns heads; two chains of products
+        float acc[R][2][4];
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            y[r][t][e] = fmaf(k.x, acc[r][0][2 * t + e] + acc[r][1][2 * t + e], k.y * qs[r][e]);
+          for (int u = 0; u < 2; ++u) acc[r][u][0] = acc[r][u][1] = acc[r][u][2] = acc[r][u][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+          uint32_t k[4];
+          ldmatrix_x4(k, at ^ (32 * i));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t a0 = even(k[2 * u]), a1 = even(k[2 * u + 1]), a2 = odd(k[2 * u]), a3 = odd(k[2 * u + 1]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) mma(acc[r][u], a0, a1, a2, a3, qb[r][2 * i + u][0], qb[r][2 * i + u][1]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint2 w = lds64(blk + 32 * D + 8 * gid + 64 * t);
+          const float2 k = half2_to_float2(w.x), v = half2_to_float2(w.y);
+          vs[2 * g + t] = v.x;
+          vz[2 * g + t] = fmaf(128.f, v.x, v.y);
+          vbits[2 * g + t] = w.y & 0xFFFFu;
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              y[r][2 * g + t][e] = fmaf(k.x, acc[r][0][2 * t + e] + acc[r][1][2 * t + e], k.y * qs[r][e]);
+        }
       }
       if (Formed) {
         float far = 0.f;
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2 * P; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) y[r][t][e] *= unscale[r][e], far = fmaxf(far, fabsf(y[r][t][e]));
         if (p.s.cap_log2 != 0.f) {
           // (the vote skips a form that no score here needs; each score's own is its own)
           if (__builtin_expect(__any_sync(0xffffffffu, !cap_is_near(far, p.s)), 0)) {
 #pragma unroll
-            for (int j = 0; j < 4 * R; ++j) y[j >> 2][(j >> 1) & 1][j & 1] = capped(y[j >> 2][(j >> 1) & 1][j & 1], p.s);
+            for (int j = 0; j < 4 * P * R; ++j) {
+              float& x = y[j / (4 * P)][(j >> 1) % (2 * P)][j & 1];
+              x = capped(x, p.s);
+            }
           } else {
 #pragma unroll
-            for (int j = 0; j < 4 * R; ++j) y[j >> 2][(j >> 1) & 1][j & 1] = capped_near(y[j >> 2][(j >> 1) & 1][j & 1], p.s);
+            for (int j = 0; j < 4 * P * R; ++j) {
+              float& x = y[j / (4 * P)][(j >> 1) % (2 * P)][j & 1];
+              x = capped_near(x, p.s);
+            }
           }
         }
         if (p.s.slopes) {
@@ -539,18 +563,18 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2 * P; ++t)
 #pragma unroll
               for (int e = 0; e < 2; ++e) y[r][t][e] = fmaf(slope[r][e], away + 8.f * t, y[r][t][e]);
         }
       }
-      const bool gone = (ring_dead >> st) & 1u;
-      if (gone || tok < cur.first || tok + kPageTokens > cur.len) {
+      const uint32_t gone = (ring_dead >> (P * st)) & ((1u << P) - 1);
+      if (gone || tok < cur.first || tok + P * kPageTokens > cur.len) {
         // what a stale slot holds is anything
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 2 * P; ++t) {
           const int at_tok = tok + 8 * t + gid;
-          if (gone || at_tok < cur.first || at_tok >= cur.len) {
+          if (((gone >> (t >> 1)) & 1u) || at_tok < cur.first || at_tok >= cur.len) {
             vs[t] = vz[t] = 0.f;
             vbits[t] = 0;
 #pragma unroll
@@ -558,7 +582,8 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
           }
         }
       }
-      const uint32_t smax = max(vbits[0], vbits[1]);   // (fp16 values >= 0 order as integers)
+      uint32_t smax = max(vbits[0], vbits[1]);   // (fp16 values >= 0 order as integers)
+      if (P == 2) smax = max(smax, max(vbits[2 * P - 2], vbits[2 * P - 1]));
       bool raise = smax > vs_top;
       float top[R][2];
 #pragma unroll
@@ -566,6 +591,7 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           top[r][e] = fmaxf(y[r][0][e], y[r][1][e]);
+          if (P == 2) top[r][e] = fmaxf(top[r][e], fmaxf(y[r][2 * P - 2][e], y[r][2 * P - 1][e]));
           raise = raise | (top[r][e] > thr[r][e]);
         }
       if (__any_sync(0xffffffffu, raise)) {
@@ -591,58 +617,61 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
           for (int i = 0; i < C; ++i) o[r][i][0] *= f[0], o[r][i][1] *= f[1], o[r][i][2] *= f[0], o[r][i][3] *= f[1];
         }
       }
-      // P's operands: the weights times the values' scales, in two parts
-      uint32_t hi[R][2], part[R][2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float s = vs[t] * vs_mul;
+      for (int g = 0; g < P; ++g) {
+        // P's operands: the weights times the values' scales, in two parts
+        uint32_t hi[R][2], part[R][2];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float w[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float g = exp2_fast(fmaf(y[r][t][e] - m[r][e], us[r][e], 7.f));
-            l[r][e] += g;
-            zs[r][e] = fmaf(g, vz[t], zs[r][e]);
-            w[e] = g * s;
-          }
-          const uint32_t h = pack_half2(w[0], w[1]);
-          const float2 hf = half2_to_float2(h);
-          const uint32_t rest = pack_half2(w[0] - hf.x, w[1] - hf.y);
-          if (G == 4) {                     // (columns 4 to 7 take the second parts)
-            hi[r][t] = movmatrix_trans(low_part ? rest : h);
-          } else {
-            hi[r][t] = movmatrix_trans(h);
-            part[r][t] = movmatrix_trans(rest);
-          }
-        }
-      }
-      // O: rows are channels
-#pragma unroll
-      for (int i = 0; i < C / 2; ++i) {
-        uint32_t v[4];
-        ldmatrix_x4_t(v, (at + 16 * D) ^ (32 * i));
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t a0 = even_signed(v[2 * u]), a1 = odd_signed(v[2 * u]);
-          const uint32_t a2 = even_signed(v[2 * u + 1]), a3 = odd_signed(v[2 * u + 1]);
+        for (int t = 0; t < 2; ++t) {
+          const float s = vs[2 * g + t] * vs_mul;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            mma(o[r][2 * i + u], a0, a1, a2, a3, hi[r][0], hi[r][1]);
-            if (G > 4) mma(o[r][2 * i + u], a0, a1, a2, a3, part[r][0], part[r][1]);
+            float w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x = exp2_fast(fmaf(y[r][2 * g + t][e] - m[r][e], us[r][e], 7.f));
+              l[r][e] += x;
+              zs[r][e] = fmaf(x, vz[2 * g + t], zs[r][e]);
+              w[e] = x * s;
+            }
+            const uint32_t h = pack_half2(w[0], w[1]);
+            const float2 hf = half2_to_float2(h);
+            const uint32_t rest = pack_half2(w[0] - hf.x, w[1] - hf.y);
+            if (G == 4) {                   // (columns 4 to 7 take the second parts)
+              hi[r][t] = movmatrix_trans(low_part ? rest : h);
+            } else {
+              hi[r][t] = movmatrix_trans(h);
+              part[r][t] = movmatrix_trans(rest);
+            }
+          }
+        }
+        // O: rows are channels
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+          uint32_t v[4];
+          ldmatrix_x4_t(v, (blk0 + g * kBlock + lm + 16 * D) ^ (32 * i));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t a0 = even_signed(v[2 * u]), a1 = odd_signed(v[2 * u]);
+            const uint32_t a2 = even_signed(v[2 * u + 1]), a3 = odd_signed(v[2 * u + 1]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              mma(o[r][2 * i + u], a0, a1, a2, a3, hi[r][0], hi[r][1]);
+              if (G > 4) mma(o[r][2 * i + u], a0, a1, a2, a3, part[r][0], part[r][1]);
+            }
           }
         }
       }
       __syncwarp();                         // the stage has been read
       --flying;
       bring();
-      tok += kWarps * kPageTokens;
+      tok += P * kWarps * kPageTokens;
       st = st + 1 == kStages ? 0 : st + 1;
       parity ^= st == 0;
     }
 
     if (more) ask_q(sm_next[warp]);
-    // The warps' states of this segment, kJoinHeads heads at a time.  (All with
+    // The warps' states of this segment, kJoin heads at a time.  (All with
     // the weights' 2^7; a warp without a token has l = 0, whatever its m.)
     const float un = pow2i(ve);             // of the scales
 #pragma unroll
@@ -661,13 +690,13 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
     }
     const bool whole = cur.off == 0 && cur.hi - cur.lo == cur.pages;
     const int slot = 2 * blockIdx.x + (cur.off == 0);
-    for (int h0 = 0; h0 < group; h0 += kJoinHeads) {
+    for (int h0 = 0; h0 < group; h0 += kJoin) {
       if (h0) __syncthreads();              // the heads before have been read
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int h = 8 * r + 2 * tig - h0;
-        if (h >= 0 && h < kJoinHeads && !low_part) {
-          float2* to = reinterpret_cast<float2*>(buf + (warp * kJoinHeads + h) * D + 2 * gid);
+        if (h >= 0 && h < kJoin && !low_part) {
+          float2* to = reinterpret_cast<float2*>(buf + (warp * kJoin + h) * D + 2 * gid);
 #pragma unroll
           for (int i = 0; i < C; ++i) {
             to[8 * i] = make_float2(fmaf(o[r][i][0], un, zs[r][0]), fmaf(o[r][i][2], un, zs[r][0]));
@@ -676,7 +705,7 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
         }
       }
       __syncthreads();
-      join_warps<D, kWarps>(p, hq0, h0, group, whole ? -1 : slot, cur.b, buf, sm_m, sm_l);
+      join_warps<D, kWarps, kJoin>(p, hq0, h0, group, whole ? -1 : slot, cur.b, buf, sm_m, sm_l);
     }
     if (!whole && threadIdx.x == 0) sm_part[cur.off == 0] = {cur.at - cur.off, cur.pages, cur.b, hq0, group};
     has_part |= whole ? 0 : 1 << (cur.off == 0);
@@ -714,8 +743,8 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
 
 template <int D, int G, bool Formed>
 cudaError_t launch(const Int8DecodeParams& p, cudaStream_t stream) {
-  // the ring, and the warps' states of kJoinHeads heads
-  constexpr int kRing = warps_of(G) * stages_of(G) * int8_block_bytes(D), bytes = kRing + warps_of(G) * kJoinHeads * D * 4;
+  // the ring, and the warps' states of the heads that are joined at a time
+  constexpr int bytes = warps_of(G) * (stages_of(G) * pages_of(D) * int8_block_bytes(D) + join_heads(G) * D * 4);
   static_assert((kCtas + 1) * kHeads * 4 + 32 * warps_of(G) * 16 <= bytes);   // the parts' weights and partial sums
   const cudaError_t e = set_smem_limit<decode_int8_kernel<D, G, Formed>>(bytes);
   if (e != cudaSuccess) return e;
