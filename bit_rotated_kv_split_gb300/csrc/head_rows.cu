@@ -9,7 +9,7 @@
 // w_other.  C and S belong to a lane and a token, so every head of the token takes two
 // products a channel.  (With an octet a lane and its partner by shuffle, every channel
 // was unpacked twice and every row reduced by twice the lanes: 30k tokens appended in 157
-// us where this takes 148.)
+// us where two octets a lane took 149.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -149,35 +149,35 @@ __device__ __forceinline__ uint32_t ends8(const uint4& u) {
   return max_bf16x2(prmt(hi2, lo2, 0x5410), prmt(hi2, lo2, 0x7632));
 }
 
-// Quantises the row of which this lane holds the 16 bf16 values u, over `Lanes`
-// lanes: zero = the least value, rounded down to fp16; scale = (greatest - zero) /
-// 255, rounded up, so that no value lies outside the codes; code = (x - zero) /
-// scale to nearest even, of exact differences and quotients.  *pair = (scale, zero);
-// *held: zero + scale code, rounded to fp32 and that to bf16.  Returns the codes of the
-// two octets.
+// A row's scale and zero, of which this lane holds the 16 bf16 values u, over `Lanes`
+// lanes: zero = the least value, rounded down to fp16; scale = (greatest - zero) / 255,
+// rounded up, so that no value lies outside the codes.
 //
 // The extremes are taken on packed bf16.  The scale is a product with 1/255 rounded up,
 // and one fp16 less where that still reaches the greatest value (255 s has 19 bits,
-// exact in fp32).  A quotient is taken by an approximate reciprocal and checked: its
-// error is below 255 (2^-22 + 2^-24) < 1e-4 of a step, and where the remainder t - k s
-// (one fma) comes within 2e-4 of half a step it is divided out.
+// exact in fp32).
+struct RowScale {
+  float s, z;
+  uint32_t pair;      // (s, z), fp16 bits
+  bool clamped;       // some of its values lie beyond tau
+};
 template <int Lanes>
-__device__ __forceinline__ uint4 quantise16(const Octets& u, float tau, uint32_t* pair, Octets* held) {
+__device__ __forceinline__ RowScale scale_of(const Octets& u, float tau) {
   uint32_t ends = max_bf16x2(ends8(u.u0), ends8(u.u1));
 #pragma unroll
   for (int m = 1; m < Lanes; m <<= 1) ends = max_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, m));
   float hi = bf16_lo(ends), lo = -bf16_hi(ends);
-  const uint32_t w[8] = {u.u0.x, u.u0.y, u.u0.z, u.u0.w, u.u1.x, u.u1.y, u.u1.z, u.u1.w};
-  float2 x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = bf16_pair(w[i]);
-  if (!(hi <= tau && lo >= -tau)) {       // beyond tau, or a NaN, which becomes -tau; the test is the row's
+  RowScale r;
+  r.clamped = !(hi <= tau && lo >= -tau);   // or a NaN, which becomes -tau; the test is the row's
+  if (r.clamped) {
+    const uint32_t w[8] = {u.u0.x, u.u0.y, u.u0.z, u.u0.w, u.u1.x, u.u1.y, u.u1.z, u.u1.w};
     hi = -tau, lo = tau;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      x[i] = make_float2(fminf(fmaxf(x[i].x, -tau), tau), fminf(fmaxf(x[i].y, -tau), tau));
-      hi = fmaxf(hi, fmaxf(x[i].x, x[i].y));
-      lo = fminf(lo, fminf(x[i].x, x[i].y));
+      const float2 x = bf16_pair(w[i]);
+      const float y0 = fminf(fmaxf(x.x, -tau), tau), y1 = fminf(fmaxf(x.y, -tau), tau);
+      hi = fmaxf(hi, fmaxf(y0, y1));
+      lo = fminf(lo, fminf(y0, y1));
     }
     const uint32_t row = ((1u << Lanes) - 1) << (threadIdx.x & 31 & ~(Lanes - 1));
 #pragma unroll
@@ -187,40 +187,59 @@ __device__ __forceinline__ uint4 quantise16(const Octets& u, float tau, uint32_t
     }
   }
   const __half zh = __float2half_rd(lo);
-  const float z = __half2float(zh), range = __fsub_ru(hi, z);
+  r.z = __half2float(zh);
+  const float range = __fsub_ru(hi, r.z);
   uint32_t sh = __half_as_ushort(__float2half_ru(__fmul_ru(range, 0x1.010102p-8f)));   // (just above 1 / 255)
   if (sh && 255.f * __half2float(__ushort_as_half(uint16_t(sh - 1))) >= range) --sh;
-  const float s = __half2float(__ushort_as_half(uint16_t(sh)));
-  *pair = sh | (uint32_t(__half_as_ushort(zh)) << 16);
+  r.s = __half2float(__ushort_as_half(uint16_t(sh)));
+  r.pair = sh | (uint32_t(__half_as_ushort(zh)) << 16);
+  return r;
+}
+
+// The codes of an octet: (x - zero) / scale to nearest even, of exact differences and
+// quotients.  *held: zero + scale code, rounded to fp32 and that to bf16.
+//
+// A quotient is taken by an approximate reciprocal and checked: its error is below
+// 255 (2^-22 + 2^-24) < 1e-4 of a step, and where the remainder t - k s (one fma) comes
+// within 2e-4 of half a step it is divided out.  (An octet at a time: with the row's
+// sixteen values at once the kernel spilled.)
+__device__ __forceinline__ uint2 encode8(const uint4& u, const RowScale& r, float tau, uint4* held) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float2 x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = bf16_pair(w[i]);
+  if (r.clamped)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[i] = make_float2(fminf(fmaxf(x[i].x, -tau), tau), fminf(fmaxf(x[i].y, -tau), tau));
   constexpr float kRound = 12582912.f;   // 1.5 2^23: the sum's low byte is the rounded integer
-  const float2 inv = twice(rcp_fast(s));
-  float2 k[8];
+  const float2 inv = twice(rcp_fast(r.s));
+  float2 k[4];
   float off = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 t = add2(x[i], twice(-z));
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = add2(x[i], twice(-r.z));
     k[i] = fma2(t, inv, twice(kRound));
-    const float2 rest = fma2(fma2(k[i], twice(-1.f), twice(kRound)), twice(s), t);
+    const float2 rest = fma2(fma2(k[i], twice(-1.f), twice(kRound)), twice(r.s), t);
     off = fmaxf(off, fmaxf(fabsf(rest.x), fabsf(rest.y)));
   }
-  if (!(s > 0.f)) {                       // a constant row that fp16 holds
+  if (!(r.s > 0.f)) {                     // a constant row that fp16 holds
 #pragma unroll
-    for (int i = 0; i < 8; ++i) k[i] = twice(kRound);
-  } else if (off >= s * 0.4998f) {
+    for (int i = 0; i < 4; ++i) k[i] = twice(kRound);
+  } else if (off >= r.s * 0.4998f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      k[i] = make_float2(kRound + rintf(__fdiv_rn(sub_odd(x[i].x, z), s)), kRound + rintf(__fdiv_rn(sub_odd(x[i].y, z), s)));
+    for (int i = 0; i < 4; ++i)
+      k[i] = make_float2(kRound + rintf(__fdiv_rn(sub_odd(x[i].x, r.z), r.s)), kRound + rintf(__fdiv_rn(sub_odd(x[i].y, r.z), r.s)));
   }
-  uint32_t b[8], v[8];
+  uint32_t b[4], v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 y = fma2(fma2(k[i], twice(-1.f), twice(kRound)), twice(-s), twice(z));
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = fma2(fma2(k[i], twice(-1.f), twice(kRound)), twice(-r.s), twice(r.z));
     v[i] = pack_bf162(y.x, y.y);
     b[i] = prmt(__float_as_uint(k[i].x), __float_as_uint(k[i].y), 0x0040);
   }
-  held->u0 = make_uint4(v[0], v[1], v[2], v[3]);
-  held->u1 = make_uint4(v[4], v[5], v[6], v[7]);
-  return make_uint4(prmt(b[0], b[1], 0x5410), prmt(b[2], b[3], 0x5410), prmt(b[4], b[5], 0x5410), prmt(b[6], b[7], 0x5410));
+  *held = make_uint4(v[0], v[1], v[2], v[3]);
+  return make_uint2(prmt(b[0], b[1], 0x5410), prmt(b[2], b[3], 0x5410));
 }
 
 // One warp takes `slots_per_warp` slots of one token: its q heads two slots at a
@@ -228,11 +247,11 @@ __device__ __forceinline__ uint4 quantise16(const Octets& u, float tau, uint32_t
 // ones ahead of the token's place.
 //
 // Bound by the bytes that the warps keep in flight and by issue (30k tokens appended, 821
-// MB: 148 us, 5.5 TB/s, 81 % of a plain copy's rate; normed and rotated only, 634 MB: 101
-// us, 92 %).  Set aside, each measured on the append: rows by bulk copies into rings that
-// run ahead over several tokens (176 us: more instructions a row), k and v rows side by
-// side (151, spilled), q and k, v rows in CTAs of their own (157), four or six CTAs an SM
-// (153, 161).
+// MB: 148 us, 5.55 TB/s, 82 % of a plain copy's rate, of which the quantisation costs
+// some 19; normed and rotated only, 634 MB: 98 us, 95 %).  Set aside, each
+// measured on the append: rows by bulk copies into rings that run ahead over several
+// tokens (176 us: more instructions a row), k and v rows side by side (151, spilled), q
+// rows and k, v rows in CTAs of their own (157), four or six CTAs an SM (153, 150).
 template <int D, bool Interleaved, bool Append>
 __global__ void __launch_bounds__(kRowThreads, 5)
     head_rows_kernel(const __grid_constant__ HeadRowsParams p, int slots_per_warp) {
@@ -250,20 +269,21 @@ __global__ void __launch_bounds__(kRowThreads, 5)
   const bool halves = !Interleaved && li < h;
   const int e0 = halves ? li : 2 * li, e1 = halves ? li + h : 2 * li + 1;
 
-  // the lane's octets of slot s (zeros from slot `to` and past the last head)
+  // The lane's octets of slot s (zeros from slot `to` and past the last head).  Rows are read
+  // and written once, so both are marked for early eviction (rotation 101 -> 98 us).
   auto load = [&](const uint16_t* row, int s, int to, int heads) {
     Octets x;
     x.u0 = x.u1 = make_uint4(0, 0, 0, 0);
     const int head = s * kRows + sub;
     if (s < to && head < heads) {
-      x.u0 = *reinterpret_cast<const uint4*>(row + head * D + 8 * e0);
-      x.u1 = *reinterpret_cast<const uint4*>(row + head * D + 8 * e1);
+      x.u0 = __ldcs(reinterpret_cast<const uint4*>(row + head * D + 8 * e0));
+      x.u1 = __ldcs(reinterpret_cast<const uint4*>(row + head * D + 8 * e1));
     }
     return x;
   };
   auto store = [&](uint16_t* row, int head, const Octets& x) {
-    *reinterpret_cast<uint4*>(row + head * D + 8 * e0) = x.u0;
-    *reinterpret_cast<uint4*>(row + head * D + 8 * e1) = x.u1;
+    __stcs(reinterpret_cast<uint4*>(row + head * D + 8 * e0), x.u0);
+    __stcs(reinterpret_cast<uint4*>(row + head * D + 8 * e1), x.u1);
   };
   const uint16_t* q_row = p.q + i * p.q_stride;
   const uint16_t* k_row = p.k + i * p.k_stride;
@@ -338,16 +358,18 @@ __global__ void __launch_bounds__(kRowThreads, 5)
       turn16<D, Interleaved>(x, f, a, p.k_weight != nullptr, p.eps);
       if (p.k_out && valid) store(p.k_out + row, head, x);
     }
-    uint32_t pair;
-    Octets held;
-    const uint4 codes = quantise16<kLanes>(x, is_v ? p.tau_v : p.tau_k, &pair, &held);   // of the rounded row
+    const float tau = is_v ? p.tau_v : p.tau_k;
+    const RowScale scale = scale_of<kLanes>(x, tau);   // of the rounded row
     if (!valid) continue;
     uint8_t* block = base + int64_t(head) * int8_block_bytes(D) + (is_v ? 16 * D : 0);
-    *reinterpret_cast<uint2*>(block + at0) = make_uint2(codes.x, codes.y);
-    *reinterpret_cast<uint2*>(block + at1) = make_uint2(codes.z, codes.w);
-    if (li == 0) *reinterpret_cast<uint32_t*>(block + int8_pairs(D, slot) + (is_v ? 4 - 16 * D : 0)) = pair;
     uint16_t* out = is_v ? p.v_held : p.k_held;
-    if (out) store(out + row, head, held);
+    if (li == 0) *reinterpret_cast<uint32_t*>(block + int8_pairs(D, slot) + (is_v ? 4 - 16 * D : 0)) = scale.pair;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint4 held;
+      *reinterpret_cast<uint2*>(block + (e ? at1 : at0)) = encode8(e ? x.u1 : x.u0, scale, tau, &held);
+      if (out) __stcs(reinterpret_cast<uint4*>(out + row + head * D + 8 * (e ? e1 : e0)), held);
+    }
   }
 }
 
