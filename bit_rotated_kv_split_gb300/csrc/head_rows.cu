@@ -133,7 +133,7 @@ __device__ __forceinline__ void turn16(Octets& x, const Factors& f, const Angles
     // (a channel that stays takes nothing of a partner that may be infinite)
     if (a.on0) y = fma2(Interleaved ? make_float2(p.y, p.x) : q, f.s0[i], y);
     if (a.on1) z = fma2(Interleaved ? make_float2(q.y, q.x) : p, f.s1[i], z);
-    if (norm) y = mul2(y, twice(r)), z = mul2(z, twice(r));
+    y = mul2(y, twice(r)), z = mul2(z, twice(r));
     out0[i] = pack_bf162(y.x, y.y);
     out1[i] = pack_bf162(z.x, z.y);
   }
@@ -246,12 +246,13 @@ __device__ __forceinline__ uint2 encode8(const uint4& u, const RowScale& r, floa
 // time, then its k and v heads, the next loads ahead of the present work and the first
 // ones ahead of the token's place.
 //
-// Bound by the bytes that the warps keep in flight and by issue (30k tokens appended, 821
-// MB: 148 us, 5.55 TB/s, 82 % of a plain copy's rate, of which the quantisation costs
-// some 19; normed and rotated only, 634 MB: 98 us, 95 %).  Set aside, each
-// measured on the append: rows by bulk copies into rings that run ahead over several
-// tokens (176 us: more instructions a row), k and v rows side by side (151, spilled), q
-// rows and k, v rows in CTAs of their own (157), four or six CTAs an SM (153, 150).
+// Bound by issue and by the bytes that the warps keep in flight (30k tokens appended, 821
+// MB: 144 us, 5.7 TB/s, 84 % of a plain copy's rate, issue 67 %, of which the
+// quantisation costs some 19 us; normed and rotated only, 634 MB: 96 us, 97 %).  Set
+// aside, each measured on the append when it took 149: rows by bulk copies into rings
+// that run ahead over several tokens (176: more instructions a row), k and v rows side
+// by side (151, spilled), q rows and k, v rows in CTAs of their own (157), four or six CTAs
+// an SM (153, 150), a value's two octets' codes in one store (145).
 template <int D, bool Interleaved, bool Append>
 __global__ void __launch_bounds__(kRowThreads, 5)
     head_rows_kernel(const __grid_constant__ HeadRowsParams p, int slots_per_warp) {
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(kRowThreads, 5)
   const int e0 = halves ? li : 2 * li, e1 = halves ? li + h : 2 * li + 1;
 
   // The lane's octets of slot s (zeros from slot `to` and past the last head).  Rows are read
-  // and written once, so both are marked for early eviction (rotation 101 -> 98 us).
+  // and written once, so both are marked for early eviction (rotation 101 us without, 98 with).
   auto load = [&](const uint16_t* row, int s, int to, int heads) {
     Octets x;
     x.u0 = x.u1 = make_uint4(0, 0, 0, 0);
@@ -340,12 +341,23 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     rows(begin_k, end_k, p.c.n_kv, k_row, p.k_out + i * p.k_out_stride, p.k_weight, first);
     return;
   }
+  // (v does not turn: its octets lie side by side)
   const uint16_t* v_row = p.v + i * p.v_stride;
-  auto load_kv = [&](int s) { return s < sk ? load(k_row, s, end_k, p.c.n_kv) : load(v_row, s - sk, end_k - sk, p.c.n_kv); };
+  const int64_t row = i * p.c.n_kv * D;
+  auto load_kv = [&](int s) {
+    if (s < sk) return load(k_row, s, end_k, p.c.n_kv);
+    Octets x;
+    x.u0 = x.u1 = make_uint4(0, 0, 0, 0);
+    const int head = (s - sk) * kRows + sub;
+    if (s < end_k && head < p.c.n_kv) {
+      x.u0 = __ldcs(reinterpret_cast<const uint4*>(v_row + head * D + 16 * li));
+      x.u1 = __ldcs(reinterpret_cast<const uint4*>(v_row + head * D + 16 * li) + 1);
+    }
+    return x;
+  };
   Octets next = load_kv(begin_k);
   Factors f;
   factors_of<Interleaved>(&f, a, p.k_weight);
-  const int at0 = int8_octet(D, slot, e0), at1 = int8_octet(D, slot, e1);
 #pragma unroll 1
   for (int s = begin_k; s < end_k; ++s) {
     Octets x = next;
@@ -353,7 +365,6 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     const bool is_v = s >= sk;
     const int head = (is_v ? s - sk : s) * kRows + sub;
     const bool valid = head < p.c.n_kv;
-    const int64_t row = i * p.c.n_kv * D;
     if (!is_v) {
       turn16<D, Interleaved>(x, f, a, p.k_weight != nullptr, p.eps);
       if (p.k_out && valid) store(p.k_out + row, head, x);
@@ -364,12 +375,12 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     uint8_t* block = base + int64_t(head) * int8_block_bytes(D) + (is_v ? 16 * D : 0);
     uint16_t* out = is_v ? p.v_held : p.k_held;
     if (li == 0) *reinterpret_cast<uint32_t*>(block + int8_pairs(D, slot) + (is_v ? 4 - 16 * D : 0)) = scale.pair;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint4 held;
-      *reinterpret_cast<uint2*>(block + (e ? at1 : at0)) = encode8(e ? x.u1 : x.u0, scale, tau, &held);
-      if (out) __stcs(reinterpret_cast<uint4*>(out + row + head * D + 8 * (e ? e1 : e0)), held);
-    }
+    const int o0 = is_v ? 2 * li : e0, o1 = is_v ? 2 * li + 1 : e1;
+    uint4 held;
+    *reinterpret_cast<uint2*>(block + int8_octet(D, slot, o0)) = encode8(x.u0, scale, tau, &held);
+    if (out) __stcs(reinterpret_cast<uint4*>(out + row + head * D + 8 * o0), held);
+    *reinterpret_cast<uint2*>(block + int8_octet(D, slot, o1)) = encode8(x.u1, scale, tau, &held);
+    if (out) __stcs(reinterpret_cast<uint4*>(out + row + head * D + 8 * o1), held);
   }
 }
 
