@@ -247,8 +247,8 @@ __device__ __forceinline__ uint2 encode8(const uint4& u, const RowScale& r, floa
 // ones ahead of the token's place.
 //
 // Bound by issue and by the bytes that the warps keep in flight (30k tokens appended, 821
-// MB: 144 us, 5.7 TB/s, 84 % of a plain copy's rate, issue 67 %, of which the
-// quantisation costs some 19 us; normed and rotated only, 634 MB: 96 us, 97 %).  Set
+// MB: 144 us, 5.7 TB/s, 84 % of a plain copy's rate, issue 62 %; the
+// quantisation costs some 19 us of it; normed and rotated only, 634 MB: 96 us, 97 %).  Set
 // aside, each measured on the append when it took 149: rows by bulk copies into rings
 // that run ahead over several tokens (176: more instructions a row), k and v rows side
 // by side (151, spilled), q rows and k, v rows in CTAs of their own (157), four or six CTAs
