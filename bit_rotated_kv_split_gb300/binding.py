@@ -652,7 +652,7 @@ def oscar_rope_table(freq, cos_sin, magnitude: float = 1.0, first: int = 0, stre
     _contiguous("cos_sin", cos_sin, shape, 4)
     # (a copy of the few numbers: the array's own address costs more to ask for)
     _on_device("oscar_rope_table", stream, (cos_sin,), lib.oscar_rope_table, (
-        freq.tobytes(), 2 * pairs, magnitude, first, shape[0], cos_sin.data_ptr()))
+        freq.tobytes(), 2 * pairs, float(magnitude), int(first), shape[0], cos_sin.data_ptr()))
 
 
 def norm_desc(q_weight=None, k_weight=None, eps: float = 1e-6) -> HeadNorm:

@@ -41,21 +41,24 @@ __device__ __forceinline__ uint8_t* token_block(const PagedCache& c, int req, in
   return c.pages + int64_t(page) * c.n_kv * int8_block_bytes(D);
 }
 
-// A lane's octets of a row, e0 and e1, and their angles.
+// Lane i's octets of a row, e0 and e1, and their angles.
 template <bool Interleaved>
 struct Angles {
   int e0, e1;
   bool on0, on1;      // they turn (in halves: with one another)
   const float* row;   // of cos_sin, at the first angle of e0
   int half;           // to the sines
-  __device__ __forceinline__ Angles(const RopeParams& r, int64_t at, int i) {
+  __device__ __forceinline__ Angles(const RopeParams& r, int i) {
     const int h = r.rot / 16;               // octets of a half
     on0 = Interleaved ? 2 * i < 2 * h : i < h;
     on1 = Interleaved ? 2 * i + 1 < 2 * h : on0;
     e0 = Interleaved || !on0 ? 2 * i : i;
     e1 = Interleaved || !on0 ? 2 * i + 1 : i + h;
     half = r.rot / 2;
-    row = r.cos_sin + at * r.rot + (Interleaved ? 4 : 8) * e0;
+    row = nullptr;
+  }
+  __device__ __forceinline__ void turn_to(const RopeParams& r, int64_t at) {
+    if (on0) row = r.cos_sin + at * r.rot + (Interleaved ? 4 : 8) * e0;
   }
 };
 
@@ -266,9 +269,8 @@ __global__ void __launch_bounds__(kRowThreads, 5)
   const int64_t i = w / warps_per_token;
   if (i >= p.n) return;
   const int part = int(w - i * warps_per_token), begin = part * slots_per_warp, end = min(slots, begin + slots_per_warp);
-  const int h = p.rope.rot / 16;
-  const bool halves = !Interleaved && li < h;
-  const int e0 = halves ? li : 2 * li, e1 = halves ? li + h : 2 * li + 1;
+  Angles<Interleaved> a(p.rope, li);
+  const int e0 = a.e0, e1 = a.e1;
 
   // The lane's octets of slot s (zeros from slot `to` and past the last head).  Rows are read
   // and written once, so both are marked for early eviction (rotation 101 us without, 98 with).
@@ -305,15 +307,13 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     slot = pos % kPageTokens;
     at = pos;
   }
-  if (p.rope.rot != 0) {
-    if (p.rope_pos) at = p.rope_pos[i];
-    if (!Append && at == -1) return;       // a padding row
-    if (at < 0 || at >= p.rope.n_positions) {
-      if (report) flag(p.c.dev_status, OSCAR_DEV_LENGTH);
-      return;
-    }
+  if (p.rope_pos) at = p.rope_pos[i];
+  if (!Append && at == -1) return;         // a padding row
+  if (p.rope.rot != 0 && (at < 0 || at >= p.rope.n_positions)) {
+    if (report) flag(p.c.dev_status, OSCAR_DEV_LENGTH);
+    return;
   }
-  const Angles<Interleaved> a(p.rope, at, li);
+  a.turn_to(p.rope, at);
 
   auto rows = [&](int from, int to, int heads, const uint16_t* src, uint16_t* dst, const uint16_t* weight, Octets (&next)[kBatch]) {
     Factors f;

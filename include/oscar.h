@@ -771,7 +771,7 @@ oscar_status oscar_rope_frequencies(int32_t rot_dim, double theta, const oscar_r
  *
  *   freq: host [rot_dim / 2], 0 <= freq <= 6 radians (of oscar_rope_frequencies, or any
  *   others; read during the call).  Angles are reduced exactly: an entry is off by
- *   2^-23 of its own size and (first + j) 2^-64 of a turn at the most, at any position.  rot_dim a
+ *   2^-21 of its own size and (first + j) 2^-64 of a turn at the most, at any position.  rot_dim a
  *   multiple of 16, 16 .. 128; 0 <= first, n <= 2^40.  n = 0 is a no-op.  Async.
  */
 oscar_status oscar_rope_table(const double* freq, int32_t rot_dim, double magnitude, int64_t first, int64_t n,
@@ -794,11 +794,11 @@ typedef struct oscar_head_norm {
  *   head_dim bf16) and of k row i is normed (norm NULL, or without that weight: not)
  *   and then rotated by row pos[i] of rope->cos_sin as in oscar_rope_append_int4
  *   (rope NULL: not), to row i of q_out and k_out.  fp32 arithmetic, one rounding to
- *   bf16 at the end.  The mean of the squares is fp32: rows above 2^63 in magnitude
- *   are the caller's to scale.
+ *   bf16 at the end.  The sum of the squares is fp32: heads with channels above 2^60 in
+ *   magnitude are the caller's to scale.
  *   pos: device int32 [n]; may be NULL without a rotation.  pos[i] = -1 marks a padding
- *   row: it is left as it was.  Any other position outside cos_sin skips the item and
- *   sets OSCAR_DEV_LENGTH in *dev_status (device int32, nullable).
+ *   row: it is left as it was.  With a rotation, any other position outside cos_sin skips
+ *   the item and sets OSCAR_DEV_LENGTH in *dev_status (device int32, nullable).
  *   q and q_out may be NULL together, and so may k and k_out.  Rows 16-byte aligned, strides
  *   multiples of 8 elements and at least a row.  q_out may be q where the strides are
  *   equal, and k_out k; no other overlap.  head_dim 64 or 128.  n = 0 is a no-op.  Async.

@@ -211,6 +211,13 @@ def test_norm_rope_skips_and_flags():
     assert int(status.item()) == 0                   # a padding row is no fault
     B.oscar_norm_rope(None, rope, q, k, pos, qo, ko)   # and without the word
     torch.cuda.synchronize()
+    # without a rotation a position says only whether the row is padding
+    qo.fill_(-7.0), ko.fill_(-7.0)
+    w = dev_bf16(np.ones(d))
+    B.oscar_norm_rope(B.norm_desc(w, w), None, q, k, i32([3, -1, 9, 10 ** 9, -2, 0]), qo, ko, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and (qo[1] == -7.0).all() and (ko[1] == -7.0).all()
+    assert not (qo[[0, 2, 3, 4, 5]] == -7.0).any()
 
 
 def test_norm_rope_bad_values_stay_in_their_rows():
