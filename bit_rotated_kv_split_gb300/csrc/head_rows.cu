@@ -24,23 +24,6 @@
 namespace oscar {
 namespace {
 
-// The block of (req, pos), KV head 0, or nullptr (skip) for a padding row, a
-// place outside the table or a page outside the pool.
-template <int D>
-__device__ __forceinline__ uint8_t* token_block(const PagedCache& c, int req, int pos, bool report) {
-  if (req == -1) return nullptr;
-  if (req < 0 || req >= c.batch || pos < 0 || pos / kPageTokens >= c.max_pages) {
-    if (report) flag(c.dev_status, OSCAR_DEV_LENGTH);
-    return nullptr;
-  }
-  const int page = c.page_table[int64_t(req) * c.max_pages + pos / kPageTokens];
-  if (page < 0 || page >= c.n_pages) {
-    if (report) flag(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
-    return nullptr;
-  }
-  return c.pages + int64_t(page) * c.n_kv * int8_block_bytes(D);
-}
-
 // Lane i's octets of a row, e0 and e1, and their angles.
 template <bool Interleaved>
 struct Angles {
@@ -302,7 +285,7 @@ __global__ void __launch_bounds__(kRowThreads, 5)
   int slot = 0;
   if (Append) {
     const int pos = p.dst_pos[i];
-    base = token_block<D>(p.c, p.dst_req[i], pos, report);
+    base = block_of_token(p.c, int8_block_bytes(D), p.dst_req[i], pos, report);
     if (!base) return;
     slot = pos % kPageTokens;
     at = pos;
@@ -418,7 +401,7 @@ __global__ void __launch_bounds__(kRowThreads)
   uint64_t mine = 0;                      // lane t: token t's block and slot (blocks are 128-byte aligned)
   if (lane < count) {
     const int pos = p.src_pos[i0 + lane];
-    const uint8_t* base = token_block<D>(p.c, p.src_req[i0 + lane], pos, part == 0);
+    const uint8_t* base = block_of_token(p.c, int8_block_bytes(D), p.src_req[i0 + lane], pos, part == 0);
     if (base) mine = reinterpret_cast<uint64_t>(base) | uint64_t(pos % kPageTokens);
   }
   const int begin = part * slots_per_warp, end = min(slots, begin + slots_per_warp);

@@ -91,20 +91,8 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& u, float tau, int lan
   return word;
 }
 
-// The block of (req, pos), KV head 0, or nullptr (skip) for a padding row, a
-// place outside the table or a page outside the pool.
 __device__ __forceinline__ uint8_t* token_block(const Int4Cache& c, int req, int pos, bool report) {
-  if (req == -1) return nullptr;
-  if (req < 0 || req >= c.batch || pos < 0 || pos / kPageTokens >= c.max_pages) {
-    if (report) flag(c.dev_status, OSCAR_DEV_LENGTH);
-    return nullptr;
-  }
-  const int page = c.page_table[int64_t(req) * c.max_pages + pos / kPageTokens];
-  if (page < 0 || page >= c.n_pages) {
-    if (report) flag(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
-    return nullptr;
-  }
-  return c.pages + int64_t(page) * c.n_kv * int4_block_bytes(c.d, c.ng_k, c.ng_v);
+  return block_of_token(c, int4_block_bytes(c.d, c.ng_k, c.ng_v), req, pos, report);
 }
 
 // What a lane needs to turn an octet: octet o of a half-split head turns with

@@ -41,6 +41,7 @@
 
 #include <algorithm>
 
+#include "decode_math.cuh"
 #include "int8.h"
 #include "kernels.h"
 #include "oscar.h"
@@ -86,13 +87,6 @@ __device__ __forceinline__ int place_of(const Segment& s, int warp) {
 // that begins in it: (m, l) and the sums.
 constexpr size_t kOffMl = 4096, kOffO = kOffMl + size_t(kCtas) * 2 * kHeads * 8;
 
-// D += A (16x16 f16, row) * B (16x8 f16, col); free for the compiler to move.
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&d)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
@@ -121,26 +115,6 @@ __device__ __forceinline__ uint32_t minus_1152(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t even_signed(uint32_t w) { return minus_1152((w & kLow) | 0x64006400u); }
 __device__ __forceinline__ uint32_t odd_signed(uint32_t w) { return minus_1152(prmt(w, 0x64646464u, 0x4341)); }
-
-__device__ __forceinline__ float max_over_quad(float v) {   // over the 4 lanes of a row
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-}
-__device__ __forceinline__ float sum_over_quad(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  return v + __shfl_xor_sync(0xffffffffu, v, 2);
-}
-__device__ __forceinline__ float max_over_rows(float v) {   // over the 8 lanes of a column pair
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-}
-__device__ __forceinline__ float sum_over_rows(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 4);
-  v += __shfl_xor_sync(0xffffffffu, v, 8);
-  return v + __shfl_xor_sync(0xffffffffu, v, 16);
-}
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
 // The logarithm of the sum, from the reference in log2 units and the sum of 2^(7 + x - m).
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.f ? (m + (log2f(l) - 7.f)) * kLn2 : l == 0.f ? -INFINITY : l; }
@@ -176,11 +150,6 @@ __device__ __forceinline__ void join_warps(const Int8DecodeParams& p, int hq0, i
       if (i % (D / 4) == 0) reinterpret_cast<float2*>(ws + kOffMl)[slot * kHeads + h] = make_float2(mx, sum);
     }
   }
-}
-
-// 2^ve with ve in [-14, 16] is at least a scale of this size (fp16 bits) and any smaller one
-__device__ __forceinline__ int scale_exponent(uint32_t bits) {
-  return min(max(((__float_as_int(half2_to_float2(bits).x) >> 23) & 255) - 126, -14), 16);
 }
 
 // A run in more than one share: its place in the row, pages, request, first

@@ -7,6 +7,8 @@
 
 #include <algorithm>
 
+#include "int4.h"
+#include "oscar.h"
 #include "ptx.cuh"
 #include "score.cuh"
 
@@ -61,6 +63,23 @@ __device__ __forceinline__ float sub_odd(float a, float b) {
 
 __device__ __forceinline__ void flag(int32_t* dev_status, int bit) {
   if (dev_status) atomicOr(dev_status, bit);
+}
+
+// The block of (req, pos), KV head 0, or nullptr (skip) for a padding row, a
+// place outside the table or a page outside the pool.
+__device__ __forceinline__ uint8_t* block_of_token(const PagedCache& c, int block_bytes, int req, int pos,
+                                                   bool report) {
+  if (req == -1) return nullptr;
+  if (req < 0 || req >= c.batch || pos < 0 || pos / kPageTokens >= c.max_pages) {
+    if (report) flag(c.dev_status, OSCAR_DEV_LENGTH);
+    return nullptr;
+  }
+  const int page = c.page_table[int64_t(req) * c.max_pages + pos / kPageTokens];
+  if (page < 0 || page >= c.n_pages) {
+    if (report) flag(c.dev_status, OSCAR_DEV_PAGE_BOUNDS);
+    return nullptr;
+  }
+  return c.pages + int64_t(page) * c.n_kv * block_bytes;
 }
 
 __device__ __forceinline__ void load8(float (&x)[8], const float* p, int n) {
