@@ -181,6 +181,7 @@ extern "C" oscar_status oscar_gather_int8(const oscar_int8_desc* desc, const int
     return OSCAR_ERR_INVALID_ARG;
   if (!aligned(src_req, 4) || !aligned(src_pos, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
     return OSCAR_ERR_ALIGNMENT;
+  if (k_out == v_out) return OSCAR_ERR_INVALID_ARG;   // each row would be written twice
   p.src_req = src_req;
   p.src_pos = src_pos;
   p.n = n;

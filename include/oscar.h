@@ -889,8 +889,8 @@ oscar_status oscar_rope_append_int8(const oscar_int8_desc* desc, const oscar_hea
  *   src_pos[i] of request src_req[i], to row i of k_out and v_out (k_out + i * k_stride,
  *   H_kv heads of d).  src_req[i] = -1 and the skips are those of
  *   oscar_rope_append_int8: a skipped row is left as it was.  src_req, src_pos: device
- *   int32 [n].  Rows 16-byte aligned, strides multiples of 8.  seq_len is not read.  n = 0 is
- *   a no-op.  Async.
+ *   int32 [n].  Rows 16-byte aligned, strides multiples of 8; no row of k_out may overlap one
+ *   of v_out.  seq_len is not read.  n = 0 is a no-op.  Async.
  */
 oscar_status oscar_gather_int8(const oscar_int8_desc* desc, const int32_t* src_req, const int32_t* src_pos, int32_t n,
                                uint16_t* k_out, int64_t k_stride, uint16_t* v_out, int64_t v_stride, void* stream);

@@ -242,6 +242,12 @@ def test_gather_refusals(built_lib, over, status):
     assert _gather(B, _desc(), **over) == status
 
 
+def test_gather_refuses_one_place_for_keys_and_values(built_lib):
+    from bit_rotated_kv_split_gb300 import binding as B
+    assert _gather(B, _desc(), k=FAKE * 2, v=FAKE * 2) == 1
+    assert _gather(B, _desc(), k=FAKE * 2, v=FAKE * 2, n=0) == 0
+
+
 @pytest.mark.parametrize("over,status", [
     (dict(q=None), 1), (dict(out=None), 1), (dict(qs=1000), 1), (dict(q=FAKE + 8), 2), (dict(out=FAKE + 8), 2),
     (dict(lse=FAKE + 2), 2), (dict(ws=FAKE + 128), 2), (dict(size=0), 3),
