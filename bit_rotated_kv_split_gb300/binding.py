@@ -431,15 +431,25 @@ def prompt_desc(batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_
     return d
 
 
-_torch = _bf16 = _i32 = None
+_torch = _bf16 = _i32 = _raw_stream = _current_device = None
+
+
+def _load_torch():
+    """What the calls on tensors take from torch, all of it at once: at the first of them, whichever it is."""
+    global _torch, _bf16, _i32, _raw_stream, _current_device
+    import torch
+    _bf16, _i32 = torch.bfloat16, torch.int32
+    # the current stream's handle without a Stream object around it (3 us a call less)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _torch = torch
 
 
 def _half(t):
     """bfloat16 or raw 16-bit integers: fp16 rows have the size of bf16's and would be read as such."""
-    global _torch, _bf16, _i32
     if _torch is None:
-        import torch
-        _torch, _bf16, _i32 = torch, torch.bfloat16, torch.int32
+        _load_torch()
     return t.dtype is _torch.bfloat16 or (t.element_size() == 2 and not t.is_floating_point())
 
 
@@ -496,22 +506,13 @@ def _places(name, t, n):
             _index(name, t, n)
 
 
-_raw_stream = _current_device = None
-
-
 def _on_device(name, stream, tensors, fn, args, descs=()):
     """Calls the library with the tensors' device current and, without a stream, on that device's current stream.
 
     descs: descriptors (or None) whose tensors' device is known.
     """
-    global _torch, _raw_stream, _current_device
-    if _raw_stream is None:
-        import torch
-        _torch = torch
-        # the current stream's handle without a Stream object around it (3 us a call less)
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda index: torch.cuda.current_stream(index).cuda_stream)
-        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if _torch is None:
+        _load_torch()
     index = tensors[0].get_device()
     if index < 0:
         raise ValueError("%s: every tensor must be on one CUDA device" % name)

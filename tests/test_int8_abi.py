@@ -2,6 +2,7 @@
 sizes, frequencies, refusals before any launch, the binding's own checks and the
 oracle's packing (no GPU needed)."""
 import ctypes
+import os
 
 import numpy as np
 import pytest
@@ -317,3 +318,16 @@ def test_oracle_table_agrees_with_plain_doubles():
     t = O.rope_table(freq, 5, 20)
     a = np.arange(5, 25)[:, None] * freq
     np.testing.assert_allclose(t, np.concatenate([np.cos(a), np.sin(a)], 1), atol=1e-14)
+
+
+@pytest.mark.parametrize("first", ["B.oscar_rope_table(np.zeros(16), torch.zeros(4, 32))",
+                                   "B.oscar_gather_int8(B.Int8Desc(), None, None, torch.zeros(0, 0, 0), torch.zeros(0, 0, 0))"])
+def test_the_first_call_of_a_process_leaves_the_fast_checks_on(built_lib, first):
+    """Whatever the process calls first, the short checks of later calls know their types."""
+    import subprocess
+    import sys
+    code = "\n".join(["import numpy as np, torch", "from bit_rotated_kv_split_gb300 import binding as B", "try:", "    " + first,
+                      "except ValueError:", "    pass", "assert B._bf16 is torch.bfloat16 and B._i32 is torch.int32"])
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
