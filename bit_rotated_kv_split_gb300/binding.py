@@ -651,9 +651,12 @@ def oscar_rope_table(freq, cos_sin, magnitude: float = 1.0, first: int = 0, stre
     if len(shape) != 2 or shape[1] != 2 * pairs:
         raise ValueError("freq must be [rot_dim / 2] and cos_sin [n][rot_dim]")
     _contiguous("cos_sin", cos_sin, shape, 4)
+    first = int(first)
+    if not -2 ** 63 <= first < 2 ** 63:
+        raise ValueError("first: %d is no 64-bit integer" % first)
     # (a copy of the few numbers: the array's own address costs more to ask for)
     _on_device("oscar_rope_table", stream, (cos_sin,), lib.oscar_rope_table, (
-        freq.tobytes(), 2 * pairs, float(magnitude), int(first), shape[0], cos_sin.data_ptr()))
+        freq.tobytes(), 2 * pairs, float(magnitude), first, shape[0], cos_sin.data_ptr()))
 
 
 def norm_desc(q_weight=None, k_weight=None, eps: float = 1e-6) -> HeadNorm:

@@ -331,3 +331,12 @@ def test_the_first_call_of_a_process_leaves_the_fast_checks_on(built_lib, first)
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("first", [2 ** 64, 2 ** 63, -2 ** 63 - 1, 2 ** 64 + 5])
+def test_table_refuses_positions_beyond_64_bits(built_lib, first):
+    """ctypes would take them modulo 2^64, as other positions."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    with pytest.raises(ValueError, match="first"):
+        B.oscar_rope_table(np.zeros(16), torch.zeros(4, 32), first=first)
