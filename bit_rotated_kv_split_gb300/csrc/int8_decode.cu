@@ -21,7 +21,7 @@
 //   S = K q:     A = the K codes: ldmatrix gives a lane 4 channels' bytes of a token, two
 //                operand registers of one operation each: a byte c alone in an fp16 is
 //                the subnormal c 2^-24, exactly.  q is scaled by a power of two per head
-//                to just below fp16's end, exact for bf16.
+//                to just below fp16's end, exact for bf16 (the largest finite ones too).
 //                x = scale (sum c q) + zero (sum q).
 //   O += V^T P:  A = the V codes less 128, by ldmatrix with transposition; B = P scale_V.
 //                (Without the subtraction, one operation more per operand, the sums
@@ -393,6 +393,8 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
     const int n_it = max(0, (cur.hi - lo + P * kWarps - 1) / (P * kWarps));
 
     // Query operands, scaled by 2^(141 - ex) so that a head's largest channel is in [2^14, 2^15).
+    // The dot products are kept times 2^11 (in qs and at each key's scale): what takes them
+    // back, 2^(ex - 128), is then within fp32 for every finite query.
     uint32_t qb[R][C][2];
     float qs[R][2], unscale[R][2], slope[R][2];   // of columns 2 tig, 2 tig + 1
 #pragma unroll
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
         top = fmaxf(top, fmaxf(fabsf(bf16_lo(uq[r][i].y)), fabsf(bf16_hi(uq[r][i].y))));
       }
       top = max_over_quad(top);
-      const int ex = min(max((__float_as_int(top) >> 23) & 255, 14), 243);
+      const int ex = min(max((__float_as_int(top) >> 23) & 255, 14), 254);
       const float up = pow2i(141 - ex);
 #pragma unroll
       for (int i = 0; i < C; ++i) {
@@ -414,14 +416,15 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
         qb[r][i][0] = pack_half2(q0, q2);
         qb[r][i][1] = pack_half2(q1, q3);
       }
-      sum = sum_over_quad(sum) * 5.9604644775390625e-8f;     // 2^-24, as the codes carry
-      const float un = pow2i(ex - 117);                      // 2^24 / up
+      sum = sum_over_quad(sum) * 1.220703125e-4f;            // 2^-13: 2^-24, as the codes carry, times 2^11
+      const float un = pow2i(ex - 128);                      // 2^13 / up
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int col = 2 * tig + e, h = G == 4 ? col & 3 : col + 8 * r;
         qs[r][e] = __shfl_sync(0xffffffffu, sum, 4 * col);
         unscale[r][e] = __shfl_sync(0xffffffffu, un, 4 * col);
-        if (p.s.cap_log2 == 0.f) unscale[r][e] *= p.s.scale_log2;   // (with a cap, capped() takes the scale)
+        if (p.s.cap_log2 == 0.f)            // (with a cap, capped() takes the scale)
+          unscale[r][e] = fminf(unscale[r][e] * p.s.scale_log2, FLT_MAX);
         slope[r][e] = Formed && p.s.slopes && h < group ? p.s.slopes[hq0 + h] * kLog2e : 0.f;
       }
     }
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              y[r][2 * g + t][e] = fmaf(k.x, acc[r][0][2 * t + e] + acc[r][1][2 * t + e], k.y * qs[r][e]);
+              y[r][2 * g + t][e] = fmaf(2048.f * k.x, acc[r][0][2 * t + e] + acc[r][1][2 * t + e], k.y * qs[r][e]);
         }
       }
       if (Formed) {

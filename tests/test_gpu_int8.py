@@ -603,6 +603,38 @@ def test_decode_extreme_sizes(scale_q, scale_v):
             assert abs(host(lse)[b, h] - want_lse[0]) <= 2.0 ** -13 + err + 2.0 ** -22 * abs(want_lse[0])
 
 
+@pytest.mark.parametrize("hq,d,form", [(4, 128, {}), (8, 64, {}), (16, 128, {}), (4, 64, dict(softcap=3.0)), (6, 128, dict(slopes=True))])
+@pytest.mark.parametrize("power", [110, 118, 120])
+def test_decode_queries_up_to_the_types_end(hq, d, form, power):
+    """Queries of 2^112 to 2^122 whose scale makes ordinary scores of them."""
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(15, [700, 48, 1], hq, 1, d)
+    q = O.bf16(L.g.standard_normal((3, hq, d)) * 2.0 ** power)
+    scale = float(np.float32(2.0 ** -power / np.sqrt(d)))
+    form = dict(form, scale=scale)
+    if form.get("slopes"):
+        form["slopes"] = 2.0 ** -np.arange(1.0, hq + 1)
+    out, lse = decode(L, q, B.score_desc(scale, form.get("softcap", 0.0), 0, dev_f32(form["slopes"]) if "slopes" in form else None))
+    assert L.status() == 0
+    check_decode(L, q, out, lse, **form)
+
+
+@pytest.mark.parametrize("hq,softcap", [(4, 0.0), (16, 0.0), (8, 30.0)])
+def test_decode_largest_queries_on_keys_of_zeros(hq, softcap):
+    """The largest finite channels of either sign: every score is 0, and the result the mean."""
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(16, [333, 5], hq, 1, 128, fill=False)
+    for b, n in enumerate(L.lens):
+        L.k.append(L.put(b, np.arange(n), 0, np.zeros((n, 1, 128))))
+        L.v.append(L.put(b, np.arange(n), 1, O.bf16(L.g.standard_normal((n, 1, 128)))))
+    L.upload()
+    end = 255.0 * 2.0 ** 120
+    q = np.where(L.g.random((2, hq, 128)) < 0.5, end, -end)
+    q[:, 1, 3:] = 2.0 ** -100
+    out, lse = decode(L, q, B.score_desc(0.0, softcap))
+    check_decode(L, q, out, lse, softcap=softcap)
+
+
 @pytest.mark.parametrize("ratio", [2.0 ** -14, 2.0 ** -20])
 def test_decode_values_far_below_anothers_keep_their_bits(ratio):
     """A token of large values and no weight beside small ones that have all of it."""
