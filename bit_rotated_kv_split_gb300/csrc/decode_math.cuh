@@ -1,9 +1,14 @@
-// Device helpers of the decodes over paged layers: their products, reductions
-// over a product's rows and columns, and the exponent of a scale.
+// Helpers of the decodes over paged layers: their products, reductions over a
+// product's rows and columns, the exponent of a scale, and what takes a dot product
+// of scaled queries back.
 #pragma once
 
+#include <cfloat>
 #include <cstdint>
 
+#include <algorithm>
+
+#include "int4.h"
 #include "ptx.cuh"
 
 namespace oscar {
@@ -38,6 +43,24 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 // 2^ve with ve in [-14, 16] is at least a scale of this size (fp16 bits) and any smaller one
 __device__ __forceinline__ int scale_exponent(uint32_t bits) {
   return min(max(((__float_as_int(half2_to_float2(bits).x) >> 23) & 255) - 126, -14), 16);
+}
+
+// A query head with a largest channel in [2^(ex - 127), 2^(ex - 126)), 14 <= ex <= 254 (every
+// finite bf16), is held times 2^(141 - ex) beside codes times 2^-24, so its dot products are
+// to be multiplied by 2^(ex - 117), which may pass fp32's end.  With a cap they are taken
+// to 2^-11 of themselves, and capped() has constants to match (in_units).  Without one the
+// score's scale is in the factor too, and where that passes fp32's end only a dot product
+// of 0 gives a score within bounds: it is to stay 0.
+constexpr float kUnits = 2048.f;
+__device__ __forceinline__ float unscale_of(int ex, const ScoreParams& s) {
+  const float f = pow2i(ex - 128);
+  return s.cap_log2 != 0.f ? f : fminf(f * s.scale_log2 * kUnits, FLT_MAX);
+}
+inline ScoreParams in_units(ScoreParams s) {
+  const auto times = [](float x) { return std::min(std::max(x * kUnits, -FLT_MAX), FLT_MAX); };
+  s.cap_in = times(s.cap_in);
+  for (float& c : s.cap_near) c = times(c);
+  return s;
 }
 
 }  // namespace oscar

@@ -393,8 +393,6 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
     const int n_it = max(0, (cur.hi - lo + P * kWarps - 1) / (P * kWarps));
 
     // Query operands, scaled by 2^(141 - ex) so that a head's largest channel is in [2^14, 2^15).
-    // The dot products are kept times 2^11 (in qs and at each key's scale): what takes them
-    // back, 2^(ex - 128), is then within fp32 for every finite query.
     uint32_t qb[R][C][2];
     float qs[R][2], unscale[R][2], slope[R][2];   // of columns 2 tig, 2 tig + 1
 #pragma unroll
@@ -416,15 +414,12 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
         qb[r][i][0] = pack_half2(q0, q2);
         qb[r][i][1] = pack_half2(q1, q3);
       }
-      sum = sum_over_quad(sum) * 1.220703125e-4f;            // 2^-13: 2^-24, as the codes carry, times 2^11
-      const float un = pow2i(ex - 128);                      // 2^13 / up
+      sum = sum_over_quad(sum) * 5.9604644775390625e-8f;     // 2^-24, as the codes carry
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int col = 2 * tig + e, h = G == 4 ? col & 3 : col + 8 * r;
         qs[r][e] = __shfl_sync(0xffffffffu, sum, 4 * col);
-        unscale[r][e] = __shfl_sync(0xffffffffu, un, 4 * col);
-        if (p.s.cap_log2 == 0.f)            // (with a cap, capped() takes the scale)
-          unscale[r][e] = fminf(unscale[r][e] * p.s.scale_log2, FLT_MAX);
+        unscale[r][e] = unscale_of(__shfl_sync(0xffffffffu, ex, 4 * col), p.s);
         slope[r][e] = Formed && p.s.slopes && h < group ? p.s.slopes[hq0 + h] * kLog2e : 0.f;
       }
     }
@@ -503,7 +498,7 @@ __global__ void __launch_bounds__(32 * warps_of(G), kPerSm) decode_int8_kernel(c
           for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              y[r][2 * g + t][e] = fmaf(2048.f * k.x, acc[r][0][2 * t + e] + acc[r][1][2 * t + e], k.y * qs[r][e]);
+              y[r][2 * g + t][e] = fmaf(k.x, acc[r][0][2 * t + e] + acc[r][1][2 * t + e], k.y * qs[r][e]);
         }
       }
       if (Formed) {
@@ -743,7 +738,9 @@ cudaError_t launch_g(const Int8DecodeParams& p, cudaStream_t stream) {
 size_t int8_decode_workspace_bytes(const PagedCache& c) { return kOffO + size_t(kCtas) * 2 * kHeads * c.d * 4; }
 
 cudaError_t launch_decode_int8(const Int8DecodeParams& p, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_g<128>(p, stream) : launch_g<64>(p, stream);
+  Int8DecodeParams u = p;
+  u.s = in_units(p.s);
+  return p.c.d == 128 ? launch_g<128>(u, stream) : launch_g<64>(u, stream);
 }
 
 }  // namespace oscar
