@@ -240,7 +240,7 @@ __device__ __noinline__ void scan_wide(const Int4DecodeParams& p, Walk walk, int
 #pragma unroll
         for (int h = 0; h < kJoinHeads; ++h) {
           float y = x[h] + __shfl_xor_sync(0xffffffffu, x[h], 16);
-          y = p.s.cap_log2 != 0.f ? capped(y, p.s) : y * p.s.scale_log2;
+          y = p.s.cap_log2 != 0.f ? capped(y * (1.f / kUnits), p.s) : y * p.s.scale_log2;
           y = j >= cur.first && j < cur.len ? fmaf(slope[h], float(j - (cur.len - 1)), y) : -INFINITY;
           float mn = fmaxf(m[h], y);
 #pragma unroll
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(q[w][i]));
       }
       top = max_over_quad(top);
-      const int ex = min(max((__float_as_int(top) >> 23) & 255, 14), 243);
+      const int ex = min(max((__float_as_int(top) >> 23) & 255, 14), 254);
       const float up = pow2i(141 - ex);
       float sum[NGK];
 #pragma unroll
@@ -516,7 +516,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         qb[2 * w + 1][0] = pack_half2(q[w][2], q[w][6]);
         qb[2 * w + 1][1] = pack_half2(q[w][3] * 0.0625f, q[w][7] * 0.0625f);
       }
-      const float un = pow2i(ex - 117);     // 2^24 / up
 #pragma unroll
       for (int g = 0; g < NGK; ++g) {
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
@@ -528,8 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int from_lane = 4 * (2 * tig + e);
 #pragma unroll
         for (int g = 0; g < NGK; ++g) qs[g][e] = __shfl_sync(0xffffffffu, sum[g], from_lane);
-        unscale[e] = __shfl_sync(0xffffffffu, un, from_lane);
-        if (p.s.cap_log2 == 0.f) unscale[e] *= p.s.scale_log2;   // (with a cap, capped() takes the scale)
+        unscale[e] = unscale_of(__shfl_sync(0xffffffffu, ex, from_lane), p.s);
         slope[e] = Formed && p.s.slopes && 2 * tig + e < heads ? p.s.slopes[hq0 + 2 * tig + e] * kLog2e : 0.f;
       }
     }
@@ -842,7 +840,9 @@ cudaError_t launch_k(const Int4DecodeParams& p, cudaStream_t stream) {
 size_t int4_decode_workspace_bytes(const Int4Cache& c) { return kOffO + size_t(kCtas) * 2 * kHeads * c.d * 4; }
 
 cudaError_t launch_decode_int4(const Int4DecodeParams& p, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_k<128>(p, stream) : launch_k<64>(p, stream);
+  Int4DecodeParams u = p;
+  u.s = in_units(p.s);
+  return p.c.d == 128 ? launch_k<128>(u, stream) : launch_k<64>(u, stream);
 }
 
 }  // namespace oscar

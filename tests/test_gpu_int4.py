@@ -751,6 +751,42 @@ def test_decode_queries_of_all_sizes_with_keys_apart(lens):
                 np.testing.assert_allclose(out[b, h], L.v[b][(h + 1) * n // 5, 0], rtol=2.0 ** -8 + 2.0 ** -10, atol=2.0 ** -9)
 
 
+@pytest.mark.parametrize("d,hq,gk,gv,mods", [(128, 4, 128, 128, {}), (64, 12, 32, 64, {}), (128, 8, 64, 32, dict(softcap=3.0)),
+                                             (64, 3, 64, 64, dict(slopes=True))])
+@pytest.mark.parametrize("power", [110, 118, 120])
+def test_decode_queries_up_to_the_types_end(d, hq, gk, gv, mods, power):
+    """Queries of 2^112 to 2^122 whose scale makes ordinary scores of them."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(97, [700, 48, 1], hq, 1, d, gk, gv)
+    q = O.bf16(L.g.standard_normal((3, hq, d)) * 2.0 ** power)
+    mods, sl = dict(mods, scale=float(np.float32(2.0 ** -power / np.sqrt(d)))), None
+    if mods.get("slopes"):
+        mods["slopes"] = 2.0 ** -np.arange(1.0, hq + 1)
+        sl = torch.from_numpy(mods["slopes"].astype(np.float32)).cuda()
+    out = host(run_decode(L, dev_bf16(q), B.score_desc(mods["scale"], mods.get("softcap", 0.0), 0, sl)))
+    assert L.status() == 0
+    ref, bound = weighted_ref(L, q, **mods)
+    assert (np.abs(out - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("hq,softcap", [(4, 0.0), (16, 30.0)])
+def test_decode_largest_queries_on_keys_of_zeros(hq, softcap):
+    """The largest finite channels of either sign: every score is 0, and the result the mean."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(98, [333, 5], hq, 1, 128, 32, 128, fill=False)
+    for b, n in enumerate(L.lens):
+        L.k.append(L.put(b, np.arange(n), 0, np.zeros((n, 1, 128))))
+        L.v.append(L.put(b, np.arange(n), 1, O.bf16(L.g.standard_normal((n, 1, 128)))))
+    L.cache.pages.copy_(torch.from_numpy(L.pool.reshape(-1)))
+    end = 255.0 * 2.0 ** 120
+    q = np.where(L.g.random((2, hq, 128)) < 0.5, end, -end)
+    out = host(run_decode(L, dev_bf16(q), B.score_desc(0.0, softcap)))
+    ref, bound = weighted_ref(L, q, softcap=softcap)
+    assert (np.abs(out - ref) <= bound).all()
+
+
 @pytest.mark.parametrize("lens,hq,hk,d,gk,gv,mods", RAGGED + DECODES)
 def test_decode_within_the_weighted_bound(lens, hq, hk, d, gk, gv, mods):
     """The batches above with each key's error counted with its weight, which for long requests is a small part of what the
