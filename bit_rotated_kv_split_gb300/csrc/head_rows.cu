@@ -91,26 +91,55 @@ struct Octets {
   uint4 u0, u1;
 };
 
+// The mean of a row's squares, and eps; whole warps call it.
+template <int D>
+__device__ __forceinline__ float mean_square(const Octets& x, float eps) {
+  const uint32_t u[4] = {x.u0.x, x.u0.y, x.u0.z, x.u0.w}, v[4] = {x.u1.x, x.u1.y, x.u1.z, x.u1.w};
+  float2 sum = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = bf16_pair(u[i]), q = bf16_pair(v[i]);
+    sum = fma2(p, p, sum);
+    sum1 = fma2(q, q, sum1);
+  }
+  sum = add2(sum, sum1);
+  float all = sum.x + sum.y;
+#pragma unroll
+  for (int m = 1; m < D / 16; m <<= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
+  return fmaf(all, 1.f / D, eps);
+}
+
+// Below this a mean may have lost squares below fp32's end (which takes an eps as small).
+constexpr float kSmallMean = 0x1p-90f;
+
+// Multiplies the octets of the rows with such a mean by 2^80, exactly; the rows' means then.
+// Zeros without an eps are to stay zeros.  Whole warps call it.
+template <int D>
+__device__ __forceinline__ float raise(Octets& x, float mean, float eps) {
+  const float up = mean < kSmallMean ? 0x1p80f : 1.f;
+  auto times = [&](uint32_t& w) {
+    const float2 p = bf16_pair(w);
+    w = pack_bf162(p.x * up, p.y * up);
+  };
+  times(x.u0.x), times(x.u0.y), times(x.u0.z), times(x.u0.w);
+  times(x.u1.x), times(x.u1.y), times(x.u1.z), times(x.u1.w);
+  mean = mean_square<D>(x, eps * up * up);
+  return mean == 0.f ? INFINITY : mean;
+}
+
 // Norms (where `norm`) and rotates the octets held in x; whole warps call it.
 // fp32 throughout: the sum of squares in a fixed order, one rounding to bf16.
-template <int D, bool Interleaved>
+// Small: eps is below kSmallMean.  (For every eps in one kernel, the test and the second
+// sum of squares cost the append 1 to 3 % and the rotation 4.)
+template <int D, bool Interleaved, bool Small>
 __device__ __forceinline__ void turn16(Octets& x, const Factors& f, const Angles<Interleaved>& a, bool norm, float eps) {
-  const uint32_t u[4] = {x.u0.x, x.u0.y, x.u0.z, x.u0.w}, v[4] = {x.u1.x, x.u1.y, x.u1.z, x.u1.w};
   float r = 1.f;
   if (norm) {
-    float2 sum = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 p = bf16_pair(u[i]), q = bf16_pair(v[i]);
-      sum = fma2(p, p, sum);
-      sum1 = fma2(q, q, sum1);
-    }
-    sum = add2(sum, sum1);
-    float all = sum.x + sum.y;
-#pragma unroll
-    for (int m = 1; m < D / 16; m <<= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
-    r = rsqrtf(fmaf(all, 1.f / D, eps));
+    float mean = mean_square<D>(x, eps);
+    if (Small && __any_sync(0xffffffffu, mean < kSmallMean)) mean = raise<D>(x, mean, eps);
+    r = rsqrtf(mean);
   }
+  const uint32_t u[4] = {x.u0.x, x.u0.y, x.u0.z, x.u0.w}, v[4] = {x.u1.x, x.u1.y, x.u1.z, x.u1.w};
   uint32_t out0[4], out1[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -239,7 +268,7 @@ __device__ __forceinline__ uint2 encode8(const uint4& u, const RowScale& r, floa
 // that run ahead over several tokens (176: more instructions a row), k and v rows side
 // by side (151, spilled), q rows and k, v rows in CTAs of their own (157), four or six CTAs
 // an SM (153, 150), a value's two octets' codes in one store (145).
-template <int D, bool Interleaved, bool Append>
+template <int D, bool Interleaved, bool Append, bool Small>
 __global__ void __launch_bounds__(kRowThreads, 5)
     head_rows_kernel(const __grid_constant__ HeadRowsParams p, int slots_per_warp) {
   pdl_wait();
@@ -309,7 +338,7 @@ __global__ void __launch_bounds__(kRowThreads, 5)
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         if (s0 + u >= to) break;
-        turn16<D, Interleaved>(x[u], f, a, weight != nullptr, p.eps);
+        turn16<D, Interleaved, Small>(x[u], f, a, weight != nullptr, p.eps);
         const int head = (s0 + u) * kRows + sub;
         if (head < heads) store(dst, head, x[u]);
       }
@@ -349,7 +378,7 @@ __global__ void __launch_bounds__(kRowThreads, 5)
     const int head = (is_v ? s - sk : s) * kRows + sub;
     const bool valid = head < p.c.n_kv;
     if (!is_v) {
-      turn16<D, Interleaved>(x, f, a, p.k_weight != nullptr, p.eps);
+      turn16<D, Interleaved, Small>(x, f, a, p.k_weight != nullptr, p.eps);
       if (p.k_out && valid) store(p.k_out + row, head, x);
     }
     const float tau = is_v ? p.tau_v : p.tau_k;
@@ -450,9 +479,13 @@ cudaError_t launch_head_rows(const HeadRowsParams& p, cudaStream_t stream) {
   unsigned blocks = 0;
   const cudaError_t e = grid_of(int64_t(p.n) * ((slots + slots_per_warp - 1) / slots_per_warp), &blocks);
   if (e != cudaSuccess) return e;
-  auto* kernel = p.c.d == 128 ? (p.rope.interleaved ? head_rows_kernel<128, true, Append> : head_rows_kernel<128, false, Append>)
-                              : (p.rope.interleaved ? head_rows_kernel<64, true, Append> : head_rows_kernel<64, false, Append>);
-  return launch_pdl(kernel, dim3(blocks), dim3(kRowThreads), 0, stream, p, slots_per_warp);
+  auto launch = [&](auto* kernel) { return launch_pdl(kernel, dim3(blocks), dim3(kRowThreads), 0, stream, p, slots_per_warp); };
+  const bool wide = p.c.d == 128, inter = p.rope.interleaved;
+  if ((p.q_weight || p.k_weight) && p.eps < kSmallMean)
+    return launch(wide ? (inter ? head_rows_kernel<128, true, Append, true> : head_rows_kernel<128, false, Append, true>)
+                       : (inter ? head_rows_kernel<64, true, Append, true> : head_rows_kernel<64, false, Append, true>));
+  return launch(wide ? (inter ? head_rows_kernel<128, true, Append, false> : head_rows_kernel<128, false, Append, false>)
+                     : (inter ? head_rows_kernel<64, true, Append, false> : head_rows_kernel<64, false, Append, false>));
 }
 
 }  // namespace

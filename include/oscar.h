@@ -795,7 +795,8 @@ typedef struct oscar_head_norm {
  *   and then rotated by row pos[i] of rope->cos_sin as in oscar_rope_append_int4
  *   (rope NULL: not), to row i of q_out and k_out.  fp32 arithmetic, one rounding to
  *   bf16 at the end.  The sum of the squares is fp32: heads with channels above 2^60 in
- *   magnitude are the caller's to scale.
+ *   magnitude are the caller's to scale.  Small ones are normed whatever the eps, and a head
+ *   of zeros stays zeros, without an eps too.
  *   pos: device int32 [n]; may be NULL without a rotation.  pos[i] = -1 marks a padding
  *   row: it is left as it was.  With a rotation, any other position outside cos_sin skips
  *   the item and sets OSCAR_DEV_LENGTH in *dev_status (device int32, nullable).

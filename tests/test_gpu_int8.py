@@ -244,6 +244,46 @@ def test_norm_rope_bad_values_stay_in_their_rows():
     assert bad[2, 1].isnan().all() and not bad[2, [0, 2, 3]].isnan().any() and not bad[0].isnan().any()
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-38, 1e-30, 1e-20])
+def test_norm_of_the_smallest_rows(eps, inter):
+    """Rows of every size down to bf16's least number, whose squares are below fp32: normed as larger ones are; rows of zeros
+    stay zeros, with no eps either."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    d, hq, hk = 128, 5, 2
+    g = np.random.default_rng(6)
+    sizes = [-133, -132, -128, -126, -120, -100, -80, -75, -70, -64, -60, -50, -46, -45, -44, -43, -40, -30, 0]
+    n = len(sizes) + 1
+    q, k = (O.bf16(g.standard_normal((n, h, d))) for h in (hq, hk))
+    for x in (q, k):
+        for i, e in enumerate(sizes):
+            y = x[i] * 2.0 ** e                      # (below 2^-126 bf16 keeps multiples of 2^-133)
+            x[i] = np.where(np.abs(y) < 2.0 ** -126, np.rint(y * 2.0 ** 133) * 2.0 ** -133, y)
+        x[-1] = 0.0
+        x[3, 0] = 0.0
+        x[3, 0, 77] = 2.0 ** -133                    # one channel alone, the least there is
+        x[4, 1] = 2.0 ** -80                         # a constant row
+    eps = float(np.float32(eps))
+    wq, wk = (O.bf16(1 + 0.3 * g.standard_normal(d)) for _ in range(2))
+    norm = B.norm_desc(dev_bf16(wq), dev_bf16(wk), eps)
+    cs = angles(50, 64)
+    pos = g.integers(0, 50, n)
+    tq, tk = dev_bf16(q), dev_bf16(k)
+    assert (host(tq) == q).all() and (host(tk) == k).all()
+    qo, ko = torch.empty_like(tq), torch.empty_like(tk)
+    B.oscar_norm_rope(norm, B.rope_desc(dev_f32(cs), 64, inter), tq, tk, i32(pos), qo, ko)
+    torch.cuda.synchronize()
+    for got, x, w in ((qo, q, wq), (ko, k, wk)):
+        zeros = (x == 0).all(-1, keepdims=True)
+        want, terms = rotated(np.where(zeros, 1.0, x), w, cs[pos], inter, eps)
+        want, terms = np.where(zeros, 0.0, want), np.where(zeros, 0.0, terms)
+        # below bf16's normal range a result is off by half a step of 2^-133; where eps makes them small, two products
+        # of a row's numbers below fp32's normal range by half of 2^-149 each, times the root
+        near = 2.0 ** -134 + (2.0 ** -149 / np.sqrt(eps) if eps > 2.0 ** -90 else 0.0) * np.abs(w).max()
+        assert (np.abs(host(got) - want) <= HALF_BF16 * np.abs(want) + 2.0 ** -19 * terms + near).all()
+
+
 # ---------------------------------------------------------------- append and read back
 
 APPENDS = [
@@ -409,6 +449,24 @@ def test_append_nan_and_infinity_stay_in_their_rows():
     torch.cuda.synchronize()
     for which, rows in ((0, k), (1, v)):
         O.int8_store_rows(L.pool, L.table[0, [0] * n], np.arange(n), which, *O.int8_quantize(rows, 100.0))
+    np.testing.assert_array_equal(L.gpu_pool(), L.pool)
+
+
+def test_append_of_a_key_of_zeros_without_eps():
+    """Its page holds zeros (a NaN would stand there as -tau)."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    d, hk, n = 64, 3, 5
+    L = Layer(17, [n], hk, hk, d, fill=False)
+    k, v = (O.bf16(L.g.standard_normal((n, hk, d))) for _ in range(2))
+    k[2, 1], k[3] = 0.0, 0.0
+    k[4, 2] = 2.0 ** -90
+    w = dev_bf16(np.ones(d))
+    k_out = torch.empty(n, hk, d, dtype=torch.bfloat16, device="cuda")
+    B.oscar_rope_append_int8(L.desc, B.norm_desc(w, w, 0.0), None, None, dev_bf16(k), dev_bf16(v), i32(np.zeros(n)), i32(np.arange(n)), None, k_out)
+    torch.cuda.synchronize()
+    assert (k_out[2, 1] == 0).all() and (k_out[3] == 0).all() and (k_out[4, 2] == 1).all()
+    L.put(0, np.arange(n), 0, host(k_out)), L.put(0, np.arange(n), 1, v)
     np.testing.assert_array_equal(L.gpu_pool(), L.pool)
 
 
