@@ -30,13 +30,14 @@ bool in_place_ok(const uint16_t* x, int64_t stride, const uint16_t* out, int64_t
   return x != out || stride == out_stride;
 }
 
-// The fraction of a turn, in 2^-64, that a position adds at w radians: w / 2 pi as a
-// double and its rest, so that the 64 bits are good to about 2^-100 w.
+// The fraction of a turn that a position adds at w radians, to the nearest 2^-64: w / 2 pi
+// as a double and its rest, which together are good to about 2^-104 of it.
 uint64_t turn_of(double w) {
   const double inv = 0.15915494309189535, rest = -9.839338337591243e-18;   // 1 / 2 pi
   const double t = w * inv, e = std::fma(w, inv, -t) + w * rest;
-  // t < 1 (w <= 6), and e is below 2^-53: both times 2^64 fit, and the products are exact
-  return uint64_t(t * 0x1p64) + uint64_t(int64_t(e * 0x1p64));
+  // t < 1 (w <= 6): times 2^64 it fits, and splits exactly; |e| 2^64 is below 2^11
+  const double whole = std::floor(t * 0x1p64);
+  return uint64_t(whole) + uint64_t(std::llrint((t * 0x1p64 - whole) + e * 0x1p64));
 }
 
 }  // namespace

@@ -2,7 +2,8 @@
 //
 // The angle is held as a 64-bit fraction of a turn, which wraps by itself: the
 // angle of any position is one integer product, and the next of a thread's
-// positions one addition, without rounding.  The nearest quarter turn is taken off in
+// positions one addition, without rounding beyond that of one position's turn to 2^-64
+// (at position 2^40 it makes 2^-25 of a turn).  The nearest quarter turn is taken off in
 // integers; what is left, at most an eighth of a turn (pi / 4), goes to fp32 with 24
 // bits whatever its size, and sine and cosine are their Taylor polynomials there (to
 // x^9 and x^10; the next terms are below 2e-9 and 2e-10).

@@ -770,9 +770,10 @@ oscar_status oscar_rope_frequencies(int32_t rot_dim, double theta, const oscar_r
  * then their sines, all times magnitude.
  *
  *   freq: host [rot_dim / 2], 0 <= freq <= 6 radians (of oscar_rope_frequencies, or any
- *   others; read during the call).  Angles are reduced exactly: an entry is off by
- *   2^-21 of its own size and (first + j) 2^-64 of a turn at the most, at any position.  rot_dim a
- *   multiple of 16, 16 .. 128; 0 <= first, n <= 2^40.  n = 0 is a no-op.  Async.
+ *   others; read during the call).  An entry is off by 2^-21 of its own size and
+ *   (first + j) 2^-65 of a turn at the most (the turn of one position is rounded to 2^-64;
+ *   products with it and wraps are exact).  rot_dim a multiple of 16, 16 .. 128;
+ *   0 <= first, n <= 2^40.  n = 0 is a no-op.  Async.
  */
 oscar_status oscar_rope_table(const double* freq, int32_t rot_dim, double magnitude, int64_t first, int64_t n,
                               float* cos_sin, void* stream);

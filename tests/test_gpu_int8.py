@@ -127,6 +127,31 @@ def test_table_matches_oracle(rot, n, first, magnitude):
     assert (out[n] == -9.0).all()
 
 
+@pytest.mark.parametrize("magnitude", [1.0, -3.0])
+def test_table_far_positions_within_half_a_step_a_position(magnitude):
+    """Sines next to 0 near 2^40 positions: what the step's rounding to 2^-64 of a turn leaves, (first + j) 2^-65, shows there."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    freq, _ = B.oscar_rope_frequencies(128, 1e6)
+    two_pi = 6283185307179586476925286766559005768394338798750211641949889   # times 10^-60
+    turns = []                                       # of one position, times 2^200
+    for w in freq:
+        num, den = float(w).as_integer_ratio()
+        turns.append(num * 10 ** 60 * 2 ** 200 // (den * two_pi))
+    seen = 0
+    for i, t in enumerate(turns):
+        at = range(2 ** 40 - 20000, 2 ** 40)
+        first = min(at, key=lambda p: min(p * t % 2 ** 200, -p * t % 2 ** 200))
+        out = torch.empty(1, 128, dtype=torch.float32, device="cuda")
+        B.oscar_rope_table(freq, out, magnitude=magnitude, first=first)
+        want = O.rope_table(freq, first, 1, magnitude)
+        near = 2.0 ** -21 * np.abs(want) + (2 * np.pi * first * 2.0 ** -65 + 2.0 ** -50) * abs(magnitude)
+        assert (np.abs(host(out) - want) <= near).all(), i
+        # the test sees a step off by more than that: the sine's own part of the bound is far below
+        seen += 2.0 ** -21 * abs(want[0, 64 + i]) < 0.2 * 2 * np.pi * first * 2.0 ** -66 * abs(magnitude)
+    assert seen > 20
+
+
 # ---------------------------------------------------------------- norm and rotation
 
 def rotated(x, weight, cs, inter, eps=1e-6):
