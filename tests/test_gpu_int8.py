@@ -617,6 +617,24 @@ def test_decode_shared_and_permuted_pages():
     check_decode(L, q, out, lse)
 
 
+def test_decode_bits_do_not_depend_on_the_places_of_pages():
+    """The same blocks at other places of the pool, behind another table: the same bits."""
+    import torch
+    L = Layer(6, [800, 3000, 17], 8, 2, 128)
+    q = O.bf16(L.g.standard_normal((3, 8, 128)))
+    out, lse = decode(L, q)
+    check_decode(L, q, out, lse)
+    for seed in (0, 1):
+        order = np.random.default_rng(seed).permutation(len(L.pool))     # block i goes to order[i]
+        moved = np.empty_like(L.pool)
+        moved[order] = L.pool
+        L.cache.pages.copy_(torch.from_numpy(moved.reshape(-1)))
+        L.cache.page_table.copy_(torch.from_numpy(np.where(L.table < 0, -1, order[L.table]).astype(np.int32)))
+        again, lse2 = decode(L, q)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+    assert L.status() == 0
+
+
 def test_decode_lengths_and_pages_out_of_bounds():
     import torch
     from bit_rotated_kv_split_gb300 import binding as B
