@@ -788,8 +788,9 @@ typedef struct oscar_head_norm {
 
 /*
  * oscar_norm_rope - norm and rotation of the query and key rows of n tokens, for
- * layers whose cache is filled by another call (oscar_quantize_append and
- * oscar_decode_step take keys as they come out of this one).
+ * layers whose cache is filled by another call: oscar_quantize_append and
+ * oscar_decode_step take keys as they come out of this one, and so does
+ * oscar_rope_append_int4, which has no norm of its own, without a rotation (rope NULL).
  *
  *   For item i < n: every head of q row i (q + i * q_stride, n_q_heads heads of
  *   head_dim bf16) and of k row i is normed (norm NULL, or without that weight: not)

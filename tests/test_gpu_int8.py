@@ -1009,3 +1009,30 @@ def test_rows_for_a_two_bit_layer():
     changed = (ring != cache.recent_k).reshape(-1, 256).any(1).nonzero().flatten().tolist()
     assert set(changed) <= set(src.tolist()) and torch.isfinite(out).all()
     assert int(cache.dev_status.item()) == 0
+
+
+def test_normed_heads_into_a_four_bit_layer():
+    """Heads normed and rotated by the one call, then appended without a rotation: the cache of those very rows."""
+    import torch
+    import test_gpu_int4 as F
+    from bit_rotated_kv_split_gb300 import binding as B
+    d, hq, hk, n = 128, 8, 2, 83
+    L = F.Layer(23, [n], hq, hk, d, 64, 128, fill=False)
+    q, k, v = (O.bf16(L.g.standard_normal((n, h, d))) for h in (hq, hk, hk))
+    wq, wk = (O.bf16(1 + 0.2 * L.g.standard_normal(d)) for _ in range(2))
+    cs = angles(n, d)
+    tq, tk, tv = dev_bf16(np.concatenate([q, k, v], 1)).split([hq, hk, hk], 1)
+    norm, rope = B.norm_desc(dev_bf16(wq), dev_bf16(wk)), B.rope_desc(dev_f32(cs), d)
+    req, pos = i32(np.zeros(n)), i32(np.arange(n))
+    k_rot = torch.empty(n, hk, d, dtype=torch.bfloat16, device="cuda")
+    B.oscar_norm_rope(norm, rope, tq, tk, pos, tq, k_rot)                 # the queries in place
+    B.oscar_rope_append_int4(L.desc, None, None, k_rot, tv, req, pos, None)
+    torch.cuda.synchronize()
+    for got, x, w in ((tq, q, wq), (k_rot, k, wk)):
+        want, terms = rotated(x, w, cs, False)
+        assert (np.abs(host(got) - want) <= HALF_BF16 * np.abs(want) + 2.0 ** -19 * terms).all()
+    L.k.append(L.put(0, np.arange(n), 0, host(k_rot))), L.v.append(L.put(0, np.arange(n), 1, v))
+    np.testing.assert_array_equal(L.gpu_pool(), L.pool)
+    out = host(F.run_decode(L, tq[-1:]))
+    ref, bound = F.weighted_ref(L, host(tq)[-1:])
+    assert (np.abs(out - ref) <= bound).all() and L.status() == 0
