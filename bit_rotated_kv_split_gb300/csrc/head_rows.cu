@@ -9,7 +9,7 @@
 // w_other.  C and S belong to a lane and a token, so every head of the token takes two
 // products a channel.  (With an octet a lane and its partner by shuffle, every channel
 // was unpacked twice and every row reduced by twice the lanes: 30k tokens appended in 157
-// us where two octets a lane took 149.)
+// us where two octets a lane took 149, before the steps that follow.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -217,7 +217,8 @@ __device__ __forceinline__ RowScale scale_of(const Octets& u, float tau) {
 // A quotient is taken by an approximate reciprocal and checked: its error is below
 // 255 (2^-22 + 2^-24) < 1e-4 of a step, and where the remainder t - k s (one fma) comes
 // within 2e-4 of half a step it is divided out.  (An octet at a time: with the row's
-// sixteen values at once the kernel spilled.)
+// sixteen values at once the kernel spilled more; so it spills 8 bytes, for heads of 128 in
+// halves alone.)
 __device__ __forceinline__ uint2 encode8(const uint4& u, const RowScale& r, float tau, uint4* held) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   float2 x[4];
@@ -262,8 +263,8 @@ __device__ __forceinline__ uint2 encode8(const uint4& u, const RowScale& r, floa
 // ones ahead of the token's place.
 //
 // Bound by issue and by the bytes that the warps keep in flight (30k tokens appended, 821
-// MB: 144 us, 5.7 TB/s, 84 % of a plain copy's rate, issue 62 %; the
-// quantisation costs some 19 us of it; normed and rotated only, 634 MB: 96 us, 97 %).  Set
+// MB: 145 us, 5.6 TB/s, 83 % of a plain copy's rate, issue 62 %; the
+// quantisation costs some 19 us of it; normed and rotated only, 634 MB: 97 us, 96 %).  Set
 // aside, each measured on the append when it took 149: rows by bulk copies into rings
 // that run ahead over several tokens (176: more instructions a row), k and v rows side
 // by side (151, spilled), q rows and k, v rows in CTAs of their own (157), four or six CTAs

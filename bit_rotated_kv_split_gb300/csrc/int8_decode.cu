@@ -6,10 +6,10 @@
 // last CTA of a run to finish joins its parts.
 //
 // Bound by HBM where it is long: 8 requests of 100k tokens (8 KV heads x 128, 1.69 GB)
-// take 247 us, 6.85 TB/s, the rate of a plain copy.  One of them (211 MB, 31 us at that
+// take 244 to 247 us, 6.85 TB/s, the rate of a plain copy.  One of them (211 MB, 31 us at that
 // rate) takes 41.0: shares 1.2 us, first pages at 3 to 5, scans done at 31 to 34, warps'
 // joins by 34.7, tickets by 35.6, last parts joined at 39 to 40.  28 ragged requests of
-// 2k to 32k (654 MB, 96 us): 109 us, their scans done over 20 us (the memory serves SMs
+// 2k to 32k (654 MB, 96 us), scores capped: 109 us, their scans done over 20 us (the memory serves SMs
 // unevenly by some 8 %, and the work is dealt out beforehand).
 //
 // A warp takes every 6th page (or pair of pages) of a run with an online softmax of its own, so

@@ -1,5 +1,5 @@
 // Device side of the score's form (scale, cap, distance bias, window),
-// shared by the 4-bit decode and the prompt attention.
+// shared by the decodes over paged layers and the prompt attention.
 #pragma once
 
 #include <cfloat>
