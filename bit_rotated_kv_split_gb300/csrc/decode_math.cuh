@@ -48,18 +48,19 @@ __device__ __forceinline__ int scale_exponent(uint32_t bits) {
 // A query head with a largest channel in [2^(ex - 127), 2^(ex - 126)), 14 <= ex <= 254 (every
 // finite bf16), is held times 2^(141 - ex) beside codes times 2^-24, so its dot products are
 // to be multiplied by 2^(ex - 117), which may pass fp32's end.  With a cap they are taken
-// to 2^-11 of themselves, and capped() has constants to match (in_units).  Without one the
-// score's scale is in the factor too, and where that passes fp32's end only a dot product
-// of 0 gives a score within bounds: it is to stay 0.
-constexpr float kUnits = 2048.f;
+// to s.unit of themselves, and capped() has constants to match (in_units).  Without
+// one the score's scale is in the factor too, and where that passes fp32's end only a dot
+// product of 0 gives a score within bounds: it is to stay 0.
+// (A scale of 2^100 would take the constants past fp32's end; scores of large queries are
+// far beyond any cap then.)
 __device__ __forceinline__ float unscale_of(int ex, const ScoreParams& s) {
   const float f = pow2i(ex - 128);
-  return s.cap_log2 != 0.f ? f : fminf(f * s.scale_log2 * kUnits, FLT_MAX);
+  return fminf(s.cap_log2 != 0.f ? f * (2048.f * s.unit) : f * s.scale_log2 * 2048.f, FLT_MAX);
 }
 inline ScoreParams in_units(ScoreParams s) {
-  const auto times = [](float x) { return std::min(std::max(x * kUnits, -FLT_MAX), FLT_MAX); };
-  s.cap_in = times(s.cap_in);
-  for (float& c : s.cap_near) c = times(c);
+  s.unit = s.scale_log2 < 0x1p100f ? 0x1p-11f : 1.f;
+  s.cap_in = std::min(s.cap_in / s.unit, FLT_MAX);   // (past it only with a cap that is next to nothing)
+  for (float& c : s.cap_near) c /= s.unit;
   return s;
 }
 

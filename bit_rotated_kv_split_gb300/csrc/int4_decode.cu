@@ -240,7 +240,7 @@ __device__ __noinline__ void scan_wide(const Int4DecodeParams& p, Walk walk, int
 #pragma unroll
         for (int h = 0; h < kJoinHeads; ++h) {
           float y = x[h] + __shfl_xor_sync(0xffffffffu, x[h], 16);
-          y = p.s.cap_log2 != 0.f ? capped(y * (1.f / kUnits), p.s) : y * p.s.scale_log2;
+          y = p.s.cap_log2 != 0.f ? capped(y * p.s.unit, p.s) : y * p.s.scale_log2;
           y = j >= cur.first && j < cur.len ? fmaf(slope[h], float(j - (cur.len - 1)), y) : -INFINITY;
           float mn = fmaxf(m[h], y);
 #pragma unroll

@@ -787,6 +787,27 @@ def test_decode_largest_queries_on_keys_of_zeros(hq, softcap):
     assert (np.abs(out - ref) <= bound).all()
 
 
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+@pytest.mark.parametrize("d,hq,gk,gv", [(128, 4, 128, 32), (64, 9, 64, 64)])
+def test_decode_smallest_queries_with_scales_to_match(d, hq, gk, gv, softcap):
+    """Queries of 2^-120 and a scale of 2^120: ordinary scores, also where the values' scales lie far apart."""
+    import torch
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(99, [700, 48, 1], hq, 1, d, gk, gv)
+    big = np.ones((1, 1, d))
+    big[..., 5] = 2.0 ** 15
+    L.v[0][300] = L.put(0, [300], 1, big)[0]         # (a second scan)
+    L.cache.pages.copy_(torch.from_numpy(L.pool.reshape(-1)))
+    q = O.bf16(L.g.standard_normal((3, hq, d)))
+    q = np.where(np.abs(q) < 2.0 ** -6, 0.0, q) * 2.0 ** -120
+    scale = float(np.float32(2.0 ** 120 / np.sqrt(d)))
+    tq = dev_bf16(q)
+    assert (host(tq) == q).all()
+    out = host(run_decode(L, tq, B.score_desc(scale, softcap, 0, None)))
+    ref, bound = weighted_ref(L, q, scale=scale, softcap=softcap)
+    assert (np.abs(out - ref) <= bound).all()
+
+
 @pytest.mark.parametrize("lens,hq,hk,d,gk,gv,mods", RAGGED + DECODES)
 def test_decode_within_the_weighted_bound(lens, hq, hk, d, gk, gv, mods):
     """The batches above with each key's error counted with its weight, which for long requests is a small part of what the

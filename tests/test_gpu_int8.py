@@ -736,6 +736,21 @@ def test_decode_largest_queries_on_keys_of_zeros(hq, softcap):
     check_decode(L, q, out, lse, softcap=softcap)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+@pytest.mark.parametrize("hq,d", [(4, 128), (9, 64)])
+def test_decode_smallest_queries_with_scales_to_match(hq, d, softcap):
+    """Queries of 2^-120 and a scale of 2^120: ordinary scores."""
+    from bit_rotated_kv_split_gb300 import binding as B
+    L = Layer(18, [700, 48, 1], hq, 1, d)
+    q = O.bf16(L.g.standard_normal((3, hq, d)))
+    q = np.where(np.abs(q) < 2.0 ** -6, 0.0, q) * 2.0 ** -120
+    scale = float(np.float32(2.0 ** 120 / np.sqrt(d)))
+    tq = dev_bf16(q)
+    assert (host(tq) == q).all()
+    out, lse = decode(L, tq, B.score_desc(scale, softcap))
+    check_decode(L, q, out, lse, scale=scale, softcap=softcap)
+
+
 @pytest.mark.parametrize("ratio", [2.0 ** -14, 2.0 ** -20])
 def test_decode_values_far_below_anothers_keep_their_bits(ratio):
     """A token of large values and no weight beside small ones that have all of it."""
